@@ -412,6 +412,113 @@ pkv_status pkv_merge_states_bf16(const void* o_parts, const float* lse_parts, in
                                  int32_t num_rows, int32_t num_heads, int32_t head_dim, void* out,
                                  float* lse, void* stream);
 
+/*
+ * Rotary append, for every pairing and width: pkv_rope_kv_append (half-split pairs over the whole
+ * head, Q in place) with
+ *   rotary_dim    R, even, 2 <= R <= head_dim: the first R values of each head are rotated, the rest
+ *                 pass through (partial rotary)
+ *   interleaved   0: pair i is (i, i + R/2) (half-split);  non-zero: (2i, 2i + 1) (neighbours)
+ *   cos_sin       fp32 [max_position, R] (device), 16-byte aligned: row p holds the cosines of pairs
+ *                 0 .. R/2 - 1, then their sines (pkv_rotary_cos_sin_table, or the caller's own)
+ *   q, q_out      both null (num_q_heads 0), or bf16 [num_tokens, num_q_heads, head_dim]: q_out
+ *                 receives the rotated Q; it is q itself (in place) or does not overlap it
+ * For pair (a, b) and position p: x'[a] = x[a] cos - x[b] sin, x'[b] = x[b] cos + x[a] sin, in fp32
+ * with one rounding.  Positions, slots, padding tokens (slot < 0: K/V not written, Q rotated) and
+ * err_word as for pkv_rope_kv_append.  head_dim a multiple of 8, at most 256; num_tokens *
+ * (2 * num_kv_heads + num_q_heads) < 2^31.
+ */
+pkv_status pkv_rotary_kv_append(const pkv_pool* pool, const void* k_new, const void* v_new,
+                                const int64_t* slot_mapping, const int32_t* positions,
+                                const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                                int32_t interleaved, const void* q, void* q_out, int32_t num_q_heads,
+                                int32_t num_tokens, uint32_t* err_word, void* stream);
+
+/*
+ * The cos/sin table pkv_rotary_kv_append reads, with a long-context scaling of the frequencies
+ * f_i = theta^(-2i/R), i < R/2 (scaling NULL or PKV_ROPE_UNSCALED: none).  Row p of table fp32
+ * [max_position, rotary_dim] receives cos(p f'_i) m, then sin(p f'_i) m; angles in double precision,
+ * rounded once.  m = 1 except for YARN.
+ *   PKV_ROPE_LINEAR  f' = f / factor (position interpolation)
+ *   PKV_ROPE_BANDED  with turns = original_max_position f / (2 pi): f' = f above `high` turns,
+ *                    f / factor below `low`, and s f + (1 - s) f / factor between, s = (turns - low) /
+ *                    (high - low) (the frequency bands of HF Llama checkpoints' long-context
+ *                    scaling: low 1, high 4)
+ *   PKV_ROPE_YARN    (Peng et al., "YaRN", 2023; theta > 1) with dim(b) = R ln(original_max_position /
+ *                    (2 pi b)) / (2 ln theta), lo = max(floor(dim(high)), 0), hi = min(ceil(dim(low)),
+ *                    R - 1): ramp_i = clamp((i - lo) / (hi - lo), 0, 1), f' = f / factor ramp_i +
+ *                    f (1 - ramp_i); low and high are its beta_slow and beta_fast (1 and 32);
+ *                    m = attention_factor (0.1 ln(factor) + 1 in the paper)
+ * factor >= 1, 0 < low < high, original_max_position > 0, attention_factor > 0 where they are used.
+ */
+typedef enum {
+  PKV_ROPE_UNSCALED = 0,
+  PKV_ROPE_LINEAR = 1,
+  PKV_ROPE_BANDED = 2,
+  PKV_ROPE_YARN = 3
+} pkv_rope_scaling_kind;
+
+typedef struct {
+  int32_t kind; /* pkv_rope_scaling_kind */
+  double factor;
+  double original_max_position;
+  double low;
+  double high;
+  double attention_factor;
+} pkv_rope_scaling;
+
+pkv_status pkv_rotary_cos_sin_table(float* table, int32_t max_position, int32_t rotary_dim, double theta,
+                                    const pkv_rope_scaling* scaling, void* stream);
+
+/*
+ * The 8-bit cache.  K and V are held as e4m3 with one fp32 scale per row and head: the value at
+ * (slot, head, d) is k8[slot, head, d] * k_scale[slot, head].  What the appends write: k8 =
+ * e4m3(x / scale), rounded to nearest even, with the smallest power of two scale >= 2^-126 for which
+ * the row's largest finite |x| is at most 448 scale; a NaN or an infinity is stored as NaN and does
+ * not count for the scale, and what would round up to 2^128 is stored as 240 * 2^120.  The attention and the read-back take any scale that is positive and a
+ * normal fp32 number (a calibrated one per head, say); for powers of two reading back is exact.
+ */
+typedef struct {
+  void* k;              /* e4m3 [num_pages, page_size, num_kv_heads, head_dim], 16-byte aligned */
+  void* v;              /* same shape as k */
+  float* k_scale;       /* fp32 [num_pages, page_size, num_kv_heads], 16-byte aligned */
+  float* v_scale;       /* same shape as k_scale */
+  int64_t num_pages;
+  int32_t page_size;    /* >= 1 */
+  int32_t num_kv_heads; /* >= 1 */
+  int32_t head_dim;     /* attention: 64 or 128; append and read-back: any multiple of 8 */
+} pkv_pool_fp8;
+
+/*
+ * pkv_kv_append and pkv_rotary_kv_append into an 8-bit cache.  K (rotated in fp32, not rounded in
+ * between) and V are quantised as they are written; Q, where given, is rotated to bf16.  Arguments,
+ * limits and errors as for pkv_rotary_kv_append; slots must be distinct within one call.
+ */
+pkv_status pkv_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new, const void* v_new,
+                             const int64_t* slot_mapping, int32_t num_tokens, uint32_t* err_word,
+                             void* stream);
+pkv_status pkv_rotary_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new, const void* v_new,
+                                    const int64_t* slot_mapping, const int32_t* positions,
+                                    const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                                    int32_t interleaved, const void* q, void* q_out, int32_t num_q_heads,
+                                    int32_t num_tokens, uint32_t* err_word, void* stream);
+
+/*
+ * Read-back of an 8-bit cache: position j < kv_lens[b] of request b goes to row out_indptr[b] + j
+ * of k_out and v_out as bf16(k8 * k_scale).  Other rows are left as they were.  With out_indptr at
+ * multiples of a page size the copy is a paged cache itself, for the calls that read bf16 (an
+ * extend over cached prefixes, say).
+ *   kv_indptr, kv_indices, kv_lens  as for pkv_paged_gather; kv_lens[b] >= 0
+ *   out_indptr    int32 [batch_size+1] (device), non-decreasing
+ *   k_out, v_out  bf16 [num_out_rows, num_kv_heads, head_dim] (device), 16-byte aligned
+ *   err_word      nullable; PKV_DEVERR_LENGTH for a request longer than its pages or than
+ *                 out_indptr[b+1] - out_indptr[b] (its rows past those are not written), PKV_DEVERR_ROW_OOB for
+ *                 rows outside the output, PKV_DEVERR_PAGE_OOB
+ */
+pkv_status pkv_paged_gather_fp8(const pkv_pool_fp8* pool, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, const int32_t* kv_lens, int32_t batch_size,
+                                const int32_t* out_indptr, int32_t num_out_rows, void* k_out, void* v_out,
+                                uint32_t* err_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

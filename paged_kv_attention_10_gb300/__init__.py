@@ -12,6 +12,7 @@ Names follow the C ABI in ``include/pagedkv.h`` (``pkv_kv_append`` -> ``kv_appen
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -22,7 +23,8 @@ __all__ = [
     "paged_decode", "paged_decode_noalloc", "extend_workspace_size", "paged_extend",
     "merge_states", "shared_prefix_workspace_size", "shared_prefix_attention", "cascade_decode",
     "status_string", "version", "selftest_bounded_wait", "validate_page_table", "validate_slots",
-    "rope_cos_sin_table", "rope_kv_append", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
+    "rope_cos_sin_table", "rope_kv_append", "rotary_kv_append", "rotary_cos_sin_table",
+    "kv_append_fp8", "rotary_kv_append_fp8", "paged_gather_fp8", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
     "DEVERR_TIMEOUT", "DEVERR_INTERNAL", "DEVERR_ROW_OOB",
 ]
 
@@ -50,6 +52,16 @@ class CascadeSizes(ctypes.Structure):
                 ("num_part_indices", _c_i32), ("num_suffix_indices", _c_i32)]
 
 
+class PoolFP8(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _c_i64),
+                ("page_size", _c_i32), ("num_kv_heads", _c_i32), ("head_dim", _c_i32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", _c_i32), ("factor", ctypes.c_double), ("original_max_position", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("attention_factor", ctypes.c_double)]
+
+
 class PagedKVError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -69,6 +81,7 @@ def load():
         raise RuntimeError(f"{_LIB_PATH} is not built; run paged_kv_attention_10_gb300.build.build()")
     lib = ctypes.CDLL(_LIB_PATH)
     P = ctypes.POINTER(Pool)
+    P8 = ctypes.POINTER(PoolFP8)
     sig = {
         "pkv_status_string": (ctypes.c_char_p, [_c_i32]),
         "pkv_version": (_c_i32, []),
@@ -101,6 +114,14 @@ def load():
                                             _c_i32, _c_i32, _c_i32, _c_i32, ctypes.POINTER(CascadeSizes),
                                             _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i32,
                                             _c_i32]),
+        "pkv_rotary_kv_append": (_c_i32, [P, _vp, _vp, _vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _vp, _vp,
+                                          _c_i32, _c_i32, _vp, _vp]),
+        "pkv_rotary_cos_sin_table": (_c_i32, [_vp, _c_i32, _c_i32, ctypes.c_double,
+                                              ctypes.POINTER(RopeScaling), _vp]),
+        "pkv_kv_append_fp8": (_c_i32, [P8, _vp, _vp, _vp, _c_i32, _vp, _vp]),
+        "pkv_rotary_kv_append_fp8": (_c_i32, [P8, _vp, _vp, _vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _vp,
+                                              _vp, _c_i32, _c_i32, _vp, _vp]),
+        "pkv_paged_gather_fp8": (_c_i32, [P8, _vp, _vp, _vp, _c_i32, _vp, _c_i32, _vp, _vp, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -501,3 +522,161 @@ def cascade_decode(q, k_pool, v_pool, plan, sm_scale: float, out=None, lse=None,
                  sm_scale, out=o_parts[S], lse=lse_parts[S], workspace=decode_workspace,
                  err_word=err_word, stream=stream)
     return merge_states(o_parts, lse_parts, out=out, lse=lse, stream=stream)
+
+
+# ---------------------------------------------------------------------------------------------
+# rotary append, 8-bit cache
+# ---------------------------------------------------------------------------------------------
+def _pool_fp8(k_pool, v_pool, k_scale, v_scale) -> PoolFP8:
+    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"{n} must be torch.float8_e4m3fn (or its bytes as torch.uint8), got {t.dtype}")
+        _need(t, n, t.dtype, k_pool.device)
+    _need(k_scale, "k_scale", torch.float32, k_pool.device)
+    _need(v_scale, "v_scale", torch.float32, k_pool.device)
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must both be [num_pages, page_size, num_kv_heads, head_dim]")
+    if k_scale.shape != k_pool.shape[:3] or v_scale.shape != k_scale.shape:
+        raise ValueError("k_scale and v_scale must both be [num_pages, page_size, num_kv_heads]")
+    n, ps, hkv, d = k_pool.shape
+    return PoolFP8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, ps, hkv, d)
+
+
+def _run(dev, stream, fn: str, *args):
+    """_call on dev's current stream (or the given one); dev is made current only when it is not."""
+    if torch.cuda.current_device() == dev.index:
+        _call(fn, *args, _stream_ptr(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            _call(fn, *args, _stream_ptr(stream, dev))
+
+
+def _new_rows(pool, dev, k_new, v_new, slot_mapping, err_word):
+    """Check the new rows of an append; returns the number of tokens."""
+    _need(k_new, "k_new", torch.bfloat16, dev)
+    _need(v_new, "v_new", torch.bfloat16, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    if err_word is not None:
+        _need(err_word, "err_word", torch.int32, dev)
+    T = slot_mapping.numel()
+    if k_new.shape != (T, pool.num_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
+        raise ValueError("k_new/v_new must be [num_tokens, num_kv_heads, head_dim]")
+    return T
+
+
+def _rotary(fn, pool, dev, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out, interleaved,
+            err_word, stream):
+    T = _new_rows(pool, dev, k_new, v_new, slot_mapping, err_word)
+    _need(positions, "positions", torch.int32, dev)
+    _need(cos_sin, "cos_sin", torch.float32, dev)
+    if positions.numel() != T or cos_sin.dim() != 2:
+        raise ValueError("positions must be [num_tokens] and cos_sin [max_position, rotary_dim]")
+    max_position, rotary_dim = cos_sin.shape
+    if rotary_dim % 2 or not 2 <= rotary_dim <= pool.head_dim:
+        raise ValueError("cos_sin's rotary_dim must be even and at most head_dim")
+    Hq = 0
+    if q is not None:
+        _need(q, "q", torch.bfloat16, dev)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != pool.head_dim:
+            raise ValueError("q must be [num_tokens, num_q_heads, head_dim]")
+        if q_out is None:
+            q_out = q
+        _need(q_out, "q_out", torch.bfloat16, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        Hq = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _run(dev, stream, fn, ctypes.byref(pool), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(positions),
+         _ptr(cos_sin), max_position, rotary_dim, int(bool(interleaved)), _ptr(q), _ptr(q_out), Hq, T,
+         _ptr(err_word))
+
+
+def rotary_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, positions, cos_sin, q=None, q_out=None,
+                     interleaved: bool = False, err_word=None, stream=None) -> None:
+    """Rotate k_new (and q into q_out, in place when q_out is None) by their positions and write K/V
+    into the pool slots.  The first cos_sin.shape[1] values of each head are rotated, in half-split
+    or (``interleaved``) neighbouring pairs; negative slots are padding."""
+    pool = _pool(k_pool, v_pool)
+    _rotary("pkv_rotary_kv_append", pool, k_pool.device, k_new, v_new, slot_mapping, positions, cos_sin,
+            q, q_out, interleaved, err_word, stream)
+
+
+def rotary_kv_append_fp8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, positions, cos_sin,
+                         q=None, q_out=None, interleaved: bool = False, err_word=None, stream=None) -> None:
+    """rotary_kv_append into an 8-bit cache: K (rotated) and V quantised to e4m3 as they are written,
+    with a power-of-two scale per row and head."""
+    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    _rotary("pkv_rotary_kv_append_fp8", pool, k_pool.device, k_new, v_new, slot_mapping, positions, cos_sin,
+            q, q_out, interleaved, err_word, stream)
+
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "banded": 2, "yarn": 3}
+
+
+def rotary_cos_sin_table(max_position: int, rotary_dim: int, theta: float, scaling: str = "none",
+                         factor: float = 1.0, original_max_position: float = 0.0,
+                         low: Optional[float] = None, high: Optional[float] = None,
+                         attention_factor: Optional[float] = None, device=None, out=None,
+                         stream=None) -> torch.Tensor:
+    """The fp32 [max_position, rotary_dim] cos/sin table rotary_kv_append reads, with the frequencies
+    scaled for long contexts: "none", "linear" (divided by factor), "banded" (low/high turns over the
+    original context, 1 and 4 by default) or "yarn" (beta_slow/beta_fast, 1 and 32 by default;
+    attention_factor 0.1 ln(factor) + 1 by default).  Built once, like a model's rotary buffer."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
+    if low is None:
+        low = 1.0
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    if attention_factor is None:
+        attention_factor = 0.1 * math.log(factor) + 1.0 if factor > 0 else 1.0
+    spec = RopeScaling(_ROPE_SCALING[scaling], float(factor), float(original_max_position), float(low),
+                       float(high), float(attention_factor))
+    dev = torch.device(device) if device is not None else torch.device("cuda")
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if out is None:
+        out = torch.empty((max_position, rotary_dim), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float32, dev)
+    if out.shape != (max_position, rotary_dim):
+        raise ValueError("out must be [max_position, rotary_dim]")
+    _run(dev, stream, "pkv_rotary_cos_sin_table", _ptr(out), int(max_position), int(rotary_dim), float(theta),
+         ctypes.byref(spec))
+    return out
+
+
+def kv_append_fp8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, err_word=None,
+                  stream=None) -> None:
+    """Quantise k_new[t], v_new[t] to e4m3 with a power-of-two scale per row and head and write them
+    into pool slot slot_mapping[t] (negative = skip)."""
+    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    dev = k_pool.device
+    T = _new_rows(pool, dev, k_new, v_new, slot_mapping, err_word)
+    _run(dev, stream, "pkv_kv_append_fp8", ctypes.byref(pool), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T,
+         _ptr(err_word))
+
+
+def paged_gather_fp8(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, out_indptr, k_out,
+                     v_out, err_word=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Read an 8-bit cache back as bf16: position j of request b goes to row out_indptr[b] + j of
+    k_out/v_out [num_out_rows, num_kv_heads, head_dim]; other rows are left as they were."""
+    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    dev = k_pool.device
+    for t, n in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"), (kv_lens, "kv_lens"),
+                 (out_indptr, "out_indptr")):
+        _need(t, n, torch.int32, dev)
+    _need(k_out, "k_out", torch.bfloat16, dev)
+    _need(v_out, "v_out", torch.bfloat16, dev)
+    if err_word is not None:
+        _need(err_word, "err_word", torch.int32, dev)
+    B = kv_lens.numel()
+    if kv_indptr.numel() != B + 1 or out_indptr.numel() != B + 1:
+        raise ValueError("kv_indptr and out_indptr must have batch_size + 1 entries")
+    if k_out.dim() != 3 or k_out.shape[1:] != (pool.num_kv_heads, pool.head_dim) or v_out.shape != k_out.shape:
+        raise ValueError("k_out/v_out must be [num_out_rows, num_kv_heads, head_dim]")
+    _run(dev, stream, "pkv_paged_gather_fp8", ctypes.byref(pool), _ptr(kv_indptr), _ptr(kv_indices),
+         _ptr(kv_lens), B, _ptr(out_indptr), k_out.shape[0], _ptr(k_out), _ptr(v_out), _ptr(err_word))
+    return k_out, v_out

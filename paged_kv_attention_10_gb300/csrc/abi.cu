@@ -6,6 +6,7 @@
 #include <utility>
 #include <vector>
 
+#include "quant.cuh"
 #include "tc05.cuh"
 
 namespace pkv_host {
@@ -43,6 +44,13 @@ bool valid_pool(const pkv_pool* p) {
   if ((p->head_dim % 8) != 0) return false;
   if (!aligned16(p->k) || !aligned16(p->v)) return false;
   return true;
+}
+
+bool valid_pool8(const pkv_pool_fp8* p) {
+  if (!p || !p->k || !p->v || !p->k_scale || !p->v_scale) return false;
+  if (p->num_pages <= 0 || p->page_size <= 0 || p->num_kv_heads <= 0 || p->head_dim <= 0) return false;
+  if ((p->head_dim % 8) != 0) return false;
+  return aligned16(p->k) && aligned16(p->v) && aligned16(p->k_scale) && aligned16(p->v_scale);
 }
 
 namespace {

@@ -1,0 +1,163 @@
+// Read-back of an 8-bit paged cache: every request's rows in position order as bf16.
+//
+// bf16(x8 * scale) per value: exact for the power-of-two scales the append writes.  Bound by HBM
+// (one byte in, two out).  A CTA takes tiles of 16 output rows: 16 threads find the request of a row
+// by binary search over out_indptr (which its L1 holds after the first tile) and the row's slot,
+// then all threads copy 8 values at a time, K and V, with the loads of several chunks in flight.
+#include "quant.cuh"
+
+namespace {
+
+using namespace pkv;
+
+constexpr int kRows = 16;
+constexpr int kThreads = 256;
+
+struct GatherArgs {
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* kv_lens;
+  const int32_t* out_indptr;
+  int32_t batch, num_out_rows, page_size, Hkv;
+  int64_t num_pages;
+  FastDiv cpr;  // 8-value chunks of a token row
+  FastDiv cph;  // ... of a head
+  uint4* k_out;
+  uint4* v_out;
+  uint32_t* err_word;
+};
+
+PKV_DEV uint4 dequant8(uint2 u, float s) {
+  uint32_t h[4];
+  unpack_e4m3x4(u.x, h[0], h[1]);
+  unpack_e4m3x4(u.y, h[2], h[3]);
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    r[i] = pack_bf16x2(f.x * s, f.y * s);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Slot of output row `row`, or -1: a row of no request, behind its request's end, or of a bad page.
+PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
+  int lo = 0, hi = a.batch;  // the last b in [0, batch] with out_indptr[b] <= row
+  if (row < __ldg(a.out_indptr)) return -1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(a.out_indptr + mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  if (lo == a.batch) return -1;
+  const int32_t j = row - __ldg(a.out_indptr + lo);
+  if (j < 0 || j >= __ldg(a.kv_lens + lo)) return -1;
+  const int32_t p0 = __ldg(a.kv_indptr + lo), np = __ldg(a.kv_indptr + lo + 1) - p0;
+  const int32_t pidx = j / a.page_size;
+  if (pidx >= np) {
+    report(a.err_word, PKV_DEVERR_LENGTH);
+    return -1;
+  }
+  const int32_t page = __ldg(a.kv_indices + p0 + pidx);
+  if (page < 0 || page >= a.num_pages) {
+    report(a.err_word, PKV_DEVERR_PAGE_OOB);
+    return -1;
+  }
+  return (int64_t)page * a.page_size + (j - pidx * a.page_size);
+}
+
+__global__ void __launch_bounds__(kThreads) paged_gather8_kernel(const __grid_constant__ GatherArgs a) {
+  __shared__ int64_t s_slot[2][kRows];
+  // what the copies below cannot see: a request whose rows do not hold its length, or lie outside out
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.batch; b += gridDim.x * kThreads) {
+    const int64_t o0 = __ldg(a.out_indptr + b), o1 = __ldg(a.out_indptr + b + 1);
+    const int32_t n = __ldg(a.kv_lens + b);
+    if (n < 0 || n > o1 - o0) report(a.err_word, PKV_DEVERR_LENGTH);
+    if (n > 0 && (o0 < 0 || o0 + n > a.num_out_rows)) report(a.err_word, PKV_DEVERR_ROW_OOB);
+  }
+  const uint32_t cpr = a.cpr.d;
+  const uint2* k8 = reinterpret_cast<const uint2*>(a.k_pool);
+  const uint2* v8 = reinterpret_cast<const uint2*>(a.v_pool);
+  const int tiles = (a.num_out_rows + kRows - 1) / kRows;
+  int buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    const int32_t row0 = tile * kRows;
+    if (threadIdx.x < kRows)
+      s_slot[buf][threadIdx.x] = row0 + (int)threadIdx.x < a.num_out_rows ? find_slot(a, row0 + threadIdx.x) : -1;
+    __syncthreads();  // one per tile: the next tile's slots go to the other buffer
+    const uint32_t n = kRows * cpr;
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * kThreads) {
+      uint2 k[4], v[4];
+      float ks[4], vs[4];
+      bool on[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t i = i0 + u * kThreads;
+        uint32_t r, c;
+        a.cpr.divmod(i < n ? i : 0, r, c);
+        const int64_t slot = s_slot[buf][r];
+        on[u] = i < n && slot >= 0;
+        if (on[u]) {
+          const int64_t src = slot * cpr + c;
+          k[u] = __ldg(k8 + src);
+          v[u] = __ldg(v8 + src);
+          const int64_t hs = slot * a.Hkv + a.cph.quot(c);
+          ks[u] = __ldg(a.k_scale + hs);
+          vs[u] = __ldg(a.v_scale + hs);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (on[u]) {
+          const int64_t dst = (int64_t)row0 * cpr + i0 + u * kThreads;
+          a.k_out[dst] = dequant8(k[u], ks[u]);
+          a.v_out[dst] = dequant8(v[u], vs[u]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+extern "C" pkv_status pkv_paged_gather_fp8(const pkv_pool_fp8* pool, const int32_t* kv_indptr,
+                                           const int32_t* kv_indices, const int32_t* kv_lens,
+                                           int32_t batch_size, const int32_t* out_indptr,
+                                           int32_t num_out_rows, void* k_out, void* v_out,
+                                           uint32_t* err_word, void* stream) {
+  pkv_host::NvtxRange nvtx_range("pkv_paged_gather_fp8");
+  if (!pkv_host::valid_pool8(pool) || batch_size < 0 || num_out_rows < 0) return PKV_ERR_INVALID_ARG;
+  if (batch_size == 0 || num_out_rows == 0) return PKV_OK;
+  if (!kv_indptr || !kv_indices || !kv_lens || !out_indptr || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
+  if (!pkv_host::aligned16(k_out) || !pkv_host::aligned16(v_out)) return PKV_ERR_INVALID_ARG;
+  const int64_t cpr = (int64_t)pool->num_kv_heads * (pool->head_dim / 8);
+  if (cpr > 0x7fffffffLL / kRows || num_out_rows > 0x7fffffff - kRows) return PKV_ERR_UNSUPPORTED;
+  GatherArgs a;
+  a.k_pool = (const uint8_t*)pool->k;
+  a.v_pool = (const uint8_t*)pool->v;
+  a.k_scale = pool->k_scale;
+  a.v_scale = pool->v_scale;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.kv_lens = kv_lens;
+  a.out_indptr = out_indptr;
+  a.batch = batch_size;
+  a.num_out_rows = num_out_rows;
+  a.page_size = pool->page_size;
+  a.Hkv = pool->num_kv_heads;
+  a.num_pages = pool->num_pages;
+  a.cpr = FastDiv((uint32_t)cpr);
+  a.cph = FastDiv((uint32_t)(pool->head_dim / 8));
+  a.k_out = (uint4*)k_out;
+  a.v_out = (uint4*)v_out;
+  a.err_word = err_word;
+  int64_t blocks = (num_out_rows + kRows - 1) / kRows;
+  const int64_t cap = (int64_t)pkv_host::sm_count() * 8;
+  if (cap > 0 && blocks > cap) blocks = cap;
+  paged_gather8_kernel<<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(a);
+  return pkv_host::launch_status();
+}
