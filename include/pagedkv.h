@@ -519,6 +519,22 @@ pkv_status pkv_paged_gather_fp8(const pkv_pool_fp8* pool, const int32_t* kv_indp
                                 const int32_t* out_indptr, int32_t num_out_rows, void* k_out, void* v_out,
                                 uint32_t* err_word, void* stream);
 
+/*
+ * Paged decode over an 8-bit cache: pkv_paged_decode_ctas with the values k8 k_scale and v8 v_scale.
+ * Page lists, q, out, lse, max_ctas, errors and the treatment of kv_lens[b] == 0 as there;
+ * head_dim 64 or 128, num_q_heads / num_kv_heads <= 16.  The softmax weights (times v_scale) are
+ * rounded to f16 for the second product; sums are fp32.
+ *   workspace  device, 256-byte aligned, at least pkv_decode_fp8_workspace_size(...) bytes; needs no
+ *              initialisation, and is not shared with a call in flight on another stream
+ */
+size_t pkv_decode_fp8_workspace_size(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim);
+pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t batch_size,
+                                int32_t num_q_heads, const int32_t* kv_indptr, const int32_t* kv_indices,
+                                const int32_t* kv_lens, float sm_scale, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                                int32_t max_ctas, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

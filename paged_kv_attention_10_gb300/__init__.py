@@ -24,7 +24,8 @@ __all__ = [
     "merge_states", "shared_prefix_workspace_size", "shared_prefix_attention", "cascade_decode",
     "status_string", "version", "selftest_bounded_wait", "validate_page_table", "validate_slots",
     "rope_cos_sin_table", "rope_kv_append", "rotary_kv_append", "rotary_cos_sin_table",
-    "kv_append_fp8", "rotary_kv_append_fp8", "paged_gather_fp8", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
+    "kv_append_fp8", "rotary_kv_append_fp8", "paged_gather_fp8",
+    "decode_fp8_workspace_size", "paged_decode_fp8", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
     "DEVERR_TIMEOUT", "DEVERR_INTERNAL", "DEVERR_ROW_OOB",
 ]
 
@@ -121,6 +122,9 @@ def load():
         "pkv_kv_append_fp8": (_c_i32, [P8, _vp, _vp, _vp, _c_i32, _vp, _vp]),
         "pkv_rotary_kv_append_fp8": (_c_i32, [P8, _vp, _vp, _vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _vp,
                                               _vp, _c_i32, _c_i32, _vp, _vp]),
+        "pkv_decode_fp8_workspace_size": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
+        "pkv_paged_decode_fp8": (_c_i32, [P8, _vp, _c_i32, _c_i32, _vp, _vp, _vp, _c_f32, _vp, _vp, _vp,
+                                          _c_sz, _vp, _c_i32, _vp]),
         "pkv_paged_gather_fp8": (_c_i32, [P8, _vp, _vp, _vp, _c_i32, _vp, _c_i32, _vp, _vp, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
@@ -680,3 +684,60 @@ def paged_gather_fp8(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv
     _run(dev, stream, "pkv_paged_gather_fp8", ctypes.byref(pool), _ptr(kv_indptr), _ptr(kv_indices),
          _ptr(kv_lens), B, _ptr(out_indptr), k_out.shape[0], _ptr(k_out), _ptr(v_out), _ptr(err_word))
     return k_out, v_out
+
+
+def decode_fp8_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim, device=None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(load().pkv_decode_fp8_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim))
+
+
+def _attention_io(q, dev, rows, out, lse, return_lse, err_word):
+    """Check (or make) the outputs of an attention call over q [N, Hq, D]; rows: N, if it is known."""
+    _need(q, "q", torch.bfloat16, dev)
+    if q.dim() != 3 or (rows is not None and q.shape[0] != rows):
+        raise ValueError("q must be [num_rows, num_q_heads, head_dim]")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [num_rows, num_q_heads]")
+    if err_word is not None:
+        _need(err_word, "err_word", torch.int32, dev)
+    return out, lse
+
+
+def _page_table(dev, kv_indptr, kv_indices, B):
+    _need(kv_indptr, "kv_indptr", torch.int32, dev)
+    _need(kv_indices, "kv_indices", torch.int32, dev)
+    if kv_indptr.numel() != B + 1:
+        raise ValueError("kv_indptr must have batch_size + 1 entries")
+
+
+def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, sm_scale: float,
+                     out=None, lse=None, workspace=None, err_word=None, stream=None, return_lse=True,
+                     max_ctas=0):
+    """Decode attention of q [B, Hq, D] over each request's pages of an 8-bit cache.  Returns
+    (out, lse); arguments as for paged_decode."""
+    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    dev = k_pool.device
+    _need(kv_lens, "kv_lens", torch.int32, dev)
+    B = kv_lens.numel()
+    _page_table(dev, kv_indptr, kv_indices, B)
+    out, lse = _attention_io(q, dev, B, out, lse, return_lse, err_word)
+    if q.shape[2] != pool.head_dim:
+        raise ValueError("q and the pool differ in head_dim")
+    Hq = q.shape[1]
+    if workspace is None:
+        need = decode_fp8_workspace_size(B, Hq, pool.num_kv_heads, pool.head_dim, dev)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    _run(dev, stream, "pkv_paged_decode_fp8", ctypes.byref(pool), _ptr(q), B, Hq, _ptr(kv_indptr),
+         _ptr(kv_indices), _ptr(kv_lens), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+         workspace.numel(), _ptr(err_word), int(max_ctas))
+    return out, lse

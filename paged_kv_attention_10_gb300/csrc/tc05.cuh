@@ -178,4 +178,7 @@ namespace pkv_host {
 // d1 and d2, box {b0, b1, b2}.  False if the driver rejects it.  Defined in abi.cu.
 bool encode_tmap_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                     uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
+// The same of bytes, with the 128-byte swizzle for rows of 128 bytes and the 64-byte one for 64 (b0).
+bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
 }  // namespace pkv_host

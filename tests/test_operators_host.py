@@ -125,3 +125,23 @@ def test_binding_refuses_host_tensors_and_wrong_types(pkv):
         pkv.kv_append_fp8(k8, k8, k, k, new, new, slots)
     with pytest.raises(ValueError, match="scaling"):
         pkv.rotary_cos_sin_table(8, 64, 1e4, scaling="other")
+
+
+def test_decode_fp8_refusals(pkv, lib):
+    f = lib.pkv_paged_decode_fp8
+    good = _pool8(pkv)
+
+    def call(pool=good, q=SOME, B=2, Hq=4, indptr=SOME, out=SOME, ws=SOME, n=0, ctas=0):
+        return f(pool, q, B, Hq, indptr, SOME, SOME, 1.0, out, None, ws, n, None, ctas, None)
+
+    assert call(B=0) == OK
+    assert call(pool=None) == INVALID
+    assert call(B=-1) == INVALID
+    assert call(Hq=0) == INVALID
+    assert call(ctas=-1) == INVALID
+    assert call(q=None) == INVALID and call(indptr=None) == INVALID and call(out=None) == INVALID
+    assert call(q=ODD) == INVALID and call(out=ODD) == INVALID
+    assert call(Hq=5) == INVALID                       # not a multiple of the KV heads
+    assert call(Hq=34) == UNSUPPORTED                  # 17 query heads per KV head
+    assert call(pool=_pool8(pkv, D=32)) == UNSUPPORTED
+    assert call(B=1 << 30) == UNSUPPORTED
