@@ -535,6 +535,48 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
                                 void* workspace, size_t workspace_bytes, uint32_t* err_word,
                                 int32_t max_ctas, void* stream);
 
+/*
+ * Attention of trees of drafted tokens over a paged cache (speculative decoding: one pass verifies
+ * every branch).  Request b's drafted tokens are rows qo_indptr[b] .. qo_indptr[b+1] of q; token t of
+ * the request is at pool position prefix_lens[b] + t of its page list (append their K/V first).  Token
+ * i sees every position j < prefix_lens[b], and position prefix_lens[b] + t exactly where bit t % 32
+ * of word t / 32 of its mask row is set -- its ancestors and itself for a tree, any set otherwise (a
+ * token does not see itself unless its bit says so).
+ *   q          bf16 [num_q_tokens, num_q_heads, head_dim]; qo_indptr int32 [batch_size+1];
+ *              prefix_lens int32 [batch_size], >= 0 (device)
+ *   tree_mask  uint32 [num_q_tokens, mask_words] (device), 32 * mask_words >= max_tree_len; bits of
+ *              tokens the request does not have are ignored
+ *   max_tree_len  an upper bound of qo_indptr[b+1] - qo_indptr[b], at most 1024; rows of a request past
+ *              it are reported (PKV_DEVERR_LENGTH) and left unwritten
+ *   out, lse   as for pkv_paged_extend; a row that sees nothing gets out = 0, lse = -inf
+ *   workspace  device, 256-byte aligned, at least pkv_tree_workspace_size(...) bytes; needs no
+ *              initialisation, and is not shared with a call in flight on another stream
+ *   err_word   nullable; PKV_DEVERR_LENGTH, PKV_DEVERR_PAGE_OOB, PKV_DEVERR_ROW_OOB (a request whose rows
+ *              lie outside q is skipped)
+ * What a drafted token's K and V hold does not reach rows that do not see it, infinities and NaNs
+ * included.  head_dim 64 or 128, any page_size, num_q_heads / num_kv_heads from 1 to 16.
+ */
+size_t pkv_tree_workspace_size(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t max_tree_len);
+pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t num_q_tokens,
+                                    const int32_t* qo_indptr, int32_t batch_size, int32_t num_q_heads,
+                                    const int32_t* kv_indptr, const int32_t* kv_indices,
+                                    const int32_t* prefix_lens, const void* tree_mask, int32_t mask_words,
+                                    int32_t max_tree_len, float sm_scale, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                                    void* stream);
+
+/*
+ * The mask of trees given by parents: parents int32 [num_tokens] (device), parents[qo_indptr[b] + t] the
+ * index within request b's tree of token t's parent, -1 (or any negative) for a root; a parent comes
+ * before its children.  Row i of tree_mask receives the bits of i and its ancestors.  A parent that
+ * does not come before its child ends that row's walk and reports PKV_DEVERR_LENGTH, as does a request of
+ * more than 32 * mask_words tokens (whose rows past that are left unwritten).
+ */
+pkv_status pkv_tree_mask_from_parents(const int32_t* parents, const int32_t* qo_indptr, int32_t batch_size,
+                                      int32_t num_tokens, int32_t max_tree_len, int32_t mask_words,
+                                      void* tree_mask, uint32_t* err_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

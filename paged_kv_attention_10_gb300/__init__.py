@@ -25,7 +25,8 @@ __all__ = [
     "status_string", "version", "selftest_bounded_wait", "validate_page_table", "validate_slots",
     "rope_cos_sin_table", "rope_kv_append", "rotary_kv_append", "rotary_cos_sin_table",
     "kv_append_fp8", "rotary_kv_append_fp8", "paged_gather_fp8",
-    "decode_fp8_workspace_size", "paged_decode_fp8", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
+    "decode_fp8_workspace_size", "paged_decode_fp8",
+    "tree_workspace_size", "paged_tree_attention", "tree_mask_from_parents", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
     "DEVERR_TIMEOUT", "DEVERR_INTERNAL", "DEVERR_ROW_OOB",
 ]
 
@@ -125,6 +126,10 @@ def load():
         "pkv_decode_fp8_workspace_size": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
         "pkv_paged_decode_fp8": (_c_i32, [P8, _vp, _c_i32, _c_i32, _vp, _vp, _vp, _c_f32, _vp, _vp, _vp,
                                           _c_sz, _vp, _c_i32, _vp]),
+        "pkv_tree_workspace_size": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
+        "pkv_paged_tree_attention": (_c_i32, [P, _vp, _c_i32, _vp, _c_i32, _c_i32, _vp, _vp, _vp, _vp,
+                                              _c_i32, _c_i32, _c_f32, _vp, _vp, _vp, _c_sz, _vp, _vp]),
+        "pkv_tree_mask_from_parents": (_c_i32, [_vp, _vp, _c_i32, _c_i32, _c_i32, _c_i32, _vp, _vp, _vp]),
         "pkv_paged_gather_fp8": (_c_i32, [P8, _vp, _vp, _vp, _c_i32, _vp, _c_i32, _vp, _vp, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
@@ -741,3 +746,68 @@ def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices,
          _ptr(kv_indices), _ptr(kv_lens), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
          workspace.numel(), _ptr(err_word), int(max_ctas))
     return out, lse
+
+
+# ---------------------------------------------------------------------------------------------
+# trees of drafted tokens
+# ---------------------------------------------------------------------------------------------
+def tree_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim, max_tree_len, device=None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(load().pkv_tree_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim,
+                                                  max_tree_len))
+
+
+def _mask_words(tree_mask, dev, rows, max_tree_len):
+    _need(tree_mask, "tree_mask", torch.int32, dev)
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != rows or 32 * tree_mask.shape[1] < max_tree_len:
+        raise ValueError("tree_mask must be [num_q_tokens, words] with 32 * words >= max_tree_len")
+    return tree_mask.shape[1]
+
+
+def paged_tree_attention(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, prefix_lens, tree_mask,
+                         max_tree_len: int, sm_scale: float, out=None, lse=None, workspace=None,
+                         err_word=None, stream=None, return_lse=True):
+    """Attention of each request's drafted tokens (rows qo_indptr[b].. of q) over its cached prefix
+    and the drafted tokens whose bits its tree_mask row (int32 [num_q_tokens, words]) sets.  Returns
+    (out, lse)."""
+    pool = _pool(k_pool, v_pool)
+    dev = k_pool.device
+    _need(qo_indptr, "qo_indptr", torch.int32, dev)
+    _need(prefix_lens, "prefix_lens", torch.int32, dev)
+    B = prefix_lens.numel()
+    _page_table(dev, kv_indptr, kv_indices, B)
+    if qo_indptr.numel() != B + 1:
+        raise ValueError("qo_indptr must have batch_size + 1 entries")
+    out, lse = _attention_io(q, dev, None, out, lse, return_lse, err_word)
+    N, Hq, D = q.shape
+    if D != pool.head_dim:
+        raise ValueError("q and the pool differ in head_dim")
+    words = _mask_words(tree_mask, dev, N, max_tree_len)
+    if workspace is None:
+        need = tree_workspace_size(B, Hq, pool.num_kv_heads, D, max_tree_len, dev)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    _run(dev, stream, "pkv_paged_tree_attention", ctypes.byref(pool), _ptr(q), N, _ptr(qo_indptr), B, Hq,
+         _ptr(kv_indptr), _ptr(kv_indices), _ptr(prefix_lens), _ptr(tree_mask), words, int(max_tree_len),
+         float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err_word))
+    return out, lse
+
+
+def tree_mask_from_parents(parents, qo_indptr, max_tree_len: int, out=None, err_word=None,
+                           stream=None) -> torch.Tensor:
+    """The tree_mask of trees given by parents (int32 [num_tokens], each the parent's index within its
+    request's tree, negative for a root; parents come before their children)."""
+    _need(parents, "parents", torch.int32)
+    dev = parents.device
+    _need(qo_indptr, "qo_indptr", torch.int32, dev)
+    if parents.dim() != 1 or qo_indptr.numel() < 1:
+        raise ValueError("parents must be [num_tokens] and qo_indptr [batch_size + 1]")
+    if err_word is not None:
+        _need(err_word, "err_word", torch.int32, dev)
+    N = parents.numel()
+    if out is None:
+        out = torch.zeros((N, -(-int(max_tree_len) // 32)), dtype=torch.int32, device=dev)
+    words = _mask_words(out, dev, N, max_tree_len)
+    _run(dev, stream, "pkv_tree_mask_from_parents", _ptr(parents), _ptr(qo_indptr), qo_indptr.numel() - 1, N,
+         int(max_tree_len), words, _ptr(out), _ptr(err_word))
+    return out

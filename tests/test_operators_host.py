@@ -145,3 +145,30 @@ def test_decode_fp8_refusals(pkv, lib):
     assert call(Hq=34) == UNSUPPORTED                  # 17 query heads per KV head
     assert call(pool=_pool8(pkv, D=32)) == UNSUPPORTED
     assert call(B=1 << 30) == UNSUPPORTED
+
+
+def test_tree_refusals(pkv, lib):
+    f = lib.pkv_paged_tree_attention
+    good = _pool(pkv)
+
+    def call(pool=good, q=SOME, N=6, qo=SOME, B=2, Hq=4, mask=SOME, words=1, most=3, out=SOME, ws=SOME, n=0):
+        return f(pool, q, N, qo, B, Hq, SOME, SOME, SOME, mask, words, most, 1.0, out, None, ws, n, None, None)
+
+    assert call(B=0) == OK and call(N=0) == OK and call(most=0) == OK
+    assert call(pool=None) == INVALID
+    assert call(B=-1) == INVALID and call(N=-1) == INVALID and call(most=-1) == INVALID
+    assert call(Hq=0) == INVALID and call(Hq=5) == INVALID
+    assert call(words=-1) == INVALID
+    assert call(most=33) == INVALID                    # one word holds 32 tokens
+    for missing in ("q", "qo", "mask", "out"):
+        assert call(**{missing: None}) == INVALID
+    assert call(q=ODD) == INVALID and call(out=ODD) == INVALID
+    assert call(pool=_pool(pkv, pages=1 << 28)) == UNSUPPORTED
+
+    g = lib.pkv_tree_mask_from_parents
+    assert g(SOME, SOME, 0, 4, 4, 1, SOME, None, None) == OK
+    assert g(SOME, SOME, 1, 4, 33, 1, SOME, None, None) == INVALID
+    assert g(None, SOME, 1, 4, 4, 1, SOME, None, None) == INVALID
+    assert g(SOME, SOME, 1, -4, 4, 1, SOME, None, None) == INVALID
+    assert g(SOME, SOME, 65536, 4, 4, 1, SOME, None, None) == UNSUPPORTED
+    assert g(SOME, SOME, 1, 4, 1025, 33, SOME, None, None) == UNSUPPORTED
