@@ -16,8 +16,14 @@
 //    tile and each K/V tile in shared memory serves both; with one Q tile the slots take alternate
 //    KV tiles, so that one slot's softmax runs beside the other's MMAs, and their states are joined
 //    when the segment ends.
+//  * A thread owns a row, and a warp can read only its quarter of TMEM's lanes, so a unit of at most 32
+//    (64) rows would leave three (two) of a slot's four softmax warps idle while the busy ones took
+//    128 columns of every tile each, and that chain, not memory, would set the pace.  The rows are
+//    therefore loaded four times (twice) into the tile, the MMA's rows being there anyway: each
+//    copy takes 32 (64) of the tile's columns, writes zeros for P elsewhere, and ends up with a state
+//    of its own; the copies' states are joined in the epilogue.
 //  * Twelve warps: K producer (which also walks the stream and publishes the segments), QK issuer, PV
-//    issuer, V producer, and four softmax warps per slot, one thread per row.
+//    issuer, V and Q producer, and four softmax warps per slot, one thread per row.
 //  * Only tiles that reach past the prefix are masked.  There the V rows behind the last position
 //    and the infinities and NaNs of drafted tokens become 0 in shared memory (weight 0 times them
 //    would be NaN for rows that do not see them); rows that do see them get them added when they are
@@ -37,6 +43,7 @@ constexpr int kSoftmaxWarp0 = 4;      // warps 4..7 slot 0, 8..11 slot 1
 constexpr int kMaxNodes = 1024;       // drafted tokens of a request
 constexpr int kSegRing = 4;
 constexpr int kKStages = 2, kVStages = 3;
+constexpr int kUnitCost = 2;          // a unit's start and epilogue, in KV tiles of the work split
 constexpr uint32_t kHalfTile = 128 * 128;  // 128 rows of one 64-dim half, 16 KB
 constexpr uint32_t kColO = 0, kColS = 256;  // O of slot s at 128 s, S at 256 + 128 s
 
@@ -47,7 +54,12 @@ struct Cfg {
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kOffQ + 2 * kTile;
   static constexpr uint32_t kOffV = kOffK + kKStages * kTile;
-  static constexpr uint32_t kOffCtl = kOffV + kVStages * kTile;
+  // the epilogue's exchange between replicas, 2 slots x 3 x 32 rows x 32 dims fp32: at D 128 it is the
+  // second Q buffer, which one Q tile leaves free
+  static constexpr uint32_t kScratch = 2 * 3 * 32 * 32 * 4;
+  static constexpr bool kShared = kTile >= kScratch;
+  static constexpr uint32_t kOffScratch = kShared ? kOffQ + kTile : kOffV + kVStages * kTile;
+  static constexpr uint32_t kOffCtl = kOffV + kVStages * kTile + (kShared ? 0 : kScratch);
 };
 
 // A run of KV tiles of one unit that this CTA computes.
@@ -60,7 +72,7 @@ struct Seg {
   int32_t nq;      // Q tiles of the unit (1 or 2); 0: no more work
   int32_t j0, n;   // first KV tile, number of tiles
   int32_t part;    // partial state's slot, or -1: the segment is the whole unit
-  int32_t pad;
+  int32_t rep;     // copies of the Q rows in the tile (1, 2 or 4)
 };
 
 struct Ctl {
@@ -74,6 +86,7 @@ struct Ctl {
   uint64_t s_free[2];  // PV done
   uint64_t o_free;     // O read by the epilogue
   uint64_t x_full, x_free;  // the slots' exchange of row states
+  uint32_t epilogues;       // warps done with the scratch, counted over all segments
   uint64_t qk_done, pv_done;
   uint32_t tmem_base;
   uint32_t bad_any;
@@ -81,6 +94,7 @@ struct Ctl {
   float xm[2][kBM], xl[2][kBM];  // row maxima and sums of the slots
 };
 constexpr uint32_t kSmemLimit = 227 * 1024;
+static_assert(kMaxNodes / 32 == 32, "a warp clears the notes");
 static_assert(Cfg<128>::kOffCtl + sizeof(Ctl) <= kSmemLimit, "shared memory");
 
 // The unit that a CTA's share ends in the middle of, for the merge: its parts are the slots
@@ -92,7 +106,8 @@ struct Cut {
 };
 
 struct TreeArgs {
-  CUtensorMap tm_q, tm_k, tm_v;
+  CUtensorMap tm_q[3];  // box of the tokens of 128, 64 and 32 rows
+  CUtensorMap tm_k, tm_v;
   const int32_t* qo_indptr;
   const int32_t* kv_indptr;
   const int32_t* kv_indices;
@@ -108,7 +123,7 @@ struct TreeArgs {
   int32_t page_size, box_rows;
   int32_t num_kv_heads, num_q_heads, group;
   int32_t tpt;        // tokens per Q tile
-  int32_t rows_used;  // group * tpt
+  int32_t tpt2, tpt4; // ... of which 2 or 4 copies fit into the tile
   int32_t batch, num_q_tokens, max_nodes;
   float scale_log2;
   Cut* cut;           // [CTAs]
@@ -291,6 +306,7 @@ struct Producer {
 struct Req {
   int32_t q0, T, P, p0, np;
   int32_t pairs, tiles;  // Q tile pairs, KV tiles (0: nothing to do)
+  int32_t cost;          // of a unit in the stream: its tiles and what an epilogue costs
 };
 
 __device__ Req load_req(const TreeArgs& a, int b, bool check) {
@@ -301,7 +317,7 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   r.p0 = __ldg(a.kv_indptr + b);
   r.np = __ldg(a.kv_indptr + b + 1) - r.p0;
   r.T = min(max(rows, 0), a.max_nodes);
-  r.pairs = r.tiles = 0;
+  r.pairs = r.tiles = r.cost = 0;
   uint32_t bad = 0;
   if (rows < 0 || rows > a.max_nodes || r.P < 0 || r.P > 0x7fffffff - kMaxNodes - kBN) bad = PKV_DEVERR_LENGTH;
   if (rows > 0 && (r.q0 < 0 || r.q0 > a.num_q_tokens - rows)) bad |= PKV_DEVERR_ROW_OOB;
@@ -309,6 +325,7 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   if (r.T > 0 && r.P >= 0 && r.P <= 0x7fffffff - kMaxNodes - kBN && !(bad & PKV_DEVERR_ROW_OOB)) {
     r.pairs = (r.T + 2 * a.tpt - 1) / (2 * a.tpt);
     r.tiles = (r.P + r.T + kBN - 1) / kBN;
+    r.cost = r.tiles + kUnitCost;
   }
   return r;
 }
@@ -316,14 +333,18 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
 // K producer warp: walks this CTA's share of the stream, publishes each segment, loads its Q and K.
 template <int D, bool kRows>
 __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
-  using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   Producer<D, kRows> k(a, ctl, sb, false);
   int64_t total = 0;
-  for (int i = lane; i < a.batch; i += 32) {
-    const Req r = load_req(a, i, cta == 0);
-    total += (int64_t)r.pairs * r.tiles;
+  for (int i = lane; i < a.batch; i += 128) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {  // four requests' loads in flight
+      if (i + 32 * u < a.batch) {
+        const Req r = load_req(a, i + 32 * u, cta == 0);
+        total += (int64_t)r.pairs * r.cost;
+      }
+    }
   }
   total = warp_sum(total) * a.num_kv_heads;
   int64_t share = (total + gridDim.x - 1) / gridDim.x;
@@ -331,7 +352,7 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
   const int64_t c0 = cta * share, c1 = min(total, c0 + share);
 
   bool ok = true;
-  int nseg = 0, nqt = 0;
+  int nseg = 0;
   Cut cut = {};
   auto publish = [&](const Seg& s) -> bool {
     const int r = nseg % kSegRing;
@@ -348,7 +369,7 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
   for (int b0 = 0; b0 < a.batch && base < c1 && ok; b0 += 32) {
     Req r = {};
     if (b0 + lane < a.batch) r = load_req(a, b0 + lane, false);
-    const int64_t len = (int64_t)r.pairs * r.tiles * a.num_kv_heads;
+    const int64_t len = (int64_t)r.pairs * r.cost * a.num_kv_heads;
     int64_t incl = len;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -369,10 +390,11 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
       const int pairs = __shfl_sync(0xffffffffu, r.pairs, src);
       const int tiles = __shfl_sync(0xffffffffu, r.tiles, src);
       const int64_t r0 = __shfl_sync(0xffffffffu, rs, src);
+      const int cost = __shfl_sync(0xffffffffu, r.cost, src);
       const int units = pairs * a.num_kv_heads;
       // units in the order (KV head, pair): the first that reaches into the share
-      for (int u = (int)max((int64_t)0, (c0 - r0) / tiles); u < units && ok; ++u) {
-        const int64_t us = r0 + (int64_t)u * tiles, ue = us + tiles;
+      for (int u = (int)max((int64_t)0, (c0 - r0) / cost); u < units && ok; ++u) {
+        const int64_t us = r0 + (int64_t)u * cost, ue = us + tiles;  // (the rest is the epilogue's time)
         if (us >= c1) break;
         const int64_t s0 = max(us, c0), s1 = min(ue, c1);
         if (s0 >= s1) continue;
@@ -382,21 +404,9 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
         s.j0 = (int)(s0 - us);
         s.n = (int)(s1 - s0);
         s.part = s0 == us && s1 == ue ? -1 : 2 * cta + (us >= c0 ? 1 : 0);
-        s.pad = 0;
+        s.rep = s.nq == 2 ? 1 : s.T - s.t0 <= a.tpt4 ? 4 : s.T - s.t0 <= a.tpt2 ? 2 : 1;
         if (us >= c0 && ue > c1) cut = Cut{(int32_t)((ue - 1) / share) - cta + 1, s.q0, s.T, s.t0, s.h, s.nq, {0, 0}};
         ok = publish(s);
-        for (int i = 0; i < s.nq && ok; ++i, ++nqt) {
-          const int qb = nqt & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[qb], ((nqt >> 1) & 1) ^ 1));
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&ctl->q_full[qb], C::kHalves * a.rows_used * 128);
-#pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_3d(sb + C::kOffQ + qb * C::kTile + hf * kHalfTile, &a.tm_q, hf * 64, s.h * a.group,
-                          s.q0 + s.t0 + i * a.tpt, &ctl->q_full[qb]);
-          }
-          __syncwarp();
-        }
         ok = ok && k.run(s);
       }
     }
@@ -409,21 +419,46 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   if (lane == 0) a.cut[cta] = cut;
   k.drain();
-  for (int i = max(0, nqt - 2); i < nqt; ++i) mbar_wait(&ctl->q_full[i & 1], (i >> 1) & 1);
 }
 
+// V and Q producer warp.  One Q tile always takes the first Q buffer, so that the second is free for
+// the epilogue's scratch; two Q tiles wait until that is no longer read.
 template <int D, bool kRows>
 __device__ void tree_load_v(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
   Producer<D, kRows> v(a, ctl, sb, true);
+  int uses[2] = {0, 0};
   Seg s;
-  for (int i = 0;; ++i) {
-    if (!next_seg(ctl, i, s) || (s.nq > 0 && !v.run(s))) {
-      if ((threadIdx.x & 31) == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      break;
+  bool ok = true;
+  for (int i = 0; ok; ++i) {
+    ok = next_seg(ctl, i, s);
+    if (!ok || s.nq == 0) break;
+    if (C::kShared && s.nq == 2) {
+      const uint64_t t0 = globaltimer_ns();
+      while (ok && atomicAdd(&ctl->epilogues, 0u) < 8u * (uint32_t)i) ok = globaltimer_ns() - t0 <= kWaitLimitNs;
+      ok = __all_sync(0xffffffffu, ok);
     }
-    if (s.nq == 0) break;
+    const int level = s.rep == 1 ? 0 : s.rep == 2 ? 1 : 2;
+    const int tokens = level == 0 ? a.tpt : level == 1 ? a.tpt2 : a.tpt4;
+    for (int q = 0; q < s.nq && ok; ++q, ++uses[q - 1]) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[q], (uses[q] & 1) ^ 1));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl->q_full[q], C::kHalves * s.rep * tokens * a.group * 128);
+      __syncwarp();
+      if (lane < C::kHalves * s.rep) {
+        const int hf = lane % C::kHalves, copy = lane / C::kHalves;
+        tma_load_3d(sb + C::kOffQ + q * C::kTile + hf * kHalfTile + copy * (kBM / s.rep) * 128, &a.tm_q[level], hf * 64,
+                    s.h * a.group, s.q0 + s.t0 + q * a.tpt, &ctl->q_full[q]);
+      }
+    }
+    ok = ok && v.run(s);
   }
+  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   v.drain();
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (uses[q] > 0) mbar_wait(&ctl->q_full[q], (uses[q] - 1) & 1);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -444,13 +479,13 @@ __device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
   constexpr uint32_t idesc = umma_idesc_bf16(kBM, kBN, false);
   const uint64_t qdesc0 = smem_desc_sw128(sb + C::kOffQ, 16, 1024);
   const uint64_t kdesc0 = smem_desc_sw128(sb + C::kOffK, 16, 1024);
-  uint32_t kt = 0, nqt = 0, used[2] = {0, 0};  // K tiles, Q tiles, uses of each slot so far
+  uint32_t kt = 0, qt[2] = {0, 0}, used[2] = {0, 0};  // K tiles, uses of the Q buffers and the slots so far
   Seg s;
   for (int i = 0;; ++i) {
     if (!next_seg_thread(ctl, i, s)) return false;
     if (s.nq == 0) return true;
     for (int q = 0; q < s.nq; ++q)
-      if (!mbar_wait(&ctl->q_full[(nqt + q) & 1], ((nqt + q) >> 1) & 1)) return false;
+      if (!mbar_wait(&ctl->q_full[q], qt[q] & 1)) return false;
     for (int j = 0; j < s.n; ++j, ++kt) {
       const uint32_t st = kt % kKStages;
       if (!mbar_wait(&ctl->k_full[st], (kt / kKStages) & 1)) return false;
@@ -459,7 +494,7 @@ __device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
         const int slot = s.nq == 2 ? q : (j & 1);
         if (!mbar_wait(&ctl->s_free[slot], (used[slot] & 1) ^ 1)) return false;
         tc_fence_after();
-        const uint64_t qdesc = qdesc0 + ((((nqt + q) & 1) * C::kTile) >> 4);
+        const uint64_t qdesc = qdesc0 + ((q * C::kTile) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kHalfTile + (ks & 3) * 32) >> 4;
@@ -470,55 +505,8 @@ __device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
       }
       umma_commit(&ctl->k_empty[st]);
     }
-    for (int q = 0; q < s.nq; ++q, ++nqt) umma_commit(&ctl->q_empty[nqt & 1]);
+    for (int q = 0; q < s.nq; ++q, ++qt[q - 1]) umma_commit(&ctl->q_empty[q]);
   }
-}
-
-template <int D>
-__device__ bool tree_mma_pv(Ctl* ctl, uint32_t sb, uint32_t tmem) {
-  using C = Cfg<D>;
-  constexpr uint32_t idesc = umma_idesc_bf16(kBM, D, true);
-  const uint64_t vdesc0 = smem_desc_sw128(sb + C::kOffV, kHalfTile, 1024);
-  uint32_t vt = 0, used[2] = {0, 0};
-  Seg s;
-  for (int i = 0;; ++i) {
-    if (!next_seg_thread(ctl, i, s)) return false;
-    if (s.nq == 0) return true;
-    if (!mbar_wait(&ctl->o_free, (i & 1) ^ 1)) return false;
-    for (int j = 0; j < s.n; ++j, ++vt) {
-      const uint32_t st = vt % kVStages;
-      const uint64_t vdesc = vdesc0 + ((st * C::kTile) >> 4);
-      for (int q = 0; q < s.nq; ++q) {
-        const int slot = s.nq == 2 ? q : (j & 1);
-        const bool first = s.nq == 2 ? j == 0 : j < 2;
-        if (!mbar_wait(&ctl->p_full[slot], used[slot] & 1)) return false;
-        if (!mbar_wait(&ctl->v_full[st], (vt / kVStages) & 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < kBN / 16; ++ks)
-          umma_ts(tmem + kColO + slot * 128, tmem + kColS + slot * 128 + ks * 8, vdesc + ((ks * 2048) >> 4), idesc,
-                  !first || ks > 0);
-        umma_commit(&ctl->s_free[slot]);
-        ++used[slot];
-      }
-      umma_commit(&ctl->v_empty[st]);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------------------------
-// Softmax and epilogue
-// ---------------------------------------------------------------------------------------------
-// Which of the 32 positions of drafted-token offsets t0 .. t0 + 31 (t0 may be negative: the prefix)
-// a row with mask words m (nullptr: an unused row) sees.
-PKV_DEV uint32_t visible(const uint32_t* m, int words, int T, int t0) {
-  if (t0 <= -32) return 0xffffffffu;
-  if (t0 >= T) return 0u;
-  auto word = [&](int w) -> uint32_t { return w < 0 ? 0xffffffffu : (m && w < words ? __ldg(m + w) : 0u); };
-  const int w = t0 >> 5, sh = t0 & 31;
-  uint32_t v = __funnelshift_r(word(w), sh ? word(w + 1) : 0u, sh);
-  if (T - t0 < 32) v &= (1u << (T - t0)) - 1u;
-  return v;
 }
 
 // A pair of bf16 values with the non-finite ones replaced by 0.
@@ -527,56 +515,146 @@ PKV_DEV uint32_t finite_bf16x2(uint32_t u) {
   if ((u & 0x7f800000u) == 0x7f800000u) u &= 0x0000ffffu;
   return u;
 }
+// Non-zero where a pair holds an infinity or a NaN: an exponent of ones carries into the sign's place.
+PKV_DEV uint32_t nonfinite_bits(uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // What no weight may touch in a tile of V becomes zeros: the rows behind the last position, and the
-// infinities and NaNs of drafted tokens, which are noted.  One thread per row; the prefix's rows are
-// left alone.
+// infinities and NaNs of drafted tokens, which are noted.  By one warp, a row per lane at a time; the
+// prefix's rows are left alone.
 template <int D>
-__device__ void clean_v(uint8_t* vtile, Ctl* ctl, const Seg& s, int pos0, int r) {
+__device__ void clean_v(uint8_t* vtile, Ctl* ctl, const Seg& s, int pos0) {
   using C = Cfg<D>;
-  const int t = pos0 + r - s.P;
-  if (t < 0) return;
-  uint8_t* row = vtile + r * 128;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < C::kHalves * 8; ++i) {
-    uint4* at = reinterpret_cast<uint4*>(row + (i >> 3) * kHalfTile + (((i + r) & 7) << 4));
+  constexpr int kChunks = C::kHalves * 8;
+  const int lane = threadIdx.x & 31;
+  for (int r = max(0, s.P - pos0) + lane; r < kBN; r += 32) {
+    const int t = pos0 + r - s.P;
+    uint8_t* row = vtile + r * 128;
+    auto at = [&](int i) {  // chunks in an order that spreads the lanes over the banks
+      return reinterpret_cast<uint4*>(row + (i >> 3) * kHalfTile + (((i + r) & 7) << 4));
+    };
     if (t >= s.T) {
-      *at = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) *at(i) = make_uint4(0u, 0u, 0u, 0u);
     } else {
-      const uint4 u = *at;
-      const uint4 f = make_uint4(finite_bf16x2(u.x), finite_bf16x2(u.y), finite_bf16x2(u.z), finite_bf16x2(u.w));
-      if (f.x != u.x || f.y != u.y || f.z != u.z || f.w != u.w) {
-        *at = f;
-        bad = true;
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const uint4 u = *at(i);
+        bad |= nonfinite_bits(u.x) | nonfinite_bits(u.y) | nonfinite_bits(u.z) | nonfinite_bits(u.w);
+      }
+      if (bad) {
+#pragma unroll 1
+        for (int i = 0; i < kChunks; ++i) {
+          const uint4 u = *at(i);
+          *at(i) = make_uint4(finite_bf16x2(u.x), finite_bf16x2(u.y), finite_bf16x2(u.z), finite_bf16x2(u.w));
+        }
+        atomicOr(&ctl->bad[t >> 5], 1u << (t & 31));
+        ctl->bad_any = 1u;
       }
     }
   }
-  if (bad) {
-    atomicOr(&ctl->bad[t >> 5], 1u << (t & 31));
-    ctl->bad_any = 1u;
+  fence_proxy_async_smem();  // before the MMA reads the tile
+  __syncwarp();
+}
+
+// PV warp.  Its first lane issues; the whole warp cleans the V tiles that reach past the prefix, while
+// the softmax is still at work on their scores.
+template <int D>
+__device__ bool tree_mma_pv(Ctl* ctl, uint8_t* smem, uint32_t tmem) {
+  using C = Cfg<D>;
+  constexpr uint32_t idesc = umma_idesc_bf16(kBM, D, true);
+  const int lane = threadIdx.x & 31;
+  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem) + C::kOffV, kHalfTile, 1024);
+  uint32_t vt = 0, used[2] = {0, 0};
+  auto wait = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+  Seg s;
+  for (int i = 0;; ++i) {
+    if (!next_seg(ctl, i, s)) return false;
+    if (s.nq == 0) return true;
+    if (!wait(&ctl->o_free, (i & 1) ^ 1)) return false;  // the last segment's O and notes have been read
+    if (ctl->bad_any) {
+      ctl->bad[lane] = 0u;
+      __syncwarp();
+      if (lane == 0) ctl->bad_any = 0u;
+      __syncwarp();
+    }
+    for (int j = 0; j < s.n; ++j, ++vt) {
+      const uint32_t st = vt % kVStages;
+      const uint64_t vdesc = vdesc0 + ((st * C::kTile) >> 4);
+      const int pos0 = (s.j0 + j) * kBN;
+      if (!wait(&ctl->v_full[st], (vt / kVStages) & 1)) return false;
+      if (pos0 + kBN > s.P) clean_v<D>(smem + C::kOffV + st * C::kTile, ctl, s, pos0);
+      for (int q = 0; q < s.nq; ++q) {
+        const int slot = s.nq == 2 ? q : (j & 1);
+        const bool first = s.nq == 2 ? j == 0 : j < 2;
+        if (!wait(&ctl->p_full[slot], used[slot] & 1)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int ks = 0; ks < kBN / 16; ++ks)
+            umma_ts(tmem + kColO + slot * 128, tmem + kColS + slot * 128 + ks * 8, vdesc + ((ks * 2048) >> 4), idesc,
+                    !first || ks > 0);
+          umma_commit(&ctl->s_free[slot]);
+        }
+        __syncwarp();
+        ++used[slot];
+      }
+      if (lane == 0) umma_commit(&ctl->v_empty[st]);
+    }
+    if (lane == 0) mbar_arrive(&ctl->x_full);  // this segment's notes are made
   }
 }
 
-// Adds the non-finite values of dims [d0, d0 + 32) of the noted drafted tokens that the row sees.
-template <int D>
-__device__ void add_nonfinite(const TreeArgs& a, const Ctl* ctl, const Seg& s, const uint32_t* m, int d0,
-                              float (&v)[32]) {
-  for (int w = 0; w < (s.T + 31) / 32; ++w) {
-    uint32_t hit = ctl->bad[w] & (m && w < a.words ? __ldg(m + w) : 0u);
+// ---------------------------------------------------------------------------------------------
+// Softmax and epilogue
+// ---------------------------------------------------------------------------------------------
+// A row's mask words: the first four in registers (loaded before they are needed), others from memory.
+struct MaskRow {
+  const uint32_t* m;  // nullptr: an unused row
+  int32_t words;
+  uint32_t w[4];
+};
+
+PKV_DEV void load_mask(MaskRow& k) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k.w[i] = k.m && i < k.words ? __ldg(k.m + i) : 0u;
+}
+
+// Which of the 32 positions of drafted-token offsets t0 .. t0 + 31 (t0 may be negative: the prefix)
+// the row sees, T drafted tokens in all.
+PKV_DEV uint32_t visible(const MaskRow& k, int T, int t0) {
+  if (t0 <= -32) return 0xffffffffu;
+  if (t0 >= T) return 0u;
+  auto word = [&](int i) -> uint32_t {
+    if (i < 0) return 0xffffffffu;
+    if (i < 4) return i < 2 ? (i == 0 ? k.w[0] : k.w[1]) : (i == 2 ? k.w[2] : k.w[3]);
+    return k.m && i < k.words ? __ldg(k.m + i) : 0u;
+  };
+  const int w = t0 >> 5, sh = t0 & 31;
+  uint32_t v = __funnelshift_r(word(w), sh ? word(w + 1) : 0u, sh);
+  if (T - t0 < 32) v &= (1u << (T - t0)) - 1u;
+  return v;
+}
+
+// Adds the non-finite values of dims [d0, d0 + n) of the noted drafted tokens that the row sees to what
+// this thread has written at `to` (the rest of them is in it already).
+template <int D, typename T>
+__device__ __noinline__ void add_nonfinite(const TreeArgs& a, const Ctl* ctl, int P, int nodes, int p0, int np, int h,
+                                           const uint32_t* m, int d0, int n, T* to) {
+  for (int w = 0; w < (nodes + 31) / 32; ++w) {
+    uint32_t hit = ctl->bad[w] & (w < a.words ? __ldg(m + w) : 0u);
     while (hit) {
       const int t = 32 * w + __ffs(hit) - 1;
       hit &= hit - 1;
-      const int pos = s.P + t, pidx = pos / a.page_size;
-      if (pidx >= s.np) continue;
-      const int32_t page = __ldg(a.kv_indices + s.p0 + pidx);
+      const int pos = P + t, pidx = pos / a.page_size;
+      if (pidx >= np) continue;
+      const int32_t page = __ldg(a.kv_indices + p0 + pidx);
       if (page < 0 || page >= a.num_pages) continue;
       const __nv_bfloat16* src =
-          a.v_pool + (((int64_t)page * a.page_size + pos % a.page_size) * a.num_kv_heads + s.h) * D + d0;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
+          a.v_pool + (((int64_t)page * a.page_size + pos % a.page_size) * a.num_kv_heads + h) * D + d0;
+      for (int i = 0; i < n; ++i) {
         const float x = __bfloat162float(src[i]);
-        if (!(fabsf(x) < INFINITY)) v[i] += x;
+        if (!(fabsf(x) < INFINITY)) to[i] = (T)((float)to[i] + x);
       }
     }
   }
@@ -595,6 +673,46 @@ PKV_DEV float max32(const float (&v)[32]) {
   return fmaxf(max3f(max3f(a[0], a[1], a[2]), max3f(a[3], a[4], a[5]), max3f(a[6], a[7], a[8])), fmaxf(a[9], a[10]));
 }
 
+// Packed pairs of fp32.
+PKV_DEV uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+PKV_DEV void split_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+PKV_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+PKV_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The weights 2^(v sc + neg) of 32 scores as bf16 pairs, and their sum.
+PKV_DEV float weights32(const float (&v)[32], float sc, float neg, uint32_t (&pk)[16]) {
+  const uint64_t sc2 = f32x2(sc, sc), neg2 = f32x2(neg, neg);
+  uint64_t t0 = f32x2(0.f, 0.f), t1 = t0;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    float x0, x1, x2, x3;
+    split_f32x2(fma_f32x2(f32x2(v[2 * e], v[2 * e + 1]), sc2, neg2), x0, x1);
+    split_f32x2(fma_f32x2(f32x2(v[2 * e + 2], v[2 * e + 3]), sc2, neg2), x2, x3);
+    const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+    t0 = add_f32x2(t0, f32x2(p0, p1));
+    t1 = add_f32x2(t1, f32x2(p2, p3));
+    pk[e] = pack_bf16x2(p0, p1);
+    pk[e + 1] = pack_bf16x2(p2, p3);
+  }
+  float lo, hi;
+  split_f32x2(add_f32x2(t0, t1), lo, hi);
+  return lo + hi;
+}
+
 template <int D>
 __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_t tmem) {
   using C = Cfg<D>;
@@ -606,11 +724,9 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
   const uint32_t ts = tq + kColS + slot * 128;
   const uint32_t to = tq + kColO + slot * 128;
   const int G = a.group;
-  const int rt = r / G, g = r - rt * G;  // token of the tile, head of the group
   const bool pos_scale = a.scale_log2 > 0.f;
   const float sc = pos_scale ? a.scale_log2 : 1.f;
   uint32_t used[2] = {0, 0};  // uses of both slots before this segment
-  uint32_t vt0 = 0;           // V tiles before this segment
   bool ok = true;
 
   for (int i = 0; ok; ++i) {
@@ -621,10 +737,16 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
     }
     if (s.nq == 0) break;
     const bool two = s.nq == 2;
+    // the thread's row among the distinct ones, and its copy's share of a tile's four 32-column chunks
+    const int rr = s.rep == 4 ? lane : s.rep == 2 ? r & 63 : r;
+    const int copy = s.rep == 4 ? wq : s.rep == 2 ? wq >> 1 : 0;
+    const int nch = 4 / s.rep, ch0 = copy * nch;
+    const int rt = rr / G, g = rr - rt * G;  // token of the tile, head of the group
     const int tok = s.t0 + (two ? slot * a.tpt : 0) + rt;
-    const bool valid = r < a.rows_used && tok < s.T;
+    const bool valid = rt < (s.rep == 4 ? a.tpt4 : s.rep == 2 ? a.tpt2 : a.tpt) && tok < s.T;
     const bool warp_live = __any_sync(0xffffffffu, valid);
-    const uint32_t* mrow = valid ? a.mask + (int64_t)(s.q0 + tok) * a.words : nullptr;
+    MaskRow mask{valid ? a.mask + (int64_t)(s.q0 + tok) * a.words : nullptr, a.words, {0u, 0u, 0u, 0u}};
+    if ((s.j0 + s.n) * kBN > s.P) load_mask(mask);
     float m = -INFINITY, l = 0.f;  // running maximum of the scaled (log2) scores, sum of weights
     uint32_t n_used = used[slot];
 
@@ -635,22 +757,26 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
       if (!ok) break;
       tc_fence_after();
       if (warp_live) {
-        uint32_t vis[4];
+        if (special || !pos_scale) {  // masked (and scaled) scores take the place of the scores
+#pragma unroll 1
+          for (int ch = ch0; ch < ch0 + nch; ++ch) {
+            float v[32];
+            tmem_ld32(ts + ch * 32, v);
+            const uint32_t vis = special ? visible(mask, s.T, pos0 + 32 * ch - s.P) : 0xffffffffu;
+            const float mul = pos_scale ? 1.f : a.scale_log2;
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] * mul : -INFINITY;
+            tmem_st32(ts + ch * 32, v);
+          }
+          tmem_wait_st();
+        }
+        float v[32];
         float mx = -INFINITY;
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          float v[32];
+#pragma unroll 1
+        for (int ch = ch0 + nch - 1; ch >= ch0; --ch) {
           tmem_ld32(ts + ch * 32, v);
-          vis[ch] = special ? visible(mrow, a.words, s.T, pos0 + 32 * ch - s.P) : 0xffffffffu;
           tmem_wait_ld();
-          if (!pos_scale) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= a.scale_log2;
-          }
-          if (special) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (vis[ch] >> e) & 1u ? v[e] : -INFINITY;
-          }
           mx = fmaxf(mx, max32(v));
         }
         mx *= sc;
@@ -660,31 +786,22 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
         const float m_ref = resc ? m_new : m;
         const float corr = resc ? ex2(m - m_ref) : 1.f;
         const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen so far: every weight is 0
-        float tot = 0.f;
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          float v[32];
+        uint32_t pk[16];
+        float tot = weights32(v, sc, neg, pk);  // v holds the first chunk
+        // P of chunk ch goes over columns of S of chunk ch / 2, which has been read
+        tmem_st16(ts + ch0 * 16, pk);
+#pragma unroll 1
+        for (int ch = ch0 + 1; ch < ch0 + nch; ++ch) {
           tmem_ld32(ts + ch * 32, v);
           tmem_wait_ld();
-          if (!pos_scale) {
+          tot += weights32(v, sc, neg, pk);
+          tmem_st16(ts + ch * 16, pk);
+        }
+        if (nch < 4) {  // the other copies' columns
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= a.scale_log2;
-          }
-          if (special) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (vis[ch] >> e) & 1u ? v[e] : -INFINITY;
-          }
-          uint32_t pk[16];
-          float t0 = 0.f, t1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(v[2 * e], sc, neg)), p1 = ex2(fmaf(v[2 * e + 1], sc, neg));
-            t0 += p0;
-            t1 += p1;
-            pk[e] = pack_bf16x2(p0, p1);
-          }
-          tot += t0 + t1;
-          tmem_st16(ts + ch * 16, pk);  // over scores that are read: P of chunk ch lies in S of chunk ch / 2
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+#pragma unroll 1
+          for (int ch = nch; ch < 4; ++ch) tmem_st16(ts + ((ch0 + ch) & 3) * 16, pk);
         }
         l = l * corr + tot;
         m = m_ref;
@@ -692,22 +809,14 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
         if (later && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
-            float o[32];
-            tmem_ld32(to + ch * 32, o);
+            tmem_ld32(to + ch * 32, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= corr;
-            tmem_st32(to + ch * 32, o);
+            for (int e = 0; e < 32; ++e) v[e] *= corr;
+            tmem_st32(to + ch * 32, v);
           }
         }
         tmem_wait_st();
-      }
-      if (special && (!two || slot == 0)) {  // slot 0's PV of a tile is issued before slot 1's
-        const uint32_t vt = vt0 + jj;
-        ok = __all_sync(0xffffffffu, mbar_wait(&ctl->v_full[vt % kVStages], (vt / kVStages) & 1));
-        if (!ok) break;
-        clean_v<D>(smem + C::kOffV + (vt % kVStages) * C::kTile, ctl, s, pos0, r);
-        fence_proxy_async_smem();
       }
       tc_fence_before();
       __syncwarp();
@@ -723,11 +832,10 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
       used[0] += (s.n + 1) / 2;
       used[1] += s.n / 2;
     }
-    vt0 += s.n;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (used[k] > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->s_free[k], (used[k] - 1) & 1));
-    // the slots' row states change hands (the previous segment's have been read)
+    // the row states of slots and copies change hands (the previous segment's have been read)
     ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->x_free, (i & 1) ^ 1));
     if (!ok) break;
     ctl->xm[slot][r] = m;
@@ -736,76 +844,133 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
     if (lane == 0) mbar_arrive(&ctl->x_full);
     ok = __all_sync(0xffffffffu, mbar_wait(&ctl->x_full, i & 1));
     if (!ok) break;
+    // From here to the end of the segment nothing can give up: all eight warps have come this far.
     tc_fence_after();
     const bool any_bad = ctl->bad_any != 0u;
-    float f_mine = 1.f, f_other = 0.f, lt = l, mt = m;
+    float mt = m, lt = l, om = -INFINITY;  // over every state of the row; the other slot's of this thread
     if (!two) {
-      const float om = ctl->xm[slot ^ 1][r], ol = ctl->xl[slot ^ 1][r];
-      mt = fmaxf(m, om);
-      f_mine = m == -INFINITY ? 0.f : ex2(m - mt);
-      f_other = om == -INFINITY ? 0.f : ex2(om - mt);
-      lt = l * f_mine + ol * f_other;
+      const int step = kBM / s.rep;
+      float km[8], kl[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool on = (k >> 1) < s.rep;
+        km[k] = on ? ctl->xm[k & 1][rr + (k >> 1) * step] : -INFINITY;
+        kl[k] = on ? ctl->xl[k & 1][rr + (k >> 1) * step] : 0.f;
+      }
+      om = ctl->xm[slot ^ 1][r];
+      mt = max3f(max3f(km[0], km[1], km[2]), max3f(km[3], km[4], km[5]), fmaxf(km[6], km[7]));
+      lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) lt += kl[k] * (km[k] == -INFINITY ? 0.f : ex2(km[k] - mt));
     }
     const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    const float lse_v = (mt + log2f(lt)) * kLn2;
+    const float f_mine = m == -INFINITY ? 0.f : ex2(m - mt) * inv;
+    const float f_other = om == -INFINITY ? 0.f : ex2(om - mt) * inv;
+    const bool nan = !(lt == lt);  // a NaN among the scores: in every dim
+    // (a slot or copy that saw nothing may hold anything: its O must not be used)
+    const bool plain = __all_sync(0xffffffffu, !valid || (f_mine > 0.f && (two || f_other > 0.f)));
     const int64_t orow = (int64_t)(s.q0 + tok) * a.num_q_heads + (int64_t)s.h * G + g;
-    const int prow = (two ? slot * kBM : 0) + r;
-    if (warp_live) {
-      // two Q tiles: all dims of the thread's own O; one: half of the dims, from both slots' O
-      const int c0 = two ? 0 : slot * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
+    const int prow = (two ? slot * kBM : 0) + rr;
+    // Two Q tiles: all dims of the thread's own O.  One: half of the dims, from both slots' O; of 32 dims
+    // a copy finishes 32 / rep, for which the other copies leave theirs in scratch, so it reads its
+    // groups of 8 dims rotated: the first 4 / rep are its own.
+    const int c0 = two ? 0 : slot * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
+    const int own = 4 / s.rep, rot = copy * own;
+    float* scratch = reinterpret_cast<float*>(smem + C::kOffScratch) + slot * 3 * 32 * 32 + lane;
 #pragma unroll 1
-      for (int ch = c0; ch < c1; ++ch) {
-        float o[32];
+    for (int ch = c0; ch < c1; ++ch) {
+      float o[32];
+      if (two) {
         tmem_ld32(to + ch * 32, o);
-        if (!two) {
-          float x[32];
-          tmem_ld32(tq + kColO + (slot ^ 1) * 128 + ch * 32, x);
-          tmem_wait_ld();
-          // a slot that took no tile holds nothing: its factor is 0 and its O is not read
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = plain || f_mine > 0.f ? o[e] * f_mine : 0.f;
+      } else {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t col = ch * 32 + ((j + rot) & 3) * 8;
+          tmem_ld8(to + col, o + 8 * j);
+          tmem_ld8(tq + kColO + (slot ^ 1) * 128 + col, x + 8 * j);
+        }
+        tmem_wait_ld();
+        if (plain) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(x[e], f_other, o[e] * f_mine);
+        } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             o[e] = (f_mine > 0.f ? o[e] * f_mine : 0.f) + (f_other > 0.f ? x[e] * f_other : 0.f);
-        } else {
-          tmem_wait_ld();
         }
+      }
+      if (nan) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = inv == 0.f ? 0.f : o[e] * inv;
-        if (valid) {
-          if (any_bad) add_nonfinite<D>(a, ctl, s, mrow, ch * 32, o);
+        for (int e = 0; e < 32; ++e) o[e] = lt;
+      }
+      // scratch: areas of [8 dims][32 rows]; with four copies area 3 d + j - 1 is for copy d from the copy j
+      // before it, with two area 4 (row block) + 2 d + j - 2 for copy d's group j - 2
+      if (s.rep == 4) {
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {
+          float* to_copy = scratch + (3 * ((copy + j) & 3) + j - 1) * 256;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) to_copy[e * 32] = o[8 * j + e];
+        }
+        named_bar_sync(1 + slot, 128);
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] += scratch[(3 * copy + j - 1) * 256 + e * 32];
+        named_bar_sync(1 + slot, 128);
+      } else if (s.rep == 2) {
+        float* block = scratch + (wq & 1) * 4 * 256;
+#pragma unroll
+        for (int j = 2; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) block[(2 * (copy ^ 1) + j - 2) * 256 + e * 32] = o[8 * j + e];
+        named_bar_sync(1 + slot, 128);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[8 * j + e] += block[(2 * copy + j) * 256 + e * 32];
+        named_bar_sync(1 + slot, 128);
+      }
+      if (valid) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= own) continue;
+          const int d0 = ch * 32 + ((j + rot) & 3) * 8;
+          const int e = 8 * j;
           if (s.part < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + ch * 32);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                                  pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+            __nv_bfloat16* dst = a.out + orow * D + d0;
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+            if (any_bad) add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 8, dst);
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + ((int64_t)s.part * a.part_rows + prow) * D + ch * 32);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            float* dst = a.part_o + ((int64_t)s.part * a.part_rows + prow) * D + d0;
+            *reinterpret_cast<float4*>(dst) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            *reinterpret_cast<float4*>(dst + 4) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+            if (any_bad) add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 8, dst);
           }
         }
       }
-      if (valid && (two || slot == 0)) {
-        if (s.part >= 0)
-          a.part_lse[(int64_t)s.part * a.part_rows + prow] = lse_v;
-        else if (a.lse)
-          a.lse[orow] = lse_v;
-      }
+    }
+    if (valid && copy == 0 && (two || slot == 0)) {
+      const float lse_v = (mt + log2f(lt)) * kLn2;
+      if (s.part >= 0)
+        a.part_lse[(int64_t)s.part * a.part_rows + prow] = lse_v;
+      else if (a.lse)
+        a.lse[orow] = lse_v;
     }
     tc_fence_before();
+    fence_proxy_async_smem();  // the scratch may become a Q tile
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&ctl->o_free);
       mbar_arrive(&ctl->x_free);
-    }
-    if (any_bad) {  // the notes are cleared between everyone's last reading and the next segment's first note
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->x_free, i & 1));
-      if (!ok) break;
-      if (slot == 0) {
-        if (r < kMaxNodes / 32) ctl->bad[r] = 0u;
-        if (r == 0) ctl->bad_any = 0u;
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      __threadfence_block();
+      atomicAdd(&ctl->epilogues, 1u);
     }
   }
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
@@ -846,14 +1011,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
       mbar_init(&ctl->v_empty[i], 1);
     }
     mbar_init(&ctl->o_free, 8);
-    mbar_init(&ctl->x_full, 8);
+    mbar_init(&ctl->x_full, 8 + 1);  // and the PV warp's notes
     mbar_init(&ctl->x_free, 8);
     mbar_init(&ctl->qk_done, 1);
     mbar_init(&ctl->pv_done, 1);
     ctl->bad_any = 0u;
+    ctl->epilogues = 0u;
     for (int i = 0; i < kMaxNodes / 32; ++i) ctl->bad[i] = 0u;
     fence_mbar_init();
-    prefetch_tmap(&a.tm_q);
+    for (int i = 0; i < 3; ++i) prefetch_tmap(&a.tm_q[i]);
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
   }
@@ -878,8 +1044,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
     }
     __syncwarp();
   } else if (warp == 2) {
+    const bool ok = tree_mma_pv<D>(ctl, smem, tmem);
     if (lane == 0) {
-      if (!tree_mma_pv<D>(ctl, sb, tmem)) report(a.err_word, PKV_DEVERR_TIMEOUT);
+      if (!ok) report(a.err_word, PKV_DEVERR_TIMEOUT);
       umma_commit(&ctl->pv_done);
       if (!mbar_wait(&ctl->pv_done, 0)) report(a.err_word, PKV_DEVERR_TIMEOUT);
     }
@@ -911,7 +1078,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   const int prow = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int r = prow & (kBM - 1), tile = prow / kBM;
   const int tok = cut.t0 + tile * a.tpt + r / a.group;
-  if (tile >= cut.nq || r >= a.rows_used || tok >= cut.T) return;
+  if (tile >= cut.nq || r >= a.group * a.tpt || tok >= cut.T) return;
   constexpr int VPL = D / 32;
   auto slot = [&](int p) -> int64_t { return ((int64_t)2 * (c + p) + (p == 0 ? 1 : 0)) * a.part_rows + prow; };
   float mx = -INFINITY;
@@ -1094,7 +1261,12 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   const uint64_t rows = (uint64_t)pool->num_pages * ps;
   const uint64_t Db = (uint64_t)D * 2;
   a.box_rows = rows_path ? 8 : (ps < kBN ? ps : kBN);
-  if (!pkv_host::encode_tmap_3d(&a.tm_q, q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, p.tpt) ||
+  a.tpt = p.tpt;
+  a.tpt2 = 64 / p.G;
+  a.tpt4 = 32 / p.G;
+  if (!pkv_host::encode_tmap_3d(&a.tm_q[0], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt) ||
+      !pkv_host::encode_tmap_3d(&a.tm_q[1], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt2) ||
+      !pkv_host::encode_tmap_3d(&a.tm_q[2], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt4) ||
       !pkv_host::encode_tmap_3d(&a.tm_k, pool->k, D, Hkv, rows, Db, Hkv * Db, 64, 1, a.box_rows) ||
       !pkv_host::encode_tmap_3d(&a.tm_v, pool->v, D, Hkv, rows, Db, Hkv * Db, 64, 1, a.box_rows))
     return PKV_ERR_CUDA;
@@ -1114,8 +1286,6 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   a.num_kv_heads = pool->num_kv_heads;
   a.num_q_heads = num_q_heads;
   a.group = p.G;
-  a.tpt = p.tpt;
-  a.rows_used = p.G * p.tpt;
   a.batch = batch_size;
   a.num_q_tokens = num_q_tokens;
   a.max_nodes = max_tree_len;

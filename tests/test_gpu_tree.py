@@ -227,9 +227,12 @@ def test_errors_are_reported(lib):
     out, _, err = call(lib, dict(s, prefix=torch.tensor([-1, 60], device="cuda", dtype=torch.int32)))
     assert err == lib.DEVERR_LENGTH and torch.equal(out[9:], ref[0][9:])
     fill = torch.full_like(s["q"], 7.0)
-    out, _, err = call(lib, dict(s, most=5), out=fill)  # the first request has nine
+    out, lse, err = call(lib, dict(s, most=5), out=fill)  # the first request has nine
     assert err == lib.DEVERR_LENGTH and torch.equal(out[9:], ref[0][9:])
-    assert torch.equal(out[:5], ref[0][:5]) and torch.all(out[5:9] == 7.0)
+    assert torch.all(out[5:9] == 7.0)  # five are covered, and see none of the other four
+    prefix, nodes, qo, Hq, Hkv = s["host"]
+    five = dict(s, host=((100,), (5,), qo, Hq, Hkv), rows=[s["rows"][0][:105]], seen=[s["seen"][0][:5, :5]])
+    verify(five, out, lse)
     out, _, err = call(lib, dict(s, qo=torch.tensor([0, 9, 15], device="cuda", dtype=torch.int32)))
     assert err == lib.DEVERR_ROW_OOB and torch.equal(out[:9], ref[0][:9])
 
