@@ -536,71 +536,107 @@ def cascade_decode(q, k_pool, v_pool, plan, sm_scale: float, out=None, lse=None,
 # ---------------------------------------------------------------------------------------------
 # rotary append, 8-bit cache
 # ---------------------------------------------------------------------------------------------
-def _pool_fp8(k_pool, v_pool, k_scale, v_scale) -> PoolFP8:
-    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise TypeError(f"{n} must be torch.float8_e4m3fn (or its bytes as torch.uint8), got {t.dtype}")
-        _need(t, n, t.dtype, k_pool.device)
-    _need(k_scale, "k_scale", torch.float32, k_pool.device)
-    _need(v_scale, "v_scale", torch.float32, k_pool.device)
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
-        raise ValueError("k_pool and v_pool must both be [num_pages, page_size, num_kv_heads, head_dim]")
-    if k_scale.shape != k_pool.shape[:3] or v_scale.shape != k_scale.shape:
-        raise ValueError("k_scale and v_scale must both be [num_pages, page_size, num_kv_heads]")
-    n, ps, hkv, d = k_pool.shape
-    return PoolFP8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, ps, hkv, d)
+# Small steps are bound by the host, so these calls check a tensor with a few attribute reads and hand
+# its address on as a number; only a tensor that fails goes through _need, which says why.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_E4M3 = torch.float8_e4m3fn
 
 
-def _run(dev, stream, fn: str, *args):
-    """_call on dev's current stream (or the given one); dev is made current only when it is not."""
-    if torch.cuda.current_device() == dev.index:
-        _call(fn, *args, _stream_ptr(stream, dev))
+def _addr(t, name, dtype, index):
+    """The address of a contiguous tensor of the given type on CUDA device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, torch.device("cuda", index))
+    return t.data_ptr()
+
+
+def _addr_or_none(t, name, dtype, index):
+    return None if t is None else _addr(t, name, dtype, index)
+
+
+def _device_index(t, name):
+    """The CUDA device index of the tensor that the others have to be beside."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.get_device()
+
+
+def _run(index, stream, fn: str, *args):
+    """Call the library on device `index`'s current stream (or the given one); the device is made
+    current only when it is not."""
+    f = getattr(_lib if _lib is not None else load(), fn)
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current() == index:
+        st = f(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            _call(fn, *args, _stream_ptr(stream, dev))
+        with torch.cuda.device(index):
+            st = f(*args, raw)
+    if st != 0:
+        raise PagedKVError(fn, st)
 
 
-def _new_rows(pool, dev, k_new, v_new, slot_mapping, err_word):
-    """Check the new rows of an append; returns the number of tokens."""
-    _need(k_new, "k_new", torch.bfloat16, dev)
-    _need(v_new, "v_new", torch.bfloat16, dev)
-    _need(slot_mapping, "slot_mapping", torch.int64, dev)
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
+def _pool_bf16(k_pool, v_pool):
+    """(pool, its device index, its shape) of a bf16 cache."""
+    index = _device_index(k_pool, "k_pool")
+    k, v = _addr(k_pool, "k_pool", _BF16, index), _addr(v_pool, "v_pool", _BF16, index)
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape:
+        raise ValueError("k_pool and v_pool must both be [num_pages, page_size, num_kv_heads, head_dim]")
+    return Pool(k, v, *shape), index, shape
+
+
+def _pool_fp8(k_pool, v_pool, k_scale, v_scale):
+    """(pool, its device index, its shape) of an 8-bit cache."""
+    if isinstance(k_pool, torch.Tensor) and k_pool.dtype not in (_E4M3, _U8):
+        raise TypeError(f"k_pool must be torch.float8_e4m3fn (or its bytes as torch.uint8), got {k_pool.dtype}")
+    index = _device_index(k_pool, "k_pool")
+    k, v = _addr(k_pool, "k_pool", k_pool.dtype, index), _addr(v_pool, "v_pool", k_pool.dtype, index)
+    ks, vs = _addr(k_scale, "k_scale", _F32, index), _addr(v_scale, "v_scale", _F32, index)
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape:
+        raise ValueError("k_pool and v_pool must both be [num_pages, page_size, num_kv_heads, head_dim]")
+    if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+        raise ValueError("k_scale and v_scale must both be [num_pages, page_size, num_kv_heads]")
+    return PoolFP8(k, v, ks, vs, *shape), index, shape
+
+
+def _new_rows(index, shape, k_new, v_new, slot_mapping):
+    """Check the new rows of an append: their addresses, the slots' and the number of tokens."""
+    at = (_addr(k_new, "k_new", _BF16, index), _addr(v_new, "v_new", _BF16, index),
+          _addr(slot_mapping, "slot_mapping", _I64, index))
     T = slot_mapping.numel()
-    if k_new.shape != (T, pool.num_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
+    if k_new.shape != (T, shape[2], shape[3]) or v_new.shape != k_new.shape:
         raise ValueError("k_new/v_new must be [num_tokens, num_kv_heads, head_dim]")
-    return T
+    return at, T
 
 
-def _rotary(fn, pool, dev, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out, interleaved,
+def _rotary(fn, pool, index, shape, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out, interleaved,
             err_word, stream):
-    T = _new_rows(pool, dev, k_new, v_new, slot_mapping, err_word)
-    _need(positions, "positions", torch.int32, dev)
-    _need(cos_sin, "cos_sin", torch.float32, dev)
+    rows, T = _new_rows(index, shape, k_new, v_new, slot_mapping)
+    pos, table = _addr(positions, "positions", _I32, index), _addr(cos_sin, "cos_sin", _F32, index)
     if positions.numel() != T or cos_sin.dim() != 2:
         raise ValueError("positions must be [num_tokens] and cos_sin [max_position, rotary_dim]")
     max_position, rotary_dim = cos_sin.shape
-    if rotary_dim % 2 or not 2 <= rotary_dim <= pool.head_dim:
+    if rotary_dim % 2 or not 2 <= rotary_dim <= shape[3]:
         raise ValueError("cos_sin's rotary_dim must be even and at most head_dim")
+    q_at = out_at = None
     Hq = 0
     if q is not None:
-        _need(q, "q", torch.bfloat16, dev)
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != pool.head_dim:
+        q_at = _addr(q, "q", _BF16, index)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != shape[3]:
             raise ValueError("q must be [num_tokens, num_q_heads, head_dim]")
-        if q_out is None:
-            q_out = q
-        _need(q_out, "q_out", torch.bfloat16, dev)
-        if q_out.shape != q.shape:
+        out_at = q_at if q_out is None else _addr(q_out, "q_out", _BF16, index)
+        if q_out is not None and q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
         Hq = q.shape[1]
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _run(dev, stream, fn, ctypes.byref(pool), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(positions),
-         _ptr(cos_sin), max_position, rotary_dim, int(bool(interleaved)), _ptr(q), _ptr(q_out), Hq, T,
-         _ptr(err_word))
+    _run(index, stream, fn, pool, *rows, pos, table, max_position, rotary_dim, 1 if interleaved else 0, q_at, out_at,
+         Hq, T, _addr_or_none(err_word, "err_word", _I32, index))
 
 
 def rotary_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, positions, cos_sin, q=None, q_out=None,
@@ -608,18 +644,18 @@ def rotary_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, positions, cos_
     """Rotate k_new (and q into q_out, in place when q_out is None) by their positions and write K/V
     into the pool slots.  The first cos_sin.shape[1] values of each head are rotated, in half-split
     or (``interleaved``) neighbouring pairs; negative slots are padding."""
-    pool = _pool(k_pool, v_pool)
-    _rotary("pkv_rotary_kv_append", pool, k_pool.device, k_new, v_new, slot_mapping, positions, cos_sin,
-            q, q_out, interleaved, err_word, stream)
+    pool, index, shape = _pool_bf16(k_pool, v_pool)
+    _rotary("pkv_rotary_kv_append", pool, index, shape, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out,
+            interleaved, err_word, stream)
 
 
 def rotary_kv_append_fp8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, positions, cos_sin,
                          q=None, q_out=None, interleaved: bool = False, err_word=None, stream=None) -> None:
     """rotary_kv_append into an 8-bit cache: K (rotated) and V quantised to e4m3 as they are written,
     with a power-of-two scale per row and head."""
-    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
-    _rotary("pkv_rotary_kv_append_fp8", pool, k_pool.device, k_new, v_new, slot_mapping, positions, cos_sin,
-            q, q_out, interleaved, err_word, stream)
+    pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    _rotary("pkv_rotary_kv_append_fp8", pool, index, shape, k_new, v_new, slot_mapping, positions, cos_sin, q,
+            q_out, interleaved, err_word, stream)
 
 
 _ROPE_SCALING = {"none": 0, "linear": 1, "banded": 2, "yarn": 3}
@@ -652,8 +688,8 @@ def rotary_cos_sin_table(max_position: int, rotary_dim: int, theta: float, scali
     _need(out, "out", torch.float32, dev)
     if out.shape != (max_position, rotary_dim):
         raise ValueError("out must be [max_position, rotary_dim]")
-    _run(dev, stream, "pkv_rotary_cos_sin_table", _ptr(out), int(max_position), int(rotary_dim), float(theta),
-         ctypes.byref(spec))
+    _run(dev.index, stream, "pkv_rotary_cos_sin_table", out.data_ptr(), int(max_position), int(rotary_dim),
+         float(theta), spec)
     return out
 
 
@@ -661,33 +697,26 @@ def kv_append_fp8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, 
                   stream=None) -> None:
     """Quantise k_new[t], v_new[t] to e4m3 with a power-of-two scale per row and head and write them
     into pool slot slot_mapping[t] (negative = skip)."""
-    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    T = _new_rows(pool, dev, k_new, v_new, slot_mapping, err_word)
-    _run(dev, stream, "pkv_kv_append_fp8", ctypes.byref(pool), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T,
-         _ptr(err_word))
+    pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    rows, T = _new_rows(index, shape, k_new, v_new, slot_mapping)
+    _run(index, stream, "pkv_kv_append_fp8", pool, *rows, T, _addr_or_none(err_word, "err_word", _I32, index))
 
 
 def paged_gather_fp8(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, out_indptr, k_out,
                      v_out, err_word=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Read an 8-bit cache back as bf16: position j of request b goes to row out_indptr[b] + j of
     k_out/v_out [num_out_rows, num_kv_heads, head_dim]; other rows are left as they were."""
-    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    for t, n in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"), (kv_lens, "kv_lens"),
-                 (out_indptr, "out_indptr")):
-        _need(t, n, torch.int32, dev)
-    _need(k_out, "k_out", torch.bfloat16, dev)
-    _need(v_out, "v_out", torch.bfloat16, dev)
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
+    pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    at = [_addr(t, n, _I32, index) for t, n in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"),
+                                                (kv_lens, "kv_lens"), (out_indptr, "out_indptr"))]
+    ko, vo = _addr(k_out, "k_out", _BF16, index), _addr(v_out, "v_out", _BF16, index)
     B = kv_lens.numel()
     if kv_indptr.numel() != B + 1 or out_indptr.numel() != B + 1:
         raise ValueError("kv_indptr and out_indptr must have batch_size + 1 entries")
-    if k_out.dim() != 3 or k_out.shape[1:] != (pool.num_kv_heads, pool.head_dim) or v_out.shape != k_out.shape:
+    if k_out.dim() != 3 or k_out.shape[1:] != shape[2:] or v_out.shape != k_out.shape:
         raise ValueError("k_out/v_out must be [num_out_rows, num_kv_heads, head_dim]")
-    _run(dev, stream, "pkv_paged_gather_fp8", ctypes.byref(pool), _ptr(kv_indptr), _ptr(kv_indices),
-         _ptr(kv_lens), B, _ptr(out_indptr), k_out.shape[0], _ptr(k_out), _ptr(v_out), _ptr(err_word))
+    _run(index, stream, "pkv_paged_gather_fp8", pool, *at[:3], B, at[3], k_out.shape[0], ko, vo,
+         _addr_or_none(err_word, "err_word", _I32, index))
     return k_out, v_out
 
 
@@ -696,32 +725,29 @@ def decode_fp8_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim, d
         return int(load().pkv_decode_fp8_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim))
 
 
-def _attention_io(q, dev, rows, out, lse, return_lse, err_word):
-    """Check (or make) the outputs of an attention call over q [N, Hq, D]; rows: N, if it is known."""
-    _need(q, "q", torch.bfloat16, dev)
-    if q.dim() != 3 or (rows is not None and q.shape[0] != rows):
-        raise ValueError("q must be [num_rows, num_q_heads, head_dim]")
+def _attention_io(q, index, head_dim, out, lse, return_lse):
+    """Check (or make) the outputs of an attention call over q [N, Hq, D]: (out, lse, the addresses of
+    q, out and lse)."""
+    at = _addr(q, "q", _BF16, index)
+    if q.dim() != 3 or q.shape[2] != head_dim:
+        raise ValueError("q must be [num_rows, num_q_heads, head_dim], with the pool's head_dim")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, dev)
+    o_at = _addr(out, "out", _BF16, index)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, dev)
-        if lse.shape != q.shape[:2]:
-            raise ValueError("lse must be [num_rows, num_q_heads]")
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
-    return out, lse
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    l_at = _addr_or_none(lse, "lse", _F32, index)
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [num_rows, num_q_heads]")
+    return out, lse, at, o_at, l_at
 
 
-def _page_table(dev, kv_indptr, kv_indices, B):
-    _need(kv_indptr, "kv_indptr", torch.int32, dev)
-    _need(kv_indices, "kv_indices", torch.int32, dev)
+def _page_table(index, kv_indptr, kv_indices, B):
     if kv_indptr.numel() != B + 1:
         raise ValueError("kv_indptr must have batch_size + 1 entries")
+    return _addr(kv_indptr, "kv_indptr", _I32, index), _addr(kv_indices, "kv_indices", _I32, index)
 
 
 def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, sm_scale: float,
@@ -729,22 +755,20 @@ def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices,
                      max_ctas=0):
     """Decode attention of q [B, Hq, D] over each request's pages of an 8-bit cache.  Returns
     (out, lse); arguments as for paged_decode."""
-    pool = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    _need(kv_lens, "kv_lens", torch.int32, dev)
+    pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
+    lens = _addr(kv_lens, "kv_lens", _I32, index)
     B = kv_lens.numel()
-    _page_table(dev, kv_indptr, kv_indices, B)
-    out, lse = _attention_io(q, dev, B, out, lse, return_lse, err_word)
-    if q.shape[2] != pool.head_dim:
-        raise ValueError("q and the pool differ in head_dim")
+    indptr, indices = _page_table(index, kv_indptr, kv_indices, B)
+    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse)
+    if q.shape[0] != B:
+        raise ValueError("q must have one row per request")
     Hq = q.shape[1]
     if workspace is None:
-        need = decode_fp8_workspace_size(B, Hq, pool.num_kv_heads, pool.head_dim, dev)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    _run(dev, stream, "pkv_paged_decode_fp8", ctypes.byref(pool), _ptr(q), B, Hq, _ptr(kv_indptr),
-         _ptr(kv_indices), _ptr(kv_lens), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
-         workspace.numel(), _ptr(err_word), int(max_ctas))
+        need = decode_fp8_workspace_size(B, Hq, shape[2], shape[3], index)
+        workspace = torch.empty(max(need, 256), dtype=_U8, device=q.device)
+    _run(index, stream, "pkv_paged_decode_fp8", pool, q_at, B, Hq, indptr, indices, lens, sm_scale, o_at, l_at,
+         _addr(workspace, "workspace", _U8, index), workspace.numel(), _addr_or_none(err_word, "err_word", _I32, index),
+         max_ctas)
     return out, lse
 
 
@@ -757,11 +781,11 @@ def tree_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim, max_tre
                                                   max_tree_len))
 
 
-def _mask_words(tree_mask, dev, rows, max_tree_len):
-    _need(tree_mask, "tree_mask", torch.int32, dev)
+def _mask_words(tree_mask, index, rows, max_tree_len):
+    at = _addr(tree_mask, "tree_mask", _I32, index)
     if tree_mask.dim() != 2 or tree_mask.shape[0] != rows or 32 * tree_mask.shape[1] < max_tree_len:
         raise ValueError("tree_mask must be [num_q_tokens, words] with 32 * words >= max_tree_len")
-    return tree_mask.shape[1]
+    return at, tree_mask.shape[1]
 
 
 def paged_tree_attention(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, prefix_lens, tree_mask,
@@ -770,26 +794,21 @@ def paged_tree_attention(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, pr
     """Attention of each request's drafted tokens (rows qo_indptr[b].. of q) over its cached prefix
     and the drafted tokens whose bits its tree_mask row (int32 [num_q_tokens, words]) sets.  Returns
     (out, lse)."""
-    pool = _pool(k_pool, v_pool)
-    dev = k_pool.device
-    _need(qo_indptr, "qo_indptr", torch.int32, dev)
-    _need(prefix_lens, "prefix_lens", torch.int32, dev)
+    pool, index, shape = _pool_bf16(k_pool, v_pool)
+    qo, prefix = _addr(qo_indptr, "qo_indptr", _I32, index), _addr(prefix_lens, "prefix_lens", _I32, index)
     B = prefix_lens.numel()
-    _page_table(dev, kv_indptr, kv_indices, B)
+    indptr, indices = _page_table(index, kv_indptr, kv_indices, B)
     if qo_indptr.numel() != B + 1:
         raise ValueError("qo_indptr must have batch_size + 1 entries")
-    out, lse = _attention_io(q, dev, None, out, lse, return_lse, err_word)
+    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse)
     N, Hq, D = q.shape
-    if D != pool.head_dim:
-        raise ValueError("q and the pool differ in head_dim")
-    words = _mask_words(tree_mask, dev, N, max_tree_len)
+    mask, words = _mask_words(tree_mask, index, N, max_tree_len)
     if workspace is None:
-        need = tree_workspace_size(B, Hq, pool.num_kv_heads, D, max_tree_len, dev)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    _run(dev, stream, "pkv_paged_tree_attention", ctypes.byref(pool), _ptr(q), N, _ptr(qo_indptr), B, Hq,
-         _ptr(kv_indptr), _ptr(kv_indices), _ptr(prefix_lens), _ptr(tree_mask), words, int(max_tree_len),
-         float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err_word))
+        need = tree_workspace_size(B, Hq, shape[2], D, max_tree_len, index)
+        workspace = torch.empty(max(need, 256), dtype=_U8, device=q.device)
+    _run(index, stream, "pkv_paged_tree_attention", pool, q_at, N, qo, B, Hq, indptr, indices, prefix, mask, words,
+         max_tree_len, sm_scale, o_at, l_at, _addr(workspace, "workspace", _U8, index), workspace.numel(),
+         _addr_or_none(err_word, "err_word", _I32, index))
     return out, lse
 
 
@@ -797,17 +816,14 @@ def tree_mask_from_parents(parents, qo_indptr, max_tree_len: int, out=None, err_
                            stream=None) -> torch.Tensor:
     """The tree_mask of trees given by parents (int32 [num_tokens], each the parent's index within its
     request's tree, negative for a root; parents come before their children)."""
-    _need(parents, "parents", torch.int32)
-    dev = parents.device
-    _need(qo_indptr, "qo_indptr", torch.int32, dev)
+    index = _device_index(parents, "parents")
+    at, qo = _addr(parents, "parents", _I32, index), _addr(qo_indptr, "qo_indptr", _I32, index)
     if parents.dim() != 1 or qo_indptr.numel() < 1:
         raise ValueError("parents must be [num_tokens] and qo_indptr [batch_size + 1]")
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
     N = parents.numel()
     if out is None:
-        out = torch.zeros((N, -(-int(max_tree_len) // 32)), dtype=torch.int32, device=dev)
-    words = _mask_words(out, dev, N, max_tree_len)
-    _run(dev, stream, "pkv_tree_mask_from_parents", _ptr(parents), _ptr(qo_indptr), qo_indptr.numel() - 1, N,
-         int(max_tree_len), words, _ptr(out), _ptr(err_word))
+        out = torch.zeros((N, -(-int(max_tree_len) // 32)), dtype=_I32, device=parents.device)
+    mask, words = _mask_words(out, index, N, max_tree_len)
+    _run(index, stream, "pkv_tree_mask_from_parents", at, qo, qo_indptr.numel() - 1, N, max_tree_len, words, mask,
+         _addr_or_none(err_word, "err_word", _I32, index))
     return out
