@@ -52,6 +52,7 @@ struct Decode8Args {
   const float* v_scale;
   int64_t num_pages;
   int32_t page_size, num_kv_heads;
+  FastDiv page_div;  // by page_size
   const __nv_bfloat16* q;
   int32_t batch, num_q_heads;
   const int32_t* kv_indptr;
@@ -108,18 +109,24 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Producer warp: walk the CTA's share of the slice stream and fill stages.
+// Producer warps, one for K and one for V: each walks the CTA's share of the slice stream and fills
+// its part of the stages; K's also writes the headers.  A stage is a few hundred cycles of address work
+// for a warp and about 1400 of memory time, so one warp for both held the stream back (8 x 32768
+// positions, D 128: 105 us against 93 with two, loads alone).
 // ---------------------------------------------------------------------------------------------
 template <int D, bool TMA>
 __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr* hdr, uint64_t* full,
-                                 uint64_t* empty) {
+                                 uint64_t* empty, bool v) {
   const int lane = threadIdx.x & 31;
-  const int NS = a.num_stages, Ts = a.stage_tokens, W = a.W, HC = a.HC, nhg = a.nhg, ps = a.page_size;
+  const int NS = a.num_stages, Ts = a.stage_tokens, W = a.W, HC = a.HC, nhg = a.nhg;
   const uint32_t region = a.kv_region;
+  const CUtensorMap* tm = v ? &a.tm_v : &a.tm_k;
+  const uint8_t* pool = v ? a.v_pool : a.k_pool;
+  const float* scale = v ? a.v_scale : a.k_scale;
   // Page indices come from a register window of 96 consecutive entries (three 32-lane slices), its
   // last third loaded 32 pages before a stage can need it.  Usable while one stage spans at most
   // 33 pages.
-  const bool windowed = (Ts - 1) / ps + 1 <= 32;
+  const bool windowed = (Ts - 1) / a.page_size + 1 <= 32;
 
   int64_t sumS = 0;  // slices over all requests
   for (int i = lane; i < a.batch; i += 32) sumS += (max(0, __ldg(a.kv_lens + i)) + kSlice - 1) / kSlice;
@@ -133,18 +140,11 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
   int stage = 0;
   uint32_t phase = 0;
   bool ok = true;
-  int32_t cur_p0 = 0, cur_p1 = 0;  // page list of the request being streamed
+  int32_t cur_p0 = 0, cur_np = 0;  // page list of the request being streamed
   int win_b = -1, wbase = 0;
   int32_t w0 = -1, w1 = -1, w2 = -1;
   auto entry = [&](int pidx) -> int32_t {  // page-list entry of the current request; -1 past its end
-    const int64_t s = (int64_t)cur_p0 + pidx;
-    return (pidx >= 0 && s < cur_p1) ? __ldg(a.kv_indices + s) : -1;
-  };
-  auto window_page = [&](int pidx) -> int32_t {  // all lanes must call; pidx - wbase < 64
-    const int k = pidx - wbase;
-    const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
-    const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
-    return k < 32 ? v0 : v1;
+    return pidx < cur_np ? __ldg(a.kv_indices + cur_p0 + pidx) : -1;
   };
   int nissued = 0;
   auto next_stage = [&]() {
@@ -156,14 +156,14 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
   };
 
   auto emit = [&](int unit, int b, int hg, int tok0, int ntok, int flags) -> bool {
-    if (unit >= 0 && (flags & kSegFirst)) {
+    if (unit >= 0 && !v && (flags & kSegFirst)) {
       const int hqu = HC * a.group;  // the unit's queries, on their way to L2 before they are read
       const char* qb = reinterpret_cast<const char*>(a.q + ((int64_t)b * a.num_q_heads + (int64_t)hg * hqu) * D);
       for (int off = lane * 128; off < hqu * D * 2; off += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(qb + off));
     }
     if (unit >= 0 && windowed) {
-      const int first_page = tok0 / ps;
+      const int first_page = a.page_div.quot(tok0);
       if (b != win_b || first_page < wbase) {
         win_b = b;
         wbase = first_page;
@@ -178,97 +178,72 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
         w2 = entry(wbase + 64 + lane);
       }
     }
-    if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) {
-      if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      return false;
-    }
-    if (lane == 0) hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, 0, 0};
-    uint8_t* kst = stages + (size_t)stage * a.stage_bytes;
-    uint8_t* vst = kst + region;
-    const uint32_t sst = smem_u32(vst + region);
-    if (unit < 0) {
-      if (lane == 0) mbar_arrive(&full[stage]);
-      cp_async_arrive(&full[stage]);
-      next_stage();
-      return true;
-    }
-    // token lane + 32 r of the stage: its pool row, or -1 (past the stage, or a bad index, reported)
-    uint32_t bad = 0;
-    auto slot_of = [&](int tok, bool in) -> int64_t {  // all lanes call (shuffles)
-      const int pidx = tok / ps;
-      const int32_t page = windowed ? window_page(in ? pidx : tok0 / ps) : (in ? entry(pidx) : -1);
-      if (!in) return -1;
-      if ((int64_t)cur_p0 + pidx >= cur_p1) {
-        bad |= PKV_DEVERR_LENGTH;
-        return -1;
-      }
-      if (page < 0 || page >= a.num_pages) {
-        bad |= PKV_DEVERR_PAGE_OOB;
-        return -1;
-      }
-      return (int64_t)page * ps + (tok - pidx * ps);
-    };
-    auto scales = [&](int64_t slot, int j) {  // the HC scales of token j of the stage, K then V
-      const float* ks = a.k_scale + slot * a.num_kv_heads + hg * HC;
-      const float* vs = a.v_scale + slot * a.num_kv_heads + hg * HC;
-      const uint32_t kd = sst + (uint32_t)(j * HC) * 4, vd = kd + (uint32_t)(Ts * HC) * 4;
-      if ((HC & 3) == 0) {
-        for (int i = 0; i < HC; i += 4) {
-          cp_async16(kd + 4 * i, ks + i);
-          cp_async16(vd + 4 * i, vs + i);
-        }
-      } else {
-        for (int i = 0; i < HC; ++i) {
-          cp_async4(kd + 4 * i, ks + i);
-          cp_async4(vd + 4 * i, vs + i);
-        }
-      }
-    };
-    if constexpr (TMA) {
-      // lane i fetches box i: box_rows tokens inside one page
-      const int R = a.box_rows, nbox = Ts / R;
-      const int tok = tok0 + R * lane;
-      const int64_t row = slot_of(tok, lane < nbox && tok < tok0 + ntok);
-      const int nload = __popc(__ballot_sync(0xffffffffu, row >= 0));
-      const uint32_t box = (uint32_t)(HC * R * D);
-      if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)nload * box * 2);
-      __syncwarp();
-      if (row >= 0) {
-        tma_load_3d(smem_u32(kst) + lane * box, &a.tm_k, 0, (int)row, hg * HC, &full[stage]);
-        tma_load_3d(smem_u32(vst) + lane * box, &a.tm_v, 0, (int)row, hg * HC, &full[stage]);
-      }
-      for (int r = 0; r < W; ++r) {
+    uint64_t* bar = &full[stage];
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) return false;
+    if (!v && lane == 0) hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, 0, 0};
+    if (unit >= 0) {
+      const uint32_t dst = smem_u32(stages + (size_t)stage * a.stage_bytes) + (v ? region : 0u);
+      const uint32_t sdst = smem_u32(stages + (size_t)stage * a.stage_bytes) + 2 * region + (v ? (uint32_t)(Ts * HC) * 4 : 0u);
+      uint32_t bad = 0;
+      for (int r = 0; r < W; ++r) {  // 32 tokens at a time: this lane's pool row, or -1
         const int j = lane + 32 * r;
-        const int64_t slot = slot_of(tok0 + j, j < ntok);
-        if (slot >= 0) scales(slot, j);
-      }
-    } else {
-      const uint32_t RB = (uint32_t)(HC * D);
-      uint32_t n = 0;
-      // the byte count of the stage first, the copies after it (the barrier must not complete early)
-      int64_t slots[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int j = lane + 32 * r;
-        slots[r] = r < W ? slot_of(tok0 + j, j < ntok) : -1;
-        n += slots[r] >= 0;
-      }
-      n = warp_sum(n);
-      if (lane == 0) mbar_arrive_expect_tx(&full[stage], n * RB * 2);
-      __syncwarp();
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        if (slots[r] >= 0) {
-          const int j = lane + 32 * r;
-          const int64_t src = (slots[r] * a.num_kv_heads + hg * HC) * D;
-          bulk_g2s(kst + (size_t)j * a.row_stride, a.k_pool + src, RB, &full[stage]);
-          bulk_g2s(vst + (size_t)j * a.row_stride, a.v_pool + src, RB, &full[stage]);
-          scales(slots[r], j);
+        const bool in = j < ntok;
+        uint32_t pidx, prow;
+        a.page_div.divmod((uint32_t)(tok0 + (in ? j : 0)), pidx, prow);
+        int32_t page;
+        if (windowed) {
+          const int k = (int)pidx - wbase;  // < 64
+          const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
+          const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
+          page = k < 32 ? v0 : v1;
+        } else {
+          page = in ? entry((int)pidx) : -1;
+        }
+        int64_t slot = -1;
+        if (in) {
+          if ((int)pidx >= cur_np)
+            bad |= PKV_DEVERR_LENGTH;
+          else if (page < 0 || page >= a.num_pages)
+            bad |= PKV_DEVERR_PAGE_OOB;
+          else
+            slot = (int64_t)page * a.page_size + prow;
+        }
+        if constexpr (TMA) {
+          // boxes of R tokens inside one page: the one of tokens R i .. has the row of its first token
+          const int R = a.box_rows;
+          const int first = lane * R;
+          const int row = __shfl_sync(0xffffffffu, (int)slot, first & 31);
+          const bool mine = first < 32 && row >= 0;
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+          const uint32_t box = (uint32_t)(HC * R * D);
+          if (lane == 0) mbar_expect_tx(bar, n * box);
+          __syncwarp();
+          if (mine) tma_load_3d(dst + (uint32_t)(32 / R * r + lane) * box, tm, 0, row, hg * HC, bar);
+        } else {
+          const uint32_t RB = (uint32_t)(HC * D);
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, slot >= 0));
+          if (lane == 0) mbar_expect_tx(bar, n * RB);
+          __syncwarp();
+          if (slot >= 0)
+            bulk_g2s(stages + (size_t)stage * a.stage_bytes + (v ? region : 0u) + (size_t)j * a.row_stride,
+                     pool + (slot * a.num_kv_heads + hg * HC) * D, RB, bar);
+        }
+        if (slot >= 0) {  // the token's HC scales
+          const float* src = scale + slot * a.num_kv_heads + hg * HC;
+          const uint32_t sd = sdst + (uint32_t)(j * HC) * 4;
+          if ((HC & 3) == 0) {
+            for (int i = 0; i < HC; i += 4) cp_async16(sd + 4 * i, src + i);
+          } else {
+            for (int i = 0; i < HC; ++i) cp_async4(sd + 4 * i, src + i);
+          }
         }
       }
+      if (bad && !v) report(a.err_word, bad);
     }
-    if (bad) report(a.err_word, bad);
-    cp_async_arrive(&full[stage]);
+    // the arrival that lets the stage complete comes after every byte count
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    cp_async_arrive(bar);
     next_stage();
     return true;
   };
@@ -299,7 +274,7 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
         const int64_t Sb = __shfl_sync(0xffffffffu, S, src_lane);
         const int64_t rsb = __shfl_sync(0xffffffffu, rs, src_lane);
         cur_p0 = __shfl_sync(0xffffffffu, ip0, src_lane);
-        cur_p1 = __shfl_sync(0xffffffffu, ip1, src_lane);
+        cur_np = __shfl_sync(0xffffffffu, ip1, src_lane) - cur_p0;
         for (int hg = 0; hg < nhg && ok; ++hg) {
           const int64_t us = rsb + (int64_t)hg * Sb, ue = us + Sb;
           const int64_t s0 = max(us, c0), s1 = min(ue, c1);
@@ -319,7 +294,8 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
       base += nhg * __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  if (ok) emit(-1, 0, 0, 0, 0, 0);
+  ok = ok && emit(-1, 0, 0, 0, 0, 0);
+  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   // No copy into this CTA's shared memory is in flight when it exits (bounded waits; immediate on
   // the normal path, where the consumers have seen every stage complete).
   for (int k = 0; k < min(nissued, NS); ++k) {
@@ -431,35 +407,13 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
     const int nv = min(kSlice, h.ntok - si * kSlice);
     const uint32_t kb = stages_u32 + (uint32_t)stage * a.stage_bytes;
     const uint32_t vb = kb + region;
-    if (nv > 0 && nv < kSlice) {
-      // rows past the request's end hold unused pool slots (the boxes bring them, possibly NaN) or
-      // what shared memory held before: V rows there become 0 so that weight 0 times V stays 0
-      // (scores there are masked by a select).
-      uint8_t* vreg = stages + (size_t)stage * a.stage_bytes + region;
-      for (int idx = lane; idx < (kSlice - nv) * NK; idx += 32) {
-        const int t = si * kSlice + nv + idx / NK, ch = idx % NK;
-        uint32_t off;
-        if (TMA)
-          off = (uint32_t)(((t / a.box_rows) * HC + hl) * a.box_rows + t % a.box_rows) * D;
-        else
-          off = (uint32_t)(t * a.row_stride + hl * D);
-        *reinterpret_cast<uint4*>(vreg + off + ch * 16) = make_uint4(0u, 0u, 0u, 0u);  // whole rows: any order
-      }
-      __syncwarp();
-    }
+    const float* sc = reinterpret_cast<const float*>(stages + (size_t)stage * a.stage_bytes + 2 * region) +
+                      (si * kSlice + g) * HC + hl;  // K scales of tokens g, g + 8, ... of the slice; V's Ts rows on
+    float s[2][2][NT][4];  // [half][chunk parity]: four independent accumulation chains
+    float ksc[4];
     if (nv > 0) {
-      // scales of tokens g, g + 8, g + 16, g + 24 of the slice
-      const float* sc = reinterpret_cast<const float*>(stages + (size_t)stage * a.stage_bytes + 2 * region) +
-                        (si * kSlice + g) * HC + hl;
-      float ksc[4], vm[4], ve[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ksc[i] = sc[8 * i * HC];
-        const uint32_t u = __float_as_uint(sc[(Ts + 8 * i) * HC]);
-        ve[i] = (float)((int)(u >> 23) - 127);
-        vm[i] = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
-      }
-      float s[2][2][NT][4];  // [half][chunk parity]: four independent accumulation chains
+      for (int i = 0; i < 4; ++i) ksc[i] = sc[8 * i * HC];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -484,6 +438,37 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
               mma_f16_16816(s[hf][pr][nt], a0, a1, a2, a3, qf[nt][2 * j + pr][0], qf[nt][2 * j + pr][1]);
           }
         }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);  // K is read: its buffer is free while V is still in use
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[NS + stage], phase))) {
+      if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+      break;
+    }
+    if (nv > 0 && nv < kSlice) {
+      // rows past the request's end hold unused pool slots (the boxes bring them, possibly NaN) or
+      // what shared memory held before: V rows there become 0 so that weight 0 times V stays 0
+      // (scores there are masked by a select).
+      uint8_t* vreg = stages + (size_t)stage * a.stage_bytes + region;
+      for (int idx = lane; idx < (kSlice - nv) * NK; idx += 32) {
+        const int t = si * kSlice + nv + idx / NK, ch = idx % NK;
+        uint32_t off;
+        if (TMA)
+          off = (uint32_t)(((t / a.box_rows) * HC + hl) * a.box_rows + t % a.box_rows) * D;
+        else
+          off = (uint32_t)(t * a.row_stride + hl * D);
+        *reinterpret_cast<uint4*>(vreg + off + ch * 16) = make_uint4(0u, 0u, 0u, 0u);  // whole rows: any order
+      }
+      __syncwarp();
+    }
+    if (nv > 0) {
+      float vm[4], ve[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u = __float_as_uint(sc[(Ts + 8 * i) * HC]);
+        ve[i] = (float)((int)(u >> 23) - 127);
+        vm[i] = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
       }
       uint32_t bp[2][NT][2];
 #pragma unroll
@@ -558,7 +543,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
     }
     if (nv > 0 && nv < kSlice) fence_proxy_async_smem();  // zeros above, before the next async fill
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);
+    if (lane == 0) mbar_arrive(&empty[NS + stage]);
 
     if (h.flags & kSegLast) {
       if (W > 1) {
@@ -652,7 +637,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
 }
 
 template <int D, int NT, bool TMA>
-__global__ void __launch_bounds__(288, 1) paged_decode8_kernel(const __grid_constant__ Decode8Args a) {
+__global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_constant__ Decode8Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int NS = a.num_stages;
   const int NC = a.HC * a.W;
@@ -663,12 +648,12 @@ __global__ void __launch_bounds__(288, 1) paged_decode8_kernel(const __grid_cons
   uint8_t* stages = smem;
   StageHdr* hdr = reinterpret_cast<StageHdr*>(smem + (size_t)NS * a.stage_bytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(hdr + NS);
-  uint64_t* empty = full + NS;
-  float* mbuf = reinterpret_cast<float*>(empty + NS);
+  uint64_t* empty = full + 2 * NS;  // K's barriers, then V's
+  float* mbuf = reinterpret_cast<float*>(empty + 2 * NS);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1 + 32);  // the byte count, and every producer lane's scale copies
+    for (int s = 0; s < 2 * NS; ++s) {
+      mbar_init(&full[s], 1 + 32);  // a producer's go-ahead, and every lane's scale copies
       mbar_init(&empty[s], NC);
     }
     fence_mbar_init();
@@ -682,7 +667,9 @@ __global__ void __launch_bounds__(288, 1) paged_decode8_kernel(const __grid_cons
 
   const int warp = threadIdx.x >> 5;
   if (warp == NC) {
-    decode8_producer<D, TMA>(a, stages, hdr, full, empty);
+    decode8_producer<D, TMA>(a, stages, hdr, full, empty, false);
+  } else if (warp == NC + 1) {
+    decode8_producer<D, TMA>(a, stages, hdr, full + NS, empty + NS, true);
   } else if (warp < NC) {
     decode8_consumer<D, NT, TMA>(a, stages, hdr, full, empty, mbuf);
   }
@@ -805,11 +792,11 @@ bool make_plan(int B, int Hq, int Hkv, int D, int ncta, Plan& p, int page_size =
   p.stage = (2 * p.region + (uint32_t)(2 * p.Ts * p.HC * 4) + 1023u) & ~1023u;
   const int mf = p.NT * (6 + (D / 16) * 4);
   const size_t mbytes = p.W > 1 ? (size_t)(p.W - 1) * p.HC * mf * 32 * 4 : 0;
-  const size_t fixed = mbytes + (size_t)kMaxStages * (sizeof(StageHdr) + 16);
+  const size_t fixed = mbytes + (size_t)kMaxStages * (sizeof(StageHdr) + 32);
   if (fixed + 2 * (size_t)p.stage > kSmemBudget) return false;
   p.NS = (int)((kSmemBudget - fixed) / p.stage);
   if (p.NS > kMaxStages) p.NS = kMaxStages;
-  p.smem = (size_t)p.NS * p.stage + (size_t)p.NS * (sizeof(StageHdr) + 16) + mbytes;
+  p.smem = (size_t)p.NS * p.stage + (size_t)p.NS * (sizeof(StageHdr) + 32) + mbytes;
   p.ncta = ncta;
   p.nunits = (int64_t)B * p.nhg;
   p.nparts = p.ncta + p.nunits;
@@ -834,7 +821,7 @@ pkv_status launch(const Plan& p, const Decode8Args& a, cudaStream_t st) {
       return PKV_ERR_CUDA;
     if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<p.ncta, (p.HC * p.W + 1) * 32, p.smem, st>>>(a);
+  kern<<<p.ncta, (p.HC * p.W + 2) * 32, p.smem, st>>>(a);
   const pkv_status s = pkv_host::launch_status();
   if (s != PKV_OK) return s;
   cudaLaunchConfig_t cfg = {};
@@ -893,6 +880,7 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
   a.v_scale = pool->v_scale;
   a.num_pages = pool->num_pages;
   a.page_size = pool->page_size;
+  a.page_div = FastDiv((uint32_t)pool->page_size);
   a.num_kv_heads = pool->num_kv_heads;
   a.q = (const __nv_bfloat16*)q;
   a.batch = batch_size;
