@@ -115,8 +115,8 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
 // positions, D 128: 105 us against 93 with two, loads alone).
 // ---------------------------------------------------------------------------------------------
 template <int D, bool TMA>
-__device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr* hdr, uint64_t* full,
-                                 uint64_t* empty, bool v) {
+__device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
+                                 uint64_t* full, uint64_t* empty, bool v) {
   const int lane = threadIdx.x & 31;
   const int NS = a.num_stages, Ts = a.stage_tokens, W = a.W, HC = a.HC, nhg = a.nhg;
   const uint32_t region = a.kv_region;
@@ -128,8 +128,17 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
   // 33 pages.
   const bool windowed = (Ts - 1) / a.page_size + 1 <= 32;
 
-  int64_t sumS = 0;  // slices over all requests
-  for (int i = lane; i < a.batch; i += 32) sumS += (max(0, __ldg(a.kv_lens + i)) + kSlice - 1) / kSlice;
+  // the first 32 requests' numbers in one round of loads, which the walk below starts with
+  const bool in0 = lane < a.batch;
+  const int32_t first_len = in0 ? max(0, __ldg(a.kv_lens + lane)) : 0;
+  const int32_t first_p0 = in0 ? __ldg(a.kv_indptr + lane) : 0;
+  const int32_t first_p1 = in0 ? __ldg(a.kv_indptr + lane + 1) : 0;
+  int64_t sumS = ((int64_t)first_len + kSlice - 1) / kSlice;  // slices over all requests
+  for (int i = 32 + lane; i < a.batch; i += 128) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)  // four loads in flight
+      if (i + 32 * u < a.batch) sumS += ((int64_t)max(0, __ldg(a.kv_lens + i + 32 * u)) + kSlice - 1) / kSlice;
+  }
   sumS = warp_sum(sumS);
   const int64_t T = sumS * nhg;
   int64_t share = (T + gridDim.x - 1) / gridDim.x;
@@ -180,7 +189,10 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
     }
     uint64_t* bar = &full[stage];
     if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) return false;
-    if (!v && lane == 0) hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, 0, 0};
+    if (!v && lane == 0) {  // the consumers read the header, and a new unit's queries, while the stage is on its way
+      hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, 0, 0};
+      mbar_arrive(&hdr_full[stage]);
+    }
     if (unit >= 0) {
       const uint32_t dst = smem_u32(stages + (size_t)stage * a.stage_bytes) + (v ? region : 0u);
       const uint32_t sdst = smem_u32(stages + (size_t)stage * a.stage_bytes) + 2 * region + (v ? (uint32_t)(Ts * HC) * 4 : 0u);
@@ -253,10 +265,14 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
     for (int b0 = 0; b0 < a.batch && base < c1 && ok; b0 += 32) {
       const int b = b0 + lane;
       const bool in = b < a.batch;
-      const int64_t L = in ? (int64_t)max(0, __ldg(a.kv_lens + b)) : 0;
+      int64_t L = first_len;
+      int32_t ip0 = first_p0, ip1 = first_p1;
+      if (b0 > 0) {
+        L = in ? (int64_t)max(0, __ldg(a.kv_lens + b)) : 0;
+        ip0 = in ? __ldg(a.kv_indptr + b) : 0;
+        ip1 = in ? __ldg(a.kv_indptr + b + 1) : 0;
+      }
       const int64_t S = (L + kSlice - 1) / kSlice;
-      const int32_t ip0 = in ? __ldg(a.kv_indptr + b) : 0;
-      const int32_t ip1 = in ? __ldg(a.kv_indptr + b + 1) : 0;
       int64_t incl = S;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -295,6 +311,10 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
     }
   }
   ok = ok && emit(-1, 0, 0, 0, 0, 0);
+  // The merge may be scheduled once every CTA has issued its last copies (it waits for this grid's
+  // completion before it reads): early enough to hide its launch, late enough not to hold thread
+  // slots that kernels on other streams could use.
+  if (!v) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   // No copy into this CTA's shared memory is in flight when it exits (bounded waits; immediate on
   // the normal path, where the consumers have seen every stage complete).
@@ -311,8 +331,8 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
 // Consumer warps: 32-position steps of one KV head with its G query heads.
 // ---------------------------------------------------------------------------------------------
 template <int D, int NT, bool TMA>
-__device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr* hdr, uint64_t* full,
-                                 uint64_t* empty, float* mbuf) {
+__device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
+                                 uint64_t* full, uint64_t* empty, float* mbuf) {
   constexpr int NK = D / 16;                      // 16-byte chunks of a row: k-steps of K q, row tiles of O
   constexpr int MF = NT * (6 + NK * 4);           // floats per lane merged between the warps of a head
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -353,7 +373,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
   int stage = 0;
   uint32_t phase = 0;
   while (true) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&hdr_full[stage], phase))) {
       if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
       break;
     }
@@ -404,12 +424,17 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
       }
     }
 
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
+      if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+      break;
+    }
     const int nv = min(kSlice, h.ntok - si * kSlice);
     const uint32_t kb = stages_u32 + (uint32_t)stage * a.stage_bytes;
     const uint32_t vb = kb + region;
     const float* sc = reinterpret_cast<const float*>(stages + (size_t)stage * a.stage_bytes + 2 * region) +
                       (si * kSlice + g) * HC + hl;  // K scales of tokens g, g + 8, ... of the slice; V's Ts rows on
-    float s[2][2][NT][4];  // [half][chunk parity]: four independent accumulation chains
+    constexpr int PR = NT == 1 ? 2 : 1;
+    float s[2][PR][NT][4];  // [half][chunk parity]: four independent accumulation chains
     float ksc[4];
     if (nv > 0) {
 #pragma unroll
@@ -417,7 +442,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int pr = 0; pr < 2; ++pr)
+        for (int pr = 0; pr < PR; ++pr)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -435,7 +460,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
             unpack_e4m3x4(r[2 * pr + 1], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(s[hf][pr][nt], a0, a1, a2, a3, qf[nt][2 * j + pr][0], qf[nt][2 * j + pr][1]);
+              mma_f16_16816(s[hf][pr % PR][nt], a0, a1, a2, a3, qf[nt][2 * j + pr][0], qf[nt][2 * j + pr][1]);
           }
         }
       }
@@ -480,7 +505,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 2 * hf + (i >> 1);  // token g + 8 row
-            const float v = (s[hf][0][nt][i] + s[hf][1][nt][i]) * qs[nt][i & 1] * ksc[row];
+            const float v = (PR == 2 ? s[hf][0][nt][i] + s[hf][PR - 1][nt][i] : s[hf][0][nt][i]) * qs[nt][i & 1] * ksc[row];
             x[hf][i] = g + 8 * row < nv ? v : -INFINITY;
             mx[i & 1] = fmaxf(mx[i & 1], x[hf][i]);
             mxe[i & 1] = fmaxf(mxe[i & 1], x[hf][i] + ve[row]);
@@ -647,11 +672,13 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
   }
   uint8_t* stages = smem;
   StageHdr* hdr = reinterpret_cast<StageHdr*>(smem + (size_t)NS * a.stage_bytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(hdr + NS);
+  uint64_t* hdr_full = reinterpret_cast<uint64_t*>(hdr + NS);
+  uint64_t* full = hdr_full + NS;
   uint64_t* empty = full + 2 * NS;  // K's barriers, then V's
   float* mbuf = reinterpret_cast<float*>(empty + 2 * NS);
 
   if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(&hdr_full[s], 1);
     for (int s = 0; s < 2 * NS; ++s) {
       mbar_init(&full[s], 1 + 32);  // a producer's go-ahead, and every lane's scale copies
       mbar_init(&empty[s], NC);
@@ -667,14 +694,12 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
 
   const int warp = threadIdx.x >> 5;
   if (warp == NC) {
-    decode8_producer<D, TMA>(a, stages, hdr, full, empty, false);
+    decode8_producer<D, TMA>(a, stages, hdr, hdr_full, full, empty, false);
   } else if (warp == NC + 1) {
-    decode8_producer<D, TMA>(a, stages, hdr, full + NS, empty + NS, true);
+    decode8_producer<D, TMA>(a, stages, hdr, hdr_full, full + NS, empty + NS, true);
   } else if (warp < NC) {
-    decode8_consumer<D, NT, TMA>(a, stages, hdr, full, empty, mbuf);
+    decode8_consumer<D, NT, TMA>(a, stages, hdr, hdr_full, full, empty, mbuf);
   }
-  // The merge may be scheduled from here on (it waits for this grid's completion before it reads).
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -712,22 +737,19 @@ __global__ void __launch_bounds__(256) decode8_merge_kernel(const __grid_constan
     if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
     return;
   }
+  // One pass: the partials' LSEs (one per lane) and the first sixteen partial rows are loaded together,
+  // so up to 32 partials cost one trip to L2; more rescale what they found.
   const float* plse = a.part_lse + qhl;
-  float mx = -INFINITY;
-  for (int p = first + lane; p <= last; p += 32) mx = fmaxf(mx, __ldg(plse + (int64_t)p * HQU));
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-  float acc[VPL] = {};
-  float tot = 0.f;
   const float* po = a.part_o + (int64_t)qhl * D + lane * VPL;
+  float mx = -INFINITY, tot = 0.f;
+  float acc[VPL] = {};
   for (int base = first; base <= last; base += 32) {
     const int n = min(32, last - base + 1);
-    const float w = lane < n ? __expf(__ldg(plse + (int64_t)(base + lane) * HQU) - mx) : 0.f;
-    tot += w;
-    for (int i0 = 0; i0 < n; i0 += 8) {  // eight partials in flight
-      float x[8][VPL];
+    const float pl = lane < n ? __ldg(plse + (int64_t)(base + lane) * HQU) : -INFINITY;
+    float x[16][VPL];
+    auto load = [&](int i0) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 16; ++k) {
         const float* src = po + (int64_t)(base + i0 + k) * HQU * D;
         if (i0 + k < n) {
           if constexpr (VPL == 4)
@@ -739,8 +761,22 @@ __global__ void __launch_bounds__(256) decode8_merge_kernel(const __grid_constan
           for (int v = 0; v < VPL; ++v) x[k][v] = 0.f;
         }
       }
+    };
+    load(0);
+    float mn = pl;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+    for (int s = 16; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
+    mn = fmaxf(mx, mn);
+    const float corr = __expf(mx - mn);  // 0 on the first round
+    mx = mn;
+    const float w = lane < n ? __expf(pl - mx) : 0.f;
+    tot = tot * corr + w;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) acc[v] *= corr;
+    for (int i0 = 0; i0 < n; i0 += 16) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, (i0 + k) & 31);
 #pragma unroll
         for (int v = 0; v < VPL; ++v) acc[v] += wk * x[k][v];
@@ -792,11 +828,11 @@ bool make_plan(int B, int Hq, int Hkv, int D, int ncta, Plan& p, int page_size =
   p.stage = (2 * p.region + (uint32_t)(2 * p.Ts * p.HC * 4) + 1023u) & ~1023u;
   const int mf = p.NT * (6 + (D / 16) * 4);
   const size_t mbytes = p.W > 1 ? (size_t)(p.W - 1) * p.HC * mf * 32 * 4 : 0;
-  const size_t fixed = mbytes + (size_t)kMaxStages * (sizeof(StageHdr) + 32);
+  const size_t fixed = mbytes + (size_t)kMaxStages * (sizeof(StageHdr) + 40);
   if (fixed + 2 * (size_t)p.stage > kSmemBudget) return false;
   p.NS = (int)((kSmemBudget - fixed) / p.stage);
   if (p.NS > kMaxStages) p.NS = kMaxStages;
-  p.smem = (size_t)p.NS * p.stage + (size_t)p.NS * (sizeof(StageHdr) + 32) + mbytes;
+  p.smem = (size_t)p.NS * p.stage + (size_t)p.NS * (sizeof(StageHdr) + 40) + mbytes;
   p.ncta = ncta;
   p.nunits = (int64_t)B * p.nhg;
   p.nparts = p.ncta + p.nunits;

@@ -7,17 +7,21 @@
 // one rounding at the end; the values from R on pass through.  In the 8-bit cache a row is
 // quantised from those fp32 values (quant.cuh), so K is rounded once, to e4m3.
 //
-// Bound by HBM: a thread holds one 16-byte chunk of a (token, head) row, D/8 lanes of a warp hold a
-// row, and consecutive groups take consecutive heads, so loads and stores are whole lines.  The
-// half-split partner comes from another lane of the row by shuffle and the row's maximum by
-// xor-shuffles, so every value is read once.
+// Bound by HBM.  A row of a head is held by D/16 lanes, two 16-byte chunks each: for half-split
+// pairs the chunk and its partner R/2 further on, so that a pair never leaves its lane, for
+// neighbouring pairs (and without a rotation) two chunks side by side.  A warp takes four such steps of
+// one token, all of whose loads are issued before the token's position and slot are needed, and
+// loads the token's cosines and sines once for all of them.  (With one chunk per lane, a shuffle for the
+// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us; DESIGN's
+// table has the figure of this form.)  Widths that are no multiple of 16 (half) or 8 (neighbours) take a
+// kernel of one chunk per lane that reads its partners one by one.
 #include "quant.cuh"
 
 namespace {
 
 using namespace pkv;
 
-enum { kNone = 0, kHalf = 1, kPairs = 2, kAnyWidth = 3 };
+enum { kNone = 0, kHalf = 1, kPairs = 2 };
 
 struct AppendArgs {
   void* k_pool;
@@ -34,8 +38,10 @@ struct AppendArgs {
   int32_t max_position, R, interleaved;
   int32_t T, Hkv, Hq, D;
   int64_t num_slots;
-  uint32_t rows;   // T * heads
-  FastDiv heads;   // rows of a token: Hkv K heads, Hkv V heads, Hq Q heads
+  int32_t heads;     // rows of a token: Hkv K heads, Hkv V heads, Hq Q heads
+  FastDiv row_div;   // general widths: by heads
+  FastDiv item_div;  // by the warps of a token
+  uint32_t items;    // warps (rows, for the general widths) of the call
   uint32_t* err_word;
 };
 
@@ -49,152 +55,260 @@ PKV_DEV void unpack8(const uint4& u, float (&f)[8]) {
   }
 }
 
-// Chunk c (8 values) of a row rotated.  All lanes of the row call it together (shuffles); `src` is
-// the row, for the general widths.
-template <int ROT>
-PKV_DEV void rotate_chunk(const AppendArgs& a, const __nv_bfloat16* src, const float* cs, int c, int lane0,
-                          unsigned mask, const uint4& u, float (&x)[8]) {
+PKV_DEV uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Largest finite |x| of the row, as bits, over the L lanes that hold it.
+template <int L>
+PKV_DEV uint32_t row_max(uint32_t m, unsigned mask) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+  return m;
+}
+
+// 8 values times 2^-k as e4m3.
+PKV_DEV uint2 quantise8(float (&x)[8], int k) {
+  const float inv = exp2i(-k);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  if (k == kE4m3MaxExp) {  // keep the largest rows below 2^128: no rounding up to 256 * 2^120
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (fabsf(x[e]) > 240.f && fabsf(x[e]) < INFINITY) x[e] = copysignf(240.f, x[e]);
+  }
+  return make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
+}
+
+struct Row {
+  const __nv_bfloat16* src;
+  int kind;  // 0 K, 1 V, 2 Q
+  int head;
+};
+
+PKV_DEV Row row_of(const AppendArgs& a, uint32_t t, int h) {
+  Row r;
+  r.kind = h >= 2 * a.Hkv ? 2 : h >= a.Hkv ? 1 : 0;
+  r.head = h - r.kind * a.Hkv;
+  r.src = r.kind == 2 ? a.q + ((int64_t)t * a.Hq + r.head) * a.D
+                      : (r.kind == 1 ? a.v_new : a.k_new) + ((int64_t)t * a.Hkv + r.head) * a.D;
+  return r;
+}
+
+// The token's position is usable; false (reported once, by `reporter`) skips the token.
+PKV_DEV bool position_ok(const AppendArgs& a, int pos, bool reporter) {
+  if (pos >= 0 && pos < a.max_position) return true;
+  if (reporter) report(a.err_word, PKV_DEVERR_LENGTH);
+  return false;
+}
+PKV_DEV bool slot_ok(const AppendArgs& a, int64_t slot, bool reporter) {
+  if (slot >= 0 && slot < a.num_slots) return true;  // a negative slot is padding
+  if (slot >= 0 && reporter) report(a.err_word, PKV_DEVERR_SLOT_OOB);
+  return false;
+}
+
+constexpr int kSteps = 4;
+
+// L lanes hold a row (the power of two at or above its units of two chunks); a warp takes kSteps
+// times 32 / L rows of one token.
+template <bool FP8, int ROT, int L>
+__global__ void __launch_bounds__(256) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kRows = 32 / L;
+  const int lane = threadIdx.x & 31;
+  const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (item >= a.items) return;
+  uint32_t t, part;
+  a.item_div.divmod(item, t, part);
+  const int u = lane & (L - 1), row0 = (int)part * kSteps * kRows + lane / L;
+  const unsigned mask = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+  // this lane's chunks; the rotated ones come first, in pairs R/2 apart for half-split pairs
+  const int hc = a.R / 16;
+  const bool paired = ROT == kHalf && u < hc;
+  const int c0 = ROT == kHalf ? (paired ? u : 2 * hc + 2 * (u - hc)) : 2 * u;
+  const int c1 = paired ? u + hc : c0 + 1;
+  const bool has0 = 8 * c0 < a.D, has1 = 8 * c1 < a.D;
+
+  const int64_t slot = __ldg(a.slots + t);
+  const int pos = ROT != kNone ? __ldg(a.positions + t) : 0;
+  uint4 v0[kSteps], v1[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int h = row0 + i * kRows;
+    v0[i] = v1[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < a.heads) {
+      const uint4* src = reinterpret_cast<const uint4*>(row_of(a, t, h).src);
+      if (has0) v0[i] = src[c0];
+      if (has1) v1[i] = src[c1];
+    }
+  }
+  const bool reporter = part == 0 && lane == 0;
+  float co[8], si[8];  // of the lane's eight pairs
+  if constexpr (ROT != kNone) {
+    if (!position_ok(a, pos, reporter)) return;
+    const float* cs = a.cos_sin + (int64_t)pos * a.R;
+    const int p = ROT == kHalf ? 8 * c0 : 4 * c0;
+    const bool lo = ROT == kHalf ? paired : 8 * c0 < a.R, hi = ROT == kHalf ? paired : 8 * c1 < a.R;
+    float4 z = make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 ca = lo ? __ldg(reinterpret_cast<const float4*>(cs + p)) : z;
+    const float4 cb = hi ? __ldg(reinterpret_cast<const float4*>(cs + p + 4)) : z;
+    z = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 sa = lo ? __ldg(reinterpret_cast<const float4*>(cs + a.R / 2 + p)) : z;
+    const float4 sb = hi ? __ldg(reinterpret_cast<const float4*>(cs + a.R / 2 + p + 4)) : z;
+    co[0] = ca.x, co[1] = ca.y, co[2] = ca.z, co[3] = ca.w, co[4] = cb.x, co[5] = cb.y, co[6] = cb.z, co[7] = cb.w;
+    si[0] = sa.x, si[1] = sa.y, si[2] = sa.z, si[3] = sa.w, si[4] = sb.x, si[5] = sb.y, si[6] = sb.z, si[7] = sb.w;
+  }
+  const bool cached = slot_ok(a, slot, reporter);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int h = row0 + i * kRows;
+    if (h >= a.heads) break;
+    const Row r = row_of(a, t, h);
+    const bool is_q = r.kind == 2;
+    if (!is_q && !cached) continue;
+    const bool turn0 = ROT != kNone && r.kind != 1 && (ROT == kHalf ? paired : 8 * c0 < a.R);
+    const bool turn1 = ROT != kNone && r.kind != 1 && (ROT == kHalf ? paired : 8 * c1 < a.R);
+    float x0[8], x1[8];
+    unpack8(v0[i], x0);
+    unpack8(v1[i], x1);
+    if constexpr (ROT == kHalf) {
+      if (turn0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float lo = x0[e], hi = x1[e];
+          x0[e] = fmaf(lo, co[e], -hi * si[e]);
+          x1[e] = fmaf(hi, co[e], lo * si[e]);
+        }
+      }
+    } else if constexpr (ROT == kPairs) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (turn0) {
+          const float lo = x0[2 * e], hi = x0[2 * e + 1];
+          x0[2 * e] = fmaf(lo, co[e], -hi * si[e]);
+          x0[2 * e + 1] = fmaf(hi, co[e], lo * si[e]);
+        }
+        if (turn1) {
+          const float lo = x1[2 * e], hi = x1[2 * e + 1];
+          x1[2 * e] = fmaf(lo, co[4 + e], -hi * si[4 + e]);
+          x1[2 * e + 1] = fmaf(hi, co[4 + e], lo * si[4 + e]);
+        }
+      }
+    }
+    if (FP8 && !is_q) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, max(finite_abs_bits(x0[e]), finite_abs_bits(x1[e])));
+      const int k = e4m3_scale_exp(row_max<L>(m, mask));
+      const int64_t dst = slot * a.Hkv + r.head;
+      uint8_t* out = (uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * a.D;
+      const uint2 p0 = quantise8(x0, k), p1 = quantise8(x1, k);
+      if (has0) *reinterpret_cast<uint2*>(out + 8 * c0) = p0;
+      if (has1) *reinterpret_cast<uint2*>(out + 8 * c1) = p1;
+      if (u == 0) (r.kind == 1 ? a.v_scale : a.k_scale)[dst] = exp2i(k);
+    } else {
+      uint4* out = reinterpret_cast<uint4*>(is_q ? a.q_out + ((int64_t)t * a.Hq + r.head) * a.D
+                                                 : (__nv_bfloat16*)(r.kind == 1 ? a.v_pool : a.k_pool) +
+                                                       (slot * a.Hkv + r.head) * a.D);
+      if (has0) out[c0] = turn0 ? pack8(x0) : v0[i];
+      if (has1) out[c1] = turn1 ? pack8(x1) : v1[i];
+    }
+  }
+}
+
+// Any even width: one chunk per lane, L lanes per row, partners read one by one.
+template <bool FP8, int L>
+__global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_constant__ AppendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int c = lane & (L - 1);
+  const unsigned mask = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+  const bool has = 8 * c < a.D;
   const int R = a.R, half = R / 2;
-  if constexpr (ROT == kHalf) {  // R a multiple of 16: the partner is the same place of another chunk
-    const int hc = R / 16;
-    const int partner = c < hc ? c + hc : c < 2 * hc ? c - hc : c;
-    uint4 w;
-    w.x = __shfl_sync(mask, u.x, lane0 + partner);
-    w.y = __shfl_sync(mask, u.y, lane0 + partner);
-    w.z = __shfl_sync(mask, u.z, lane0 + partner);
-    w.w = __shfl_sync(mask, u.w, lane0 + partner);
-    if (c < 2 * hc) {
-      float y[8];
-      unpack8(w, y);
-      const int p = 8 * (c < hc ? c : c - hc);
-      const float sign = c < hc ? -1.f : 1.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 co = __ldg(reinterpret_cast<const float4*>(cs + p + 4 * h));
-        const float4 si = __ldg(reinterpret_cast<const float4*>(cs + half + p + 4 * h));
-        x[4 * h + 0] = fmaf(x[4 * h + 0], co.x, sign * y[4 * h + 0] * si.x);
-        x[4 * h + 1] = fmaf(x[4 * h + 1], co.y, sign * y[4 * h + 1] * si.y);
-        x[4 * h + 2] = fmaf(x[4 * h + 2], co.z, sign * y[4 * h + 2] * si.z);
-        x[4 * h + 3] = fmaf(x[4 * h + 3], co.w, sign * y[4 * h + 3] * si.w);
-      }
-    }
-  } else if constexpr (ROT == kPairs) {  // R a multiple of 8: four whole pairs in the chunk
-    if (8 * c < R) {
-      const float4 co = __ldg(reinterpret_cast<const float4*>(cs + 4 * c));
-      const float4 si = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * c));
-      const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = x[2 * i], hi = x[2 * i + 1];
-        x[2 * i] = fmaf(lo, cv[i], -hi * sv[i]);
-        x[2 * i + 1] = fmaf(hi, cv[i], lo * sv[i]);
-      }
-    }
-  } else if constexpr (ROT == kAnyWidth) {  // any even R: partners read one by one
+  const uint32_t row = blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (row >= a.items) return;
+  uint32_t t, h;
+  a.row_div.divmod(row, t, h);
+  const Row r = row_of(a, t, (int)h);
+  const bool is_q = r.kind == 2, reporter = h == 0 && c == 0;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (has) v = reinterpret_cast<const uint4*>(r.src)[c];
+  const int pos = __ldg(a.positions + t);
+  if (!position_ok(a, pos, reporter)) return;
+  const int64_t slot = __ldg(a.slots + t);
+  const bool cached = slot_ok(a, slot, reporter);
+  if (!is_q && !cached) return;
+  float x[8];
+  unpack8(v, x);
+  if (r.kind != 1 && has) {
+    const float* cs = a.cos_sin + (int64_t)pos * R;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int j = 8 * c + e;
       if (j < R) {
         const int i = a.interleaved ? j >> 1 : (j < half ? j : j - half);
         const bool first = a.interleaved ? !(j & 1) : j < half;
-        const int pj = a.interleaved ? j ^ 1 : (first ? j + half : j - half);
-        const float y = __bfloat162float(src[pj]);
+        const float y = __bfloat162float(r.src[a.interleaved ? j ^ 1 : (first ? j + half : j - half)]);
         x[e] = fmaf(x[e], __ldg(cs + i), (first ? -y : y) * __ldg(cs + half + i));
       }
     }
   }
-}
-
-// LPR lanes hold one row: the power of two at or above D / 8.
-template <bool FP8, int ROT, int LPR>
-__global__ void __launch_bounds__(256) append_rows_kernel(const __grid_constant__ AppendArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int c = lane & (LPR - 1), lane0 = lane & ~(LPR - 1);
-  const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << lane0;
-  const bool has = 8 * c < a.D;
-  const uint32_t step = gridDim.x * (256 / LPR);
-  for (uint32_t r = (blockIdx.x * 256 + threadIdx.x) / LPR; r < a.rows; r += step) {
-    uint32_t t, h;
-    a.heads.divmod(r, t, h);
-    const bool is_q = h >= 2u * a.Hkv, is_v = !is_q && h >= (uint32_t)a.Hkv;
-    const int hh = (int)h - (is_q ? 2 * a.Hkv : is_v ? a.Hkv : 0);
-    // the row, its position and its slot are loaded together
-    const __nv_bfloat16* src = is_q ? a.q + ((int64_t)t * a.Hq + hh) * a.D
-                                    : (is_v ? a.v_new : a.k_new) + ((int64_t)t * a.Hkv + hh) * a.D;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (has) u = *reinterpret_cast<const uint4*>(src + 8 * c);
-    const int64_t slot = is_q ? 0 : __ldg(a.slots + t);
-    int pos = 0;
-    if constexpr (ROT != kNone) {
-      pos = __ldg(a.positions + t);
-      if (pos < 0 || pos >= a.max_position) {
-        if (h == 0 && c == 0) report(a.err_word, PKV_DEVERR_LENGTH);
-        continue;
-      }
-    }
-    if (slot < 0) continue;  // padding token
-    if (slot >= a.num_slots) {
-      if (h == 0 && c == 0) report(a.err_word, PKV_DEVERR_SLOT_OOB);
-      continue;
-    }
-    float x[8];
-    unpack8(u, x);
-    if (ROT != kNone && !is_v) {
-      rotate_chunk<ROT>(a, src, a.cos_sin + (int64_t)pos * a.R, c, lane0, mask, u, x);
-      if constexpr (ROT == kAnyWidth) __syncwarp(mask);  // q may be rotated in place: partners are read before stores
-    }
-    if (FP8 && !is_q) {
-      uint32_t m = 0;
+  __syncwarp(mask);  // q may be rotated in place: every lane of the row has read its partners
+  if (FP8 && !is_q) {
+    uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, finite_abs_bits(x[e]));
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-      const int k = e4m3_scale_exp(m);
-      const float inv = exp2i(-k);
-      const int64_t dst = slot * a.Hkv + hh;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= inv;
-      if (k == kE4m3MaxExp) {  // keep the largest rows below 2^128: no rounding up to 256 * 2^120
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (fabsf(x[e]) > 240.f && fabsf(x[e]) < INFINITY) x[e] = copysignf(240.f, x[e]);
-      }
-      if (has) {
-        uint2 p;
-        p.x = pack_e4m3x4(x[0], x[1], x[2], x[3]);
-        p.y = pack_e4m3x4(x[4], x[5], x[6], x[7]);
-        *reinterpret_cast<uint2*>((uint8_t*)(is_v ? a.v_pool : a.k_pool) + dst * a.D + 8 * c) = p;
-      }
-      if (c == 0) (is_v ? a.v_scale : a.k_scale)[dst] = exp2i(k);
-    } else if (has) {
-      uint4 p = u;
-      if (!is_v && (ROT != kNone) && 8 * c < a.R)
-        p = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
-      __nv_bfloat16* dst = is_q ? a.q_out + ((int64_t)t * a.Hq + hh) * a.D
-                                : (__nv_bfloat16*)(is_v ? a.v_pool : a.k_pool) + (slot * a.Hkv + hh) * a.D;
-      *reinterpret_cast<uint4*>(dst + 8 * c) = p;
-    }
+    for (int e = 0; e < 8; ++e) m = max(m, finite_abs_bits(x[e]));
+    const int k = e4m3_scale_exp(row_max<L>(m, mask));
+    const int64_t dst = slot * a.Hkv + r.head;
+    const uint2 p = quantise8(x, k);
+    if (has) *reinterpret_cast<uint2*>((uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * a.D + 8 * c) = p;
+    if (c == 0) (r.kind == 1 ? a.v_scale : a.k_scale)[dst] = exp2i(k);
+  } else if (has) {
+    uint4* out = reinterpret_cast<uint4*>(is_q ? a.q_out + ((int64_t)t * a.Hq + r.head) * a.D
+                                               : (__nv_bfloat16*)(r.kind == 1 ? a.v_pool : a.k_pool) +
+                                                     (slot * a.Hkv + r.head) * a.D);
+    out[c] = r.kind == 1 ? v : pack8(x);
   }
 }
 
+int pow2_at_least(int n) {
+  int p = 1;
+  while (p < n) p <<= 1;
+  return p;
+}
+
 template <bool FP8, int ROT>
-pkv_status launch_rows(const AppendArgs& a, cudaStream_t st) {
-  const int chunks = a.D / 8;
-  int lpr = 1;
-  while (lpr < chunks) lpr <<= 1;
-  const int64_t per_block = 256 / lpr;
-  int64_t blocks = (a.rows + per_block - 1) / per_block;
-  const int64_t cap = (int64_t)pkv_host::sm_count() * 16;
-  if (cap > 0 && blocks > cap) blocks = cap;
-  const unsigned g = (unsigned)blocks;
-  switch (lpr) {
+pkv_status launch_rows(AppendArgs a, cudaStream_t st) {
+  const int hc = a.R / 16;
+  const int units = ROT == kHalf ? hc + (a.D - 16 * hc + 15) / 16 : (a.D + 15) / 16;
+  const int L = pow2_at_least(units);
+  const int rows = kSteps * (32 / L);
+  const int64_t parts = (a.heads + rows - 1) / rows;
+  a.items = (uint32_t)(parts * a.T);
+  a.item_div = FastDiv((uint32_t)parts);
+  const unsigned g = (a.items + 7) / 8;
+  switch (L) {
     case 1: append_rows_kernel<FP8, ROT, 1><<<g, 256, 0, st>>>(a); break;
     case 2: append_rows_kernel<FP8, ROT, 2><<<g, 256, 0, st>>>(a); break;
     case 4: append_rows_kernel<FP8, ROT, 4><<<g, 256, 0, st>>>(a); break;
     case 8: append_rows_kernel<FP8, ROT, 8><<<g, 256, 0, st>>>(a); break;
-    case 16: append_rows_kernel<FP8, ROT, 16><<<g, 256, 0, st>>>(a); break;
-    default: append_rows_kernel<FP8, ROT, 32><<<g, 256, 0, st>>>(a); break;
+    default: append_rows_kernel<FP8, ROT, 16><<<g, 256, 0, st>>>(a); break;
+  }
+  return pkv_host::launch_status();
+}
+
+template <bool FP8>
+pkv_status launch_any_width(AppendArgs a, cudaStream_t st) {
+  const int L = pow2_at_least(a.D / 8);
+  a.items = (uint32_t)((int64_t)a.heads * a.T);
+  a.row_div = FastDiv((uint32_t)a.heads);
+  const unsigned per = 256 / L, g = (a.items + per - 1) / per;
+  switch (L) {
+    case 1: append_any_width_kernel<FP8, 1><<<g, 256, 0, st>>>(a); break;
+    case 2: append_any_width_kernel<FP8, 2><<<g, 256, 0, st>>>(a); break;
+    case 4: append_any_width_kernel<FP8, 4><<<g, 256, 0, st>>>(a); break;
+    case 8: append_any_width_kernel<FP8, 8><<<g, 256, 0, st>>>(a); break;
+    case 16: append_any_width_kernel<FP8, 16><<<g, 256, 0, st>>>(a); break;
+    default: append_any_width_kernel<FP8, 32><<<g, 256, 0, st>>>(a); break;
   }
   return pkv_host::launch_status();
 }
@@ -221,11 +335,10 @@ pkv_status append_rows(AppendArgs a, int64_t num_pages, int32_t page_size, bool 
   if (a.D > 256) return PKV_ERR_UNSUPPORTED;
   const int64_t heads = 2 * (int64_t)a.Hkv + a.Hq;
   if (heads * a.T > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // 31-bit row numbers
-  a.rows = (uint32_t)(heads * a.T);
-  a.heads = FastDiv((uint32_t)heads);
+  a.heads = (int32_t)heads;
   a.num_slots = num_pages * page_size;
   if (!rotary) return launch_rows<FP8, kNone>(a, st);
-  if (a.interleaved ? a.R % 8 != 0 : a.R % 16 != 0) return launch_rows<FP8, kAnyWidth>(a, st);
+  if (a.interleaved ? a.R % 8 != 0 : a.R % 16 != 0) return launch_any_width<FP8>(a, st);
   return a.interleaved ? launch_rows<FP8, kPairs>(a, st) : launch_rows<FP8, kHalf>(a, st);
 }
 

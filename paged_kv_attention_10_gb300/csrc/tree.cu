@@ -416,8 +416,12 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
     Seg end = {};
     ok = publish(end);
   }
-  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   if (lane == 0) a.cut[cta] = cut;
+  // The merge may be scheduled once every CTA has issued its last K (it waits for this grid's
+  // completion before it reads): early enough to hide its launch, late enough not to hold thread
+  // slots that kernels on other streams could use.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   k.drain();
 }
 
@@ -1060,8 +1064,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // The merge may be scheduled from here on (it waits for this grid's completion before it reads).
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1081,33 +1083,47 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   if (tile >= cut.nq || r >= a.group * a.tpt || tok >= cut.T) return;
   constexpr int VPL = D / 32;
   auto slot = [&](int p) -> int64_t { return ((int64_t)2 * (c + p) + (p == 0 ? 1 : 0)) * a.part_rows + prow; };
-  float mx = -INFINITY;
-  for (int p = lane; p < cut.parts; p += 32) mx = fmaxf(mx, __ldg(a.part_lse + slot(p)));
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+  // One pass: the parts' LSEs (one per lane) and the first sixteen rows are loaded together, so up to 32
+  // parts cost one trip to L2 and a half; more rescale what they found.
+  float mx = -INFINITY, tot = 0.f;
   float acc[VPL] = {};
-  float tot = 0.f;
   for (int p0 = 0; p0 < cut.parts; p0 += 32) {
     const int n = min(32, cut.parts - p0);
     const float pl = lane < n ? __ldg(a.part_lse + slot(p0 + lane)) : -INFINITY;
-    const float w = pl == -INFINITY ? 0.f : __expf(pl - mx);
-    tot += w;
-    for (int i0 = 0; i0 < n; i0 += 8) {  // eight partials in flight
-      float x[8][VPL];
+    float x[16][VPL];
+    auto load = [&](int i0) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) x[k][v] = 0.f;
+      for (int k = 0; k < 16; ++k) {
         if (i0 + k < n) {
           const float* src = a.part_o + slot(p0 + i0 + k) * D + lane * VPL;
           if constexpr (VPL == 4)
             *reinterpret_cast<float4*>(x[k]) = __ldg(reinterpret_cast<const float4*>(src));
           else
             *reinterpret_cast<float2*>(x[k]) = __ldg(reinterpret_cast<const float2*>(src));
+        } else {
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) x[k][v] = 0.f;
         }
       }
+    };
+    load(0);
+    float mn = pl;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+    for (int s = 16; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
+    mn = fmaxf(mx, mn);
+    if (mn > mx) {  // (not while every part so far is empty)
+      const float corr = __expf(mx - mn);
+      tot *= corr;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) acc[v] *= corr;
+      mx = mn;
+    }
+    const float w = pl == -INFINITY ? 0.f : __expf(pl - mx);
+    tot += w;
+    for (int i0 = 0; i0 < n; i0 += 16) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, (i0 + k) & 31);
         if (wk != 0.f) {
 #pragma unroll
