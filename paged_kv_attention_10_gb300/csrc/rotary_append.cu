@@ -9,11 +9,11 @@
 //
 // Bound by HBM.  A row of a head is held by D/16 lanes, two 16-byte chunks each: for half-split
 // pairs the chunk and its partner R/2 further on, so that a pair never leaves its lane, for
-// neighbouring pairs (and without a rotation) two chunks side by side.  A warp takes four such steps of
+// neighbouring pairs (and without a rotation) two chunks side by side.  A warp takes two such steps of
 // one token, all of whose loads are issued before the token's position and slot are needed, and
-// loads the token's cosines and sines once for all of them.  (With one chunk per lane, a shuffle for the
-// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us; DESIGN's
-// table has the figure of this form.)  Widths that are no multiple of 16 (half) or 8 (neighbours) take a
+// loads the token's cosines and sines once for both.  (With one chunk per lane, a shuffle for the
+// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us, now 39.)
+// Widths that are no multiple of 16 (half) or 8 (neighbours) take a
 // kernel of one chunk per lane that reads its partners one by one.
 #include "quant.cuh"
 
@@ -108,12 +108,15 @@ PKV_DEV bool slot_ok(const AppendArgs& a, int64_t slot, bool reporter) {
   return false;
 }
 
-constexpr int kSteps = 4;
+// Steps and blocks per SM, measured on 8191 tokens of 32/8 heads at D 128, R 64 (and quantising 2304 with
+// R 128): 2 steps and 4 blocks 39.0 us (15.3), 4 and 3 39.5 (16.8), 4 and 2 41.1 (17.3), 1 and 4 46.0
+// (17.1); more blocks spill.  A device copy of the same bytes takes 37.1 us (16.5).
+constexpr int kSteps = 2;
 
 // L lanes hold a row (the power of two at or above its units of two chunks); a warp takes kSteps
 // times 32 / L rows of one token.
 template <bool FP8, int ROT, int L>
-__global__ void __launch_bounds__(256) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kRows = 32 / L;
   const int lane = threadIdx.x & 31;
   const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
