@@ -42,7 +42,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4;      // warps 4..7 slot 0, 8..11 slot 1
 constexpr int kMaxNodes = 1024;       // drafted tokens of a request
 constexpr int kSegRing = 4;
-constexpr int kKStages = 2, kVStages = 3;
+constexpr int kMaxRing = 10;
 constexpr int kUnitCost = 2;          // a unit's start and epilogue, in KV tiles of the work split
 constexpr uint32_t kHalfTile = 128 * 128;  // 128 rows of one 64-dim half, 16 KB
 constexpr uint32_t kColO = 0, kColS = 256;  // O of slot s at 128 s, S at 256 + 128 s
@@ -52,14 +52,17 @@ struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTile = kHalves * kHalfTile;
   static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffK = kOffQ + 2 * kTile;
-  static constexpr uint32_t kOffV = kOffK + kKStages * kTile;
+  // One ring for K and V tiles, K of tile j at place 2 j and V at 2 j + 1: a buffer that K's product
+  // frees soon is the next V's, and the loads run 2.5 tiles ahead.  (Two K and three V buffers of their own
+  // left K's reload little more than a tile's time.)
+  static constexpr int kRing = D == 128 ? 5 : 10;
+  static constexpr uint32_t kOffRing = kOffQ + 2 * kTile;
   // the epilogue's exchange between replicas, 2 slots x 3 x 32 rows x 32 dims fp32: at D 128 it is the
   // second Q buffer, which one Q tile leaves free
   static constexpr uint32_t kScratch = 2 * 3 * 32 * 32 * 4;
   static constexpr bool kShared = kTile >= kScratch;
-  static constexpr uint32_t kOffScratch = kShared ? kOffQ + kTile : kOffV + kVStages * kTile;
-  static constexpr uint32_t kOffCtl = kOffV + kVStages * kTile + (kShared ? 0 : kScratch);
+  static constexpr uint32_t kOffScratch = kShared ? kOffQ + kTile : kOffRing + kRing * kTile;
+  static constexpr uint32_t kOffCtl = kOffRing + kRing * kTile + (kShared ? 0 : kScratch);
 };
 
 // A run of KV tiles of one unit that this CTA computes.
@@ -79,9 +82,9 @@ struct Ctl {
   Seg seg[kSegRing];
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[kKStages], k_empty[kKStages];
-  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t full[kMaxRing], empty[kMaxRing];  // the K / V ring
   uint64_t s_full[2];  // QK written
+  uint64_t qk_issued[2];
   uint64_t p_full[2];  // P written, V cleaned
   uint64_t s_free[2];  // PV done
   uint64_t o_free;     // O read by the epilogue
@@ -127,7 +130,7 @@ struct TreeArgs {
   int32_t batch, num_q_tokens, max_nodes;
   float scale_log2;
   Cut* cut;           // [CTAs]
-  float* part_o;      // [2 CTAs][part_rows][D]
+  float* part_o;      // [2 CTAs][D / 4][part_rows][4]: a warp's rows lie side by side
   float* part_lse;    // [2 CTAs][part_rows]
   int32_t part_rows;
 };
@@ -163,23 +166,16 @@ struct Producer {
   const CUtensorMap* tm;
   const __nv_bfloat16* pool;
   uint32_t base;  // of the ring, shared address
-  int stages;
-  int stage = 0;
-  uint32_t phase = 0;
-  int issued = 0;
-  int unpublished = -1;  // kRows: the stage whose copies are not announced yet
+  int item;       // place of the next tile in the ring's order: even K, odd V
+  int unpublished = -1;  // kRows: the buffer whose copies are not announced yet
 
   __device__ Producer(const TreeArgs& args, Ctl* ctl, uint32_t sb, bool v)
-      : a(args), fulls(v ? ctl->v_full : ctl->k_full), empties(v ? ctl->v_empty : ctl->k_empty),
-        tm(v ? &args.tm_v : &args.tm_k), pool(v ? args.v_pool : args.k_pool),
-        base(sb + (v ? C::kOffV : C::kOffK)), stages(v ? kVStages : kKStages) {}
+      : a(args), fulls(ctl->full), empties(ctl->empty), tm(v ? &args.tm_v : &args.tm_k),
+        pool(v ? args.v_pool : args.k_pool), base(sb + C::kOffRing), item(v ? 1 : 0) {}
 
-  __device__ void advance() {
-    ++issued;
-    if (++stage == stages) {
-      stage = 0;
-      phase ^= 1;
-    }
+  // Waits until the next tile's buffer is free.
+  __device__ bool acquire() {
+    return __all_sync(0xffffffffu, mbar_wait(&empties[item % C::kRing], ((item / C::kRing) & 1) ^ 1)) != 0;
   }
 
   // Row of the pool that holds position pos, or -1 (reported).
@@ -222,13 +218,14 @@ struct Producer {
       const bool in = half < C::kHalves && pos < kv_end;
       const int64_t row = in ? row_of(pos, k < 32 ? v0 : v1, s.np) : -1;
       const uint32_t nload = __popc(__ballot_sync(0xffffffffu, row >= 0));
-      if (!__all_sync(0xffffffffu, mbar_wait(&empties[stage], phase ^ 1))) return false;
+      if (!acquire()) return false;
+      const int stage = item % C::kRing;
       if (lane == 0) mbar_arrive_expect_tx(&fulls[stage], nload * R * 128);
       __syncwarp();
       if (row >= 0)
         tma_load_3d(base + stage * C::kTile + half * kHalfTile + box * R * 128, tm, half * 64, s.h, (int)row,
                     &fulls[stage]);
-      advance();
+      item += 2;
     }
     return true;
   }
@@ -260,8 +257,9 @@ struct Producer {
     for (int i = 0; i < 4; ++i) next[i] = slot_of(s.j0, lane + 32 * i);
     for (int j = s.j0; j < s.j0 + s.n; ++j) {
       // no free stage yet: announce the pending one now instead of behind the next issue
-      if (!__all_sync(0xffffffffu, mbar_test(&empties[stage], phase ^ 1))) publish(true);
-      if (!__all_sync(0xffffffffu, mbar_wait(&empties[stage], phase ^ 1))) return false;
+      const int stage = item % C::kRing;
+      if (!__all_sync(0xffffffffu, mbar_test(&empties[stage], ((item / C::kRing) & 1) ^ 1))) publish(true);
+      if (!acquire()) return false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (next[i] < 0) continue;
@@ -275,30 +273,29 @@ struct Producer {
             cp_async16(dst + hf * kHalfTile + ((c ^ (row & 7)) << 4), src + hf * 128 + c * 16);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      const int mine = stage;
-      advance();
+      item += 2;
 #pragma unroll
       for (int i = 0; i < 4; ++i) next[i] = slot_of(j + 1, lane + 32 * i);  // while these copies fly
       publish(false);
-      unpublished = mine;
+      unpublished = stage;
     }
     publish(true);
     return true;
   }
 
-  // No copy of this warp is in flight when the CTA exits (bounded; immediate on the normal path).
-  __device__ void drain() {
+  // No copy of this warp is in flight when the CTA exits.  With every tile issued (`all`, the normal
+  // path) the last kRing places of the order, K's and V's, are the buffers' last occupants, and the
+  // consumers have seen them land.  A place before those has been landed on, consumed and used again,
+  // and its phase could no longer be waited for.  After a wait that gave up, every buffer's is tried
+  // (bounded waits).
+  __device__ void drain(bool all) {
     if (kRows) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       publish(true);
     }
-    for (int k = 0; k < min(issued, stages); ++k) {
-      if (--stage < 0) {
-        stage = stages - 1;
-        phase ^= 1;
-      }
-      mbar_wait(&fulls[stage], phase);
-    }
+    const int end = (item & ~1);  // places issued in all, if the other warp has come as far
+    for (int i = item - 2; i >= max(0, all ? end - C::kRing : item - 2 * C::kRing); i -= 2)
+      mbar_wait(&fulls[i % C::kRing], (i / C::kRing) & 1);
   }
 };
 
@@ -330,23 +327,28 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   return r;
 }
 
-// K producer warp: walks this CTA's share of the stream, publishes each segment, loads its Q and K.
-template <int D, bool kRows>
-__device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
+// Length of the stream (K producer warp, before the set-up barrier: the walk finds the numbers in L1).
+__device__ int64_t tree_stream_length(const TreeArgs& a) {
   const int lane = threadIdx.x & 31;
-  const int cta = blockIdx.x;
-  Producer<D, kRows> k(a, ctl, sb, false);
   int64_t total = 0;
   for (int i = lane; i < a.batch; i += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {  // four requests' loads in flight
       if (i + 32 * u < a.batch) {
-        const Req r = load_req(a, i + 32 * u, cta == 0);
+        const Req r = load_req(a, i + 32 * u, blockIdx.x == 0);
         total += (int64_t)r.pairs * r.cost;
       }
     }
   }
-  total = warp_sum(total) * a.num_kv_heads;
+  return warp_sum(total) * a.num_kv_heads;
+}
+
+// K producer warp: walks this CTA's share of the stream, publishes each segment and loads its K.
+template <int D, bool kRows>
+__device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb, int64_t total) {
+  const int lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  Producer<D, kRows> k(a, ctl, sb, false);
   int64_t share = (total + gridDim.x - 1) / gridDim.x;
   if (share < 1) share = 1;
   const int64_t c0 = cta * share, c1 = min(total, c0 + share);
@@ -422,7 +424,7 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
   // slots that kernels on other streams could use.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-  k.drain();
+  k.drain(ok);
 }
 
 // V and Q producer warp.  One Q tile always takes the first Q buffer, so that the second is free for
@@ -459,7 +461,7 @@ __device__ void tree_load_v(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
     ok = ok && v.run(s);
   }
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-  v.drain();
+  v.drain(ok);
 #pragma unroll
   for (int q = 0; q < 2; ++q)
     if (uses[q] > 0) mbar_wait(&ctl->q_full[q], (uses[q] - 1) & 1);
@@ -482,7 +484,7 @@ __device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
   using C = Cfg<D>;
   constexpr uint32_t idesc = umma_idesc_bf16(kBM, kBN, false);
   const uint64_t qdesc0 = smem_desc_sw128(sb + C::kOffQ, 16, 1024);
-  const uint64_t kdesc0 = smem_desc_sw128(sb + C::kOffK, 16, 1024);
+  const uint64_t kdesc0 = smem_desc_sw128(sb + C::kOffRing, 16, 1024);
   uint32_t kt = 0, qt[2] = {0, 0}, used[2] = {0, 0};  // K tiles, uses of the Q buffers and the slots so far
   Seg s;
   for (int i = 0;; ++i) {
@@ -491,8 +493,8 @@ __device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
     for (int q = 0; q < s.nq; ++q)
       if (!mbar_wait(&ctl->q_full[q], qt[q] & 1)) return false;
     for (int j = 0; j < s.n; ++j, ++kt) {
-      const uint32_t st = kt % kKStages;
-      if (!mbar_wait(&ctl->k_full[st], (kt / kKStages) & 1)) return false;
+      const uint32_t st = (2 * kt) % C::kRing;
+      if (!mbar_wait(&ctl->full[st], ((2 * kt) / C::kRing) & 1)) return false;
       const uint64_t kdesc = kdesc0 + ((st * C::kTile) >> 4);
       for (int q = 0; q < s.nq; ++q) {
         const int slot = s.nq == 2 ? q : (j & 1);
@@ -505,9 +507,10 @@ __device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
           umma_ss(tmem + kColS + slot * 128, qdesc + off, kdesc + off, idesc, ks > 0);
         }
         umma_commit(&ctl->s_full[slot]);
+        mbar_arrive(&ctl->qk_issued[slot]);
         ++used[slot];
       }
-      umma_commit(&ctl->k_empty[st]);
+      umma_commit(&ctl->empty[st]);
     }
     for (int q = 0; q < s.nq; ++q, ++qt[q - 1]) umma_commit(&ctl->q_empty[q]);
   }
@@ -568,7 +571,7 @@ __device__ bool tree_mma_pv(Ctl* ctl, uint8_t* smem, uint32_t tmem) {
   using C = Cfg<D>;
   constexpr uint32_t idesc = umma_idesc_bf16(kBM, D, true);
   const int lane = threadIdx.x & 31;
-  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem) + C::kOffV, kHalfTile, 1024);
+  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem) + C::kOffRing, kHalfTile, 1024);
   uint32_t vt = 0, used[2] = {0, 0};
   auto wait = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
   Seg s;
@@ -583,15 +586,19 @@ __device__ bool tree_mma_pv(Ctl* ctl, uint8_t* smem, uint32_t tmem) {
       __syncwarp();
     }
     for (int j = 0; j < s.n; ++j, ++vt) {
-      const uint32_t st = vt % kVStages;
+      const uint32_t st = (2 * vt + 1) % C::kRing;
       const uint64_t vdesc = vdesc0 + ((st * C::kTile) >> 4);
       const int pos0 = (s.j0 + j) * kBN;
-      if (!wait(&ctl->v_full[st], (vt / kVStages) & 1)) return false;
-      if (pos0 + kBN > s.P) clean_v<D>(smem + C::kOffV + st * C::kTile, ctl, s, pos0);
+      if (!wait(&ctl->full[st], ((2 * vt + 1) / C::kRing) & 1)) return false;
+      if (pos0 + kBN > s.P) clean_v<D>(smem + C::kOffRing + st * C::kTile, ctl, s, pos0);
       for (int q = 0; q < s.nq; ++q) {
         const int slot = s.nq == 2 ? q : (j & 1);
         const bool first = s.nq == 2 ? j == 0 : j < 2;
         if (!wait(&ctl->p_full[slot], used[slot] & 1)) return false;
+        // With two Q tiles the order is PV 0, QK 0, PV 1, QK 1, so that each slot's products run beside the
+        // other's softmax; left to themselves the slots fall into step, both products wait for both
+        // softmaxes, and a tile takes 1.9 us instead of 1.5.
+        if (s.nq == 2 && (q == 0 || j + 1 < s.n) && !wait(&ctl->qk_issued[q ^ 1], used[q ^ 1] & 1)) return false;
         tc_fence_after();
         if (lane == 0) {
 #pragma unroll
@@ -603,7 +610,7 @@ __device__ bool tree_mma_pv(Ctl* ctl, uint8_t* smem, uint32_t tmem) {
         __syncwarp();
         ++used[slot];
       }
-      if (lane == 0) umma_commit(&ctl->v_empty[st]);
+      if (lane == 0) umma_commit(&ctl->empty[st]);
     }
     if (lane == 0) mbar_arrive(&ctl->x_full);  // this segment's notes are made
   }
@@ -717,6 +724,74 @@ PKV_DEV float weights32(const float (&v)[32], float sc, float neg, uint32_t (&pk
   return lo + hi;
 }
 
+// A row's N chunks of 32 scores from chunk ch0 on, in TMEM at ts: the new reference maximum, the factor of
+// what was summed under the old one m, P written over S as bf16 pairs, the other chunks' P zeroed, and
+// the sum of the weights.  Two passes over the scores, the next chunk's load in flight while one is
+// worked on; the first chunk stays in registers between them.
+template <int N>
+PKV_DEV float softmax_tile(uint32_t ts, int ch0, float sc, float m, float& m_ref, float& corr) {
+  float a[32], b[32];  // odd and even chunks
+  const uint32_t s0 = ts + ch0 * 32, p0 = ts + ch0 * 16;
+  float mx = -INFINITY;
+  if constexpr (N == 1) {
+    tmem_ld32(s0, b);
+    tmem_wait_ld();
+    mx = max32(b);
+  } else {
+    tmem_ld32(s0 + (N - 1) * 32, a);
+    tmem_wait_ld();
+    if constexpr (N == 4) {
+      tmem_ld32(s0 + 64, b);
+      mx = max32(a);
+      tmem_wait_ld();
+      tmem_ld32(s0 + 32, a);
+      mx = fmaxf(mx, max32(b));
+      tmem_wait_ld();
+    }
+    tmem_ld32(s0, b);
+    mx = N == 4 ? fmaxf(mx, max32(a)) : max32(a);
+    tmem_wait_ld();
+    mx = fmaxf(mx, max32(b));
+  }
+  const float m_new = fmaxf(m, mx * sc);
+  // the maximum moves only when it grows by more than 2^8, so that O is seldom rescaled
+  const bool resc = m_new > m + 8.f;
+  m_ref = resc ? m_new : m;
+  corr = resc ? ex2(m - m_ref) : 1.f;
+  const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen so far: every weight is 0
+  // P of chunk c goes over columns of S of chunk c / 2, which has been read by then
+  uint32_t pk[16];
+  float tot;
+  if constexpr (N == 1) {
+    tot = weights32(b, sc, neg, pk);
+    tmem_st16(p0, pk);
+  } else {
+    tmem_ld32(s0 + 32, a);
+    tot = weights32(b, sc, neg, pk);
+    tmem_wait_ld();
+    tmem_st16(p0, pk);
+    if constexpr (N == 4) tmem_ld32(s0 + 64, b);
+    tot += weights32(a, sc, neg, pk);
+    if constexpr (N == 4) tmem_wait_ld();
+    tmem_st16(p0 + 16, pk);
+    if constexpr (N == 4) {
+      tmem_ld32(s0 + 96, a);
+      tot += weights32(b, sc, neg, pk);
+      tmem_wait_ld();
+      tmem_st16(p0 + 32, pk);
+      tot += weights32(a, sc, neg, pk);
+      tmem_st16(p0 + 48, pk);
+    }
+  }
+  if constexpr (N < 4) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+#pragma unroll 1
+    for (int c = N; c < 4; ++c) tmem_st16(ts + ((ch0 + c) & 3) * 16, pk);
+  }
+  return tot;
+}
+
 template <int D>
 __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_t tmem) {
   using C = Cfg<D>;
@@ -775,44 +850,21 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
           }
           tmem_wait_st();
         }
-        float v[32];
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int ch = ch0 + nch - 1; ch >= ch0; --ch) {
-          tmem_ld32(ts + ch * 32, v);
-          tmem_wait_ld();
-          mx = fmaxf(mx, max32(v));
-        }
-        mx *= sc;
-        const float m_new = fmaxf(m, mx);
-        // the maximum moves only when it grows by more than 2^8, so that O is seldom rescaled
-        const bool resc = m_new > m + 8.f;
-        const float m_ref = resc ? m_new : m;
-        const float corr = resc ? ex2(m - m_ref) : 1.f;
-        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen so far: every weight is 0
-        uint32_t pk[16];
-        float tot = weights32(v, sc, neg, pk);  // v holds the first chunk
-        // P of chunk ch goes over columns of S of chunk ch / 2, which has been read
-        tmem_st16(ts + ch0 * 16, pk);
-#pragma unroll 1
-        for (int ch = ch0 + 1; ch < ch0 + nch; ++ch) {
-          tmem_ld32(ts + ch * 32, v);
-          tmem_wait_ld();
-          tot += weights32(v, sc, neg, pk);
-          tmem_st16(ts + ch * 16, pk);
-        }
-        if (nch < 4) {  // the other copies' columns
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-#pragma unroll 1
-          for (int ch = nch; ch < 4; ++ch) tmem_st16(ts + ((ch0 + ch) & 3) * 16, pk);
-        }
+        float m_ref, corr, tot;
+        if (nch == 1)
+          tot = softmax_tile<1>(ts, ch0, sc, m, m_ref, corr);
+        else if (nch == 2)
+          tot = softmax_tile<2>(ts, ch0, sc, m, m_ref, corr);
+        else
+          tot = softmax_tile<4>(ts, ch0, sc, m, m_ref, corr);
+        const bool resc = m_ref > m;
         l = l * corr + tot;
         m = m_ref;
         const bool later = two ? jj > 0 : jj > 1;  // O holds earlier tiles (whose PV is done: S was free)
         if (later && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
+            float v[32];
             tmem_ld32(to + ch * 32, v);
             tmem_wait_ld();
 #pragma unroll
@@ -952,10 +1004,14 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
                            pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
             if (any_bad) add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 8, dst);
           } else {
-            float* dst = a.part_o + ((int64_t)s.part * a.part_rows + prow) * D + d0;
+            float* dst = a.part_o + (((int64_t)s.part * (D / 4) + d0 / 4) * a.part_rows + prow) * 4;
+            float* dst1 = dst + (int64_t)a.part_rows * 4;
             *reinterpret_cast<float4*>(dst) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            *reinterpret_cast<float4*>(dst + 4) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
-            if (any_bad) add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 8, dst);
+            *reinterpret_cast<float4*>(dst1) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+            if (any_bad) {
+              add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 4, dst);
+              add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0 + 4, 4, dst1);
+            }
           }
         }
       }
@@ -994,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
   }
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kOffCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 64) {
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&ctl->seg_full[i], 1);
       mbar_init(&ctl->seg_empty[i], 3 + 8);  // V producer, QK, PV, softmax warps
@@ -1003,16 +1059,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->qk_issued[i], 1);
       mbar_init(&ctl->p_full[i], 4);
       mbar_init(&ctl->s_free[i], 1);
     }
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&ctl->k_full[i], 1);
-      mbar_init(&ctl->k_empty[i], 1);
-    }
-    for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&ctl->v_full[i], 1);
-      mbar_init(&ctl->v_empty[i], 1);
+    for (int i = 0; i < kMaxRing; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->o_free, 8);
     mbar_init(&ctl->x_full, 8 + 1);  // and the PV warp's notes
@@ -1027,6 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
   }
+  const int64_t total = warp == 0 ? tree_stream_length(a) : 0;
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, 512);
     tmem_relinquish();
@@ -1037,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
-    tree_walk<D, kRows>(a, ctl, sb);
+    tree_walk<D, kRows>(a, ctl, sb, total);
   } else if (warp == 3) {
     tree_load_v<D, kRows>(a, ctl, sb);
   } else if (warp == 1) {
@@ -1067,81 +1121,68 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------------------------
-// Merge: block (c, y) joins rows 8y .. 8y + 7 of the unit that CTA c began and did not finish, one
-// warp per row.
+// Merge: block (c, y) joins rows 32 y .. 32 y + 31 of the unit that CTA c began and did not finish.  A
+// lane is a row, a warp every eighth group of four dims, so a part's rows are read as whole lines; the
+// states are joined in one pass with a running maximum, the loads of four parts in flight.
 // ---------------------------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kGroups = D / 32;  // groups of four dims of a thread
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const Cut cut = a.cut[c];
   if (cut.parts <= 0) return;
-  const int lane = threadIdx.x & 31;
-  const int prow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int prow = blockIdx.y * 32 + lane;
   const int r = prow & (kBM - 1), tile = prow / kBM;
   const int tok = cut.t0 + tile * a.tpt + r / a.group;
   if (tile >= cut.nq || r >= a.group * a.tpt || tok >= cut.T) return;
-  constexpr int VPL = D / 32;
-  auto slot = [&](int p) -> int64_t { return ((int64_t)2 * (c + p) + (p == 0 ? 1 : 0)) * a.part_rows + prow; };
-  // One pass: the parts' LSEs (one per lane) and the first sixteen rows are loaded together, so up to 32
-  // parts cost one trip to L2 and a half; more rescale what they found.
+  auto slot = [&](int p) -> int64_t { return (int64_t)2 * (c + p) + (p == 0 ? 1 : 0); };
   float mx = -INFINITY, tot = 0.f;
-  float acc[VPL] = {};
-  for (int p0 = 0; p0 < cut.parts; p0 += 32) {
-    const int n = min(32, cut.parts - p0);
-    const float pl = lane < n ? __ldg(a.part_lse + slot(p0 + lane)) : -INFINITY;
-    float x[16][VPL];
-    auto load = [&](int i0) {
+  float acc[kGroups][4] = {};
+  for (int p0 = 0; p0 < cut.parts; p0 += 4) {
+    float pl[4];
+    float4 x[4][kGroups];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (i0 + k < n) {
-          const float* src = a.part_o + slot(p0 + i0 + k) * D + lane * VPL;
-          if constexpr (VPL == 4)
-            *reinterpret_cast<float4*>(x[k]) = __ldg(reinterpret_cast<const float4*>(src));
-          else
-            *reinterpret_cast<float2*>(x[k]) = __ldg(reinterpret_cast<const float2*>(src));
-        } else {
+    for (int k = 0; k < 4; ++k) {
+      const bool on = p0 + k < cut.parts;
+      const int64_t at = slot(on ? p0 + k : p0);
+      pl[k] = on ? __ldg(a.part_lse + at * a.part_rows + prow) : -INFINITY;
 #pragma unroll
-          for (int v = 0; v < VPL; ++v) x[k][v] = 0.f;
-        }
-      }
-    };
-    load(0);
-    float mn = pl;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
-    mn = fmaxf(mx, mn);
+      for (int i = 0; i < kGroups; ++i)
+        x[k][i] = __ldg(reinterpret_cast<const float4*>(a.part_o) + (at * (D / 4) + warp + 8 * i) * a.part_rows + prow);
+    }
+    const float mn = fmaxf(fmaxf(fmaxf(pl[0], pl[1]), fmaxf(pl[2], pl[3])), mx);
     if (mn > mx) {  // (not while every part so far is empty)
       const float corr = __expf(mx - mn);
       tot *= corr;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) acc[v] *= corr;
+      for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][v] *= corr;
       mx = mn;
     }
-    const float w = pl == -INFINITY ? 0.f : __expf(pl - mx);
-    tot += w;
-    for (int i0 = 0; i0 < n; i0 += 16) {
-      if (i0 > 0) load(i0);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, (i0 + k) & 31);
-        if (wk != 0.f) {
+    for (int k = 0; k < 4; ++k) {
+      if (pl[k] == -INFINITY) continue;  // an empty part, or none
+      const float w = __expf(pl[k] - mx);
+      tot += w;
 #pragma unroll
-          for (int v = 0; v < VPL; ++v) acc[v] += wk * x[k][v];
-        }
+      for (int i = 0; i < kGroups; ++i) {
+        acc[i][0] = fmaf(w, x[k][i].x, acc[i][0]);
+        acc[i][1] = fmaf(w, x[k][i].y, acc[i][1]);
+        acc[i][2] = fmaf(w, x[k][i].z, acc[i][2]);
+        acc[i][3] = fmaf(w, x[k][i].w, acc[i][3]);
       }
     }
   }
-  tot = warp_sum(tot);
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
   const int64_t orow = (int64_t)(cut.q0 + tok) * a.num_q_heads + (int64_t)cut.h * a.group + r % a.group;
-  __nv_bfloat16* op = a.out + orow * D + lane * VPL;
-  if constexpr (VPL == 4)
-    *reinterpret_cast<uint2*>(op) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0 && a.lse) a.lse[orow] = tot == 0.f ? -INFINITY : mx + logf(tot);
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i)
+    *reinterpret_cast<uint2*>(a.out + orow * D + (warp + 8 * i) * 4) =
+        make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+  if (warp == 0 && a.lse) a.lse[orow] = tot == 0.f ? -INFINITY : mx + logf(tot);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1222,7 +1263,7 @@ pkv_status launch(const Plan& p, const TreeArgs& a, cudaStream_t st) {
   const pkv_status s = pkv_host::launch_status();
   if (s != PKV_OK) return s;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.ncta, (unsigned)(p.part_rows / 8), 1);
+  cfg.gridDim = dim3((unsigned)p.ncta, (unsigned)(p.part_rows / 32), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
