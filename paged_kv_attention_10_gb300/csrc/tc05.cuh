@@ -29,6 +29,15 @@ PKV_DEV void tma_load_3d_hint(uint32_t dst, const CUtensorMap* tm, int x, int y,
       : "memory");
 }
 
+// Four rows y0 .. y3 of a 2-D map whose box is one row high, side by side in shared memory.
+PKV_DEV void tma_gather4(uint32_t dst, const CUtensorMap* tm, int x, int y0, int y1, int y2, int y3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Tiled TMA store, 3-D, shared -> global, tracked by the issuing thread's bulk async-group.
 PKV_DEV void tma_store_3d(const CUtensorMap* tm, int x, int y, int z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -179,6 +188,16 @@ PKV_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
 }
 
 PKV_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Wait for this thread's TMEM loads and tie v to the wait, so that nothing reads it earlier.
+PKV_DEV void tmem_wait_ld32(float (&v)[32]) {
+  tmem_wait_ld();
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]));
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
 PKV_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 }  // namespace pkv
@@ -188,7 +207,14 @@ namespace pkv_host {
 // d1 and d2, box {b0, b1, b2}.  False if the driver rejects it.  Defined in abi.cu.
 bool encode_tmap_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                     uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
-// The same of bytes, with the 128-byte swizzle for rows of 128 bytes and the 64-byte one for 64 (b0).
+// 2-D bf16 map of rows of d0 values, box 64 values x one row, 128-byte swizzle (for gathers of rows).
+// `used`: consecutive values of a row that are read together; L2 fetches 256 bytes at a time only
+// where they fill them (a head of 64 would bring its neighbour along, twice the traffic).
+bool encode_tmap_rows(CUtensorMap* m, const void* base, uint64_t d0, uint64_t rows, uint64_t used);
+// 3-D bf16 map of one head's rows of a pool [rows, heads, D], box 64 dims x 1 head x box_rows, with the same
+// choice of fetch size.
+bool encode_tmap_head(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads, uint64_t rows, uint32_t box_rows);
+// encode_tmap_3d of bytes, with the 128-byte swizzle for rows of 128 bytes and the 64-byte one for 64 (b0).
 bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                        uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
 }  // namespace pkv_host

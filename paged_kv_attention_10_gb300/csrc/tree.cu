@@ -42,7 +42,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4;      // warps 4..7 slot 0, 8..11 slot 1
 constexpr int kMaxNodes = 1024;       // drafted tokens of a request
 constexpr int kSegRing = 4;
-constexpr int kMaxRing = 10;
+constexpr int kMaxRing = 9;
 constexpr int kUnitCost = 2;          // a unit's start and epilogue, in KV tiles of the work split
 constexpr uint32_t kHalfTile = 128 * 128;  // 128 rows of one 64-dim half, 16 KB
 constexpr uint32_t kColO = 0, kColS = 256;  // O of slot s at 128 s, S at 256 + 128 s
@@ -55,7 +55,7 @@ struct Cfg {
   // One ring for K and V tiles, K of tile j at place 2 j and V at 2 j + 1: a buffer that K's product
   // frees soon is the next V's, and the loads run 2.5 tiles ahead.  (Two K and three V buffers of their own
   // left K's reload little more than a tile's time.)
-  static constexpr int kRing = D == 128 ? 5 : 10;
+  static constexpr int kRing = D == 128 ? 5 : 9;
   static constexpr uint32_t kOffRing = kOffQ + 2 * kTile;
   // the epilogue's exchange between replicas, 2 slots x 3 x 32 rows x 32 dims fp32: at D 128 it is the
   // second Q buffer, which one Q tile leaves free
@@ -117,7 +117,6 @@ struct TreeArgs {
   const int32_t* prefix_lens;
   const uint32_t* mask;  // [num_q_tokens, words]
   int32_t words;
-  const __nv_bfloat16* k_pool;
   const __nv_bfloat16* v_pool;
   __nv_bfloat16* out;
   float* lse;
@@ -135,10 +134,6 @@ struct TreeArgs {
   int32_t part_rows;
 };
 
-PKV_DEV void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // ---------------------------------------------------------------------------------------------
 // Segment ring
 // ---------------------------------------------------------------------------------------------
@@ -155,8 +150,8 @@ PKV_DEV bool next_seg(Ctl* ctl, int i, Seg& s) {
 // ---------------------------------------------------------------------------------------------
 // K / V producers
 // ---------------------------------------------------------------------------------------------
-// Copies the tiles of segments into a ring.  kRows: one row at a time by cp.async, for page sizes
-// that are not a power of two of at least 8; else TMA boxes of min(page_size, 128) rows.
+// Copies the tiles of segments into the ring.  kRows: gathers of four rows, for page sizes that are not
+// a power of two of at least 8; else TMA boxes of min(page_size, 128) rows.
 template <int D, bool kRows>
 struct Producer {
   using C = Cfg<D>;
@@ -164,14 +159,12 @@ struct Producer {
   uint64_t* fulls;
   uint64_t* empties;
   const CUtensorMap* tm;
-  const __nv_bfloat16* pool;
   uint32_t base;  // of the ring, shared address
   int item;       // place of the next tile in the ring's order: even K, odd V
-  int unpublished = -1;  // kRows: the buffer whose copies are not announced yet
 
   __device__ Producer(const TreeArgs& args, Ctl* ctl, uint32_t sb, bool v)
       : a(args), fulls(ctl->full), empties(ctl->empty), tm(v ? &args.tm_v : &args.tm_k),
-        pool(v ? args.v_pool : args.k_pool), base(sb + C::kOffRing), item(v ? 1 : 0) {}
+        base(sb + C::kOffRing), item(v ? 1 : 0) {}
 
   // Waits until the next tile's buffer is free.
   __device__ bool acquire() {
@@ -230,56 +223,35 @@ struct Producer {
     return true;
   }
 
-  // The previous stage's copies have landed: make them visible to the tensor cores, announce them.
-  __device__ void publish(bool all) {
-    if (unpublished < 0) return;
-    if (all)
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&fulls[unpublished]);
-    unpublished = -1;
-  }
-
+  // A lane gathers four rows at a time (tile::gather4), its positions 4 lane .. 4 lane + 3 of the tile, one
+  // copy per 64-dim half.  Positions behind the end repeat the last one and a bad page's (reported)
+  // read the pool's row 0: neither is seen by a row whose result means anything.
   __device__ bool run_rows(const Seg& s) {
     const int lane = threadIdx.x & 31;
     const int kv_end = s.P + s.T;
-    auto slot_of = [&](int j, int r) -> int64_t {
-      const int pos = j * kBN + r;
-      if (j >= s.j0 + s.n || pos >= kv_end) return -1;
-      const int pidx = pos / a.page_size;
-      return row_of(pos, pidx < s.np ? __ldg(a.kv_indices + s.p0 + pidx) : -1, s.np);
-    };
-    int64_t next[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) next[i] = slot_of(s.j0, lane + 32 * i);
-    for (int j = s.j0; j < s.j0 + s.n; ++j) {
-      // no free stage yet: announce the pending one now instead of behind the next issue
-      const int stage = item % C::kRing;
-      if (!__all_sync(0xffffffffu, mbar_test(&empties[stage], ((item / C::kRing) & 1) ^ 1))) publish(true);
-      if (!acquire()) return false;
+    int next[4];
+    auto rows_of = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (next[i] < 0) continue;
-        const int row = lane + 32 * i;
-        const char* src = reinterpret_cast<const char*>(pool + (next[i] * a.num_kv_heads + s.h) * D);
-        const uint32_t dst = base + stage * C::kTile + row * 128;
-#pragma unroll
-        for (int hf = 0; hf < C::kHalves; ++hf)
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            cp_async16(dst + hf * kHalfTile + ((c ^ (row & 7)) << 4), src + hf * 128 + c * 16);
+        const int pos = min(j * kBN + 4 * lane + i, kv_end - 1);
+        const int pidx = pos / a.page_size;
+        const int64_t row = row_of(pos, pidx < s.np ? __ldg(a.kv_indices + s.p0 + pidx) : -1, s.np);
+        next[i] = row < 0 ? 0 : (int)row;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      item += 2;
+    };
+    rows_of(s.j0);
+    for (int j = s.j0; j < s.j0 + s.n; ++j) {
+      if (!acquire()) return false;
+      const int stage = item % C::kRing;
+      if (lane == 0) mbar_arrive_expect_tx(&fulls[stage], C::kTile);
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) next[i] = slot_of(j + 1, lane + 32 * i);  // while these copies fly
-      publish(false);
-      unpublished = stage;
+      for (int hf = 0; hf < C::kHalves; ++hf)
+        tma_gather4(base + stage * C::kTile + hf * kHalfTile + lane * 512, tm, s.h * D + hf * 64, next[0], next[1], next[2],
+                    next[3], &fulls[stage]);
+      item += 2;
+      if (j + 1 < s.j0 + s.n) rows_of(j + 1);  // while these copies fly
     }
-    publish(true);
     return true;
   }
 
@@ -289,10 +261,6 @@ struct Producer {
   // and its phase could no longer be waited for.  After a wait that gave up, every buffer's is tried
   // (bounded waits).
   __device__ void drain(bool all) {
-    if (kRows) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      publish(true);
-    }
     const int end = (item & ~1);  // places issued in all, if the other warp has come as far
     for (int i = item - 2; i >= max(0, all ? end - C::kRing : item - 2 * C::kRing); i -= 2)
       mbar_wait(&fulls[i % C::kRing], (i / C::kRing) & 1);
@@ -735,22 +703,22 @@ PKV_DEV float softmax_tile(uint32_t ts, int ch0, float sc, float m, float& m_ref
   float mx = -INFINITY;
   if constexpr (N == 1) {
     tmem_ld32(s0, b);
-    tmem_wait_ld();
+    tmem_wait_ld32(b);
     mx = max32(b);
   } else {
     tmem_ld32(s0 + (N - 1) * 32, a);
-    tmem_wait_ld();
+    tmem_wait_ld32(a);
     if constexpr (N == 4) {
       tmem_ld32(s0 + 64, b);
       mx = max32(a);
-      tmem_wait_ld();
+      tmem_wait_ld32(b);
       tmem_ld32(s0 + 32, a);
       mx = fmaxf(mx, max32(b));
-      tmem_wait_ld();
+      tmem_wait_ld32(a);
     }
     tmem_ld32(s0, b);
     mx = N == 4 ? fmaxf(mx, max32(a)) : max32(a);
-    tmem_wait_ld();
+    tmem_wait_ld32(b);
     mx = fmaxf(mx, max32(b));
   }
   const float m_new = fmaxf(m, mx * sc);
@@ -768,16 +736,16 @@ PKV_DEV float softmax_tile(uint32_t ts, int ch0, float sc, float m, float& m_ref
   } else {
     tmem_ld32(s0 + 32, a);
     tot = weights32(b, sc, neg, pk);
-    tmem_wait_ld();
+    tmem_wait_ld32(a);
     tmem_st16(p0, pk);
     if constexpr (N == 4) tmem_ld32(s0 + 64, b);
     tot += weights32(a, sc, neg, pk);
-    if constexpr (N == 4) tmem_wait_ld();
+    if constexpr (N == 4) tmem_wait_ld32(b);
     tmem_st16(p0 + 16, pk);
     if constexpr (N == 4) {
       tmem_ld32(s0 + 96, a);
       tot += weights32(b, sc, neg, pk);
-      tmem_wait_ld();
+      tmem_wait_ld32(a);
       tmem_st16(p0 + 32, pk);
       tot += weights32(a, sc, neg, pk);
       tmem_st16(p0 + 48, pk);
@@ -843,7 +811,7 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
             tmem_ld32(ts + ch * 32, v);
             const uint32_t vis = special ? visible(mask, s.T, pos0 + 32 * ch - s.P) : 0xffffffffu;
             const float mul = pos_scale ? 1.f : a.scale_log2;
-            tmem_wait_ld();
+            tmem_wait_ld32(v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] * mul : -INFINITY;
             tmem_st32(ts + ch * 32, v);
@@ -866,7 +834,7 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
           for (int ch = 0; ch < D / 32; ++ch) {
             float v[32];
             tmem_ld32(to + ch * 32, v);
-            tmem_wait_ld();
+            tmem_wait_ld32(v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] *= corr;
             tmem_st32(to + ch * 32, v);
@@ -938,7 +906,7 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
       float o[32];
       if (two) {
         tmem_ld32(to + ch * 32, o);
-        tmem_wait_ld();
+        tmem_wait_ld32(o);
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = plain || f_mine > 0.f ? o[e] * f_mine : 0.f;
       } else {
@@ -949,7 +917,8 @@ __device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
           tmem_ld8(to + col, o + 8 * j);
           tmem_ld8(tq + kColO + (slot ^ 1) * 128 + col, x + 8 * j);
         }
-        tmem_wait_ld();
+        tmem_wait_ld32(o);
+        tmem_wait_ld32(x);
         if (plain) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = fmaf(x[e], f_other, o[e] * f_mine);
@@ -1324,8 +1293,10 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   if (!pkv_host::encode_tmap_3d(&a.tm_q[0], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt) ||
       !pkv_host::encode_tmap_3d(&a.tm_q[1], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt2) ||
       !pkv_host::encode_tmap_3d(&a.tm_q[2], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt4) ||
-      !pkv_host::encode_tmap_3d(&a.tm_k, pool->k, D, Hkv, rows, Db, Hkv * Db, 64, 1, a.box_rows) ||
-      !pkv_host::encode_tmap_3d(&a.tm_v, pool->v, D, Hkv, rows, Db, Hkv * Db, 64, 1, a.box_rows))
+      !(rows_path ? pkv_host::encode_tmap_rows(&a.tm_k, pool->k, Hkv * D, rows, D) &&
+                        pkv_host::encode_tmap_rows(&a.tm_v, pool->v, Hkv * D, rows, D)
+                  : pkv_host::encode_tmap_head(&a.tm_k, pool->k, D, Hkv, rows, a.box_rows) &&
+                        pkv_host::encode_tmap_head(&a.tm_v, pool->v, D, Hkv, rows, a.box_rows)))
     return PKV_ERR_CUDA;
   a.qo_indptr = qo_indptr;
   a.kv_indptr = kv_indptr;
@@ -1333,7 +1304,6 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   a.prefix_lens = prefix_lens;
   a.mask = (const uint32_t*)tree_mask;
   a.words = mask_words;
-  a.k_pool = (const __nv_bfloat16*)pool->k;
   a.v_pool = (const __nv_bfloat16*)pool->v;
   a.out = (__nv_bfloat16*)out;
   a.lse = lse;
