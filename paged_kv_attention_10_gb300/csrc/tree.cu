@@ -30,6 +30,7 @@
 //    written, which is what a sum with a non-zero weight would give.
 #include <atomic>
 
+#include "quant.cuh"
 #include "tc05.cuh"
 
 namespace {
@@ -123,6 +124,7 @@ struct TreeArgs {
   uint32_t* err_word;
   int64_t num_pages;
   int32_t page_size, box_rows;
+  FastDiv page_div;  // by page_size
   int32_t num_kv_heads, num_q_heads, group;
   int32_t tpt;        // tokens per Q tile
   int32_t tpt2, tpt4; // ... of which 2 or 4 copies fit into the tile
@@ -173,7 +175,7 @@ struct Producer {
 
   // Row of the pool that holds position pos, or -1 (reported).
   __device__ int64_t row_of(int pos, int32_t page, int np) {
-    const int pidx = pos / a.page_size;
+    const int pidx = (int)a.page_div.quot((uint32_t)pos);
     if (pidx >= np) {
       report(a.err_word, PKV_DEVERR_LENGTH);
       return -1;
@@ -196,16 +198,16 @@ struct Producer {
     auto entry = [&](int pidx) -> int32_t {
       return (pidx >= 0 && pidx < s.np) ? __ldg(a.kv_indices + s.p0 + pidx) : -1;
     };
-    int wbase = s.j0 * kBN / a.page_size;
+    int wbase = (int)a.page_div.quot((uint32_t)(s.j0 * kBN));
     int32_t w0 = entry(wbase + lane), w1 = entry(wbase + 32 + lane);
     for (int j = s.j0; j < s.j0 + s.n; ++j) {
-      while (j * kBN / a.page_size >= wbase + 32) {  // the upper half was loaded 32 pages ago
+      while ((int)a.page_div.quot((uint32_t)(j * kBN)) >= wbase + 32) {  // the upper half was loaded 32 pages ago
         w0 = w1;
         wbase += 32;
         w1 = entry(wbase + 32 + lane);
       }
       const int pos = j * kBN + box * R;
-      const int k = pos / a.page_size - wbase;  // < 64: a tile spans at most 16 pages
+      const int k = (int)a.page_div.quot((uint32_t)pos) - wbase;  // < 64: a tile spans at most 16 pages
       const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
       const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
       const bool in = half < C::kHalves && pos < kv_end;
@@ -224,33 +226,45 @@ struct Producer {
   }
 
   // A lane gathers four rows at a time (tile::gather4), its positions 4 lane .. 4 lane + 3 of the tile, one
-  // copy per 64-dim half.  Positions behind the end repeat the last one and a bad page's (reported)
-  // read the pool's row 0: neither is seen by a row whose result means anything.
+  // copy per 64-dim half; their pages are loaded a tile ahead.  Positions behind the end repeat the
+  // last one and a bad page's (reported) read the pool's row 0: neither is seen by a row whose result
+  // means anything.  29 requests of about 6000 positions, 8 heads at page size 1: 208 us at D 128 and 128 at
+  // D 64; 16-byte cp.async copies with the same look-ahead 262 and 251, gathers whose pages were
+  // loaded when needed 286 and 207.
   __device__ bool run_rows(const Seg& s) {
     const int lane = threadIdx.x & 31;
     const int kv_end = s.P + s.T;
-    int next[4];
-    auto rows_of = [&](int j) {
+    int32_t page[4];
+    uint32_t in_page[4];
+    bool listed[4];
+    auto load_pages = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int pos = min(j * kBN + 4 * lane + i, kv_end - 1);
-        const int pidx = pos / a.page_size;
-        const int64_t row = row_of(pos, pidx < s.np ? __ldg(a.kv_indices + s.p0 + pidx) : -1, s.np);
-        next[i] = row < 0 ? 0 : (int)row;
+        uint32_t pidx;
+        a.page_div.divmod((uint32_t)min(j * kBN + 4 * lane + i, kv_end - 1), pidx, in_page[i]);
+        listed[i] = (int)pidx < s.np;
+        page[i] = listed[i] ? __ldg(a.kv_indices + s.p0 + pidx) : 0;
       }
     };
-    rows_of(s.j0);
+    load_pages(s.j0);
     for (int j = s.j0; j < s.j0 + s.n; ++j) {
+      int row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = page[i] >= 0 && page[i] < a.num_pages;
+        if (!listed[i] || !in) report(a.err_word, !listed[i] ? PKV_DEVERR_LENGTH : PKV_DEVERR_PAGE_OOB);
+        row[i] = listed[i] && in ? page[i] * a.page_size + (int)in_page[i] : 0;
+      }
+      if (j + 1 < s.j0 + s.n) load_pages(j + 1);
       if (!acquire()) return false;
       const int stage = item % C::kRing;
       if (lane == 0) mbar_arrive_expect_tx(&fulls[stage], C::kTile);
       __syncwarp();
 #pragma unroll
       for (int hf = 0; hf < C::kHalves; ++hf)
-        tma_gather4(base + stage * C::kTile + hf * kHalfTile + lane * 512, tm, s.h * D + hf * 64, next[0], next[1], next[2],
-                    next[3], &fulls[stage]);
+        tma_gather4(base + stage * C::kTile + hf * kHalfTile + lane * 512, tm, s.h * D + hf * 64, row[0], row[1], row[2],
+                    row[3], &fulls[stage]);
       item += 2;
-      if (j + 1 < s.j0 + s.n) rows_of(j + 1);  // while these copies fly
     }
     return true;
   }
@@ -1310,6 +1324,7 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   a.err_word = err_word;
   a.num_pages = pool->num_pages;
   a.page_size = ps;
+  a.page_div = FastDiv((uint32_t)ps);
   a.num_kv_heads = pool->num_kv_heads;
   a.num_q_heads = num_q_heads;
   a.group = p.G;
