@@ -171,7 +171,7 @@ const char* pkv_status_string(pkv_status s) {
   return "unknown status";
 }
 
-int32_t pkv_version(void) { return 100; }  // 0.1.0
+int32_t pkv_version(void) { return 200; }  // 0.2.0
 
 }  // extern "C"
 
