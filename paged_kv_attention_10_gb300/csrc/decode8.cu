@@ -78,6 +78,9 @@ struct Decode8Args {
   uint32_t stage_bytes;  // K, V and the scales
 };
 
+// No request has more positions than the pool has rows; a longer kv_lens[b] (reported, its pages run
+// out) must not take the token counter past 31 bits.
+constexpr int kMaxLen = 0x7fff0000;
 constexpr int kSlice = 32;  // positions of a warp's step, and the unit of the work split
 constexpr int kMaxStages = 8;
 
@@ -130,14 +133,14 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
 
   // the first 32 requests' numbers in one round of loads, which the walk below starts with
   const bool in0 = lane < a.batch;
-  const int32_t first_len = in0 ? max(0, __ldg(a.kv_lens + lane)) : 0;
+  const int32_t first_len = in0 ? min(max(0, __ldg(a.kv_lens + lane)), kMaxLen) : 0;
   const int32_t first_p0 = in0 ? __ldg(a.kv_indptr + lane) : 0;
   const int32_t first_p1 = in0 ? __ldg(a.kv_indptr + lane + 1) : 0;
   int64_t sumS = ((int64_t)first_len + kSlice - 1) / kSlice;  // slices over all requests
   for (int i = 32 + lane; i < a.batch; i += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)  // four loads in flight
-      if (i + 32 * u < a.batch) sumS += ((int64_t)max(0, __ldg(a.kv_lens + i + 32 * u)) + kSlice - 1) / kSlice;
+      if (i + 32 * u < a.batch) sumS += (min(max(0, __ldg(a.kv_lens + i + 32 * u)), kMaxLen) + kSlice - 1) / kSlice;
   }
   sumS = warp_sum(sumS);
   const int64_t T = sumS * nhg;
@@ -268,7 +271,7 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
       int64_t L = first_len;
       int32_t ip0 = first_p0, ip1 = first_p1;
       if (b0 > 0) {
-        L = in ? (int64_t)max(0, __ldg(a.kv_lens + b)) : 0;
+        L = in ? min(max(0, __ldg(a.kv_lens + b)), kMaxLen) : 0;
         ip0 = in ? __ldg(a.kv_indptr + b) : 0;
         ip1 = in ? __ldg(a.kv_indptr + b + 1) : 0;
       }
@@ -906,6 +909,7 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
   Plan p;
   if (!make_plan(batch_size, num_q_heads, pool->num_kv_heads, D, ncta, p, pool->page_size, pool->num_pages))
     return PKV_ERR_UNSUPPORTED;
+  if (p.nparts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // 31-bit numbers of units and partials
   if (!workspace || workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_INVALID_ARG;
 

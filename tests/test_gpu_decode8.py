@@ -210,3 +210,38 @@ def test_shared_pages(lib):
     out, lse, err = decode(lib, s)
     assert err == 0
     verify(s, out, lse)
+
+
+def test_pool_past_32_bits(lib):
+    """Slots whose byte offsets pass 4 GB, for the append, the decode (boxes and rows) and the read-back."""
+    first = 280_000  # pages of 16 KB
+    shape = (first + 20, 16, 8, 128)
+    pool = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pool += [torch.ones(shape[:3], device="cuda") for _ in range(2)]
+    gen = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(300, 8, 128, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(1, 32, 128, generator=gen).to(torch.bfloat16).cuda()
+    slots = first * 16 + torch.randperm(320, generator=gen)[:300].cuda()
+    lib.kv_append_fp8(*pool, k, v, slots)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    flat = [pool[0].view(-1, 1, 8, 128), pool[1].view(-1, 1, 8, 128), pool[2].view(-1, 1, 8), pool[3].view(-1, 1, 8)]
+    out, lse = lib.paged_decode_fp8(q, *flat, i32([0, 300]), slots.int(), i32([300]), 0.1)
+    ref = {}
+    for name, x in (("k", k), ("v", v)):
+        codes, scale = cache8.quantise(oracle.as_f64(x))
+        ref[name] = cache8.e4m3_values(codes) * scale[..., None]
+    qd, o, l = oracle.as_f64(q)[0], oracle.as_f64(out)[0], oracle.as_f64(lse)[0]
+    for h in range(8):
+        a = attend(qd[4 * h: 4 * h + 4], ref["k"][:, h], ref["v"][:, h], 0.1)
+        extra = 2.0 ** -24 * a[4].max(-1)[:, None] * 4 * np.abs(ref["v"][:, h]).sum(0)
+        check(o[4 * h: 4 * h + 4], l[4 * h: 4 * h + 4], a, 300, F16, f"head {h}", extra)
+    ko, vo = (torch.zeros(320, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pages = i32(list(range(first, first + 20)))
+    lib.paged_gather_fp8(*pool, i32([0, 20]), pages, i32([320]), i32([0, 320]), ko, vo)
+    assert np.array_equal(oracle.as_f64(ko[slots - first * 16]), ref["k"])
+    assert np.array_equal(oracle.as_f64(vo[slots - first * 16]), ref["v"])
+    # the same rows as pages of 16, in page order
+    o16, l16 = lib.paged_decode_fp8(q, *pool, i32([0, 20]), pages, i32([320]), 0.1)
+    small = [x[first:].contiguous() for x in pool]
+    o2, l2 = lib.paged_decode_fp8(q, *small, i32([0, 20]), pages - first, i32([320]), 0.1)
+    assert torch.equal(o16, o2) and torch.equal(l16, l2)

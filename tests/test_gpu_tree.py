@@ -119,6 +119,7 @@ SHAPES = [
     ((30, 20, 10, 500), (0, 6, 0, 4), 8, 2, 128, 128),
     ((2500,), (1,), 16, 2, 128, 16),
     ((40,), (1024,), 1, 1, 64, 16),
+    ((190, 8, 1000), (11, 21, 43), 9, 3, 128, 16),
 ]
 
 
@@ -167,6 +168,48 @@ def test_many_requests(lib):
     out, lse, err = call(lib, s)
     assert err == 0
     verify(s, out, lse, range(0, 150, 7))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (12, 4, 64)])
+def test_many_trees_of_all_sizes(lib, Hq, Hkv, D):
+    """More units than CTAs, with one Q tile and with two, in turn on the same CTA; padding rows behind
+    the last request are left as they were."""
+    rng = np.random.default_rng(14)
+    nodes = (2.0 ** rng.uniform(0, 7, 110)).astype(int).tolist()
+    prefix = rng.integers(0, 500, 110).tolist()
+    s = make(14, prefix, nodes, Hq, Hkv, D, 16)
+    N = sum(nodes)
+    pad = lambda x, fill: torch.cat([x, torch.full((7,) + x.shape[1:], fill, dtype=x.dtype, device="cuda")])  # noqa: E731
+    s["q"], s["mask"] = pad(s["q"], 1.0), pad(s["mask"], -1)
+    fill = torch.full_like(s["q"], 7.0)
+    out, lse, err = call(lib, s, out=fill)
+    assert err == 0
+    assert torch.all(out[N:] == 7.0)
+    verify(s, out, lse, range(0, 110, 5))
+    for _ in range(3):
+        o2, l2, _ = call(lib, s)
+        assert torch.equal(o2[:N], out[:N]) and torch.equal(l2[:N], lse[:N])
+
+
+def test_pool_past_32_bits(lib):
+    """Pages whose byte offsets pass 4 GB."""
+    small = make(15, (300, 40), (20, 9), 8, 8, 128, 16)
+    n = small["k"].shape[0]
+    first = 150_000  # pages of 32 KB
+    k = torch.zeros(first + n, 16, 8, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[first:], v[first:] = small["k"], small["v"]
+    out, lse, err = call(lib, small)
+    big = dict(small, k=k, v=v, pages=small["pages"] + first)
+    o2, l2, err = call(lib, big)
+    assert err == 0 and torch.equal(out, o2) and torch.equal(lse, l2)
+    # the same cache one row a page (gathers of rows)
+    rows = torch.cat([torch.as_tensor(r) for r in small["rows"]]).int().cuda()
+    lens = torch.tensor([0, 320, 369], dtype=torch.int32).cuda()
+    one = dict(small, k=k.view(-1, 1, 8, 128), v=v.view(-1, 1, 8, 128), pages=rows + first * 16, indptr=lens)
+    o3, l3, err = call(lib, one)
+    assert err == 0
+    verify(small, o3, l3)
 
 
 def test_growing_scores(lib):
