@@ -212,6 +212,13 @@ PKV_DEV void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Programmatic dependent launch.  A kernel launched with launch_after (below) may start while the kernel
+// before it on the stream still runs, if that one has called pdl_trigger in every block (or ended
+// them); it must call pdl_wait before its first access to global memory, which returns when that
+// kernel has completed and its writes are visible.  Start-up then overlaps the kernel before it.
+PKV_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+PKV_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -229,4 +236,24 @@ bool valid_pool(const pkv_pool* p); // non-null, positive sizes, aligned
 // Process-unique id of the calling thread's current CUDA context (cuCtxGetId), 0 when there is
 // none or it cannot be read.  A context created after a device reset gets a new id.
 unsigned long long current_context_id();
+
+// Launches a kernel that calls pdl_wait (see above) on the stream.
+template <typename... P, typename... A>
+pkv_status launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+    cudaGetLastError();  // not left for a later call's check to find
+    return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
 }  // namespace pkv_host

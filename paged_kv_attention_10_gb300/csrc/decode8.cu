@@ -317,7 +317,7 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
   // The merge may be scheduled once every CTA has issued its last copies (it waits for this grid's
   // completion before it reads): early enough to hide its launch, late enough not to hold thread
   // slots that kernels on other streams could use.
-  if (!v) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!v) pdl_trigger();
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   // No copy into this CTA's shared memory is in flight when it exits (bounded waits; immediate on
   // the normal path, where the consumers have seen every stage complete).
@@ -694,6 +694,7 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
   }
   fence_proxy_async_smem();
   __syncthreads();
+  pdl_wait();
 
   const int warp = threadIdx.x >> 5;
   if (warp == NC) {
@@ -711,7 +712,8 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
 // ---------------------------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) decode8_merge_kernel(const __grid_constant__ Decode8Args a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
   const int u = blockIdx.x;
   const int b = u / a.nhg, hg = u % a.nhg;
   const int HQU = a.HC * a.group;
@@ -860,20 +862,10 @@ pkv_status launch(const Plan& p, const Decode8Args& a, cudaStream_t st) {
       return PKV_ERR_CUDA;
     if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<p.ncta, (p.HC * p.W + 2) * 32, p.smem, st>>>(a);
-  const pkv_status s = pkv_host::launch_status();
+  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.W + 2) * 32, p.smem, st, a);
   if (s != PKV_OK) return s;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8), 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, decode8_merge_kernel<D>, a) != cudaSuccess) return PKV_ERR_CUDA;
-  return pkv_host::launch_status();
+  return pkv_host::launch_after(decode8_merge_kernel<D>, dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8)), 256, 0,
+                                st, a);
 }
 
 }  // namespace

@@ -72,6 +72,8 @@ PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
 
 __global__ void __launch_bounds__(kThreads) paged_gather8_kernel(const __grid_constant__ GatherArgs a) {
   __shared__ int64_t s_slot[2][kRows];
+  pdl_trigger();
+  pdl_wait();
   // what the copies below cannot see: a request whose rows do not hold its length, or lie outside out
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.batch; b += gridDim.x * kThreads) {
     const int64_t o0 = __ldg(a.out_indptr + b), o1 = __ldg(a.out_indptr + b + 1);
@@ -158,6 +160,5 @@ extern "C" pkv_status pkv_paged_gather_fp8(const pkv_pool_fp8* pool, const int32
   int64_t blocks = (num_out_rows + kRows - 1) / kRows;
   const int64_t cap = (int64_t)pkv_host::sm_count() * 8;
   if (cap > 0 && blocks > cap) blocks = cap;
-  paged_gather8_kernel<<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(a);
-  return pkv_host::launch_status();
+  return pkv_host::launch_after(paged_gather8_kernel, dim3((unsigned)blocks), kThreads, 0, (cudaStream_t)stream, a);
 }

@@ -118,6 +118,8 @@ constexpr int kSteps = 2;
 template <bool FP8, int ROT, int L>
 __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kRows = 32 / L;
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (item >= a.items) return;
@@ -222,6 +224,8 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
 // Any even width: one chunk per lane, L lanes per row, partners read one by one.
 template <bool FP8, int L>
 __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_constant__ AppendArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int c = lane & (L - 1);
   const unsigned mask = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
@@ -290,13 +294,12 @@ pkv_status launch_rows(AppendArgs a, cudaStream_t st) {
   a.item_div = FastDiv((uint32_t)parts);
   const unsigned g = (a.items + 7) / 8;
   switch (L) {
-    case 1: append_rows_kernel<FP8, ROT, 1><<<g, 256, 0, st>>>(a); break;
-    case 2: append_rows_kernel<FP8, ROT, 2><<<g, 256, 0, st>>>(a); break;
-    case 4: append_rows_kernel<FP8, ROT, 4><<<g, 256, 0, st>>>(a); break;
-    case 8: append_rows_kernel<FP8, ROT, 8><<<g, 256, 0, st>>>(a); break;
-    default: append_rows_kernel<FP8, ROT, 16><<<g, 256, 0, st>>>(a); break;
+    case 1: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 1>, dim3(g), 256, 0, st, a);
+    case 2: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 2>, dim3(g), 256, 0, st, a);
+    case 4: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 4>, dim3(g), 256, 0, st, a);
+    case 8: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 8>, dim3(g), 256, 0, st, a);
+    default: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 16>, dim3(g), 256, 0, st, a);
   }
-  return pkv_host::launch_status();
 }
 
 template <bool FP8>
@@ -306,14 +309,13 @@ pkv_status launch_any_width(AppendArgs a, cudaStream_t st) {
   a.row_div = FastDiv((uint32_t)a.heads);
   const unsigned per = 256 / L, g = (a.items + per - 1) / per;
   switch (L) {
-    case 1: append_any_width_kernel<FP8, 1><<<g, 256, 0, st>>>(a); break;
-    case 2: append_any_width_kernel<FP8, 2><<<g, 256, 0, st>>>(a); break;
-    case 4: append_any_width_kernel<FP8, 4><<<g, 256, 0, st>>>(a); break;
-    case 8: append_any_width_kernel<FP8, 8><<<g, 256, 0, st>>>(a); break;
-    case 16: append_any_width_kernel<FP8, 16><<<g, 256, 0, st>>>(a); break;
-    default: append_any_width_kernel<FP8, 32><<<g, 256, 0, st>>>(a); break;
+    case 1: return pkv_host::launch_after(append_any_width_kernel<FP8, 1>, dim3(g), 256, 0, st, a);
+    case 2: return pkv_host::launch_after(append_any_width_kernel<FP8, 2>, dim3(g), 256, 0, st, a);
+    case 4: return pkv_host::launch_after(append_any_width_kernel<FP8, 4>, dim3(g), 256, 0, st, a);
+    case 8: return pkv_host::launch_after(append_any_width_kernel<FP8, 8>, dim3(g), 256, 0, st, a);
+    case 16: return pkv_host::launch_after(append_any_width_kernel<FP8, 16>, dim3(g), 256, 0, st, a);
+    default: return pkv_host::launch_after(append_any_width_kernel<FP8, 32>, dim3(g), 256, 0, st, a);
   }
-  return pkv_host::launch_status();
 }
 
 bool disjoint_or_same(const void* a, const void* b, size_t bytes) {

@@ -44,7 +44,8 @@ constexpr int kSoftmaxWarp0 = 4;      // warps 4..7 slot 0, 8..11 slot 1
 constexpr int kMaxNodes = 1024;       // drafted tokens of a request
 constexpr int kSegRing = 4;
 constexpr int kMaxRing = 9;
-constexpr int kUnitCost = 2;          // a unit's start and epilogue, in KV tiles of the work split
+constexpr int kUnitCost = 3;          // a unit's start and epilogue, in KV tiles of the work split (1 to 4
+                                      // tried: 64 requests of up to 16 tokens 118.9, 115.7, 114.7, 115.5 us)
 constexpr uint32_t kHalfTile = 128 * 128;  // 128 rows of one 64-dim half, 16 KB
 constexpr uint32_t kColO = 0, kColS = 256;  // O of slot s at 128 s, S at 256 + 128 s
 
@@ -404,7 +405,7 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb, int64_t tota
   // The merge may be scheduled once every CTA has issued its last K (it waits for this grid's
   // completion before it reads): early enough to hide its launch, late enough not to hold thread
   // slots that kernels on other streams could use.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   k.drain(ok);
 }
@@ -1026,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
   const uint32_t sb = smem_u32(smem);
   if (sb & 1023u) {  // the swizzled layouts need a 1024-byte aligned base
     if (threadIdx.x == 0) {
+      pdl_wait();
       report(a.err_word, PKV_DEVERR_INTERNAL);
       a.cut[blockIdx.x] = Cut{};
     }
@@ -1063,7 +1065,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
   }
-  const int64_t total = warp == 0 ? tree_stream_length(a) : 0;
+  int64_t total = 0;
+  if (warp == 0) {
+    pdl_wait();
+    total = tree_stream_length(a);
+  }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, 512);
     tmem_relinquish();
@@ -1071,6 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
@@ -1111,7 +1118,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int kGroups = D / 32;  // groups of four dims of a thread
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
   const int c = blockIdx.x;
   const Cut cut = a.cut[c];
   if (cut.parts <= 0) return;
@@ -1175,6 +1183,8 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restric
                                                         const int32_t* __restrict__ qo_indptr,
                                                         int32_t num_tokens, int32_t words,
                                                         uint32_t* __restrict__ mask, uint32_t* err_word) {
+  pdl_trigger();
+  pdl_wait();
   const int b = blockIdx.y;
   const int32_t q0 = __ldg(qo_indptr + b), rows = __ldg(qo_indptr + b + 1) - q0;
   const bool first = blockIdx.x == 0 && threadIdx.x == 0;
@@ -1242,20 +1252,9 @@ pkv_status launch(const Plan& p, const TreeArgs& a, cudaStream_t st) {
       return PKV_ERR_CUDA;
     if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<p.ncta, kThreads, smem, st>>>(a);
-  const pkv_status s = pkv_host::launch_status();
+  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), kThreads, smem, st, a);
   if (s != PKV_OK) return s;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.ncta, (unsigned)(p.part_rows / 32), 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a) != cudaSuccess) return PKV_ERR_CUDA;
-  return pkv_host::launch_status();
+  return pkv_host::launch_after(tree_merge_kernel<D>, dim3((unsigned)p.ncta, (unsigned)(p.part_rows / 32)), 256, 0, st, a);
 }
 
 }  // namespace
@@ -1353,9 +1352,8 @@ pkv_status pkv_tree_mask_from_parents(const int32_t* parents, const int32_t* qo_
   if (!parents || !qo_indptr || !tree_mask) return PKV_ERR_INVALID_ARG;
   if (batch_size > 65535 || max_tree_len > kMaxNodes) return PKV_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)((max_tree_len + 127) / 128), (unsigned)batch_size, 1);
-  tree_mask_kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(parents, qo_indptr, num_tokens, mask_words,
-                                                           (uint32_t*)tree_mask, err_word);
-  return pkv_host::launch_status();
+  return pkv_host::launch_after(tree_mask_kernel, grid, 128, 0, (cudaStream_t)stream, parents, qo_indptr, num_tokens,
+                                mask_words, (uint32_t*)tree_mask, err_word);
 }
 
 }  // extern "C"

@@ -302,3 +302,66 @@ def test_binding_refusals_on_the_device(lib):
         lib.paged_tree_attention(*args(most=1025, mask=torch.zeros(53, 40, dtype=torch.int32, device="cuda")))
     assert e.value.status == 2
     torch.cuda.synchronize()
+
+
+def test_starts_beside_the_kernel_before(lib):
+    """The kernels start while the one before them on the stream still runs and wait for it: what long
+    kernels, copies and joined streams write just before a call is what it reads, eager and captured."""
+    table = lib.rotary_cos_sin_table(1024, D, 1e6)
+    c = Cache8((0, 0))
+    q = append(lib, c, table, (500, 90))[:2].contiguous()
+    n = 1 << 26
+    slow, st, st2 = torch.zeros(n, device="cuda"), torch.cuda.Stream(), torch.cuda.Stream()
+    lens, qd = i32([0, 0]), torch.zeros_like(q)
+    out, lse = torch.empty_like(q), torch.empty(2, HQ, device="cuda")
+    ws = torch.empty(lib.decode_fp8_workspace_size(2, HQ, HKV, D), dtype=torch.uint8, device="cuda")
+    want = lib.paged_decode_fp8(q, *c.pool, c.indptr, c.indices, i32(c.lens), 0.1)
+    real = i32(c.lens)
+    host = torch.tensor(c.lens, dtype=torch.int32).pin_memory()
+    tree = TreeStep(11)
+    tws = tree_ws(lib)
+    tree.run(lib, table, tws)
+    torch.cuda.synchronize()
+    tree_want = tree.out.clone()
+    k0, tq = tree.k.clone(), tree.new["q"].clone()
+
+    def step(how):
+        lens.zero_()
+        qd.zero_()
+        slow.add_(1.0)
+        if how == "kernel":
+            lens.add_(real)
+        elif how == "copy":
+            lens.copy_(host, non_blocking=True)
+        else:
+            st2.wait_stream(st)
+            with torch.cuda.stream(st2):
+                slow.mul_(0.5)
+                lens.copy_(real)
+            st.wait_stream(st2)
+        qd.copy_(q)
+        lib.paged_decode_fp8(qd, *c.pool, c.indptr, c.indices, lens, 0.1, out=out, lse=lse, workspace=ws)
+        tree.k.zero_()
+        tree.new["q"].zero_()
+        slow.add_(1.0)
+        tree.k.copy_(k0)
+        tree.new["q"].copy_(tq)
+        tree.run(lib, table, tws)
+
+    for how in ("kernel", "copy", "join"):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            for captured in (False, True):
+                out.zero_()
+                tree.out.zero_()
+                if captured:
+                    g = torch.cuda.CUDAGraph()
+                    with torch.cuda.graph(g, stream=st):
+                        step(how)
+                    for _ in range(3):
+                        g.replay()
+                else:
+                    step(how)
+                st.synchronize()
+                assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (how, captured)
+                assert torch.equal(tree.out, tree_want), (how, captured)
