@@ -19,6 +19,9 @@
 //    fill slots (2c, 2c+1, 2c+8, 2c+9).  V^T through ldmatrix.trans pairs two dims of two tokens in a
 //    register; one byte permute makes pairs of tokens, and the output rows g, g + 8 become the
 //    neighbouring dims 2g, 2g + 1, which store as one bf16 pair.
+//  * Groups of 9 to 16 query heads take two warps per KV head, eight heads each, over the same rows in
+//    shared memory: one warp with both would convert once instead of twice but spills (16 heads of
+//    128, 16 requests of 10000 to 20000 positions: 57 us, 42 with two).
 //  * A warp takes 32 positions of one KV head at a time (the bf16 decode: 16), so the shuffles of
 //    the maxima, the rescaling of O and the barrier round are paid half as often.
 //  * The rest is the bf16 decode's plan: one persistent CTA per SM over an equal share of the stream
@@ -70,6 +73,7 @@ struct Decode8Args {
   int32_t nhg;           // head groups = num_kv_heads / HC
   int32_t W;             // consumer warps per KV head
   int32_t group;         // query heads per KV head
+  int32_t nt;            // warps that share a KV head's rows, eight of its query heads each
   int32_t box_rows;      // TMA instance: rows of a box (16 or 8)
   int32_t row_stride;    // row-copy instance: shared-memory bytes per token row
   int32_t stage_tokens;  // 32 * W
@@ -197,59 +201,105 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
       mbar_arrive(&hdr_full[stage]);
     }
     if (unit >= 0) {
-      const uint32_t dst = smem_u32(stages + (size_t)stage * a.stage_bytes) + (v ? region : 0u);
-      const uint32_t sdst = smem_u32(stages + (size_t)stage * a.stage_bytes) + 2 * region + (v ? (uint32_t)(Ts * HC) * 4 : 0u);
+      uint8_t* dst = stages + (size_t)stage * a.stage_bytes + (v ? region : 0u);
+      uint8_t* sdst = stages + (size_t)stage * a.stage_bytes + 2 * region + (v ? (size_t)Ts * HC * 4 : 0);
       uint32_t bad = 0;
-      for (int r = 0; r < W; ++r) {  // 32 tokens at a time: this lane's pool row, or -1
-        const int j = lane + 32 * r;
-        const bool in = j < ntok;
-        uint32_t pidx, prow;
-        a.page_div.divmod((uint32_t)(tok0 + (in ? j : 0)), pidx, prow);
-        int32_t page;
-        if (windowed) {
-          const int k = (int)pidx - wbase;  // < 64
-          const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
-          const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
-          page = k < 32 ? v0 : v1;
+      auto window_page = [&](uint32_t pidx) -> int32_t {  // all lanes call
+        const int k = (int)pidx - wbase;  // < 64
+        const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
+        const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
+        return k < 32 ? v0 : v1;
+      };
+      auto row_at = [&](uint32_t pidx, uint32_t in_page, int32_t page, bool in) -> int64_t {
+        if (!in) return -1;
+        if ((int)pidx >= cur_np) {
+          bad |= PKV_DEVERR_LENGTH;
+          return -1;
+        }
+        if (page < 0 || page >= a.num_pages) {
+          bad |= PKV_DEVERR_PAGE_OOB;
+          return -1;
+        }
+        return (int64_t)page * a.page_size + in_page;
+      };
+      auto copy_scales = [&](int64_t row, int j) {  // token j's HC scales, one by one
+        const float* src = scale + row * a.num_kv_heads + hg * HC;
+        const uint32_t sd = smem_u32(sdst) + (uint32_t)(j * HC) * 4;
+        if ((HC & 3) == 0) {
+          for (int i = 0; i < HC; i += 4) cp_async16(sd + 4 * i, src + i);
         } else {
-          page = in ? entry((int)pidx) : -1;
+          for (int i = 0; i < HC; ++i) cp_async4(sd + 4 * i, src + i);
         }
-        int64_t slot = -1;
-        if (in) {
-          if ((int)pidx >= cur_np)
-            bad |= PKV_DEVERR_LENGTH;
-          else if (page < 0 || page >= a.num_pages)
-            bad |= PKV_DEVERR_PAGE_OOB;
-          else
-            slot = (int64_t)page * a.page_size + prow;
+      };
+      if constexpr (TMA) {
+        // Lane i fetches box i, box_rows tokens inside one page, and their scales, which lie side by side when
+        // the CTA takes all KV heads.  (One lookup a stage: with one per 32 tokens the eight of a stage of
+        // one KV head took 4 us, and 720000 positions of it 96 us; 48 now, of the 28 that their bytes take.)
+        const int sh = a.box_rows == 16 ? 4 : 3, nbox = Ts >> sh;
+        const int tok = tok0 + (lane << sh);
+        const bool in = lane < nbox && tok < tok0 + ntok;
+        uint32_t pidx, in_page;
+        a.page_div.divmod((uint32_t)(in ? tok : tok0), pidx, in_page);
+        const int32_t page = windowed ? window_page(pidx) : in ? entry((int)pidx) : -1;
+        const int64_t row = row_at(pidx, in_page, page, in);
+        const bool side_by_side = nhg == 1;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        const uint32_t box = (uint32_t)(HC * D) << sh, sbox = (uint32_t)(HC * 4) << sh;
+        if (lane == 0) mbar_expect_tx(bar, n * (box + (side_by_side ? sbox : 0u)));
+        __syncwarp();
+        if (row >= 0) {
+          tma_load_3d(smem_u32(dst) + lane * box, tm, 0, (int)row, hg * HC, bar);
+          if (side_by_side) bulk_g2s(sdst + lane * sbox, scale + row * a.num_kv_heads, sbox, bar);
         }
-        if constexpr (TMA) {
-          // boxes of R tokens inside one page: the one of tokens R i .. has the row of its first token
-          const int R = a.box_rows;
-          const int first = lane * R;
-          const int row = __shfl_sync(0xffffffffu, (int)slot, first & 31);
-          const bool mine = first < 32 && row >= 0;
-          const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-          const uint32_t box = (uint32_t)(HC * R * D);
-          if (lane == 0) mbar_expect_tx(bar, n * box);
-          __syncwarp();
-          if (mine) tma_load_3d(dst + (uint32_t)(32 / R * r + lane) * box, tm, 0, row, hg * HC, bar);
-        } else {
-          const uint32_t RB = (uint32_t)(HC * D);
-          const uint32_t n = __popc(__ballot_sync(0xffffffffu, slot >= 0));
-          if (lane == 0) mbar_expect_tx(bar, n * RB);
-          __syncwarp();
-          if (slot >= 0)
-            bulk_g2s(stages + (size_t)stage * a.stage_bytes + (v ? region : 0u) + (size_t)j * a.row_stride,
-                     pool + (slot * a.num_kv_heads + hg * HC) * D, RB, bar);
+        if (!side_by_side) {
+          for (int r = 0; r < W; ++r) {
+            const int j = lane + 32 * r;
+            const int first = __shfl_sync(0xffffffffu, (int)row, j >> sh);
+            if (j < ntok && first >= 0) copy_scales(first + (j & (a.box_rows - 1)), j);
+          }
         }
-        if (slot >= 0) {  // the token's HC scales
-          const float* src = scale + slot * a.num_kv_heads + hg * HC;
-          const uint32_t sd = sdst + (uint32_t)(j * HC) * 4;
-          if ((HC & 3) == 0) {
-            for (int i = 0; i < HC; i += 4) cp_async16(sd + 4 * i, src + i);
+      } else {
+        // One bulk copy per token row, or, for rows of 64 or 128 bytes, 16 bytes a lane: a bulk copy takes
+        // about 80 cycles to issue whatever it brings.  24 requests at page size 1, D 128: one KV head and 20000
+        // to 40000 positions 162 us so and 200 by bulk copies, two heads and half as many positions
+        // (rows of 256 bytes) 144 and 116.  Page indices that are not in the window are loaded four rounds
+        // ahead.
+        const uint32_t RB = (uint32_t)(HC * D);
+        const bool short_rows = RB <= 128;
+        const int csh = RB == 64 ? 2 : 3;  // log2 of the 16-byte chunks of a short row
+        auto ahead = [&](int r) -> int32_t {
+          const int j = lane + 32 * r;
+          return !windowed && j < ntok ? entry((int)a.page_div.quot((uint32_t)(tok0 + j))) : -1;
+        };
+        int32_t p0 = ahead(0), p1 = ahead(1), p2 = ahead(2), p3 = ahead(3);
+#pragma unroll 1
+        for (int r = 0; r < W; ++r) {
+          const int j = lane + 32 * r;
+          const bool in = j < ntok;
+          uint32_t pidx, in_page;
+          a.page_div.divmod((uint32_t)(tok0 + (in ? j : 0)), pidx, in_page);
+          int32_t page = p0;
+          if (windowed) page = window_page(pidx);
+          p0 = p1, p1 = p2, p2 = p3, p3 = ahead(r + 4);
+          const int64_t row = row_at(pidx, in_page, page, in);
+          if (short_rows) {
+            const uint32_t to = smem_u32(dst) + 32 * r * a.row_stride;
+#pragma unroll 1
+            for (int it = lane; it < 32 << csh; it += 32) {
+              const int tk = it >> csh, ch = it & ((1 << csh) - 1);
+              const int64_t from = __shfl_sync(0xffffffffu, row, tk);
+              if (from >= 0)
+                cp_async16(to + tk * a.row_stride + ch * 16, pool + (from * a.num_kv_heads + hg * HC) * D + ch * 16);
+            }
+            if (row >= 0) copy_scales(row, j);
           } else {
-            for (int i = 0; i < HC; ++i) cp_async4(sd + 4 * i, src + i);
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) mbar_expect_tx(bar, n * RB);
+            __syncwarp();
+            if (row >= 0) {
+              bulk_g2s(dst + (size_t)j * a.row_stride, pool + (row * a.num_kv_heads + hg * HC) * D, RB, bar);
+              copy_scales(row, j);
+            }
           }
         }
       }
@@ -333,16 +383,17 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
 // ---------------------------------------------------------------------------------------------
 // Consumer warps: 32-position steps of one KV head with its G query heads.
 // ---------------------------------------------------------------------------------------------
-template <int D, int NT, bool TMA>
+template <int D, bool TMA>
 __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
-                                 uint64_t* full, uint64_t* empty, float* mbuf) {
+                                 uint64_t* full, uint64_t* empty, uint64_t* meet_bar) {
   constexpr int NK = D / 16;                      // 16-byte chunks of a row: k-steps of K q, row tiles of O
-  constexpr int MF = NT * (6 + NK * 4);           // floats per lane merged between the warps of a head
+  constexpr int MF = 6 + NK * 4;                  // floats per lane merged between the warps of a head
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HC = a.HC, W = a.W, G = a.group, Ts = a.stage_tokens;
-  const int NC = HC * W;
-  const int hl = warp % HC;  // KV head within the CTA's group
-  const int si = warp / HC;  // slice within a stage
+  const int HV = HC * a.nt;
+  const int hv = warp % HV;
+  const int hl = hv / a.nt, head0 = hv % a.nt * 8;  // KV head within the CTA's group, first of its query heads here
+  const int si = warp / HV;                         // slice within a stage
   const int g = lane >> 2, c = lane & 3;
   const int NS = a.num_stages;
   const uint32_t region = a.kv_region;
@@ -367,14 +418,22 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
   }
   const uint32_t stages_u32 = smem_u32(stages);
 
-  uint32_t qf[NT][NK][2];
-  float qs[NT][2];            // score scale (log2 units) of the lane's heads 8 nt + 2c, + 1
-  float o[NK][NT][4];
-  float m[NT][2], l[NT][2];   // running maximum of x and sum of 2^(x - m)
-  float mw[NT][2];            // running maximum of x + e, which O is relative to
+  uint32_t qf[NK][2];
+  float qs[2];        // score scale (log2 units) of the lane's heads head0 + 2c, + 1
+  float o[NK][4];
+  float m[2], l[2];   // running maximum of x and sum of 2^(x - m)
+  float mw[2];        // running maximum of x + e, which O is relative to
 
   int stage = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, met_phase = 0;
+  // All consumer warps (a bounded wait, unlike a hardware barrier's).
+  auto meet = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet_bar);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(meet_bar, met_phase));
+    met_phase ^= 1;
+    return ok;
+  };
   while (true) {
     if (!__all_sync(0xffffffffu, mbar_wait(&hdr_full[stage], phase))) {
       if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
@@ -384,47 +443,44 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
     if (h.unit < 0) break;
 
     if (h.flags & kSegFirst) {
-      // q fragments: lane (g, c) holds dims 16 ks + 4c .. + 3 of head g of each n-tile
+      // q fragments: lane (g, c) holds dims 16 ks + 4c .. + 3 of head head0 + g
+      const int head = head0 + g;
+      const bool valid = head < G;
+      const __nv_bfloat16* qp =
+          a.q + ((int64_t)h.b * a.num_q_heads + (int64_t)(h.hg * HC + hl) * G + head) * D + 4 * c;
+      uint2 raw[NK];
+      uint32_t amax = 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int head = nt * 8 + g;
-        const bool valid = head < G;
-        const __nv_bfloat16* qp =
-            a.q + ((int64_t)h.b * a.num_q_heads + (int64_t)(h.hg * HC + hl) * G + head) * D + 4 * c;
-        uint2 raw[NK];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int ks = 0; ks < NK; ++ks) {
-          raw[ks] = valid ? __ldg(reinterpret_cast<const uint2*>(qp + ks * 16)) : make_uint2(0u, 0u);
-          amax = max(amax, max(max(finite_abs_bits(__uint_as_float(raw[ks].x << 16)),
-                                   finite_abs_bits(__uint_as_float(raw[ks].x & 0xffff0000u))),
-                               max(finite_abs_bits(__uint_as_float(raw[ks].y << 16)),
-                                   finite_abs_bits(__uint_as_float(raw[ks].y & 0xffff0000u)))));
-        }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^e <= amax < 2^(e+1); q 2^(14 - e) goes into f16 and 2^(e - 14) into the score scale.  e is
-        // held at -100 and above so that both factors are normal numbers.
-        const int e = max((int)(amax >> 23) - 127, -100);
-        const float up = exp2i(14 - e);
-        const float down = a.scale_log2 * exp2i(e - 14);
-#pragma unroll
-        for (int ks = 0; ks < NK; ++ks) {
-          qf[nt][ks][0] = pack_f16x2(__uint_as_float(raw[ks].x << 16) * up,
-                                     __uint_as_float(raw[ks].x & 0xffff0000u) * up);
-          qf[nt][ks][1] = pack_f16x2(__uint_as_float(raw[ks].y << 16) * up,
-                                     __uint_as_float(raw[ks].y & 0xffff0000u) * up);
-        }
-        // heads 2c and 2c + 1 of the tile live in lanes 8c and 8c + 4
-        qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-        qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
-        m[nt][0] = m[nt][1] = mw[nt][0] = mw[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int kc = 0; kc < NK; ++kc)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[kc][nt][i] = 0.f;
+      for (int ks = 0; ks < NK; ++ks) {
+        raw[ks] = valid ? __ldg(reinterpret_cast<const uint2*>(qp + ks * 16)) : make_uint2(0u, 0u);
+        amax = max(amax, max(max(finite_abs_bits(__uint_as_float(raw[ks].x << 16)),
+                                 finite_abs_bits(__uint_as_float(raw[ks].x & 0xffff0000u))),
+                             max(finite_abs_bits(__uint_as_float(raw[ks].y << 16)),
+                                 finite_abs_bits(__uint_as_float(raw[ks].y & 0xffff0000u)))));
       }
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^e <= amax < 2^(e+1); q 2^(14 - e) goes into f16 and 2^(e - 14) into the score scale.  e is
+      // held at -100 and above so that both factors are normal numbers.
+      const int e = max((int)(amax >> 23) - 127, -100);
+      const float up = exp2i(14 - e);
+      const float down = a.scale_log2 * exp2i(e - 14);
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        qf[ks][0] = pack_f16x2(__uint_as_float(raw[ks].x << 16) * up,
+                                   __uint_as_float(raw[ks].x & 0xffff0000u) * up);
+        qf[ks][1] = pack_f16x2(__uint_as_float(raw[ks].y << 16) * up,
+                                   __uint_as_float(raw[ks].y & 0xffff0000u) * up);
+      }
+      // heads 2c and 2c + 1 of the tile live in lanes 8c and 8c + 4
+      qs[0] = __shfl_sync(0xffffffffu, down, 8 * c);
+      qs[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+      m[0] = m[1] = mw[0] = mw[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int kc = 0; kc < NK; ++kc)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[kc][i] = 0.f;
     }
 
     if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
@@ -436,8 +492,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
     const uint32_t vb = kb + region;
     const float* sc = reinterpret_cast<const float*>(stages + (size_t)stage * a.stage_bytes + 2 * region) +
                       (si * kSlice + g) * HC + hl;  // K scales of tokens g, g + 8, ... of the slice; V's Ts rows on
-    constexpr int PR = NT == 1 ? 2 : 1;
-    float s[2][PR][NT][4];  // [half][chunk parity]: four independent accumulation chains
+    float s[2][2][4];  // [half][chunk parity]: four independent accumulation chains
     float ksc[4];
     if (nv > 0) {
 #pragma unroll
@@ -445,11 +500,9 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int pr = 0; pr < PR; ++pr)
+        for (int pr = 0; pr < 2; ++pr)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[hf][pr][nt][i] = 0.f;
+          for (int i = 0; i < 4; ++i) s[hf][pr][i] = 0.f;
 #pragma unroll
       for (int j = 0; j < NK / 2; ++j) {
 #pragma unroll
@@ -461,15 +514,15 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
             uint32_t a0, a1, a2, a3;
             unpack_e4m3x4(r[2 * pr], a0, a2);
             unpack_e4m3x4(r[2 * pr + 1], a1, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(s[hf][pr % PR][nt], a0, a1, a2, a3, qf[nt][2 * j + pr][0], qf[nt][2 * j + pr][1]);
+            mma_f16_16816(s[hf][pr], a0, a1, a2, a3, qf[2 * j + pr][0], qf[2 * j + pr][1]);
           }
         }
       }
     }
+    // A segment's last stage is held when warps share a head: its memory carries their merge.
+    const bool hold = (h.flags & kSegLast) && W > 1;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);  // K is read: its buffer is free while V is still in use
+    if (!hold && lane == 0) mbar_arrive(&empty[stage]);  // K is read: its buffer is free while V is still in use
     if (!__all_sync(0xffffffffu, mbar_wait(&full[NS + stage], phase))) {
       if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
       break;
@@ -498,58 +551,55 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
         ve[i] = (float)((int)(u >> 23) - 127);
         vm[i] = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
       }
-      uint32_t bp[2][NT][2];
+      uint32_t bp[2][2];
+      float x[2][4];
+      float mx[2] = {-INFINITY, -INFINITY}, mxe[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float x[2][4];
-        float mx[2] = {-INFINITY, -INFINITY}, mxe[2] = {-INFINITY, -INFINITY};
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 2 * hf + (i >> 1);  // token g + 8 row
-            const float v = (PR == 2 ? s[hf][0][nt][i] + s[hf][PR - 1][nt][i] : s[hf][0][nt][i]) * qs[nt][i & 1] * ksc[row];
-            x[hf][i] = g + 8 * row < nv ? v : -INFINITY;
-            mx[i & 1] = fmaxf(mx[i & 1], x[hf][i]);
-            mxe[i & 1] = fmaxf(mxe[i & 1], x[hf][i] + ve[row]);
-          }
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
-            mxe[k] = fmaxf(mxe[k], __shfl_xor_sync(0xffffffffu, mxe[k], off));
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int row = 2 * hf + (i >> 1);  // token g + 8 row
+          const float v = (s[hf][0][i] + s[hf][1][i]) * qs[i & 1] * ksc[row];
+          x[hf][i] = g + 8 * row < nv ? v : -INFINITY;
+          mx[i & 1] = fmaxf(mx[i & 1], x[hf][i]);
+          mxe[i & 1] = fmaxf(mxe[i & 1], x[hf][i] + ve[row]);
         }
-        float corr[2], corrw[2];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float mn = fmaxf(m[nt][k], mx[k]), wn = fmaxf(mw[nt][k], mxe[k]);
-          corr[k] = ex2(m[nt][k] - mn);
-          corrw[k] = ex2(mw[nt][k] - wn);
-          m[nt][k] = mn;
-          mw[nt][k] = wn;
-          l[nt][k] *= corr[k];
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
+          mxe[k] = fmaxf(mxe[k], __shfl_xor_sync(0xffffffffu, mxe[k], off));
         }
+      }
+      float corr[2], corrw[2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float w[4];
+      for (int k = 0; k < 2; ++k) {
+        const float mn = fmaxf(m[k], mx[k]), wn = fmaxf(mw[k], mxe[k]);
+        corr[k] = ex2(m[k] - mn);
+        corrw[k] = ex2(mw[k] - wn);
+        m[k] = mn;
+        mw[k] = wn;
+        l[k] *= corr[k];
+      }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 2 * hf + (i >> 1), k = i & 1;
-            l[nt][k] += ex2(x[hf][i] - m[nt][k]);
-            w[i] = ex2(x[hf][i] + ve[row] - mw[nt][k]) * vm[row];
-          }
-          bp[hf][nt][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
-          bp[hf][nt][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
+      for (int hf = 0; hf < 2; ++hf) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 2 * hf + (i >> 1), k = i & 1;
+          l[k] += ex2(x[hf][i] - m[k]);
+          w[i] = ex2(x[hf][i] + ve[row] - mw[k]) * vm[row];
         }
+        bp[hf][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
+        bp[hf][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
+      }
 #pragma unroll
-        for (int kc = 0; kc < NK; ++kc) {
-          o[kc][nt][0] *= corrw[0];
-          o[kc][nt][1] *= corrw[1];
-          o[kc][nt][2] *= corrw[0];
-          o[kc][nt][3] *= corrw[1];
-        }
+      for (int kc = 0; kc < NK; ++kc) {
+        o[kc][0] *= corrw[0];
+        o[kc][1] *= corrw[1];
+        o[kc][2] *= corrw[0];
+        o[kc][3] *= corrw[1];
       }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -562,92 +612,101 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
             uint32_t a0, a1, a2, a3;
             unpack_e4m3x4(__byte_perm(r[2 * pr], 0, 0x3120), a0, a1);
             unpack_e4m3x4(__byte_perm(r[2 * pr + 1], 0, 0x3120), a2, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(o[2 * j + pr][nt], a0, a1, a2, a3, bp[hf][nt][0], bp[hf][nt][1]);
+            mma_f16_16816(o[2 * j + pr], a0, a1, a2, a3, bp[hf][0], bp[hf][1]);
           }
         }
       }
     }
     if (nv > 0 && nv < kSlice) fence_proxy_async_smem();  // zeros above, before the next async fill
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[NS + stage]);
+    if (!hold && lane == 0) mbar_arrive(&empty[NS + stage]);
 
     if (h.flags & kSegLast) {
       if (W > 1) {
-        // combine the W warps that split this head's tokens (all consumer warps reach the segment
-        // end on the same stage); a warp without a token in it holds maxima of -inf and sums of 0
-        float* buf = mbuf + ((size_t)((si > 0 ? si - 1 : 0) * HC + hl) * MF) * 32 + lane;
-        if (si > 0) {
-          int e = 0;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+        // Combine the W warps that split this head's tokens (all consumer warps reach the segment end on
+        // the same stage).  A warp without a token in the segment holds
+        // maxima of -inf and sums of 0.
+        bool met = meet();
+        float* buf = reinterpret_cast<float*>(stages + (size_t)stage * a.stage_bytes) + lane;
+        // all but one at once where their states fit into the stage, else half of them at a time
+        for (int left = W; met && left > 1;) {
+          const int keep = (uint32_t)((left - 1) * HV * MF * 128) <= 2 * region ? 1 : left / 2;
+          if (si >= keep && si < left) {
+            float* to = buf + ((si - keep) * HV + hv) * MF * 32;
+            int e = 0;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              buf[(e++) * 32] = m[nt][k];
-              buf[(e++) * 32] = l[nt][k];
-              buf[(e++) * 32] = mw[nt][k];
+              to[(e++) * 32] = m[k];
+              to[(e++) * 32] = l[k];
+              to[(e++) * 32] = mw[k];
             }
 #pragma unroll
             for (int kc = 0; kc < NK; ++kc)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) buf[(e++) * 32] = o[kc][nt][i];
+              for (int i = 0; i < 4; ++i) to[(e++) * 32] = o[kc][i];
           }
-        }
-        named_bar_sync(1, NC * 32);
-        if (si == 0) {
-          for (int w = 1; w < W; ++w) {
-            const float* ob = mbuf + ((size_t)((w - 1) * HC + hl) * MF) * 32 + lane;
-            int e = 0;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+          met = meet();
+          if (!met) break;
+          if (si < keep) {
+            for (int w = si; w < left - keep; w += keep) {
+              const float* ob = buf + (w * HV + hv) * MF * 32;
+              auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
+              int e = 0;
               float fa[2], fb[2];
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {  // warp 0 of a segment has a token: its maxima are finite numbers or NaN
+              for (int k = 0; k < 2; ++k) {
                 const float om = ob[(e++) * 32], ol = ob[(e++) * 32], ow = ob[(e++) * 32];
-                const float mn = fmaxf(m[nt][k], om), wn = fmaxf(mw[nt][k], ow);
-                l[nt][k] = l[nt][k] * ex2(m[nt][k] - mn) + ol * ex2(om - mn);
-                fa[k] = ex2(mw[nt][k] - wn);
-                fb[k] = ex2(ow - wn);
-                m[nt][k] = mn;
-                mw[nt][k] = wn;
+                const float mn = fmaxf(m[k], om), wn = fmaxf(mw[k], ow);
+                l[k] = l[k] * weight(m[k], mn) + ol * weight(om, mn);
+                fa[k] = weight(mw[k], wn);
+                fb[k] = weight(ow, wn);
+                m[k] = mn;
+                mw[k] = wn;
               }
 #pragma unroll
               for (int kc = 0; kc < NK; ++kc)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[kc][nt][i] = o[kc][nt][i] * fa[i & 1] + ob[(e++) * 32] * fb[i & 1];
+                for (int i = 0; i < 4; ++i) o[kc][i] = o[kc][i] * fa[i & 1] + ob[(e++) * 32] * fb[i & 1];
             }
           }
+          left = keep;
+          if (left > 1) met = meet();  // read before the next writes
         }
-        named_bar_sync(1, NC * 32);
+        if (!met) {
+          if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+          break;
+        }
+        fence_proxy_async_smem();  // the merge's accesses, before the next async fill
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&empty[stage]);
+          mbar_arrive(&empty[NS + stage]);
+        }
       }
       if (si == 0) {
         const bool whole = (h.flags & kStartsUnit) && (h.flags & kEndsUnit);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int k = 0; k < 2; ++k) {
+          float lt = l[k];
+          lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+          lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+          lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+          const int col = head0 + 2 * c + k;  // query head within the group
+          const float inv = ex2(mw[k] - m[k]) / lt;
+          const float lse_v = (m[k] + log2f(lt)) * kLn2;
+          if (col < G) {
+            const int qhl = hl * G + col;
+            if (whole) {
+              const int64_t qh = (int64_t)h.hg * HQU + qhl;
+              uint32_t* op = reinterpret_cast<uint32_t*>(a.out + ((int64_t)h.b * a.num_q_heads + qh) * D) + g;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float lt = l[nt][k];
-            lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-            lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-            lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-            const int col = nt * 8 + 2 * c + k;  // query head within the group
-            const float inv = ex2(mw[nt][k] - m[nt][k]) / lt;
-            const float lse_v = (m[nt][k] + log2f(lt)) * kLn2;
-            if (col < G) {
-              const int qhl = hl * G + col;
-              if (whole) {
-                const int64_t qh = (int64_t)h.hg * HQU + qhl;
-                uint32_t* op = reinterpret_cast<uint32_t*>(a.out + ((int64_t)h.b * a.num_q_heads + qh) * D) + g;
+              for (int kc = 0; kc < NK; ++kc) op[8 * kc] = pack_bf16x2(o[kc][k] * inv, o[kc][2 + k] * inv);
+              if (g == 0 && a.lse) a.lse[(int64_t)h.b * a.num_q_heads + qh] = lse_v;
+            } else {
+              float2* pp = reinterpret_cast<float2*>(a.part_o + ((int64_t)h.part * HQU + qhl) * D) + g;
 #pragma unroll
-                for (int kc = 0; kc < NK; ++kc) op[8 * kc] = pack_bf16x2(o[kc][nt][k] * inv, o[kc][nt][2 + k] * inv);
-                if (g == 0 && a.lse) a.lse[(int64_t)h.b * a.num_q_heads + qh] = lse_v;
-              } else {
-                float2* pp = reinterpret_cast<float2*>(a.part_o + ((int64_t)h.part * HQU + qhl) * D) + g;
-#pragma unroll
-                for (int kc = 0; kc < NK; ++kc) pp[8 * kc] = make_float2(o[kc][nt][k] * inv, o[kc][nt][2 + k] * inv);
-                if (g == 0) a.part_lse[(int64_t)h.part * HQU + qhl] = lse_v;
-              }
+              for (int kc = 0; kc < NK; ++kc) pp[8 * kc] = make_float2(o[kc][k] * inv, o[kc][2 + k] * inv);
+              if (g == 0) a.part_lse[(int64_t)h.part * HQU + qhl] = lse_v;
             }
           }
         }
@@ -664,11 +723,11 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
   }
 }
 
-template <int D, int NT, bool TMA>
+template <int D, bool TMA>
 __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_constant__ Decode8Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int NS = a.num_stages;
-  const int NC = a.HC * a.W;
+  const int NC = a.HC * a.nt * a.W;
   if (TMA && (smem_u32(smem) & 1023u)) {  // the swizzled stage layout needs a 1024-byte base
     if (threadIdx.x == 0) report(a.err_word, PKV_DEVERR_INTERNAL);
     return;
@@ -678,10 +737,11 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
   uint64_t* hdr_full = reinterpret_cast<uint64_t*>(hdr + NS);
   uint64_t* full = hdr_full + NS;
   uint64_t* empty = full + 2 * NS;  // K's barriers, then V's
-  float* mbuf = reinterpret_cast<float*>(empty + 2 * NS);
+  uint64_t* meet_bar = empty + 2 * NS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) mbar_init(&hdr_full[s], 1);
+    mbar_init(meet_bar, NC);
     for (int s = 0; s < 2 * NS; ++s) {
       mbar_init(&full[s], 1 + 32);  // a producer's go-ahead, and every lane's scale copies
       mbar_init(&empty[s], NC);
@@ -702,7 +762,7 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
   } else if (warp == NC + 1) {
     decode8_producer<D, TMA>(a, stages, hdr, hdr_full, full + NS, empty + NS, true);
   } else if (warp < NC) {
-    decode8_consumer<D, NT, TMA>(a, stages, hdr, hdr_full, full, empty, mbuf);
+    decode8_consumer<D, TMA>(a, stages, hdr, hdr_full, full, empty, meet_bar);
   }
 }
 
@@ -820,10 +880,10 @@ bool make_plan(int B, int Hq, int Hkv, int D, int ncta, Plan& p, int page_size =
   if (p.G > 16) return false;
   p.NT = (p.G + 7) / 8;
   p.HC = 1;
-  for (int d = 1; d <= 8; ++d)
+  for (int d = 1; d <= 8 / p.NT; ++d)
     if (Hkv % d == 0) p.HC = d;
   p.nhg = Hkv / p.HC;
-  p.W = 8 / p.HC;
+  p.W = 8 / (p.HC * p.NT);
   p.Ts = kSlice * p.W;
   const int RB = p.HC * D;
   p.RS = RB + 16;  // RB is a multiple of 64: rows 16 bytes off a multiple of 32 keep ldmatrix free of conflicts
@@ -831,13 +891,14 @@ bool make_plan(int B, int Hq, int Hkv, int D, int ncta, Plan& p, int page_size =
   p.tma = page_size > 0 && page_size % 8 == 0 && num_pages * (int64_t)page_size < 0x7fffffffLL;
   p.region = p.tma ? (uint32_t)(p.Ts * RB) : (uint32_t)(p.Ts * p.RS);
   p.stage = (2 * p.region + (uint32_t)(2 * p.Ts * p.HC * 4) + 1023u) & ~1023u;
-  const int mf = p.NT * (6 + (D / 16) * 4);
-  const size_t mbytes = p.W > 1 ? (size_t)(p.W - 1) * p.HC * mf * 32 * 4 : 0;
-  const size_t fixed = mbytes + (size_t)kMaxStages * (sizeof(StageHdr) + 40);
-  if (fixed + 2 * (size_t)p.stage > kSmemBudget) return false;
-  p.NS = (int)((kSmemBudget - fixed) / p.stage);
+  // the merge of a head's warps must fit into the stage that carries it
+  const size_t merge = (size_t)(p.W / 2) * p.HC * p.NT * (6 + (D / 16) * 4) * 32 * 4;
+  if (merge > 2 * (size_t)p.region) return false;
+  const size_t per_stage = p.stage + sizeof(StageHdr) + 40;
+  if (2 * per_stage + 8 > kSmemBudget) return false;
+  p.NS = (int)((kSmemBudget - 8) / per_stage);
   if (p.NS > kMaxStages) p.NS = kMaxStages;
-  p.smem = (size_t)p.NS * p.stage + (size_t)p.NS * (sizeof(StageHdr) + 40) + mbytes;
+  p.smem = (size_t)p.NS * per_stage + 8;
   p.ncta = ncta;
   p.nunits = (int64_t)B * p.nhg;
   p.nparts = p.ncta + p.nunits;
@@ -850,9 +911,9 @@ bool make_plan(int B, int Hq, int Hkv, int D, int ncta, Plan& p, int page_size =
   return true;
 }
 
-template <int D, int NT, bool TMA>
+template <int D, bool TMA>
 pkv_status launch(const Plan& p, const Decode8Args& a, cudaStream_t st) {
-  auto kern = paged_decode8_kernel<D, NT, TMA>;
+  auto kern = paged_decode8_kernel<D, TMA>;
   // whether this instance's dynamic shared-memory limit was raised on this device (any host thread)
   static std::atomic<bool> configured[64];
   const int dev = pkv_host::current_device();
@@ -862,7 +923,7 @@ pkv_status launch(const Plan& p, const Decode8Args& a, cudaStream_t st) {
       return PKV_ERR_CUDA;
     if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
   }
-  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.W + 2) * 32, p.smem, st, a);
+  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2) * 32, p.smem, st, a);
   if (s != PKV_OK) return s;
   return pkv_host::launch_after(decode8_merge_kernel<D>, dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8)), 256, 0,
                                 st, a);
@@ -933,6 +994,7 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
   a.nhg = p.nhg;
   a.W = p.W;
   a.group = p.G;
+  a.nt = p.NT;
   a.box_rows = p.R;
   a.row_stride = p.RS;
   a.stage_tokens = p.Ts;
@@ -948,12 +1010,8 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
       return PKV_ERR_CUDA;
   }
   cudaStream_t st = (cudaStream_t)stream;
-  if (p.tma) {
-    if (D == 128) return p.NT == 1 ? launch<128, 1, true>(p, a, st) : launch<128, 2, true>(p, a, st);
-    return p.NT == 1 ? launch<64, 1, true>(p, a, st) : launch<64, 2, true>(p, a, st);
-  }
-  if (D == 128) return p.NT == 1 ? launch<128, 1, false>(p, a, st) : launch<128, 2, false>(p, a, st);
-  return p.NT == 1 ? launch<64, 1, false>(p, a, st) : launch<64, 2, false>(p, a, st);
+  if (p.tma) return D == 128 ? launch<128, true>(p, a, st) : launch<64, true>(p, a, st);
+  return D == 128 ? launch<128, false>(p, a, st) : launch<64, false>(p, a, st);
 }
 
 }  // extern "C"
