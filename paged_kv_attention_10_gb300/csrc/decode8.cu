@@ -25,7 +25,7 @@
 //  * A warp takes 32 positions of one KV head at a time (the bf16 decode: 16), so the shuffles of
 //    the maxima, the rescaling of O and the barrier round are paid half as often.
 //  * The rest is the bf16 decode's plan: one persistent CTA per SM over an equal share of the stream
-//    of slices, TMA boxes of 16 or 8 rows (page sizes that are multiples of 8) in the 128- or 64-byte
+//    of slices, TMA boxes of 32, 16 or 8 rows (the largest that divides the page size) in the 128- or 64-byte
 //    swizzle, one bulk copy per row otherwise; the scales come by cp.async into the same stage.
 #include <atomic>
 
@@ -74,7 +74,7 @@ struct Decode8Args {
   int32_t W;             // consumer warps per KV head
   int32_t group;         // query heads per KV head
   int32_t nt;            // warps that share a KV head's rows, eight of its query heads each
-  int32_t box_rows;      // TMA instance: rows of a box (16 or 8)
+  int32_t box_rows;      // TMA instance: rows of a box (32, 16 or 8)
   int32_t row_stride;    // row-copy instance: shared-memory bytes per token row
   int32_t stage_tokens;  // 32 * W
   int32_t num_stages, num_parts;
@@ -235,7 +235,7 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
         // Lane i fetches box i, box_rows tokens inside one page, and their scales, which lie side by side when
         // the CTA takes all KV heads.  (One lookup a stage: with one per 32 tokens the eight of a stage of
         // one KV head took 4 us, and 720000 positions of it 96 us; 48 now, of the 28 that their bytes take.)
-        const int sh = a.box_rows == 16 ? 4 : 3, nbox = Ts >> sh;
+        const int sh = 31 - __clz(a.box_rows), nbox = Ts >> sh;
         const int tok = tok0 + (lane << sh);
         const bool in = lane < nbox && tok < tok0 + ntok;
         uint32_t pidx, in_page;
@@ -887,7 +887,7 @@ bool make_plan(int B, int Hq, int Hkv, int D, int ncta, Plan& p, int page_size =
   p.Ts = kSlice * p.W;
   const int RB = p.HC * D;
   p.RS = RB + 16;  // RB is a multiple of 64: rows 16 bytes off a multiple of 32 keep ldmatrix free of conflicts
-  p.R = page_size % 16 == 0 ? 16 : 8;
+  p.R = page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 8;
   p.tma = page_size > 0 && page_size % 8 == 0 && num_pages * (int64_t)page_size < 0x7fffffffLL;
   p.region = p.tma ? (uint32_t)(p.Ts * RB) : (uint32_t)(p.Ts * p.RS);
   p.stage = (2 * p.region + (uint32_t)(2 * p.Ts * p.HC * 4) + 1023u) & ~1023u;
