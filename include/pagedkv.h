@@ -554,7 +554,8 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
  *   err_word   nullable; PKV_DEVERR_LENGTH, PKV_DEVERR_PAGE_OOB, PKV_DEVERR_ROW_OOB (a request whose rows
  *              lie outside q is skipped)
  * What a drafted token's K and V hold does not reach rows that do not see it, infinities and NaNs
- * included.  head_dim 64 or 128, any page_size, num_q_heads / num_kv_heads from 1 to 16.
+ * included.  An infinity in the V of a cached position, which every row sees, makes that dimension an
+ * infinity or a NaN.  head_dim 64 or 128, any page_size, num_q_heads / num_kv_heads from 1 to 16.
  */
 size_t pkv_tree_workspace_size(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
                                int32_t head_dim, int32_t max_tree_len);
@@ -571,7 +572,8 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
  * index within request b's tree of token t's parent, -1 (or any negative) for a root; a parent comes
  * before its children.  Row i of tree_mask receives the bits of i and its ancestors.  A parent that
  * does not come before its child ends that row's walk and reports PKV_DEVERR_LENGTH, as does a request of
- * more than 32 * mask_words tokens (whose rows past that are left unwritten).
+ * more than max_tree_len tokens (whose rows past that are left unwritten).  max_tree_len <= 32 * mask_words,
+ * at most 1024.
  */
 pkv_status pkv_tree_mask_from_parents(const int32_t* parents, const int32_t* qo_indptr, int32_t batch_size,
                                       int32_t num_tokens, int32_t max_tree_len, int32_t mask_words,

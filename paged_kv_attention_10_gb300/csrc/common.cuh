@@ -216,8 +216,15 @@ PKV_DEV void named_bar_sync(int id, int nthreads) {
 // before it on the stream still runs, if that one has called pdl_trigger in every block (or ended
 // them); it must call pdl_wait before its first access to global memory, which returns when that
 // kernel has completed and its writes are visible.  Start-up then overlaps the kernel before it.
+// Such a kernel reads global memory with ld, never through the non-coherent path (__ldg, const
+// __restrict__): that one is for what nobody writes while the kernel lives, and the compiler may move
+// its loads above the wait; a kernel lives from its early start on, while others still write.
 PKV_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 PKV_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename T>
+PKV_DEV T ld(const T* p) {
+  return *p;
+}
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;

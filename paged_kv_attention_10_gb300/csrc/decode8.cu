@@ -137,14 +137,14 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
 
   // the first 32 requests' numbers in one round of loads, which the walk below starts with
   const bool in0 = lane < a.batch;
-  const int32_t first_len = in0 ? min(max(0, __ldg(a.kv_lens + lane)), kMaxLen) : 0;
-  const int32_t first_p0 = in0 ? __ldg(a.kv_indptr + lane) : 0;
-  const int32_t first_p1 = in0 ? __ldg(a.kv_indptr + lane + 1) : 0;
+  const int32_t first_len = in0 ? min(max(0, ld(a.kv_lens + lane)), kMaxLen) : 0;
+  const int32_t first_p0 = in0 ? ld(a.kv_indptr + lane) : 0;
+  const int32_t first_p1 = in0 ? ld(a.kv_indptr + lane + 1) : 0;
   int64_t sumS = ((int64_t)first_len + kSlice - 1) / kSlice;  // slices over all requests
   for (int i = 32 + lane; i < a.batch; i += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)  // four loads in flight
-      if (i + 32 * u < a.batch) sumS += (min(max(0, __ldg(a.kv_lens + i + 32 * u)), kMaxLen) + kSlice - 1) / kSlice;
+      if (i + 32 * u < a.batch) sumS += (min(max(0, ld(a.kv_lens + i + 32 * u)), kMaxLen) + kSlice - 1) / kSlice;
   }
   sumS = warp_sum(sumS);
   const int64_t T = sumS * nhg;
@@ -160,7 +160,7 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
   int win_b = -1, wbase = 0;
   int32_t w0 = -1, w1 = -1, w2 = -1;
   auto entry = [&](int pidx) -> int32_t {  // page-list entry of the current request; -1 past its end
-    return pidx < cur_np ? __ldg(a.kv_indices + cur_p0 + pidx) : -1;
+    return pidx < cur_np ? ld(a.kv_indices + cur_p0 + pidx) : -1;
   };
   int nissued = 0;
   auto next_stage = [&]() {
@@ -321,9 +321,9 @@ __device__ void decode8_producer(const Decode8Args& a, uint8_t* stages, StageHdr
       int64_t L = first_len;
       int32_t ip0 = first_p0, ip1 = first_p1;
       if (b0 > 0) {
-        L = in ? min(max(0, __ldg(a.kv_lens + b)), kMaxLen) : 0;
-        ip0 = in ? __ldg(a.kv_indptr + b) : 0;
-        ip1 = in ? __ldg(a.kv_indptr + b + 1) : 0;
+        L = in ? min(max(0, ld(a.kv_lens + b)), kMaxLen) : 0;
+        ip0 = in ? ld(a.kv_indptr + b) : 0;
+        ip1 = in ? ld(a.kv_indptr + b + 1) : 0;
       }
       const int64_t S = (L + kSlice - 1) / kSlice;
       int64_t incl = S;
@@ -452,7 +452,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
       uint32_t amax = 0;
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
-        raw[ks] = valid ? __ldg(reinterpret_cast<const uint2*>(qp + ks * 16)) : make_uint2(0u, 0u);
+        raw[ks] = valid ? ld(reinterpret_cast<const uint2*>(qp + ks * 16)) : make_uint2(0u, 0u);
         amax = max(amax, max(max(finite_abs_bits(__uint_as_float(raw[ks].x << 16)),
                                  finite_abs_bits(__uint_as_float(raw[ks].x & 0xffff0000u))),
                              max(finite_abs_bits(__uint_as_float(raw[ks].y << 16)),
@@ -729,7 +729,10 @@ __global__ void __launch_bounds__(320, 1) paged_decode8_kernel(const __grid_cons
   const int NS = a.num_stages;
   const int NC = a.HC * a.nt * a.W;
   if (TMA && (smem_u32(smem) & 1023u)) {  // the swizzled stage layout needs a 1024-byte base
-    if (threadIdx.x == 0) report(a.err_word, PKV_DEVERR_INTERNAL);
+    if (threadIdx.x == 0) {
+      pdl_wait();
+      report(a.err_word, PKV_DEVERR_INTERNAL);
+    }
     return;
   }
   uint8_t* stages = smem;
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(256) decode8_merge_kernel(const __grid_constan
     else
       *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(v[0], v[1]);
   };
-  if (__ldg(a.kv_lens + b) <= 0) {
+  if (ld(a.kv_lens + b) <= 0) {
     if (blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, PKV_DEVERR_LENGTH);
     const float zero[VPL] = {};
     store(zero);
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(256) decode8_merge_kernel(const __grid_constan
   float acc[VPL] = {};
   for (int base = first; base <= last; base += 32) {
     const int n = min(32, last - base + 1);
-    const float pl = lane < n ? __ldg(plse + (int64_t)(base + lane) * HQU) : -INFINITY;
+    const float pl = lane < n ? ld(plse + (int64_t)(base + lane) * HQU) : -INFINITY;
     float x[16][VPL];
     auto load = [&](int i0) {
 #pragma unroll
@@ -818,9 +821,9 @@ __global__ void __launch_bounds__(256) decode8_merge_kernel(const __grid_constan
         const float* src = po + (int64_t)(base + i0 + k) * HQU * D;
         if (i0 + k < n) {
           if constexpr (VPL == 4)
-            *reinterpret_cast<float4*>(x[k]) = __ldg(reinterpret_cast<const float4*>(src));
+            *reinterpret_cast<float4*>(x[k]) = ld(reinterpret_cast<const float4*>(src));
           else
-            *reinterpret_cast<float2*>(x[k]) = __ldg(reinterpret_cast<const float2*>(src));
+            *reinterpret_cast<float2*>(x[k]) = ld(reinterpret_cast<const float2*>(src));
         } else {
 #pragma unroll
           for (int v = 0; v < VPL; ++v) x[k][v] = 0.f;

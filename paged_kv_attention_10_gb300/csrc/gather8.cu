@@ -47,22 +47,22 @@ PKV_DEV uint4 dequant8(uint2 u, float s) {
 // Slot of output row `row`, or -1: a row of no request, behind its request's end, or of a bad page.
 PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
   int lo = 0, hi = a.batch;  // the last b in [0, batch] with out_indptr[b] <= row
-  if (row < __ldg(a.out_indptr)) return -1;
+  if (row < ld(a.out_indptr)) return -1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.out_indptr + mid) <= row) lo = mid;
+    if (ld(a.out_indptr + mid) <= row) lo = mid;
     else hi = mid - 1;
   }
   if (lo == a.batch) return -1;
-  const int32_t j = row - __ldg(a.out_indptr + lo);
-  if (j < 0 || j >= __ldg(a.kv_lens + lo)) return -1;
-  const int32_t p0 = __ldg(a.kv_indptr + lo), np = __ldg(a.kv_indptr + lo + 1) - p0;
+  const int32_t j = row - ld(a.out_indptr + lo);
+  if (j < 0 || j >= ld(a.kv_lens + lo)) return -1;
+  const int32_t p0 = ld(a.kv_indptr + lo), np = ld(a.kv_indptr + lo + 1) - p0;
   const int32_t pidx = j / a.page_size;
   if (pidx >= np) {
     report(a.err_word, PKV_DEVERR_LENGTH);
     return -1;
   }
-  const int32_t page = __ldg(a.kv_indices + p0 + pidx);
+  const int32_t page = ld(a.kv_indices + p0 + pidx);
   if (page < 0 || page >= a.num_pages) {
     report(a.err_word, PKV_DEVERR_PAGE_OOB);
     return -1;
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kThreads) paged_gather8_kernel(const __grid_co
   pdl_wait();
   // what the copies below cannot see: a request whose rows do not hold its length, or lie outside out
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.batch; b += gridDim.x * kThreads) {
-    const int64_t o0 = __ldg(a.out_indptr + b), o1 = __ldg(a.out_indptr + b + 1);
-    const int32_t n = __ldg(a.kv_lens + b);
+    const int64_t o0 = ld(a.out_indptr + b), o1 = ld(a.out_indptr + b + 1);
+    const int32_t n = ld(a.kv_lens + b);
     if (n < 0 || n > o1 - o0) report(a.err_word, PKV_DEVERR_LENGTH);
     if (n > 0 && (o0 < 0 || o0 + n > a.num_out_rows)) report(a.err_word, PKV_DEVERR_ROW_OOB);
   }
@@ -105,11 +105,11 @@ __global__ void __launch_bounds__(kThreads) paged_gather8_kernel(const __grid_co
         on[u] = i < n && slot >= 0;
         if (on[u]) {
           const int64_t src = slot * cpr + c;
-          k[u] = __ldg(k8 + src);
-          v[u] = __ldg(v8 + src);
+          k[u] = ld(k8 + src);
+          v[u] = ld(v8 + src);
           const int64_t hs = slot * a.Hkv + a.cph.quot(c);
-          ks[u] = __ldg(a.k_scale + hs);
-          vs[u] = __ldg(a.v_scale + hs);
+          ks[u] = ld(a.k_scale + hs);
+          vs[u] = ld(a.v_scale + hs);
         }
       }
 #pragma unroll

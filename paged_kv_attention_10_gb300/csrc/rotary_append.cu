@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
   const int c1 = paired ? u + hc : c0 + 1;
   const bool has0 = 8 * c0 < a.D, has1 = 8 * c1 < a.D;
 
-  const int64_t slot = __ldg(a.slots + t);
-  const int pos = ROT != kNone ? __ldg(a.positions + t) : 0;
+  const int64_t slot = ld(a.slots + t);
+  const int pos = ROT != kNone ? ld(a.positions + t) : 0;
   uint4 v0[kSteps], v1[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
@@ -155,11 +155,11 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
     const int p = ROT == kHalf ? 8 * c0 : 4 * c0;
     const bool lo = ROT == kHalf ? paired : 8 * c0 < a.R, hi = ROT == kHalf ? paired : 8 * c1 < a.R;
     float4 z = make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 ca = lo ? __ldg(reinterpret_cast<const float4*>(cs + p)) : z;
-    const float4 cb = hi ? __ldg(reinterpret_cast<const float4*>(cs + p + 4)) : z;
+    const float4 ca = lo ? ld(reinterpret_cast<const float4*>(cs + p)) : z;
+    const float4 cb = hi ? ld(reinterpret_cast<const float4*>(cs + p + 4)) : z;
     z = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 sa = lo ? __ldg(reinterpret_cast<const float4*>(cs + a.R / 2 + p)) : z;
-    const float4 sb = hi ? __ldg(reinterpret_cast<const float4*>(cs + a.R / 2 + p + 4)) : z;
+    const float4 sa = lo ? ld(reinterpret_cast<const float4*>(cs + a.R / 2 + p)) : z;
+    const float4 sb = hi ? ld(reinterpret_cast<const float4*>(cs + a.R / 2 + p + 4)) : z;
     co[0] = ca.x, co[1] = ca.y, co[2] = ca.z, co[3] = ca.w, co[4] = cb.x, co[5] = cb.y, co[6] = cb.z, co[7] = cb.w;
     si[0] = sa.x, si[1] = sa.y, si[2] = sa.z, si[3] = sa.w, si[4] = sb.x, si[5] = sb.y, si[6] = sb.z, si[7] = sb.w;
   }
@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_cons
   const bool is_q = r.kind == 2, reporter = h == 0 && c == 0;
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (has) v = reinterpret_cast<const uint4*>(r.src)[c];
-  const int pos = __ldg(a.positions + t);
+  const int pos = ld(a.positions + t);
   if (!position_ok(a, pos, reporter)) return;
-  const int64_t slot = __ldg(a.slots + t);
+  const int64_t slot = ld(a.slots + t);
   const bool cached = slot_ok(a, slot, reporter);
   if (!is_q && !cached) return;
   float x[8];
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_cons
         const int i = a.interleaved ? j >> 1 : (j < half ? j : j - half);
         const bool first = a.interleaved ? !(j & 1) : j < half;
         const float y = __bfloat162float(r.src[a.interleaved ? j ^ 1 : (first ? j + half : j - half)]);
-        x[e] = fmaf(x[e], __ldg(cs + i), (first ? -y : y) * __ldg(cs + half + i));
+        x[e] = fmaf(x[e], ld(cs + i), (first ? -y : y) * ld(cs + half + i));
       }
     }
   }

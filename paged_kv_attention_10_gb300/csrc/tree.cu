@@ -197,7 +197,7 @@ struct Producer {
     const int R = a.box_rows, nbox = kBN / R, kv_end = s.P + s.T;
     const int box = lane % nbox, half = lane / nbox;  // lane issues one half of one box
     auto entry = [&](int pidx) -> int32_t {
-      return (pidx >= 0 && pidx < s.np) ? __ldg(a.kv_indices + s.p0 + pidx) : -1;
+      return (pidx >= 0 && pidx < s.np) ? ld(a.kv_indices + s.p0 + pidx) : -1;
     };
     int wbase = (int)a.page_div.quot((uint32_t)(s.j0 * kBN));
     int32_t w0 = entry(wbase + lane), w1 = entry(wbase + 32 + lane);
@@ -244,7 +244,7 @@ struct Producer {
         uint32_t pidx;
         a.page_div.divmod((uint32_t)min(j * kBN + 4 * lane + i, kv_end - 1), pidx, in_page[i]);
         listed[i] = (int)pidx < s.np;
-        page[i] = listed[i] ? __ldg(a.kv_indices + s.p0 + pidx) : 0;
+        page[i] = listed[i] ? ld(a.kv_indices + s.p0 + pidx) : 0;
       }
     };
     load_pages(s.j0);
@@ -291,11 +291,11 @@ struct Req {
 
 __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   Req r;
-  r.q0 = __ldg(a.qo_indptr + b);
-  const int32_t rows = __ldg(a.qo_indptr + b + 1) - r.q0;
-  r.P = __ldg(a.prefix_lens + b);
-  r.p0 = __ldg(a.kv_indptr + b);
-  r.np = __ldg(a.kv_indptr + b + 1) - r.p0;
+  r.q0 = ld(a.qo_indptr + b);
+  const int32_t rows = ld(a.qo_indptr + b + 1) - r.q0;
+  r.P = ld(a.prefix_lens + b);
+  r.p0 = ld(a.kv_indptr + b);
+  r.np = ld(a.kv_indptr + b + 1) - r.p0;
   r.T = min(max(rows, 0), a.max_nodes);
   r.pairs = r.tiles = r.cost = 0;
   uint32_t bad = 0;
@@ -611,7 +611,7 @@ struct MaskRow {
 
 PKV_DEV void load_mask(MaskRow& k) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) k.w[i] = k.m && i < k.words ? __ldg(k.m + i) : 0u;
+  for (int i = 0; i < 4; ++i) k.w[i] = k.m && i < k.words ? ld(k.m + i) : 0u;
 }
 
 // Which of the 32 positions of drafted-token offsets t0 .. t0 + 31 (t0 may be negative: the prefix)
@@ -622,7 +622,7 @@ PKV_DEV uint32_t visible(const MaskRow& k, int T, int t0) {
   auto word = [&](int i) -> uint32_t {
     if (i < 0) return 0xffffffffu;
     if (i < 4) return i < 2 ? (i == 0 ? k.w[0] : k.w[1]) : (i == 2 ? k.w[2] : k.w[3]);
-    return k.m && i < k.words ? __ldg(k.m + i) : 0u;
+    return k.m && i < k.words ? ld(k.m + i) : 0u;
   };
   const int w = t0 >> 5, sh = t0 & 31;
   uint32_t v = __funnelshift_r(word(w), sh ? word(w + 1) : 0u, sh);
@@ -636,13 +636,13 @@ template <int D, typename T>
 __device__ __noinline__ void add_nonfinite(const TreeArgs& a, const Ctl* ctl, int P, int nodes, int p0, int np, int h,
                                            const uint32_t* m, int d0, int n, T* to) {
   for (int w = 0; w < (nodes + 31) / 32; ++w) {
-    uint32_t hit = ctl->bad[w] & (w < a.words ? __ldg(m + w) : 0u);
+    uint32_t hit = ctl->bad[w] & (w < a.words ? ld(m + w) : 0u);
     while (hit) {
       const int t = 32 * w + __ffs(hit) - 1;
       hit &= hit - 1;
       const int pos = P + t, pidx = pos / a.page_size;
       if (pidx >= np) continue;
-      const int32_t page = __ldg(a.kv_indices + p0 + pidx);
+      const int32_t page = ld(a.kv_indices + p0 + pidx);
       if (page < 0 || page >= a.num_pages) continue;
       const __nv_bfloat16* src =
           a.v_pool + (((int64_t)page * a.page_size + pos % a.page_size) * a.num_kv_heads + h) * D + d0;
@@ -1138,10 +1138,10 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     for (int k = 0; k < 4; ++k) {
       const bool on = p0 + k < cut.parts;
       const int64_t at = slot(on ? p0 + k : p0);
-      pl[k] = on ? __ldg(a.part_lse + at * a.part_rows + prow) : -INFINITY;
+      pl[k] = on ? ld(a.part_lse + at * a.part_rows + prow) : -INFINITY;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
-        x[k][i] = __ldg(reinterpret_cast<const float4*>(a.part_o) + (at * (D / 4) + warp + 8 * i) * a.part_rows + prow);
+        x[k][i] = ld(reinterpret_cast<const float4*>(a.part_o) + (at * (D / 4) + warp + 8 * i) * a.part_rows + prow);
     }
     const float mn = fmaxf(fmaxf(fmaxf(pl[0], pl[1]), fmaxf(pl[2], pl[3])), mx);
     if (mn > mx) {  // (not while every part so far is empty)
@@ -1179,16 +1179,15 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------------------------
 // The mask of a tree given by parents: row i has the bits of i and its ancestors.
 // ---------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restrict__ parents,
-                                                        const int32_t* __restrict__ qo_indptr,
-                                                        int32_t num_tokens, int32_t words,
-                                                        uint32_t* __restrict__ mask, uint32_t* err_word) {
+__global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* parents, const int32_t* qo_indptr,
+                                                        int32_t num_tokens, int32_t max_nodes, int32_t words,
+                                                        uint32_t* mask, uint32_t* err_word) {
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.y;
-  const int32_t q0 = __ldg(qo_indptr + b), rows = __ldg(qo_indptr + b + 1) - q0;
+  const int32_t q0 = ld(qo_indptr + b), rows = ld(qo_indptr + b + 1) - q0;
   const bool first = blockIdx.x == 0 && threadIdx.x == 0;
-  if (rows < 0 || rows > 32 * words) {
+  if (rows < 0 || rows > max_nodes) {
     if (first) report(err_word, PKV_DEVERR_LENGTH);
     if (rows < 0) return;
   }
@@ -1197,14 +1196,14 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restric
     return;
   }
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
-  if (t >= rows || t >= 32 * words) return;
+  if (t >= rows || t >= max_nodes) return;
   uint32_t* row = mask + (int64_t)(q0 + t) * words;
   int cur = t;  // strictly falling, so the walk ends
   for (int w = words - 1; w >= 0; --w) {
     uint32_t bits = 0;
     while (cur >= 0 && (cur >> 5) == w) {
       bits |= 1u << (cur & 31);
-      const int p = __ldg(parents + q0 + cur);
+      const int p = ld(parents + q0 + cur);
       if (p >= cur) {  // a parent comes before its children
         report(err_word, PKV_DEVERR_LENGTH);
         cur = -1;
@@ -1353,7 +1352,7 @@ pkv_status pkv_tree_mask_from_parents(const int32_t* parents, const int32_t* qo_
   if (batch_size > 65535 || max_tree_len > kMaxNodes) return PKV_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)((max_tree_len + 127) / 128), (unsigned)batch_size, 1);
   return pkv_host::launch_after(tree_mask_kernel, grid, 128, 0, (cudaStream_t)stream, parents, qo_indptr, num_tokens,
-                                mask_words, (uint32_t*)tree_mask, err_word);
+                                max_tree_len, mask_words, (uint32_t*)tree_mask, err_word);
 }
 
 }  // extern "C"

@@ -365,3 +365,60 @@ def test_starts_beside_the_kernel_before(lib):
                 st.synchronize()
                 assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (how, captured)
                 assert torch.equal(tree.out, tree_want), (how, captured)
+
+
+def test_rewritten_scales_are_seen_at_once(lib):
+    """Read-back, append, decode, read-back on one stream, again and again over the same slots: each
+    call starts while those before it run, and reads rows and scales that the call before it wrote
+    and an earlier one had read."""
+    c = Cache8((PAGE * PAGES // 2,) * 2)
+    n = sum(c.lens)
+    slots = torch.tensor(np.concatenate([c.rows(b) for b in range(2)])).cuda()
+    out_indptr, lens = i32([0, n // 2, n]), i32(c.lens)
+    data = [tokens(40 + i, n) for i in range(4)]
+    for i, t in enumerate(data):
+        t["v"] *= 2.0 ** (5 * i)
+        t["k"] *= 2.0 ** -i
+    q = tokens(7, 2)["q"]
+    shape = (n, HKV, D)
+    ws = torch.empty(lib.decode_fp8_workspace_size(2, HQ, HKV, D), dtype=torch.uint8, device="cuda")
+    outs = [dict(k0=torch.empty(shape, dtype=torch.bfloat16, device="cuda"), v0=torch.empty(shape, dtype=torch.bfloat16, device="cuda"),
+                 k1=torch.empty(shape, dtype=torch.bfloat16, device="cuda"), v1=torch.empty(shape, dtype=torch.bfloat16, device="cuda"),
+                 o=torch.empty_like(q), lse=torch.empty(2, HQ, device="cuda")) for _ in range(8)]
+
+    def run(wait):
+        for i, to in enumerate(outs):
+            t = data[i % 4]
+            lib.paged_gather_fp8(*c.pool, c.indptr, c.indices, lens, out_indptr, to["k0"], to["v0"])
+            wait()
+            lib.kv_append_fp8(*c.pool, t["k"], t["v"], slots)
+            wait()
+            lib.paged_decode_fp8(q, *c.pool, c.indptr, c.indices, lens, 0.1, out=to["o"], lse=to["lse"], workspace=ws)
+            wait()
+            lib.paged_gather_fp8(*c.pool, c.indptr, c.indices, lens, out_indptr, to["k1"], to["v1"])
+            wait()
+
+    lib.kv_append_fp8(*c.pool, data[3]["k"], data[3]["v"], slots)
+    run(torch.cuda.synchronize)
+    want = [{k: x.clone() for k, x in to.items()} for to in outs]
+    for i in range(1, 8):
+        assert torch.equal(outs[i]["k0"], outs[i - 1]["k1"]) and torch.equal(outs[i]["v0"], outs[i - 1]["v1"])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        g = torch.cuda.CUDAGraph()
+        for how in ("eager", "captured"):
+            for to in outs:
+                for x in to.values():
+                    x.zero_()
+            if how == "eager":
+                run(lambda: None)
+            else:
+                with torch.cuda.graph(g, stream=st):
+                    run(lambda: None)
+                for _ in range(3):
+                    g.replay()
+            st.synchronize()
+            for to, w in zip(outs, want):
+                for k in to:
+                    assert torch.equal(to[k], w[k]), (how, k)

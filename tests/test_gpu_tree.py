@@ -327,3 +327,12 @@ def test_mask_from_parents_reports_bad_parents(lib):
     err.zero_()
     lib.tree_mask_from_parents(i32([-1] * 4), i32([0, 5]), 8, err_word=err)
     assert int(err) == lib.DEVERR_ROW_OOB
+
+
+def test_mask_from_parents_stops_at_the_longest_tree(lib):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((12, 2), -5, dtype=torch.int32, device="cuda")
+    lib.tree_mask_from_parents(i32([-1, 0] + [-1] * 10), i32([0, 2, 12]), 7, out=out, err_word=err)
+    assert int(err) == lib.DEVERR_LENGTH
+    assert out[:9].tolist() == [[1, 0], [3, 0]] + [[1 << t, 0] for t in range(7)] and torch.all(out[9:] == -5)
