@@ -336,3 +336,23 @@ def test_mask_from_parents_stops_at_the_longest_tree(lib):
     lib.tree_mask_from_parents(i32([-1, 0] + [-1] * 10), i32([0, 2, 12]), 7, out=out, err_word=err)
     assert int(err) == lib.DEVERR_LENGTH
     assert out[:9].tolist() == [[1, 0], [3, 0]] + [[1 << t, 0] for t in range(7)] and torch.all(out[9:] == -5)
+
+
+@pytest.mark.parametrize("nodes,Hq,Hkv,D", [(30, 8, 2, 128), (50, 8, 2, 128), (60, 8, 2, 64), (5, 8, 2, 128), (12, 8, 2, 64)])
+def test_scores_that_jump_within_a_tile(lib, nodes, Hq, Hkv, D):
+    """Scores that jump up by a little and by a lot from one run of positions to the next: the reference
+    maximum moves between tiles and between the halves of one, weights already written are scaled."""
+    n = 1500 + nodes
+    s = make(8, (1500,), (nodes,), Hq, Hkv, D, 16)
+    rng = np.random.default_rng(nodes)
+    level, steps = 0.0, []
+    while sum(steps_n for steps_n, _ in steps) < n:
+        steps.append((int(rng.integers(5, 90)), level))
+        level += float(rng.choice([0.2, 1.0, 4.0, -3.0, 25.0]))
+    level = np.concatenate([np.full(c, x) for c, x in steps])[:n]
+    k = s["k"].view(-1, Hkv, D)
+    turn = torch.sign(s["q"][0, ::Hq // Hkv].float().cpu())[None]
+    k[s["rows"][0].cuda()] = (torch.tensor(level, dtype=torch.float32)[:, None, None] * turn / 3).to(torch.bfloat16).cuda()
+    out, lse, err = call(lib, s)
+    assert err == 0
+    verify(s, out, lse)
