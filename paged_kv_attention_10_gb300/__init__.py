@@ -12,6 +12,7 @@ Names follow the C ABI in ``include/pagedkv.h`` (``pkv_kv_append`` -> ``kv_appen
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 from typing import Optional, Tuple
@@ -138,6 +139,29 @@ def load():
         f.argtypes = args
     _lib = lib
     return lib
+
+
+class _CheckedInPython:
+    """Stands for the _checked module where it is not built: no call is taken."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+_checked = None
+
+
+def _load_checked():
+    """The _checked module (csrc/binding.cpp): the once-a-layer calls, checked and made without Python."""
+    global _checked
+    load()
+    try:
+        _checked = importlib.import_module("._checked", __package__)
+        if _checked.torch_version != str(torch.__version__):  # it reads the tensors of the torch it was built with
+            _checked = _CheckedInPython()
+    except ImportError:
+        _checked = _CheckedInPython()
+    return _checked
 
 
 def _host_i(t, name, dtype):
@@ -536,8 +560,9 @@ def cascade_decode(q, k_pool, v_pool, plan, sm_scale: float, out=None, lse=None,
 # ---------------------------------------------------------------------------------------------
 # rotary append, 8-bit cache
 # ---------------------------------------------------------------------------------------------
-# Small steps are bound by the host, so these calls check a tensor with a few attribute reads and hand
-# its address on as a number; only a tensor that fails goes through _need, which says why.
+# Small steps are bound by the host, so each of these calls first goes to the _checked module, which checks the
+# plain case and makes the call (None: it did neither).  What it does not take is checked here, with a few
+# attribute reads a tensor; one that fails goes through _need, which says why.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current = torch._C._cuda_getDevice
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
@@ -577,6 +602,13 @@ def _run(index, stream, fn: str, *args):
             st = f(*args, raw)
     if st != 0:
         raise PagedKVError(fn, st)
+
+
+def _done(status, fn) -> bool:
+    """Whether the _checked module has made the call."""
+    if status:
+        raise PagedKVError(fn, status)
+    return status is not None
 
 
 def _pool_bf16(k_pool, v_pool):
@@ -644,6 +676,10 @@ def rotary_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, positions, cos_
     """Rotate k_new (and q into q_out, in place when q_out is None) by their positions and write K/V
     into the pool slots.  The first cos_sin.shape[1] values of each head are rotated, in half-split
     or (``interleaved``) neighbouring pairs; negative slots are padding."""
+    if _done((_checked or _load_checked()).rotary_kv_append(
+            k_pool, v_pool, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out, bool(interleaved), err_word,
+            None if stream is None else stream.cuda_stream), "pkv_rotary_kv_append"):
+        return
     pool, index, shape = _pool_bf16(k_pool, v_pool)
     _rotary("pkv_rotary_kv_append", pool, index, shape, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out,
             interleaved, err_word, stream)
@@ -653,6 +689,10 @@ def rotary_kv_append_fp8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_ma
                          q=None, q_out=None, interleaved: bool = False, err_word=None, stream=None) -> None:
     """rotary_kv_append into an 8-bit cache: K (rotated) and V quantised to e4m3 as they are written,
     with a power-of-two scale per row and head."""
+    if _done((_checked or _load_checked()).rotary_kv_append_fp8(
+            k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, positions, cos_sin, q, q_out,
+            bool(interleaved), err_word, None if stream is None else stream.cuda_stream), "pkv_rotary_kv_append_fp8"):
+        return
     pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
     _rotary("pkv_rotary_kv_append_fp8", pool, index, shape, k_new, v_new, slot_mapping, positions, cos_sin, q,
             q_out, interleaved, err_word, stream)
@@ -697,6 +737,10 @@ def kv_append_fp8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, 
                   stream=None) -> None:
     """Quantise k_new[t], v_new[t] to e4m3 with a power-of-two scale per row and head and write them
     into pool slot slot_mapping[t] (negative = skip)."""
+    if _done((_checked or _load_checked()).kv_append_fp8(
+            k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, err_word,
+            None if stream is None else stream.cuda_stream), "pkv_kv_append_fp8"):
+        return
     pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
     rows, T = _new_rows(index, shape, k_new, v_new, slot_mapping)
     _run(index, stream, "pkv_kv_append_fp8", pool, *rows, T, _addr_or_none(err_word, "err_word", _I32, index))
@@ -706,6 +750,10 @@ def paged_gather_fp8(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv
                      v_out, err_word=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Read an 8-bit cache back as bf16: position j of request b goes to row out_indptr[b] + j of
     k_out/v_out [num_out_rows, num_kv_heads, head_dim]; other rows are left as they were."""
+    if _done((_checked or _load_checked()).paged_gather_fp8(
+            k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, out_indptr, k_out, v_out, err_word,
+            None if stream is None else stream.cuda_stream), "pkv_paged_gather_fp8"):
+        return k_out, v_out
     pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
     at = [_addr(t, n, _I32, index) for t, n in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"),
                                                 (kv_lens, "kv_lens"), (out_indptr, "out_indptr"))]
@@ -755,6 +803,11 @@ def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices,
                      max_ctas=0):
     """Decode attention of q [B, Hq, D] over each request's pages of an 8-bit cache.  Returns
     (out, lse); arguments as for paged_decode."""
+    if out is not None and workspace is not None and (lse is not None or not return_lse) and _done(
+            (_checked or _load_checked()).paged_decode_fp8(
+                k_pool, v_pool, k_scale, v_scale, q, out, lse, kv_indptr, kv_indices, kv_lens, sm_scale, workspace,
+                err_word, max_ctas, None if stream is None else stream.cuda_stream), "pkv_paged_decode_fp8"):
+        return out, lse
     pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
     lens = _addr(kv_lens, "kv_lens", _I32, index)
     B = kv_lens.numel()
@@ -794,6 +847,12 @@ def paged_tree_attention(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, pr
     """Attention of each request's drafted tokens (rows qo_indptr[b].. of q) over its cached prefix
     and the drafted tokens whose bits its tree_mask row (int32 [num_q_tokens, words]) sets.  Returns
     (out, lse)."""
+    if out is not None and workspace is not None and (lse is not None or not return_lse) and _done(
+            (_checked or _load_checked()).paged_tree_attention(
+                k_pool, v_pool, q, out, lse, qo_indptr, kv_indptr, kv_indices, prefix_lens, tree_mask, max_tree_len,
+                sm_scale, workspace, err_word, None if stream is None else stream.cuda_stream),
+            "pkv_paged_tree_attention"):
+        return out, lse
     pool, index, shape = _pool_bf16(k_pool, v_pool)
     qo, prefix = _addr(qo_indptr, "qo_indptr", _I32, index), _addr(prefix_lens, "prefix_lens", _I32, index)
     B = prefix_lens.numel()

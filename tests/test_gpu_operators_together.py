@@ -422,3 +422,62 @@ def test_rewritten_scales_are_seen_at_once(lib):
             for to, w in zip(outs, want):
                 for k in to:
                     assert torch.equal(to[k], w[k]), (how, k)
+
+
+def test_calls_checked_in_python_are_the_same(lib, monkeypatch):
+    """The binding's native module takes the plain calls; without it the Python checks make the same
+    ones, and what the module does not take (here: a whole number for the scale) goes that way."""
+    native = lib._load_checked()
+    assert native.torch_version == torch.__version__
+    table = lib.rotary_cos_sin_table(256, D, 1e6)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(lib.decode_fp8_workspace_size(2, HQ, HKV, D), dtype=torch.uint8, device="cuda")
+    tws = tree_ws(lib)
+
+    def run(scale):
+        c = Cache8((40, 90))
+        t = tokens(3, 130)
+        slots = torch.tensor(np.concatenate([c.rows(b) for b in range(2)])).cuda()
+        lib.kv_append_fp8(*c.pool, t["k"], t["v"], slots, err_word=err)
+        q = tokens(4, 2)
+        pos, at = i32([40, 90]), torch.tensor([c.slots(0, 40, 1)[0], c.slots(1, 90, 1)[0]]).cuda()
+        lens = i32([41, 91])
+        q_out = torch.empty_like(q["q"])
+        lib.rotary_kv_append_fp8(*c.pool, q["k"], q["v"], at, pos, table, q=q["q"], q_out=q_out, interleaved=True,
+                                 err_word=err)
+        out, lse = torch.empty_like(q_out), torch.empty(2, HQ, device="cuda")
+        got = lib.paged_decode_fp8(q_out, *c.pool, c.indptr, c.indices, lens, scale, out=out, lse=lse, workspace=ws,
+                                   err_word=err)
+        assert got[0] is out and got[1] is lse
+        k, v = (torch.zeros(132, HKV, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lib.paged_gather_fp8(*c.pool, c.indptr, c.indices, lens, i32([0, 41, 132]), k, v, err_word=err)
+        step = TreeStep(5)
+        step.run(lib, table, tws)
+        kb, vb = (torch.zeros(PAGES, PAGE, HKV, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lib.rotary_kv_append(kb, vb, q["k"], q["v"], at, pos, table, q=q["q"], err_word=err)
+        return [x.view(torch.uint8) if x.dtype is torch.float8_e4m3fn else x
+                for x in (*c.pool, q_out, out, lse, k, v, step.out, kb, vb, q["q"])]
+
+    calls = []
+
+    class Counting:
+        def __getattr__(self, name):
+            def call(*args):
+                status = getattr(native, name)(*args)
+                calls.append((name, status))
+                return status
+            return call
+
+    monkeypatch.setattr(lib, "_checked", Counting())
+    want = run(0.125)
+    assert {name for name, _ in calls} == {"kv_append_fp8", "rotary_kv_append_fp8", "paged_decode_fp8", "paged_gather_fp8",
+                                           "rotary_kv_append", "paged_tree_attention"}
+    assert all(status == 0 for _, status in calls)
+    calls.clear()
+    one = run(1)
+    assert ("paged_decode_fp8", None) in calls
+    monkeypatch.setattr(lib, "_checked", lib._CheckedInPython())
+    for a, b in ((want, run(0.125)), (one, run(1))):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert int(err) == 0
