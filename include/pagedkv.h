@@ -474,8 +474,9 @@ pkv_status pkv_rotary_cos_sin_table(float* table, int32_t max_position, int32_t 
  * (slot, head, d) is k8[slot, head, d] * k_scale[slot, head].  What the appends write: k8 =
  * e4m3(x / scale), rounded to nearest even, with the smallest power of two scale >= 2^-126 for which
  * the row's largest finite |x| is at most 448 scale; a NaN or an infinity is stored as NaN and does
- * not count for the scale, and what would round up to 2^128 is stored as 240 * 2^120.  The attention and the read-back take any scale that is positive and a
- * normal fp32 number (a calibrated one per head, say); for powers of two reading back is exact.
+ * not count for the scale, and what would round up to 2^128 is stored as 240 * 2^120.  The attention
+ * and the read-back take any scale that is positive and a normal fp32 number (a calibrated one per
+ * head, say); for powers of two reading back is exact.
  */
 typedef struct {
   void* k;              /* e4m3 [num_pages, page_size, num_kv_heads, head_dim], 16-byte aligned */

@@ -28,6 +28,11 @@
 //    and the infinities and NaNs of drafted tokens become 0 in shared memory (weight 0 times them
 //    would be NaN for rows that do not see them); rows that do see them get them added when they are
 //    written, which is what a sum with a non-zero weight would give.
+// Measured with 32/8 heads of 128 at page size 16: 64 requests of 1 to 16 tokens over 512 to 4096 positions
+// 111 us, 5.5 TB/s, 81 % of what a device copy reaches (bound by memory and by the ends of segments,
+// about 3 us each); 4 requests of 64 tokens over 32700 positions 129 us, 1.06 PFLOP/s, 62 % of the bytes' floor
+// and 56 % of the tensor cores' (bound by the chain of a slot: product, softmax, product, about 1.85 us a
+// tile, of which the tensor cores work 1.33); one request of 8 tokens over 1000 positions 13 us, all latency.
 #include <atomic>
 
 #include "quant.cuh"
@@ -579,8 +584,8 @@ __device__ bool tree_mma_pv(Ctl* ctl, uint8_t* smem, uint32_t tmem) {
         const bool first = s.nq == 2 ? j == 0 : j < 2;
         if (!wait(&ctl->p_full[slot], used[slot] & 1)) return false;
         // With two Q tiles the order is PV 0, QK 0, PV 1, QK 1, so that each slot's products run beside the
-        // other's softmax; left to themselves the slots fall into step, both products wait for both
-        // softmaxes, and a tile takes 1.9 us instead of 1.5.
+        // other's softmax; left to themselves the slots fall into step and both products wait for both
+        // softmaxes (4 requests of 64 tokens over 32700 positions: 134 us, 129 so).
         if (s.nq == 2 && (q == 0 || j + 1 < s.n) && !wait(&ctl->qk_issued[q ^ 1], used[q ^ 1] & 1)) return false;
         tc_fence_after();
         if (lane == 0) {
@@ -1113,7 +1118,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
 // ---------------------------------------------------------------------------------------------
 // Merge: block (c, y) joins rows 32 y .. 32 y + 31 of the unit that CTA c began and did not finish.  A
 // lane is a row, a warp every eighth group of four dims, so a part's rows are read as whole lines; the
-// states are joined in one pass with a running maximum, the loads of four parts in flight.
+// states are joined in one pass with a running maximum, the loads of four parts in flight.  5 us after
+// 64 requests of up to 16 tokens, 9 after 4 of 64 (23 MB of states, which L2 holds).
 // ---------------------------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
