@@ -315,11 +315,14 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   return r;
 }
 
-// Length of the stream (K producer warp, before the set-up barrier: the walk finds the numbers in L1).
-__device__ int64_t tree_stream_length(const TreeArgs& a) {
+// Length of the stream (K producer warp, before the set-up barrier); first: this lane's of the first 32
+// requests, which the walk starts with.
+__device__ int64_t tree_stream_length(const TreeArgs& a, Req& first) {
   const int lane = threadIdx.x & 31;
-  int64_t total = 0;
-  for (int i = lane; i < a.batch; i += 128) {
+  first = Req{};
+  if (lane < a.batch) first = load_req(a, lane, blockIdx.x == 0);
+  int64_t total = (int64_t)first.pairs * first.cost;
+  for (int i = 32 + lane; i < a.batch; i += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {  // four requests' loads in flight
       if (i + 32 * u < a.batch) {
@@ -333,7 +336,7 @@ __device__ int64_t tree_stream_length(const TreeArgs& a) {
 
 // K producer warp: walks this CTA's share of the stream, publishes each segment and loads its K.
 template <int D, bool kRows>
-__device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb, int64_t total) {
+__device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb, int64_t total, const Req& first) {
   const int lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   Producer<D, kRows> k(a, ctl, sb, false);
@@ -357,8 +360,11 @@ __device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb, int64_t tota
 
   int64_t base = 0;  // stream offset of request b0
   for (int b0 = 0; b0 < a.batch && base < c1 && ok; b0 += 32) {
-    Req r = {};
-    if (b0 + lane < a.batch) r = load_req(a, b0 + lane, false);
+    Req r = first;
+    if (b0 > 0) {
+      r = Req{};
+      if (b0 + lane < a.batch) r = load_req(a, b0 + lane, false);
+    }
     const int64_t len = (int64_t)r.pairs * r.cost * a.num_kv_heads;
     int64_t incl = len;
 #pragma unroll
@@ -1071,9 +1077,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
     prefetch_tmap(&a.tm_v);
   }
   int64_t total = 0;
+  Req first;
   if (warp == 0) {
     pdl_wait();
-    total = tree_stream_length(a);
+    total = tree_stream_length(a, first);
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, 512);
@@ -1086,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
-    tree_walk<D, kRows>(a, ctl, sb, total);
+    tree_walk<D, kRows>(a, ctl, sb, total, first);
   } else if (warp == 3) {
     tree_load_v<D, kRows>(a, ctl, sb);
   } else if (warp == 1) {
