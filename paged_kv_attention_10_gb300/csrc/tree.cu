@@ -5,34 +5,18 @@
 // each bit t of its mask row (its ancestors and itself, or whatever the caller allows).  GQA, page
 // lists and LSE as in the other attention calls; a row that sees nothing gives 0 and -inf.
 //
-// A few query rows over a long cache: bound by reading K and V once.  What the shape asks for:
-//  * One persistent CTA per SM over an equal share of the stream of 128-position KV tiles of all
-//    (request, KV head) units, so that one tree over a long context fills the GPU as well as many
-//    trees do.  A unit cut by a share's border leaves partial states, merged by log-sum-exp in a
-//    programmatic dependent launch.
-//  * The rows of a unit are (token, group head) pairs, up to two 128-row Q tiles.  S = Q K^T and
-//    O += P V run as tcgen05.mma (M 128, N 128), accumulators in TMEM: two slots, each an S buffer of
-//    128 columns (P, bf16, is written over it) and an O of 128.  With two Q tiles a slot is a Q
-//    tile and each K/V tile in shared memory serves both; with one Q tile the slots take alternate
-//    KV tiles, so that one slot's softmax runs beside the other's MMAs, and their states are joined
-//    when the segment ends.
-//  * A thread owns a row, and a warp can read only its quarter of TMEM's lanes, so a unit of at most 32
-//    (64) rows would leave three (two) of a slot's four softmax warps idle while the busy ones took
-//    128 columns of every tile each, and that chain, not memory, would set the pace.  The rows are
-//    therefore loaded four times (twice) into the tile, the MMA's rows being there anyway: each
-//    copy takes 32 (64) of the tile's columns, writes zeros for P elsewhere, and ends up with a state
-//    of its own; the copies' states are joined in the epilogue.
-//  * Twelve warps: K producer (which also walks the stream and publishes the segments), QK issuer, PV
-//    issuer, V and Q producer, and four softmax warps per slot, one thread per row.
+// A few query rows over a long cache: bound by reading K and V once.  The extend's pipeline (two
+// producer warps, QK and PV issued by two threads, P over S in TMEM, a softmax thread per row, two CTAs an SM)
+// with what the shape asks for besides:
+//  * Persistent CTAs, two per SM, each over an equal share of the stream of 64-position KV tiles of
+//    all units (request, KV head, 128-row Q tile), so that one tree over a long context fills the GPU
+//    as well as many trees do.  A unit cut by a share's border leaves fp32 partial states, merged by
+//    log-sum-exp in a programmatic dependent launch.  The CTA takes its segments one after the other, with
+//    all warps meeting between them; the other CTA of the SM fills the gap.
 //  * Only tiles that reach past the prefix are masked.  There the V rows behind the last position
 //    and the infinities and NaNs of drafted tokens become 0 in shared memory (weight 0 times them
 //    would be NaN for rows that do not see them); rows that do see them get them added when they are
 //    written, which is what a sum with a non-zero weight would give.
-// Measured with 32/8 heads of 128 at page size 16: 64 requests of 1 to 16 tokens over 512 to 4096 positions
-// 111 us, 5.5 TB/s, 81 % of what a device copy reaches (bound by memory and by the ends of segments,
-// about 3 us each); 4 requests of 64 tokens over 32700 positions 129 us, 1.06 PFLOP/s, 62 % of the bytes' floor
-// and 56 % of the tensor cores' (bound by the chain of a slot: product, softmax, product, about 1.85 us a
-// tile, of which the tensor cores work 1.33); one request of 8 tokens over 1000 positions 13 us, all latency.
 #include <atomic>
 
 #include "quant.cuh"
@@ -42,34 +26,30 @@ namespace {
 
 using namespace pkv;
 
-constexpr int kBM = 128;              // Q tile rows
-constexpr int kBN = 128;              // KV positions per tile
-constexpr int kThreads = 384;
-constexpr int kSoftmaxWarp0 = 4;      // warps 4..7 slot 0, 8..11 slot 1
-constexpr int kMaxNodes = 1024;       // drafted tokens of a request
-constexpr int kSegRing = 4;
-constexpr int kMaxRing = 9;
-constexpr int kUnitCost = 3;          // a unit's start and epilogue, in KV tiles of the work split (1 to 4
-                                      // tried: 64 requests of up to 16 tokens 118.9, 115.7, 114.7, 115.5 us)
-constexpr uint32_t kHalfTile = 128 * 128;  // 128 rows of one 64-dim half, 16 KB
-constexpr uint32_t kColO = 0, kColS = 256;  // O of slot s at 128 s, S at 256 + 128 s
+constexpr int kBM = 128;  // Q tile rows: (token, group head) pairs
+constexpr int kBN = 64;   // KV positions per tile
+// warp 0 the walk and K, warp 1 QK MMAs, warps 2..5 softmax (one per TMEM lane quadrant, a thread per
+// row), warp 6 V, warp 7 PV MMAs
+constexpr int kSoftmaxWarps = 4;
+constexpr int kVWarp = 2 + kSoftmaxWarps;
+constexpr int kPVWarp = kVWarp + 1;
+constexpr int kThreads = (kPVWarp + 1) * 32;
+constexpr int kMaxNodes = 1024;  // drafted tokens of a request
+constexpr int kUnitCost = 4;     // a unit's start and epilogue, in KV tiles of the work split
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColO = 128;  // O at columns [128, 128 + D); S buffers at [0, 64) and [64, 128)
+constexpr uint32_t kQHalf = kBM * 128;   // one 64-dim half of the Q tile, 16 KB
+constexpr uint32_t kKVHalf = kBN * 128;  // 64 positions x 64 dims, 8 KB
 
+// Operands are 64-dim halves of 128-byte swizzled rows.
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
-  static constexpr uint32_t kTile = kHalves * kHalfTile;
+  static constexpr uint32_t kKVStage = kHalves * kKVHalf;
   static constexpr uint32_t kOffQ = 0;
-  // One ring for K and V tiles, K of tile j at place 2 j and V at 2 j + 1: a buffer that K's product
-  // frees soon is the next V's, and the loads run 2.5 tiles ahead.  (Two K and three V buffers of their own
-  // left K's reload little more than a tile's time.)
-  static constexpr int kRing = D == 128 ? 5 : 9;
-  static constexpr uint32_t kOffRing = kOffQ + 2 * kTile;
-  // the epilogue's exchange between replicas, 2 slots x 3 x 32 rows x 32 dims fp32: at D 128 it is the
-  // second Q buffer, which one Q tile leaves free
-  static constexpr uint32_t kScratch = 2 * 3 * 32 * 32 * 4;
-  static constexpr bool kShared = kTile >= kScratch;
-  static constexpr uint32_t kOffScratch = kShared ? kOffQ + kTile : kOffRing + kRing * kTile;
-  static constexpr uint32_t kOffCtl = kOffRing + kRing * kTile + (kShared ? 0 : kScratch);
+  static constexpr uint32_t kOffK = kOffQ + kHalves * kQHalf;
+  static constexpr uint32_t kOffV = kOffK + 2 * kKVStage;
+  static constexpr uint32_t kOffCtl = kOffV + 2 * kKVStage;
 };
 
 // A run of KV tiles of one unit that this CTA computes.
@@ -78,46 +58,37 @@ struct Seg {
   int32_t T, P;    // drafted tokens (covered), cached positions
   int32_t p0, np;  // page list
   int32_t h;       // KV head
-  int32_t t0;      // first token of the unit's first Q tile
-  int32_t nq;      // Q tiles of the unit (1 or 2); 0: no more work
-  int32_t j0, n;   // first KV tile, number of tiles
+  int32_t t0;      // first token of the unit
+  int32_t j0, n;   // first KV tile, number of tiles (0: no more work)
   int32_t part;    // partial state's slot, or -1: the segment is the whole unit
-  int32_t rep;     // copies of the Q rows in the tile (1, 2 or 4)
 };
 
 struct Ctl {
-  Seg seg[kSegRing];
-  uint64_t seg_full[kSegRing], seg_empty[kSegRing];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t full[kMaxRing], empty[kMaxRing];  // the K / V ring
-  uint64_t s_full[2];  // QK written
-  uint64_t qk_issued[2];
-  uint64_t p_full[2];  // P written, V cleaned
-  uint64_t s_free[2];  // PV done
-  uint64_t o_free;     // O read by the epilogue
-  uint64_t x_full, x_free;  // the slots' exchange of row states
-  uint32_t epilogues;       // warps done with the scratch, counted over all segments
-  uint64_t qk_done, pv_done;
+  Seg seg;
   uint32_t tmem_base;
+  uint32_t failed;   // a wait gave up
   uint32_t bad_any;
   uint32_t bad[kMaxNodes / 32];  // drafted tokens of this segment whose V is not finite
-  float xm[2][kBM], xl[2][kBM];  // row maxima and sums of the slots
+  uint32_t pad;
+  uint64_t q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], s_free[2];  // S buffer b: QK written / its P consumed by PV
+  uint64_t p_full[2];             // P written, V cleaned
+  uint64_t qk_done, pv_done;      // every MMA of the issuing thread has completed (exit path)
+  float inv[kBM];                 // 1 / (sum of P) of each row, 0 for a row that saw nothing
 };
-constexpr uint32_t kSmemLimit = 227 * 1024;
 static_assert(kMaxNodes / 32 == 32, "a warp clears the notes");
-static_assert(Cfg<128>::kOffCtl + sizeof(Ctl) <= kSmemLimit, "shared memory");
 
 // The unit that a CTA's share ends in the middle of, for the merge: its parts are the slots
 // 2c + 1, 2(c + 1), 2(c + 2), ...
 struct Cut {
   int32_t parts;  // 0: none
-  int32_t q0, T, t0, h, nq;
-  int32_t pad[2];
+  int32_t q0, T, t0, h;
+  int32_t pad[3];
 };
 
 struct TreeArgs {
-  CUtensorMap tm_q[3];  // box of the tokens of 128, 64 and 32 rows
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_q, tm_k, tm_v;
   const int32_t* qo_indptr;
   const int32_t* kv_indptr;
   const int32_t* kv_indices;
@@ -132,166 +103,22 @@ struct TreeArgs {
   int32_t page_size, box_rows;
   FastDiv page_div;  // by page_size
   int32_t num_kv_heads, num_q_heads, group;
-  int32_t tpt;        // tokens per Q tile
-  int32_t tpt2, tpt4; // ... of which 2 or 4 copies fit into the tile
+  int32_t tpt;       // tokens per Q tile
   int32_t batch, num_q_tokens, max_nodes;
   float scale_log2;
-  Cut* cut;           // [CTAs]
-  float* part_o;      // [2 CTAs][D / 4][part_rows][4]: a warp's rows lie side by side
-  float* part_lse;    // [2 CTAs][part_rows]
-  int32_t part_rows;
+  Cut* cut;          // [CTAs]
+  float* part_o;     // [2 CTAs][D / 4][128 rows][4]: a warp's rows lie side by side
+  float* part_lse;   // [2 CTAs][128 rows]
 };
 
 // ---------------------------------------------------------------------------------------------
-// Segment ring
+// The walk over this CTA's share of the stream (warp 0)
 // ---------------------------------------------------------------------------------------------
-// Next segment for a whole warp (all lanes wait and read), then released by lane 0.  False: a wait gave up.
-PKV_DEV bool next_seg(Ctl* ctl, int i, Seg& s) {
-  const int r = i % kSegRing;
-  if (!__all_sync(0xffffffffu, mbar_wait(&ctl->seg_full[r], (i / kSegRing) & 1))) return false;
-  s = ctl->seg[r];
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->seg_empty[r]);
-  return true;
-}
-
-// ---------------------------------------------------------------------------------------------
-// K / V producers
-// ---------------------------------------------------------------------------------------------
-// Copies the tiles of segments into the ring.  kRows: gathers of four rows, for page sizes that are not
-// a power of two of at least 8; else TMA boxes of min(page_size, 128) rows.
-template <int D, bool kRows>
-struct Producer {
-  using C = Cfg<D>;
-  const TreeArgs& a;
-  uint64_t* fulls;
-  uint64_t* empties;
-  const CUtensorMap* tm;
-  uint32_t base;  // of the ring, shared address
-  int item;       // place of the next tile in the ring's order: even K, odd V
-
-  __device__ Producer(const TreeArgs& args, Ctl* ctl, uint32_t sb, bool v)
-      : a(args), fulls(ctl->full), empties(ctl->empty), tm(v ? &args.tm_v : &args.tm_k),
-        base(sb + C::kOffRing), item(v ? 1 : 0) {}
-
-  // Waits until the next tile's buffer is free.
-  __device__ bool acquire() {
-    return __all_sync(0xffffffffu, mbar_wait(&empties[item % C::kRing], ((item / C::kRing) & 1) ^ 1)) != 0;
-  }
-
-  // Row of the pool that holds position pos, or -1 (reported).
-  __device__ int64_t row_of(int pos, int32_t page, int np) {
-    const int pidx = (int)a.page_div.quot((uint32_t)pos);
-    if (pidx >= np) {
-      report(a.err_word, PKV_DEVERR_LENGTH);
-      return -1;
-    }
-    if (page < 0 || page >= a.num_pages) {
-      report(a.err_word, PKV_DEVERR_PAGE_OOB);
-      return -1;
-    }
-    return (int64_t)page * a.page_size + (pos - pidx * a.page_size);
-  }
-
-  __device__ bool run(const Seg& s) {
-    return kRows ? run_rows(s) : run_boxes(s);
-  }
-
-  __device__ bool run_boxes(const Seg& s) {
-    const int lane = threadIdx.x & 31;
-    const int R = a.box_rows, nbox = kBN / R, kv_end = s.P + s.T;
-    const int box = lane % nbox, half = lane / nbox;  // lane issues one half of one box
-    auto entry = [&](int pidx) -> int32_t {
-      return (pidx >= 0 && pidx < s.np) ? ld(a.kv_indices + s.p0 + pidx) : -1;
-    };
-    int wbase = (int)a.page_div.quot((uint32_t)(s.j0 * kBN));
-    int32_t w0 = entry(wbase + lane), w1 = entry(wbase + 32 + lane);
-    for (int j = s.j0; j < s.j0 + s.n; ++j) {
-      while ((int)a.page_div.quot((uint32_t)(j * kBN)) >= wbase + 32) {  // the upper half was loaded 32 pages ago
-        w0 = w1;
-        wbase += 32;
-        w1 = entry(wbase + 32 + lane);
-      }
-      const int pos = j * kBN + box * R;
-      const int k = (int)a.page_div.quot((uint32_t)pos) - wbase;  // < 64: a tile spans at most 16 pages
-      const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
-      const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
-      const bool in = half < C::kHalves && pos < kv_end;
-      const int64_t row = in ? row_of(pos, k < 32 ? v0 : v1, s.np) : -1;
-      const uint32_t nload = __popc(__ballot_sync(0xffffffffu, row >= 0));
-      if (!acquire()) return false;
-      const int stage = item % C::kRing;
-      if (lane == 0) mbar_arrive_expect_tx(&fulls[stage], nload * R * 128);
-      __syncwarp();
-      if (row >= 0)
-        tma_load_3d(base + stage * C::kTile + half * kHalfTile + box * R * 128, tm, half * 64, s.h, (int)row,
-                    &fulls[stage]);
-      item += 2;
-    }
-    return true;
-  }
-
-  // A lane gathers four rows at a time (tile::gather4), its positions 4 lane .. 4 lane + 3 of the tile, one
-  // copy per 64-dim half; their pages are loaded a tile ahead.  Positions behind the end repeat the
-  // last one and a bad page's (reported) read the pool's row 0: neither is seen by a row whose result
-  // means anything.  29 requests of about 6000 positions, 8 heads at page size 1: 208 us at D 128 and 128 at
-  // D 64; 16-byte cp.async copies with the same look-ahead 262 and 251, gathers whose pages were
-  // loaded when needed 286 and 207.
-  __device__ bool run_rows(const Seg& s) {
-    const int lane = threadIdx.x & 31;
-    const int kv_end = s.P + s.T;
-    int32_t page[4];
-    uint32_t in_page[4];
-    bool listed[4];
-    auto load_pages = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t pidx;
-        a.page_div.divmod((uint32_t)min(j * kBN + 4 * lane + i, kv_end - 1), pidx, in_page[i]);
-        listed[i] = (int)pidx < s.np;
-        page[i] = listed[i] ? ld(a.kv_indices + s.p0 + pidx) : 0;
-      }
-    };
-    load_pages(s.j0);
-    for (int j = s.j0; j < s.j0 + s.n; ++j) {
-      int row[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = page[i] >= 0 && page[i] < a.num_pages;
-        if (!listed[i] || !in) report(a.err_word, !listed[i] ? PKV_DEVERR_LENGTH : PKV_DEVERR_PAGE_OOB);
-        row[i] = listed[i] && in ? page[i] * a.page_size + (int)in_page[i] : 0;
-      }
-      if (j + 1 < s.j0 + s.n) load_pages(j + 1);
-      if (!acquire()) return false;
-      const int stage = item % C::kRing;
-      if (lane == 0) mbar_arrive_expect_tx(&fulls[stage], C::kTile);
-      __syncwarp();
-#pragma unroll
-      for (int hf = 0; hf < C::kHalves; ++hf)
-        tma_gather4(base + stage * C::kTile + hf * kHalfTile + lane * 512, tm, s.h * D + hf * 64, row[0], row[1], row[2],
-                    row[3], &fulls[stage]);
-      item += 2;
-    }
-    return true;
-  }
-
-  // No copy of this warp is in flight when the CTA exits.  With every tile issued (`all`, the normal
-  // path) the last kRing places of the order, K's and V's, are the buffers' last occupants, and the
-  // consumers have seen them land.  A place before those has been landed on, consumed and used again,
-  // and its phase could no longer be waited for.  After a wait that gave up, every buffer's is tried
-  // (bounded waits).
-  __device__ void drain(bool all) {
-    const int end = (item & ~1);  // places issued in all, if the other warp has come as far
-    for (int i = item - 2; i >= max(0, all ? end - C::kRing : item - 2 * C::kRing); i -= 2)
-      mbar_wait(&fulls[i % C::kRing], (i / C::kRing) & 1);
-  }
-};
-
 // What a request asks for: its rows, its KV, its units and their tiles.
 struct Req {
   int32_t q0, T, P, p0, np;
-  int32_t pairs, tiles;  // Q tile pairs, KV tiles (0: nothing to do)
-  int32_t cost;          // of a unit in the stream: its tiles and what an epilogue costs
+  int32_t qtiles, tiles;  // Q tiles, KV tiles (0: nothing to do)
+  int32_t cost;           // of a unit in the stream: its tiles and what an epilogue costs
 };
 
 __device__ Req load_req(const TreeArgs& a, int b, bool check) {
@@ -302,317 +129,278 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   r.p0 = ld(a.kv_indptr + b);
   r.np = ld(a.kv_indptr + b + 1) - r.p0;
   r.T = min(max(rows, 0), a.max_nodes);
-  r.pairs = r.tiles = r.cost = 0;
+  r.qtiles = r.tiles = r.cost = 0;
   uint32_t bad = 0;
   if (rows < 0 || rows > a.max_nodes || r.P < 0 || r.P > 0x7fffffff - kMaxNodes - kBN) bad = PKV_DEVERR_LENGTH;
   if (rows > 0 && (r.q0 < 0 || r.q0 > a.num_q_tokens - rows)) bad |= PKV_DEVERR_ROW_OOB;
   if (bad && check) report(a.err_word, bad);
   if (r.T > 0 && r.P >= 0 && r.P <= 0x7fffffff - kMaxNodes - kBN && !(bad & PKV_DEVERR_ROW_OOB)) {
-    r.pairs = (r.T + 2 * a.tpt - 1) / (2 * a.tpt);
+    r.qtiles = (r.T + a.tpt - 1) / a.tpt;
     r.tiles = (r.P + r.T + kBN - 1) / kBN;
     r.cost = r.tiles + kUnitCost;
   }
   return r;
 }
 
-// Length of the stream (K producer warp, before the set-up barrier); first: this lane's of the first 32
-// requests, which the walk starts with.
-__device__ int64_t tree_stream_length(const TreeArgs& a, Req& first) {
+struct Walk {
+  int64_t c, c1;     // next stream position, end of the share
+  int64_t share;
+  int64_t base;      // stream offset of request b0
+  int32_t b0;
+  Req r;             // of request b0 + lane
+  int64_t len, incl; // its units' length in the stream, and up to its end from `base`
+  Cut cut;
+};
+
+__device__ void walk_scan(const TreeArgs& a, Walk& w) {
+  w.len = (int64_t)w.r.qtiles * w.r.cost * a.num_kv_heads;
+  w.incl = w.len;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, w.incl, o);
+    if ((int)(threadIdx.x & 31) >= o) w.incl += t;
+  }
+}
+
+__device__ void walk_start(const TreeArgs& a, Walk& w) {
   const int lane = threadIdx.x & 31;
-  first = Req{};
-  if (lane < a.batch) first = load_req(a, lane, blockIdx.x == 0);
-  int64_t total = (int64_t)first.pairs * first.cost;
+  w.r = Req{};
+  if (lane < a.batch) w.r = load_req(a, lane, blockIdx.x == 0);
+  int64_t total = (int64_t)w.r.qtiles * w.r.cost;
   for (int i = 32 + lane; i < a.batch; i += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {  // four requests' loads in flight
       if (i + 32 * u < a.batch) {
         const Req r = load_req(a, i + 32 * u, blockIdx.x == 0);
-        total += (int64_t)r.pairs * r.cost;
+        total += (int64_t)r.qtiles * r.cost;
       }
     }
   }
-  return warp_sum(total) * a.num_kv_heads;
+  total = warp_sum(total) * a.num_kv_heads;
+  w.share = (total + gridDim.x - 1) / gridDim.x;
+  if (w.share < 1) w.share = 1;
+  w.c = (int64_t)blockIdx.x * w.share;
+  w.c1 = min(total, w.c + w.share);
+  w.base = 0;
+  w.b0 = 0;
+  w.cut = Cut{};
+  walk_scan(a, w);
 }
 
-// K producer warp: walks this CTA's share of the stream, publishes each segment and loads its K.
-template <int D, bool kRows>
-__device__ void tree_walk(const TreeArgs& a, Ctl* ctl, uint32_t sb, int64_t total, const Req& first) {
+// The next segment of the share (all lanes); n = 0 when there is none.
+__device__ Seg walk_next(const TreeArgs& a, Walk& w) {
   const int lane = threadIdx.x & 31;
-  const int cta = blockIdx.x;
-  Producer<D, kRows> k(a, ctl, sb, false);
-  int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < 1) share = 1;
-  const int64_t c0 = cta * share, c1 = min(total, c0 + share);
-
-  bool ok = true;
-  int nseg = 0;
-  Cut cut = {};
-  auto publish = [&](const Seg& s) -> bool {
-    const int r = nseg % kSegRing;
-    if (!__all_sync(0xffffffffu, mbar_wait(&ctl->seg_empty[r], ((nseg / kSegRing) & 1) ^ 1))) return false;
-    if (lane == 0) {
-      ctl->seg[r] = s;
-      mbar_arrive(&ctl->seg_full[r]);
+  Seg s{};
+  while (w.c < w.c1) {
+    const int64_t group = __shfl_sync(0xffffffffu, w.incl, 31);
+    if (w.c >= w.base + group) {  // (not past the last request: c lies in the stream)
+      w.base += group;
+      w.b0 += 32;
+      w.r = Req{};
+      if (w.b0 + lane < a.batch) w.r = load_req(a, w.b0 + lane, false);
+      walk_scan(a, w);
+      if (w.b0 >= a.batch) break;
+      continue;
     }
-    ++nseg;
-    return true;
-  };
-
-  int64_t base = 0;  // stream offset of request b0
-  for (int b0 = 0; b0 < a.batch && base < c1 && ok; b0 += 32) {
-    Req r = first;
-    if (b0 > 0) {
-      r = Req{};
-      if (b0 + lane < a.batch) r = load_req(a, b0 + lane, false);
+    const int64_t rs = w.base + w.incl - w.len;
+    const uint32_t hit = __ballot_sync(0xffffffffu, w.len > 0 && rs <= w.c && w.c < rs + w.len);
+    if (!hit) break;
+    const int src = __ffs(hit) - 1;
+    const int64_t r0 = __shfl_sync(0xffffffffu, rs, src);
+    const int tiles = __shfl_sync(0xffffffffu, w.r.tiles, src);
+    const int cost = __shfl_sync(0xffffffffu, w.r.cost, src);
+    const int qtiles = __shfl_sync(0xffffffffu, w.r.qtiles, src);
+    s.q0 = __shfl_sync(0xffffffffu, w.r.q0, src);
+    s.T = __shfl_sync(0xffffffffu, w.r.T, src);
+    s.P = __shfl_sync(0xffffffffu, w.r.P, src);
+    s.p0 = __shfl_sync(0xffffffffu, w.r.p0, src);
+    s.np = __shfl_sync(0xffffffffu, w.r.np, src);
+    const int u = (int)((w.c - r0) / cost);  // units in the order (KV head, Q tile)
+    const int64_t us = r0 + (int64_t)u * cost;
+    const int off = (int)(w.c - us);
+    if (off >= tiles) {  // the rest of the unit is its epilogue's time
+      w.c = us + cost;
+      continue;
     }
-    const int64_t len = (int64_t)r.pairs * r.cost * a.num_kv_heads;
-    int64_t incl = len;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    const int64_t rs = base + incl - len;
-    uint32_t hit = __ballot_sync(0xffffffffu, len > 0 && rs + len > c0 && rs < c1);
-    while (hit && ok) {
-      const int src = __ffs(hit) - 1;
-      hit &= hit - 1;
-      Seg s;
-      s.q0 = __shfl_sync(0xffffffffu, r.q0, src);
-      s.T = __shfl_sync(0xffffffffu, r.T, src);
-      s.P = __shfl_sync(0xffffffffu, r.P, src);
-      s.p0 = __shfl_sync(0xffffffffu, r.p0, src);
-      s.np = __shfl_sync(0xffffffffu, r.np, src);
-      const int pairs = __shfl_sync(0xffffffffu, r.pairs, src);
-      const int tiles = __shfl_sync(0xffffffffu, r.tiles, src);
-      const int64_t r0 = __shfl_sync(0xffffffffu, rs, src);
-      const int cost = __shfl_sync(0xffffffffu, r.cost, src);
-      const int units = pairs * a.num_kv_heads;
-      // units in the order (KV head, pair): the first that reaches into the share
-      for (int u = (int)max((int64_t)0, (c0 - r0) / cost); u < units && ok; ++u) {
-        const int64_t us = r0 + (int64_t)u * cost, ue = us + tiles;  // (the rest is the epilogue's time)
-        if (us >= c1) break;
-        const int64_t s0 = max(us, c0), s1 = min(ue, c1);
-        if (s0 >= s1) continue;
-        s.h = u / pairs;
-        s.t0 = (u % pairs) * 2 * a.tpt;
-        s.nq = s.T - s.t0 > a.tpt ? 2 : 1;
-        s.j0 = (int)(s0 - us);
-        s.n = (int)(s1 - s0);
-        s.part = s0 == us && s1 == ue ? -1 : 2 * cta + (us >= c0 ? 1 : 0);
-        s.rep = s.nq == 2 ? 1 : s.T - s.t0 <= a.tpt4 ? 4 : s.T - s.t0 <= a.tpt2 ? 2 : 1;
-        if (us >= c0 && ue > c1) cut = Cut{(int32_t)((ue - 1) / share) - cta + 1, s.q0, s.T, s.t0, s.h, s.nq, {0, 0}};
-        ok = publish(s);
-        ok = ok && k.run(s);
-      }
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    s.h = u / qtiles;
+    s.t0 = (u % qtiles) * a.tpt;
+    s.j0 = off;
+    s.n = (int)min((int64_t)(tiles - off), w.c1 - w.c);
+    s.part = s.n == tiles ? -1 : 2 * (int)blockIdx.x + (off == 0 ? 1 : 0);
+    if (off == 0 && s.n < tiles)
+      w.cut = Cut{(int32_t)((us + tiles - 1) / w.share) - (int)blockIdx.x + 1, s.q0, s.T, s.t0, s.h, {0, 0, 0}};
+    w.c += s.n;
+    return s;
   }
-  if (ok) {
-    Seg end = {};
-    ok = publish(end);
-  }
-  if (lane == 0) a.cut[cta] = cut;
-  // The merge may be scheduled once every CTA has issued its last K (it waits for this grid's
-  // completion before it reads): early enough to hide its launch, late enough not to hold thread
-  // slots that kernels on other streams could use.
-  pdl_trigger();
-  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-  k.drain(ok);
+  s.n = 0;
+  return s;
 }
 
-// V and Q producer warp.  One Q tile always takes the first Q buffer, so that the second is free for
-// the epilogue's scratch; two Q tiles wait until that is no longer read.
-template <int D, bool kRows>
-__device__ void tree_load_v(const TreeArgs& a, Ctl* ctl, uint32_t sb) {
+// ---------------------------------------------------------------------------------------------
+// K / V producers.  t0: tiles of this CTA before the segment.
+// ---------------------------------------------------------------------------------------------
+// No copy of this warp is left in flight after a wait that gave up (bounded waits).
+PKV_DEV void drain(uint64_t* fulls, uint32_t issued) {
+  for (uint32_t t = issued < 2 ? 0 : issued - 2; t < issued; ++t) mbar_wait(&fulls[t & 1], (t >> 1) & 1);
+}
+
+// TMA boxes of min(page_size, 64) rows, lane i box i; the page indices come from a register window of 64
+// page-list entries whose upper half is loaded 32 pages before it is needed.
+template <int D>
+__device__ bool tree_load_boxes(const TreeArgs& a, Ctl* ctl, uint32_t sb, const Seg& s, uint32_t t, bool v) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
-  Producer<D, kRows> v(a, ctl, sb, true);
-  int uses[2] = {0, 0};
-  Seg s;
-  bool ok = true;
-  for (int i = 0; ok; ++i) {
-    ok = next_seg(ctl, i, s);
-    if (!ok || s.nq == 0) break;
-    if (C::kShared && s.nq == 2) {
-      const uint64_t t0 = globaltimer_ns();
-      while (ok && atomicAdd(&ctl->epilogues, 0u) < 8u * (uint32_t)i) ok = globaltimer_ns() - t0 <= kWaitLimitNs;
-      ok = __all_sync(0xffffffffu, ok);
+  const int R = a.box_rows, nbox = kBN / R, kv_end = s.P + s.T;
+  uint64_t* fulls = v ? ctl->v_full : ctl->k_full;
+  uint64_t* empties = v ? ctl->v_empty : ctl->k_empty;
+  const CUtensorMap* tm = v ? &a.tm_v : &a.tm_k;
+  const uint32_t base = sb + (v ? C::kOffV : C::kOffK);
+  auto entry = [&](int pidx) -> int32_t {
+    return (pidx >= 0 && pidx < s.np) ? ld(a.kv_indices + s.p0 + pidx) : -1;
+  };
+  int wbase = (int)a.page_div.quot((uint32_t)(s.j0 * kBN));
+  int32_t w0 = entry(wbase + lane), w1 = entry(wbase + 32 + lane);
+  for (int j = s.j0; j < s.j0 + s.n; ++j, ++t) {
+    while ((int)a.page_div.quot((uint32_t)(j * kBN)) >= wbase + 32) {
+      w0 = w1;
+      wbase += 32;
+      w1 = entry(wbase + 32 + lane);
     }
-    const int level = s.rep == 1 ? 0 : s.rep == 2 ? 1 : 2;
-    const int tokens = level == 0 ? a.tpt : level == 1 ? a.tpt2 : a.tpt4;
-    for (int q = 0; q < s.nq && ok; ++q, ++uses[q - 1]) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[q], (uses[q] & 1) ^ 1));
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&ctl->q_full[q], C::kHalves * s.rep * tokens * a.group * 128);
-      __syncwarp();
-      if (lane < C::kHalves * s.rep) {
-        const int hf = lane % C::kHalves, copy = lane / C::kHalves;
-        tma_load_3d(sb + C::kOffQ + q * C::kTile + hf * kHalfTile + copy * (kBM / s.rep) * 128, &a.tm_q[level], hf * 64,
-                    s.h * a.group, s.q0 + s.t0 + q * a.tpt, &ctl->q_full[q]);
-      }
+    const int pos = j * kBN + min(lane, nbox - 1) * R;
+    const int pidx = (int)a.page_div.quot((uint32_t)pos), k = pidx - wbase;  // < 64: a tile spans at most 8 pages
+    const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
+    const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
+    const int32_t page = k < 32 ? v0 : v1;
+    int row = -1;
+    if (lane < nbox && pos < kv_end) {
+      if (pidx >= s.np)
+        report(a.err_word, PKV_DEVERR_LENGTH);
+      else if (page < 0 || page >= a.num_pages)
+        report(a.err_word, PKV_DEVERR_PAGE_OOB);
+      else
+        row = page * a.page_size + (pos - pidx * a.page_size);
     }
-    ok = ok && v.run(s);
-  }
-  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-  v.drain(ok);
+    const uint32_t nload = __popc(__ballot_sync(0xffffffffu, row >= 0));
+    const int st = t & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empties[st], ((t >> 1) & 1) ^ 1))) {
+      drain(fulls, t);
+      return false;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(&fulls[st], nload * R * 128 * C::kHalves);
+    __syncwarp();
+    if (row >= 0) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if (uses[q] > 0) mbar_wait(&ctl->q_full[q], (uses[q] - 1) & 1);
+      for (int hf = 0; hf < C::kHalves; ++hf)
+        tma_load_3d(base + st * C::kKVStage + hf * kKVHalf + lane * R * 128, tm, hf * 64, s.h, row, &fulls[st]);
+    }
+    __syncwarp();
+  }
+  return true;
+}
+
+// Page sizes that are not a power of two of at least 8: a lane gathers four rows at a time (tile::gather4), one
+// copy per 64-dim half, their pages loaded a tile ahead.  Positions behind the end repeat the last
+// one and a bad page's (reported) read the pool's row 0: neither is seen by a row whose result means
+// anything.
+template <int D>
+__device__ bool tree_load_rows(const TreeArgs& a, Ctl* ctl, uint32_t sb, const Seg& s, uint32_t t, bool v) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  const int kv_end = s.P + s.T;
+  uint64_t* fulls = v ? ctl->v_full : ctl->k_full;
+  uint64_t* empties = v ? ctl->v_empty : ctl->k_empty;
+  const CUtensorMap* tm = v ? &a.tm_v : &a.tm_k;
+  const uint32_t base = sb + (v ? C::kOffV : C::kOffK);
+  const int quad = lane & 15, half = lane >> 4;  // four rows, and their 64-dim half (D 64: lanes 0..15)
+  int32_t page[4];
+  uint32_t in_page[4];
+  bool listed[4];
+  auto load_pages = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t pidx;
+      a.page_div.divmod((uint32_t)min(j * kBN + 4 * quad + i, kv_end - 1), pidx, in_page[i]);
+      listed[i] = (int)pidx < s.np;
+      page[i] = listed[i] ? ld(a.kv_indices + s.p0 + pidx) : 0;
+    }
+  };
+  load_pages(s.j0);
+  for (int j = s.j0; j < s.j0 + s.n; ++j, ++t) {
+    int row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = page[i] >= 0 && page[i] < a.num_pages;
+      if (!listed[i] || !in) report(a.err_word, !listed[i] ? PKV_DEVERR_LENGTH : PKV_DEVERR_PAGE_OOB);
+      row[i] = listed[i] && in ? page[i] * a.page_size + (int)in_page[i] : 0;
+    }
+    if (j + 1 < s.j0 + s.n) load_pages(j + 1);
+    const int st = t & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empties[st], ((t >> 1) & 1) ^ 1))) {
+      drain(fulls, t);
+      return false;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(&fulls[st], C::kKVStage);
+    __syncwarp();
+    if (half < C::kHalves)
+      tma_gather4(base + st * C::kKVStage + half * kKVHalf + quad * 512, tm, s.h * D + half * 64, row[0], row[1], row[2],
+                  row[3], &fulls[st]);
+    __syncwarp();
+  }
+  return true;
 }
 
 // ---------------------------------------------------------------------------------------------
-// MMA issuers: one thread each.  A tile of a segment goes to slot (tile & 1) with one Q tile, and to
-// both slots with two.
+// MMA issuers: one thread each.
 // ---------------------------------------------------------------------------------------------
-PKV_DEV bool next_seg_thread(Ctl* ctl, int i, Seg& s) {
-  const int r = i % kSegRing;
-  if (!mbar_wait(&ctl->seg_full[r], (i / kSegRing) & 1)) return false;
-  s = ctl->seg[r];
-  mbar_arrive(&ctl->seg_empty[r]);
+template <int D>
+__device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem, const Seg& s, uint32_t seg, uint32_t t) {
+  using C = Cfg<D>;
+  constexpr uint32_t idesc = umma_idesc_bf16(kBM, kBN, false);
+  const uint64_t qdesc = smem_desc_sw128(sb + C::kOffQ, 16, 1024);
+  const uint64_t kdesc0 = smem_desc_sw128(sb + C::kOffK, 16, 1024);
+  if (!mbar_wait(&ctl->q_full, seg & 1)) return false;
+  for (int j = 0; j < s.n; ++j, ++t) {
+    const int st = t & 1;
+    const uint32_t ph = (t >> 1) & 1;
+    if (!mbar_wait(&ctl->k_full[st], ph)) return false;
+    if (!mbar_wait(&ctl->s_free[st], ph ^ 1)) return false;
+    tc_fence_after();
+    const uint64_t kdesc = kdesc0 + ((st * C::kKVStage) >> 4);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t qoff = ((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4;
+      const uint32_t koff = ((ks >> 2) * kKVHalf + (ks & 3) * 32) >> 4;
+      umma_ss(tmem + st * 64, qdesc + qoff, kdesc + koff, idesc, ks > 0);
+    }
+    umma_commit(&ctl->s_full[st]);
+    umma_commit(&ctl->k_empty[st]);
+  }
   return true;
 }
 
 template <int D>
-__device__ bool tree_mma_qk(Ctl* ctl, uint32_t sb, uint32_t tmem) {
-  using C = Cfg<D>;
-  constexpr uint32_t idesc = umma_idesc_bf16(kBM, kBN, false);
-  const uint64_t qdesc0 = smem_desc_sw128(sb + C::kOffQ, 16, 1024);
-  const uint64_t kdesc0 = smem_desc_sw128(sb + C::kOffRing, 16, 1024);
-  uint32_t kt = 0, qt[2] = {0, 0}, used[2] = {0, 0};  // K tiles, uses of the Q buffers and the slots so far
-  Seg s;
-  for (int i = 0;; ++i) {
-    if (!next_seg_thread(ctl, i, s)) return false;
-    if (s.nq == 0) return true;
-    for (int q = 0; q < s.nq; ++q)
-      if (!mbar_wait(&ctl->q_full[q], qt[q] & 1)) return false;
-    for (int j = 0; j < s.n; ++j, ++kt) {
-      const uint32_t st = (2 * kt) % C::kRing;
-      if (!mbar_wait(&ctl->full[st], ((2 * kt) / C::kRing) & 1)) return false;
-      const uint64_t kdesc = kdesc0 + ((st * C::kTile) >> 4);
-      for (int q = 0; q < s.nq; ++q) {
-        const int slot = s.nq == 2 ? q : (j & 1);
-        if (!mbar_wait(&ctl->s_free[slot], (used[slot] & 1) ^ 1)) return false;
-        tc_fence_after();
-        const uint64_t qdesc = qdesc0 + ((q * C::kTile) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * kHalfTile + (ks & 3) * 32) >> 4;
-          umma_ss(tmem + kColS + slot * 128, qdesc + off, kdesc + off, idesc, ks > 0);
-        }
-        umma_commit(&ctl->s_full[slot]);
-        mbar_arrive(&ctl->qk_issued[slot]);
-        ++used[slot];
-      }
-      umma_commit(&ctl->empty[st]);
-    }
-    for (int q = 0; q < s.nq; ++q, ++qt[q - 1]) umma_commit(&ctl->q_empty[q]);
-  }
-}
-
-// A pair of bf16 values with the non-finite ones replaced by 0.
-PKV_DEV uint32_t finite_bf16x2(uint32_t u) {
-  if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
-  if ((u & 0x7f800000u) == 0x7f800000u) u &= 0x0000ffffu;
-  return u;
-}
-// Non-zero where a pair holds an infinity or a NaN: an exponent of ones carries into the sign's place.
-PKV_DEV uint32_t nonfinite_bits(uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
-
-// What no weight may touch in a tile of V becomes zeros: the rows behind the last position, and the
-// infinities and NaNs of drafted tokens, which are noted.  By one warp, a row per lane at a time; the
-// prefix's rows are left alone.
-template <int D>
-__device__ void clean_v(uint8_t* vtile, Ctl* ctl, const Seg& s, int pos0) {
-  using C = Cfg<D>;
-  constexpr int kChunks = C::kHalves * 8;
-  const int lane = threadIdx.x & 31;
-  for (int r = max(0, s.P - pos0) + lane; r < kBN; r += 32) {
-    const int t = pos0 + r - s.P;
-    uint8_t* row = vtile + r * 128;
-    auto at = [&](int i) {  // chunks in an order that spreads the lanes over the banks
-      return reinterpret_cast<uint4*>(row + (i >> 3) * kHalfTile + (((i + r) & 7) << 4));
-    };
-    if (t >= s.T) {
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) *at(i) = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      uint32_t bad = 0;
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const uint4 u = *at(i);
-        bad |= nonfinite_bits(u.x) | nonfinite_bits(u.y) | nonfinite_bits(u.z) | nonfinite_bits(u.w);
-      }
-      if (bad) {
-#pragma unroll 1
-        for (int i = 0; i < kChunks; ++i) {
-          const uint4 u = *at(i);
-          *at(i) = make_uint4(finite_bf16x2(u.x), finite_bf16x2(u.y), finite_bf16x2(u.z), finite_bf16x2(u.w));
-        }
-        atomicOr(&ctl->bad[t >> 5], 1u << (t & 31));
-        ctl->bad_any = 1u;
-      }
-    }
-  }
-  fence_proxy_async_smem();  // before the MMA reads the tile
-  __syncwarp();
-}
-
-// PV warp.  Its first lane issues; the whole warp cleans the V tiles that reach past the prefix, while
-// the softmax is still at work on their scores.
-template <int D>
-__device__ bool tree_mma_pv(Ctl* ctl, uint8_t* smem, uint32_t tmem) {
+__device__ bool tree_mma_pv(Ctl* ctl, uint32_t sb, uint32_t tmem, const Seg& s, uint32_t t) {
   using C = Cfg<D>;
   constexpr uint32_t idesc = umma_idesc_bf16(kBM, D, true);
-  const int lane = threadIdx.x & 31;
-  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem) + C::kOffRing, kHalfTile, 1024);
-  uint32_t vt = 0, used[2] = {0, 0};
-  auto wait = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
-  Seg s;
-  for (int i = 0;; ++i) {
-    if (!next_seg(ctl, i, s)) return false;
-    if (s.nq == 0) return true;
-    if (!wait(&ctl->o_free, (i & 1) ^ 1)) return false;  // the last segment's O and notes have been read
-    if (ctl->bad_any) {
-      ctl->bad[lane] = 0u;
-      __syncwarp();
-      if (lane == 0) ctl->bad_any = 0u;
-      __syncwarp();
-    }
-    for (int j = 0; j < s.n; ++j, ++vt) {
-      const uint32_t st = (2 * vt + 1) % C::kRing;
-      const uint64_t vdesc = vdesc0 + ((st * C::kTile) >> 4);
-      const int pos0 = (s.j0 + j) * kBN;
-      if (!wait(&ctl->full[st], ((2 * vt + 1) / C::kRing) & 1)) return false;
-      if (pos0 + kBN > s.P) clean_v<D>(smem + C::kOffRing + st * C::kTile, ctl, s, pos0);
-      for (int q = 0; q < s.nq; ++q) {
-        const int slot = s.nq == 2 ? q : (j & 1);
-        const bool first = s.nq == 2 ? j == 0 : j < 2;
-        if (!wait(&ctl->p_full[slot], used[slot] & 1)) return false;
-        // With two Q tiles the order is PV 0, QK 0, PV 1, QK 1, so that each slot's products run beside the
-        // other's softmax; left to themselves the slots fall into step and both products wait for both
-        // softmaxes (4 requests of 64 tokens over 32700 positions: 134 us, 129 so).
-        if (s.nq == 2 && (q == 0 || j + 1 < s.n) && !wait(&ctl->qk_issued[q ^ 1], used[q ^ 1] & 1)) return false;
-        tc_fence_after();
-        if (lane == 0) {
+  const uint64_t vdesc0 = smem_desc_sw128(sb + C::kOffV, kKVHalf, 1024);
+  for (int j = 0; j < s.n; ++j, ++t) {
+    const int st = t & 1;
+    const uint32_t ph = (t >> 1) & 1;
+    if (!mbar_wait(&ctl->p_full[st], ph)) return false;
+    if (!mbar_wait(&ctl->v_full[st], ph)) return false;
+    tc_fence_after();
+    const uint64_t vdesc = vdesc0 + ((st * C::kKVStage) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kBN / 16; ++ks)
-            umma_ts(tmem + kColO + slot * 128, tmem + kColS + slot * 128 + ks * 8, vdesc + ((ks * 2048) >> 4), idesc,
-                    !first || ks > 0);
-          umma_commit(&ctl->s_free[slot]);
-        }
-        __syncwarp();
-        ++used[slot];
-      }
-      if (lane == 0) umma_commit(&ctl->empty[st]);
+    for (int ks = 0; ks < kBN / 16; ++ks) {
+      const uint32_t pa = tmem + st * 64 + (ks >> 1) * 32 + (ks & 1) * 8;
+      umma_ts(tmem + kColO, pa, vdesc + ((ks * 2048) >> 4), idesc, j > 0 || ks > 0);
     }
-    if (lane == 0) mbar_arrive(&ctl->x_full);  // this segment's notes are made
+    umma_commit(&ctl->v_empty[st]);
+    umma_commit(&ctl->s_free[st]);  // P consumed; also marks this PV done
   }
+  return true;
 }
 
-// ---------------------------------------------------------------------------------------------
-// Softmax and epilogue
-// ---------------------------------------------------------------------------------------------
 // A row's mask words: the first four in registers (loaded before they are needed), others from memory.
 struct MaskRow {
   const uint32_t* m;  // nullptr: an unused row
@@ -641,28 +429,49 @@ PKV_DEV uint32_t visible(const MaskRow& k, int T, int t0) {
   return v;
 }
 
-// Adds the non-finite values of dims [d0, d0 + n) of the noted drafted tokens that the row sees to what
-// this thread has written at `to` (the rest of them is in it already).
-template <int D, typename T>
-__device__ __noinline__ void add_nonfinite(const TreeArgs& a, const Ctl* ctl, int P, int nodes, int p0, int np, int h,
-                                           const uint32_t* m, int d0, int n, T* to) {
-  for (int w = 0; w < (nodes + 31) / 32; ++w) {
-    uint32_t hit = ctl->bad[w] & (w < a.words ? ld(m + w) : 0u);
-    while (hit) {
-      const int t = 32 * w + __ffs(hit) - 1;
-      hit &= hit - 1;
-      const int pos = P + t, pidx = pos / a.page_size;
-      if (pidx >= np) continue;
-      const int32_t page = ld(a.kv_indices + p0 + pidx);
-      if (page < 0 || page >= a.num_pages) continue;
-      const __nv_bfloat16* src =
-          a.v_pool + (((int64_t)page * a.page_size + pos % a.page_size) * a.num_kv_heads + h) * D + d0;
-      for (int i = 0; i < n; ++i) {
-        const float x = __bfloat162float(src[i]);
-        if (!(fabsf(x) < INFINITY)) to[i] = (T)((float)to[i] + x);
+// A pair of bf16 values with the non-finite ones replaced by 0.
+PKV_DEV uint32_t finite_bf16x2(uint32_t u) {
+  if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+  if ((u & 0x7f800000u) == 0x7f800000u) u &= 0x0000ffffu;
+  return u;
+}
+// Non-zero where a pair holds an infinity or a NaN: an exponent of ones carries into the sign's place.
+PKV_DEV uint32_t nonfinite_bits(uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+
+// What no weight may touch in a tile of V becomes zeros: the rows behind the last position, and the
+// infinities and NaNs of drafted tokens, which are noted.  By the four softmax warps, a thread per 64-dim
+// half of a row; the prefix's rows are left alone.
+template <int D>
+__device__ void clean_v(uint8_t* vtile, Ctl* ctl, const Seg& s, int pos0, int tid) {
+  using C = Cfg<D>;
+  const int row = tid & (kBN - 1), half = tid / kBN;
+  const int t = pos0 + row - s.P;
+  if (half < C::kHalves && t >= 0) {
+    uint8_t* at = vtile + half * kKVHalf + row * 128;
+    auto chunk = [&](int i) { return reinterpret_cast<uint4*>(at + (((i + row) & 7) << 4)); };  // spread over the banks
+    if (t >= s.T) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *chunk(i) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 u = *chunk(i);
+        bad |= nonfinite_bits(u.x) | nonfinite_bits(u.y) | nonfinite_bits(u.z) | nonfinite_bits(u.w);
+      }
+      if (bad) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const uint4 u = *chunk(i);
+          *chunk(i) = make_uint4(finite_bf16x2(u.x), finite_bf16x2(u.y), finite_bf16x2(u.z), finite_bf16x2(u.w));
+        }
+        atomicOr(&ctl->bad[t >> 5], 1u << (t & 31));
+        ctl->bad_any = 1u;
       }
     }
   }
+  fence_proxy_async_smem();  // before the MMA reads the tile
 }
 
 PKV_DEV float max3f(float a, float b, float c) {
@@ -698,341 +507,232 @@ PKV_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// The weights 2^(v sc + neg) of 32 scores as bf16 pairs, and their sum.
-PKV_DEV float weights32(const float (&v)[32], float sc, float neg, uint32_t (&pk)[16]) {
-  const uint64_t sc2 = f32x2(sc, sc), neg2 = f32x2(neg, neg);
-  uint64_t t0 = f32x2(0.f, 0.f), t1 = t0;
-#pragma unroll
-  for (int e = 0; e < 16; e += 2) {
-    float x0, x1, x2, x3;
-    split_f32x2(fma_f32x2(f32x2(v[2 * e], v[2 * e + 1]), sc2, neg2), x0, x1);
-    split_f32x2(fma_f32x2(f32x2(v[2 * e + 2], v[2 * e + 3]), sc2, neg2), x2, x3);
-    const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
-    t0 = add_f32x2(t0, f32x2(p0, p1));
-    t1 = add_f32x2(t1, f32x2(p2, p3));
-    pk[e] = pack_bf16x2(p0, p1);
-    pk[e + 1] = pack_bf16x2(p2, p3);
-  }
-  float lo, hi;
-  split_f32x2(add_f32x2(t0, t1), lo, hi);
-  return lo + hi;
+// acc + (float)(low or high bf16 half of v), one rounding
+PKV_DEV float add_bf16_lo(uint32_t v, float acc) {
+  float r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, lo, %2;\n\t}" : "=f"(r) : "r"(v), "f"(acc));
+  return r;
+}
+PKV_DEV float add_bf16_hi(uint32_t v, float acc) {
+  float r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, hi, %2;\n\t}" : "=f"(r) : "r"(v), "f"(acc));
+  return r;
 }
 
-// A row's N chunks of 32 scores from chunk ch0 on, in TMEM at ts: the new reference maximum, the factor of
-// what was summed under the old one m, P written over S as bf16 pairs, the other chunks' P zeroed, and
-// the sum of the weights.  Two passes over the scores, the next chunk's load in flight while one is
-// worked on; the first chunk stays in registers between them.
-template <int N>
-PKV_DEV float softmax_tile(uint32_t ts, int ch0, float sc, float m, float& m_ref, float& corr) {
-  float a[32], b[32];  // odd and even chunks
-  const uint32_t s0 = ts + ch0 * 32, p0 = ts + ch0 * 16;
-  float mx = -INFINITY;
-  if constexpr (N == 1) {
-    tmem_ld32(s0, b);
-    tmem_wait_ld32(b);
-    mx = max32(b);
-  } else {
-    tmem_ld32(s0 + (N - 1) * 32, a);
-    tmem_wait_ld32(a);
-    if constexpr (N == 4) {
-      tmem_ld32(s0 + 64, b);
-      mx = max32(a);
-      tmem_wait_ld32(b);
-      tmem_ld32(s0 + 32, a);
-      mx = fmaxf(mx, max32(b));
-      tmem_wait_ld32(a);
-    }
-    tmem_ld32(s0, b);
-    mx = N == 4 ? fmaxf(mx, max32(a)) : max32(a);
-    tmem_wait_ld32(b);
-    mx = fmaxf(mx, max32(b));
-  }
-  const float m_new = fmaxf(m, mx * sc);
-  // the maximum moves only when it grows by more than 2^8, so that O is seldom rescaled
-  const bool resc = m_new > m + 8.f;
-  m_ref = resc ? m_new : m;
-  corr = resc ? ex2(m - m_ref) : 1.f;
-  const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen so far: every weight is 0
-  // P of chunk c goes over columns of S of chunk c / 2, which has been read by then
-  uint32_t pk[16];
-  float tot;
-  if constexpr (N == 1) {
-    tot = weights32(b, sc, neg, pk);
-    tmem_st16(p0, pk);
-  } else {
-    tmem_ld32(s0 + 32, a);
-    tot = weights32(b, sc, neg, pk);
-    tmem_wait_ld32(a);
-    tmem_st16(p0, pk);
-    if constexpr (N == 4) tmem_ld32(s0 + 64, b);
-    tot += weights32(a, sc, neg, pk);
-    if constexpr (N == 4) tmem_wait_ld32(b);
-    tmem_st16(p0 + 16, pk);
-    if constexpr (N == 4) {
-      tmem_ld32(s0 + 96, a);
-      tot += weights32(b, sc, neg, pk);
-      tmem_wait_ld32(a);
-      tmem_st16(p0 + 32, pk);
-      tot += weights32(a, sc, neg, pk);
-      tmem_st16(p0 + 48, pk);
-    }
-  }
-  if constexpr (N < 4) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) pk[e] = 0u;
-#pragma unroll 1
-    for (int c = N; c < 4; ++c) tmem_st16(ts + ((ch0 + c) & 3) * 16, pk);
-  }
-  return tot;
-}
-
+// A thread owns a row of the tile.
 template <int D>
-__device__ void tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_t tmem) {
+__device__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_t tmem, const Seg& s, uint32_t t) {
   using C = Cfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot = (warp - kSoftmaxWarp0) >> 2;
-  const int wq = warp & 3;       // TMEM lane quadrant
-  const int r = wq * 32 + lane;  // tile row
-  const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
-  const uint32_t ts = tq + kColS + slot * 128;
-  const uint32_t to = tq + kColO + slot * 128;
+  const int wq = warp & 3;       // TMEM lane quadrant this warp may access
+  const int r = wq * 32 + lane;  // tile row == TMEM lane
+  const int tid = (warp - 2) * 32 + lane;
+  const uint32_t taddr = tmem + ((uint32_t)(wq * 32) << 16);
   const int G = a.group;
+  const int rt = r / G, g = r - rt * G;  // token of the tile, head of the group
+  const int tok = s.t0 + rt;
+  const bool valid = rt < a.tpt && tok < s.T;
+  const bool warp_live = __any_sync(0xffffffffu, valid);
   const bool pos_scale = a.scale_log2 > 0.f;
   const float sc = pos_scale ? a.scale_log2 : 1.f;
-  uint32_t used[2] = {0, 0};  // uses of both slots before this segment
-  bool ok = true;
+  MaskRow mask{valid ? a.mask + (int64_t)(s.q0 + tok) * a.words : nullptr, a.words, {0u, 0u, 0u, 0u}};
+  if ((s.j0 + s.n) * kBN > s.P) load_mask(mask);
+  float m_used = -INFINITY;  // running max of the scaled (log2) scores
+  float l = 0.f;             // sum of the weights (for the LSE)
+  float lr = 0.f;            // ... as rounded to bf16 for the PV MMA (for O)
 
-  for (int i = 0; ok; ++i) {
-    Seg s;
-    if (!next_seg(ctl, i, s)) {
-      ok = false;
-      break;
-    }
-    if (s.nq == 0) break;
-    const bool two = s.nq == 2;
-    // the thread's row among the distinct ones, and its copy's share of a tile's four 32-column chunks
-    const int rr = s.rep == 4 ? lane : s.rep == 2 ? r & 63 : r;
-    const int copy = s.rep == 4 ? wq : s.rep == 2 ? wq >> 1 : 0;
-    const int nch = 4 / s.rep, ch0 = copy * nch;
-    const int rt = rr / G, g = rr - rt * G;  // token of the tile, head of the group
-    const int tok = s.t0 + (two ? slot * a.tpt : 0) + rt;
-    const bool valid = rt < (s.rep == 4 ? a.tpt4 : s.rep == 2 ? a.tpt2 : a.tpt) && tok < s.T;
-    const bool warp_live = __any_sync(0xffffffffu, valid);
-    MaskRow mask{valid ? a.mask + (int64_t)(s.q0 + tok) * a.words : nullptr, a.words, {0u, 0u, 0u, 0u}};
-    if ((s.j0 + s.n) * kBN > s.P) load_mask(mask);
-    float m = -INFINITY, l = 0.f;  // running maximum of the scaled (log2) scores, sum of weights
-    uint32_t n_used = used[slot];
-
-    for (int jj = two ? 0 : slot; jj < s.n && ok; jj += two ? 1 : 2, ++n_used) {
-      const int pos0 = (s.j0 + jj) * kBN;
-      const bool special = pos0 + kBN > s.P;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->s_full[slot], n_used & 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (warp_live) {
-        if (special || !pos_scale) {  // masked (and scaled) scores take the place of the scores
-#pragma unroll 1
-          for (int ch = ch0; ch < ch0 + nch; ++ch) {
-            float v[32];
-            tmem_ld32(ts + ch * 32, v);
-            const uint32_t vis = special ? visible(mask, s.T, pos0 + 32 * ch - s.P) : 0xffffffffu;
-            const float mul = pos_scale ? 1.f : a.scale_log2;
-            tmem_wait_ld32(v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] * mul : -INFINITY;
-            tmem_st32(ts + ch * 32, v);
-          }
-          tmem_wait_st();
-        }
-        float m_ref, corr, tot;
-        if (nch == 1)
-          tot = softmax_tile<1>(ts, ch0, sc, m, m_ref, corr);
-        else if (nch == 2)
-          tot = softmax_tile<2>(ts, ch0, sc, m, m_ref, corr);
-        else
-          tot = softmax_tile<4>(ts, ch0, sc, m, m_ref, corr);
-        const bool resc = m_ref > m;
-        l = l * corr + tot;
-        m = m_ref;
-        const bool later = two ? jj > 0 : jj > 1;  // O holds earlier tiles (whose PV is done: S was free)
-        if (later && __any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
-            float v[32];
-            tmem_ld32(to + ch * 32, v);
-            tmem_wait_ld32(v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= corr;
-            tmem_st32(to + ch * 32, v);
-          }
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->p_full[slot]);
-    }
-    if (!ok) break;
-
-    // every PV of the segment is done, in both slots
-    if (two) {
-      used[0] += s.n;
-      used[1] += s.n;
-    } else {
-      used[0] += (s.n + 1) / 2;
-      used[1] += s.n / 2;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (used[k] > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->s_free[k], (used[k] - 1) & 1));
-    // the row states of slots and copies change hands (the previous segment's have been read)
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->x_free, (i & 1) ^ 1));
-    if (!ok) break;
-    ctl->xm[slot][r] = m;
-    ctl->xl[slot][r] = l;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->x_full);
-    ok = __all_sync(0xffffffffu, mbar_wait(&ctl->x_full, i & 1));
-    if (!ok) break;
-    // From here to the end of the segment nothing can give up: all eight warps have come this far.
+  for (int j = 0; j < s.n; ++j, ++t) {
+    const int st = t & 1;
+    const uint32_t ph = (t >> 1) & 1;
+    const int pos0 = (s.j0 + j) * kBN;
+    const bool special = pos0 + kBN > s.P;
+    if (!__all_sync(0xffffffffu, mbar_wait(&ctl->s_full[st], ph))) return false;
     tc_fence_after();
-    const bool any_bad = ctl->bad_any != 0u;
-    float mt = m, lt = l, om = -INFINITY;  // over every state of the row; the other slot's of this thread
-    if (!two) {
-      const int step = kBM / s.rep;
-      float km[8], kl[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool on = (k >> 1) < s.rep;
-        km[k] = on ? ctl->xm[k & 1][rr + (k >> 1) * step] : -INFINITY;
-        kl[k] = on ? ctl->xl[k & 1][rr + (k >> 1) * step] : 0.f;
+    if (warp_live) {
+      float s0[32], s1[32];  // the row's scores, positions [0, 32) and [32, 64) of the tile
+      uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
+      if (special) {
+        see0 = visible(mask, s.T, pos0 - s.P);
+        see1 = visible(mask, s.T, pos0 + 32 - s.P);
       }
-      om = ctl->xm[slot ^ 1][r];
-      mt = max3f(max3f(km[0], km[1], km[2]), max3f(km[3], km[4], km[5]), fmaxf(km[6], km[7]));
-      lt = 0.f;
+      __syncwarp();
+      tmem_fetch32(taddr + st * 64, s0);
+      tmem_fetch32(taddr + st * 64 + 32, s1);
+      tmem_wait_ld32(s0);
+      tmem_wait_ld32(s1);
+      if (!pos_scale) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) lt += kl[k] * (km[k] == -INFINITY ? 0.f : ex2(km[k] - mt));
-    }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    const float f_mine = m == -INFINITY ? 0.f : ex2(m - mt) * inv;
-    const float f_other = om == -INFINITY ? 0.f : ex2(om - mt) * inv;
-    const bool nan = !(lt == lt);  // a NaN among the scores: in every dim
-    // (a slot or copy that saw nothing may hold anything: its O must not be used)
-    const bool plain = __all_sync(0xffffffffu, !valid || (f_mine > 0.f && (two || f_other > 0.f)));
-    const int64_t orow = (int64_t)(s.q0 + tok) * a.num_q_heads + (int64_t)s.h * G + g;
-    const int prow = (two ? slot * kBM : 0) + rr;
-    // Two Q tiles: all dims of the thread's own O.  One: half of the dims, from both slots' O; of 32 dims
-    // a copy finishes 32 / rep, for which the other copies leave theirs in scratch, so it reads its
-    // groups of 8 dims rotated: the first 4 / rep are its own.
-    const int c0 = two ? 0 : slot * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
-    const int own = 4 / s.rep, rot = copy * own;
-    float* scratch = reinterpret_cast<float*>(smem + C::kOffScratch) + slot * 3 * 32 * 32 + lane;
+        for (int c = 0; c < 32; ++c) {
+          s0[c] *= a.scale_log2;
+          s1[c] *= a.scale_log2;
+        }
+      }
+      if (special) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          s0[c] = (see0 >> c) & 1u ? s0[c] : -INFINITY;
+          s1[c] = (see1 >> c) & 1u ? s1[c] : -INFINITY;
+        }
+      }
+      const float m_new = fmaxf(m_used, fmaxf(max32(s0), max32(s1)) * sc);
+      // the maximum moves only when it grows by more than 2^8, so that O is seldom rescaled
+      const bool resc = m_new > m_used + 8.f;
+      const float m_ref = resc ? m_new : m_used;
+      const float corr = resc ? ex2(m_used - m_ref) : 1.f;
+      const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen so far: every weight is 0
+      const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(neg, neg);
+      float tot = 0.f, rtot = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float(&sv)[32] = hf ? s1 : s0;
+        uint32_t pk[16];
+        uint64_t acc_a = f32x2(0.f, 0.f), acc_b = f32x2(0.f, 0.f);
+        float rs0 = 0.f, rs1 = 0.f, rs2 = 0.f, rs3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          float x0, x1, x2, x3;
+          split_f32x2(fma_f32x2(f32x2(sv[2 * c], sv[2 * c + 1]), sc2, nm2), x0, x1);
+          split_f32x2(fma_f32x2(f32x2(sv[2 * c + 2], sv[2 * c + 3]), sc2, nm2), x2, x3);
+          const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+          acc_a = add_f32x2(acc_a, f32x2(p0, p1));
+          acc_b = add_f32x2(acc_b, f32x2(p2, p3));
+          pk[c] = pack_bf16x2(p0, p1);
+          pk[c + 1] = pack_bf16x2(p2, p3);
+          rs0 = add_bf16_lo(pk[c], rs0);
+          rs1 = add_bf16_hi(pk[c], rs1);
+          rs2 = add_bf16_lo(pk[c + 1], rs2);
+          rs3 = add_bf16_hi(pk[c + 1], rs3);
+        }
+        float e0, e1;
+        split_f32x2(add_f32x2(acc_a, acc_b), e0, e1);
+        tot += e0 + e1;
+        rtot += (rs0 + rs1) + (rs2 + rs3);
+        // P (bf16 pairs) over the first 16 columns of each 32-column half of the S buffer
+        tmem_st16(taddr + st * 64 + hf * 32, pk);
+      }
+      l = l * corr + tot;
+      lr = lr * corr + rtot;
+      m_used = m_ref;
+      if (j > 0 && __any_sync(0xffffffffu, resc)) {
+        // O is rescaled only after the previous tile's PV is done
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->s_free[(t - 1) & 1], ((t - 1) >> 1) & 1))) return false;
+        tc_fence_after();
 #pragma unroll 1
-    for (int ch = c0; ch < c1; ++ch) {
-      float o[32];
-      if (two) {
-        tmem_ld32(to + ch * 32, o);
-        tmem_wait_ld32(o);
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float o[32];
+          tmem_fetch32(taddr + kColO + ch * 32, o);
+          tmem_wait_ld32(o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = plain || f_mine > 0.f ? o[e] * f_mine : 0.f;
-      } else {
-        float x[32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t col = ch * 32 + ((j + rot) & 3) * 8;
-          tmem_ld8(to + col, o + 8 * j);
-          tmem_ld8(tq + kColO + (slot ^ 1) * 128 + col, x + 8 * j);
-        }
-        tmem_wait_ld32(o);
-        tmem_wait_ld32(x);
-        if (plain) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(x[e], f_other, o[e] * f_mine);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = (f_mine > 0.f ? o[e] * f_mine : 0.f) + (f_other > 0.f ? x[e] * f_other : 0.f);
+          for (int i = 0; i < 32; ++i) o[i] *= corr;
+          tmem_st32(taddr + kColO + ch * 32, o);
         }
       }
-      if (nan) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = lt;
-      }
-      // scratch: areas of [8 dims][32 rows]; with four copies area 3 d + j - 1 is for copy d from the copy j
-      // before it, with two area 4 (row block) + 2 d + j - 2 for copy d's group j - 2
-      if (s.rep == 4) {
-#pragma unroll
-        for (int j = 1; j < 4; ++j) {
-          float* to_copy = scratch + (3 * ((copy + j) & 3) + j - 1) * 256;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) to_copy[e * 32] = o[8 * j + e];
-        }
-        named_bar_sync(1 + slot, 128);
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] += scratch[(3 * copy + j - 1) * 256 + e * 32];
-        named_bar_sync(1 + slot, 128);
-      } else if (s.rep == 2) {
-        float* block = scratch + (wq & 1) * 4 * 256;
-#pragma unroll
-        for (int j = 2; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) block[(2 * (copy ^ 1) + j - 2) * 256 + e * 32] = o[8 * j + e];
-        named_bar_sync(1 + slot, 128);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[8 * j + e] += block[(2 * copy + j) * 256 + e * 32];
-        named_bar_sync(1 + slot, 128);
-      }
-      if (valid) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= own) continue;
-          const int d0 = ch * 32 + ((j + rot) & 3) * 8;
-          const int e = 8 * j;
-          if (s.part < 0) {
-            __nv_bfloat16* dst = a.out + orow * D + d0;
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
-            if (any_bad) add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 8, dst);
-          } else {
-            float* dst = a.part_o + (((int64_t)s.part * (D / 4) + d0 / 4) * a.part_rows + prow) * 4;
-            float* dst1 = dst + (int64_t)a.part_rows * 4;
-            *reinterpret_cast<float4*>(dst) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            *reinterpret_cast<float4*>(dst1) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
-            if (any_bad) {
-              add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0, 4, dst);
-              add_nonfinite<D>(a, ctl, s.P, s.T, s.p0, s.np, s.h, mask.m, d0 + 4, 4, dst1);
-            }
-          }
-        }
-      }
+      tmem_wait_st();
     }
-    if (valid && copy == 0 && (two || slot == 0)) {
-      const float lse_v = (mt + log2f(lt)) * kLn2;
-      if (s.part >= 0)
-        a.part_lse[(int64_t)s.part * a.part_rows + prow] = lse_v;
-      else if (a.lse)
-        a.lse[orow] = lse_v;
+    if (special) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&ctl->v_full[st], ph))) return false;
+      clean_v<D>(smem + C::kOffV + st * C::kKVStage, ctl, s, pos0, tid);
     }
     tc_fence_before();
-    fence_proxy_async_smem();  // the scratch may become a Q tile
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&ctl->o_free);
-      mbar_arrive(&ctl->x_free);
-      __threadfence_block();
-      atomicAdd(&ctl->epilogues, 1u);
+    if (lane == 0) mbar_arrive(&ctl->p_full[st]);
+    __syncwarp();
+  }
+  // the last PV is done
+  const uint32_t last = t - 1;
+  if (!__all_sync(0xffffffffu, mbar_wait(&ctl->s_free[last & 1], (last >> 1) & 1))) return false;
+  ctl->inv[r] = l == 0.f ? 0.f : 1.f / lr;  // (NaN among the scores: in every dim)
+  if (valid) {
+    const float lse_v = (m_used + log2f(l)) * kLn2;
+    if (s.part >= 0)
+      a.part_lse[(int64_t)s.part * kBM + r] = lse_v;
+    else if (a.lse)
+      a.lse[(int64_t)(s.q0 + tok) * a.num_q_heads + (int64_t)s.h * G + g] = lse_v;
+  }
+  return true;
+}
+
+// Adds the non-finite values of 32 dims from d0 on of the noted drafted tokens that the row sees to o.
+template <int D>
+PKV_DEV void add_nonfinite(const TreeArgs& a, const Ctl* ctl, const Seg& s, const uint32_t* m, int d0, float (&o)[32]) {
+  for (int w = 0; w < (s.T + 31) / 32; ++w) {
+    uint32_t hit = ctl->bad[w] & (w < a.words ? ld(m + w) : 0u);
+    while (hit) {
+      const int t = 32 * w + __ffs(hit) - 1;
+      hit &= hit - 1;
+      const int pos = s.P + t, pidx = pos / a.page_size;
+      if (pidx >= s.np) continue;
+      const int32_t page = ld(a.kv_indices + s.p0 + pidx);
+      if (page < 0 || page >= a.num_pages) continue;
+      const __nv_bfloat16* src =
+          a.v_pool + (((int64_t)page * a.page_size + pos % a.page_size) * a.num_kv_heads + s.h) * D + d0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float x = __bfloat162float(src[i]);
+        if (!(fabsf(x) < INFINITY)) o[i] += x;
+      }
     }
   }
-  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+}
+
+// Epilogue, by all eight warps: warp w reads TMEM lane quadrant w % 4, the softmax warps the first 64
+// dims of their rows, the others the second 64 (D 64: the softmax warps alone).  A whole unit's rows are
+// staged over the Q buffer and leave by coalesced 16-byte stores; a part's go to scratch in fp32.
+template <int D>
+__device__ void tree_epilogue(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_t tmem, const Seg& s) {
+  using C = Cfg<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wq = warp & 3;
+  const int r = wq * 32 + lane;
+  const bool softmax_warp = warp >= 2 && warp < 2 + kSoftmaxWarps;
+  const int G = a.group;
+  const int rt = r / G, tok = s.t0 + rt;
+  const bool valid = rt < a.tpt && tok < s.T;
+  uint8_t* stage = smem + C::kOffQ;
+  tc_fence_after();
+  if ((softmax_warp || C::kHalves == 2) && __any_sync(0xffffffffu, valid)) {
+    const int hf = softmax_warp ? 0 : 1;
+    const float inv = ctl->inv[r];
+    const bool any_bad = ctl->bad_any != 0u;
+#pragma unroll 1
+    for (int ch = 0; ch < 2; ++ch) {
+      float o[32];
+      __syncwarp();
+      tmem_fetch32(tmem + ((uint32_t)(wq * 32) << 16) + kColO + hf * 64 + ch * 32, o);
+      tmem_wait_ld32(o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = inv == 0.f ? 0.f : o[e] * inv;
+      if (any_bad && valid) add_nonfinite<D>(a, ctl, s, a.mask + (int64_t)(s.q0 + tok) * a.words, hf * 64 + ch * 32, o);
+      if (s.part < 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(stage + hf * kQHalf + r * 128 + (((ch * 4 + q) ^ (r & 7)) << 4)) =
+              make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                         pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+      } else if (valid) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o) + ((int64_t)s.part * (D / 4) + hf * 16 + ch * 8) * kBM + r;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dst[q * kBM] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      }
+    }
+  }
+  if (s.part < 0) {
+    __syncthreads();
+    constexpr int kCh = D / 8;  // 16-byte chunks of a row
+    const int rows = min(a.tpt, s.T - s.t0) * G;
+    for (int i = threadIdx.x; i < rows * kCh; i += kThreads) {
+      const int row = i / kCh, c = i % kCh;
+      const int tr = row / G;
+      const int64_t orow = (int64_t)(s.q0 + s.t0 + tr) * a.num_q_heads + (int64_t)s.h * G + (row - tr * G);
+      reinterpret_cast<uint4*>(a.out + orow * D)[c] = *reinterpret_cast<const uint4*>(
+          stage + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    }
+  }
+  fence_proxy_async_smem();  // the staged rows, before the next Q lands on them
 }
 
 template <int D, bool kRows>
-__global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) paged_tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -1047,78 +747,113 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tree_kernel(const __grid_co
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kOffCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 64) {
-    for (int i = 0; i < kSegRing; ++i) {
-      mbar_init(&ctl->seg_full[i], 1);
-      mbar_init(&ctl->seg_empty[i], 3 + 8);  // V producer, QK, PV, softmax warps
-    }
+    mbar_init(&ctl->q_full, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->q_full[i], 1);
-      mbar_init(&ctl->q_empty[i], 1);
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_empty[i], 1);
+      mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->v_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->qk_issued[i], 1);
-      mbar_init(&ctl->p_full[i], 4);
       mbar_init(&ctl->s_free[i], 1);
+      mbar_init(&ctl->p_full[i], kSoftmaxWarps);
     }
-    for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
-    }
-    mbar_init(&ctl->o_free, 8);
-    mbar_init(&ctl->x_full, 8 + 1);  // and the PV warp's notes
-    mbar_init(&ctl->x_free, 8);
     mbar_init(&ctl->qk_done, 1);
     mbar_init(&ctl->pv_done, 1);
+    ctl->failed = 0u;
     ctl->bad_any = 0u;
-    ctl->epilogues = 0u;
     for (int i = 0; i < kMaxNodes / 32; ++i) ctl->bad[i] = 0u;
     fence_mbar_init();
-    for (int i = 0; i < 3; ++i) prefetch_tmap(&a.tm_q[i]);
+    prefetch_tmap(&a.tm_q);
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
   }
-  int64_t total = 0;
-  Req first;
-  if (warp == 0) {
-    pdl_wait();
-    total = tree_stream_length(a, first);
-  }
   if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_alloc(&ctl->tmem_base, kTmemCols);
     tmem_relinquish();
+  }
+  pdl_wait();
+  Walk walk;
+  if (warp == 0) {
+    walk_start(a, walk);
+    const Seg s = walk_next(a, walk);
+    if (lane == 0) ctl->seg = s;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
   const uint32_t tmem = ctl->tmem_base;
 
+  uint32_t tiles = 0;  // of this CTA so far
+  for (uint32_t i = 0;; ++i) {
+    const Seg s = ctl->seg;
+    if (s.n == 0) break;
+    bool ok = true;
+    if (threadIdx.x == 0) {
+      // [64 dims x G heads x tokens] boxes; rows behind the request's are read along and not used
+      mbar_arrive_expect_tx(&ctl->q_full, C::kHalves * a.tpt * a.group * 128);
+#pragma unroll
+      for (int hf = 0; hf < C::kHalves; ++hf)
+        tma_load_3d(sb + C::kOffQ + hf * kQHalf, &a.tm_q, hf * 64, s.h * a.group, s.q0 + s.t0, &ctl->q_full);
+    }
+    __syncwarp();
+    if (warp == 0 || warp == kVWarp) {
+      ok = kRows ? tree_load_rows<D>(a, ctl, sb, s, tiles, warp == kVWarp) : tree_load_boxes<D>(a, ctl, sb, s, tiles, warp == kVWarp);
+      if (!ok && warp == 0) mbar_wait(&ctl->q_full, i & 1);
+    } else if (warp == 1) {
+      if (lane == 0) ok = tree_mma_qk<D>(ctl, sb, tmem, s, i, tiles);
+      __syncwarp();
+    } else if (warp == kPVWarp) {
+      if (lane == 0) ok = tree_mma_pv<D>(ctl, sb, tmem, s, tiles);
+      __syncwarp();
+    } else {
+      ok = tree_softmax<D>(a, smem, ctl, tmem, s, tiles);
+    }
+    if (!ok) {
+      report(a.err_word, PKV_DEVERR_TIMEOUT);
+      ctl->failed = 1u;
+    }
+    tc_fence_before();
+    __syncthreads();  // every warp is done with the segment; O is complete unless a wait gave up
+    if (ctl->failed) {  // no copy is left in flight (bounded waits)
+      if (warp == 0) drain(ctl->k_full, tiles + s.n);
+      if (warp == kVWarp) drain(ctl->v_full, tiles + s.n);
+      break;
+    }
+    tree_epilogue<D>(a, smem, ctl, tmem, s);
+    tiles += s.n;
+    Seg next{};
+    if (warp == 0) next = walk_next(a, walk);
+    tc_fence_before();
+    __syncthreads();  // the epilogue has read O, the notes and the staged rows
+    tc_fence_after();
+    if (warp == 0) {
+      if (ctl->bad_any) {
+        ctl->bad[lane] = 0u;
+        __syncwarp();
+        if (lane == 0) ctl->bad_any = 0u;
+      }
+      if (lane == 0) ctl->seg = next;
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
-    tree_walk<D, kRows>(a, ctl, sb, total, first);
-  } else if (warp == 3) {
-    tree_load_v<D, kRows>(a, ctl, sb);
-  } else if (warp == 1) {
+    if (lane == 0) a.cut[blockIdx.x] = walk.cut;
+    pdl_trigger();
+  }
+  // every MMA has completed before TMEM is released (immediate on the normal path)
+  if (warp == 1 || warp == kPVWarp) {
     if (lane == 0) {
-      if (!tree_mma_qk<D>(ctl, sb, tmem)) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      umma_commit(&ctl->qk_done);  // its MMAs have completed before TMEM is released
-      if (!mbar_wait(&ctl->qk_done, 0)) report(a.err_word, PKV_DEVERR_TIMEOUT);
+      uint64_t* done = warp == 1 ? &ctl->qk_done : &ctl->pv_done;
+      umma_commit(done);
+      if (!mbar_wait(done, 0)) report(a.err_word, PKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == 2) {
-    const bool ok = tree_mma_pv<D>(ctl, smem, tmem);
-    if (lane == 0) {
-      if (!ok) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      umma_commit(&ctl->pv_done);
-      if (!mbar_wait(&ctl->pv_done, 0)) report(a.err_word, PKV_DEVERR_TIMEOUT);
-    }
-    __syncwarp();
-  } else {
-    tree_softmax<D>(a, smem, ctl, tmem);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -1138,9 +873,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   if (cut.parts <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int prow = blockIdx.y * 32 + lane;
-  const int r = prow & (kBM - 1), tile = prow / kBM;
-  const int tok = cut.t0 + tile * a.tpt + r / a.group;
-  if (tile >= cut.nq || r >= a.group * a.tpt || tok >= cut.T) return;
+  const int tok = cut.t0 + prow / a.group;
+  if (prow >= a.group * a.tpt || tok >= cut.T) return;
   auto slot = [&](int p) -> int64_t { return (int64_t)2 * (c + p) + (p == 0 ? 1 : 0); };
   float mx = -INFINITY, tot = 0.f;
   float acc[kGroups][4] = {};
@@ -1151,10 +885,10 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     for (int k = 0; k < 4; ++k) {
       const bool on = p0 + k < cut.parts;
       const int64_t at = slot(on ? p0 + k : p0);
-      pl[k] = on ? ld(a.part_lse + at * a.part_rows + prow) : -INFINITY;
+      pl[k] = on ? ld(a.part_lse + at * kBM + prow) : -INFINITY;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
-        x[k][i] = ld(reinterpret_cast<const float4*>(a.part_o) + (at * (D / 4) + warp + 8 * i) * a.part_rows + prow);
+        x[k][i] = ld(reinterpret_cast<const float4*>(a.part_o) + (at * (D / 4) + warp + 8 * i) * kBM + prow);
     }
     const float mn = fmaxf(fmaxf(fmaxf(pl[0], pl[1]), fmaxf(pl[2], pl[3])), mx);
     if (mn > mx) {  // (not while every part so far is empty)
@@ -1181,7 +915,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     }
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  const int64_t orow = (int64_t)(cut.q0 + tok) * a.num_q_heads + (int64_t)cut.h * a.group + r % a.group;
+  const int64_t orow = (int64_t)(cut.q0 + tok) * a.num_q_heads + (int64_t)cut.h * a.group + prow % a.group;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i)
     *reinterpret_cast<uint2*>(a.out + orow * D + (warp + 8 * i) * 4) =
@@ -1234,21 +968,20 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* parents, 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Plan {
-  int G, tpt, part_rows, ncta;
+  int G, tpt, ncta;
   size_t off_lse, off_o, ws_bytes;
 };
 
-bool make_plan(int B, int Hq, int Hkv, int D, int max_nodes, int ncta, Plan& p) {
+bool make_plan(int B, int Hq, int Hkv, int D, int max_nodes, int sms, Plan& p) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_nodes < 0 || max_nodes > kMaxNodes) return false;
   if (D != 64 && D != 128) return false;
   p.G = Hq / Hkv;
   if (p.G > 16) return false;
   p.tpt = kBM / p.G;
-  p.part_rows = max_nodes > p.tpt ? 2 * kBM : kBM;
-  p.ncta = ncta;
-  p.off_lse = align256((size_t)ncta * sizeof(Cut));
-  p.off_o = align256(p.off_lse + (size_t)2 * ncta * p.part_rows * 4);
-  p.ws_bytes = align256(p.off_o + (size_t)2 * ncta * p.part_rows * D * 4);
+  p.ncta = 2 * sms;  // two per SM
+  p.off_lse = align256((size_t)p.ncta * sizeof(Cut));
+  p.off_o = align256(p.off_lse + (size_t)2 * p.ncta * kBM * 4);
+  p.ws_bytes = align256(p.off_o + (size_t)2 * p.ncta * kBM * D * 4);
   return true;
 }
 
@@ -1266,7 +999,7 @@ pkv_status launch(const Plan& p, const TreeArgs& a, cudaStream_t st) {
   }
   const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), kThreads, smem, st, a);
   if (s != PKV_OK) return s;
-  return pkv_host::launch_after(tree_merge_kernel<D>, dim3((unsigned)p.ncta, (unsigned)(p.part_rows / 32)), 256, 0, st, a);
+  return pkv_host::launch_after(tree_merge_kernel<D>, dim3((unsigned)p.ncta, kBM / 32), 256, 0, st, a);
 }
 
 }  // namespace
@@ -1298,10 +1031,10 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   if (num_q_heads % pool->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
   if (pool->num_pages * (int64_t)pool->page_size > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   const int D = pool->head_dim;
-  const int ncta = pkv_host::sm_count();
-  if (ncta <= 0) return PKV_ERR_CUDA;
+  const int sms = pkv_host::sm_count();
+  if (sms <= 0) return PKV_ERR_CUDA;
   Plan p;
-  if (!make_plan(batch_size, num_q_heads, pool->num_kv_heads, D, max_tree_len, ncta, p)) return PKV_ERR_UNSUPPORTED;
+  if (!make_plan(batch_size, num_q_heads, pool->num_kv_heads, D, max_tree_len, sms, p)) return PKV_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_INVALID_ARG;
 
@@ -1313,11 +1046,7 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   const uint64_t Db = (uint64_t)D * 2;
   a.box_rows = rows_path ? 8 : (ps < kBN ? ps : kBN);
   a.tpt = p.tpt;
-  a.tpt2 = 64 / p.G;
-  a.tpt4 = 32 / p.G;
-  if (!pkv_host::encode_tmap_3d(&a.tm_q[0], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt) ||
-      !pkv_host::encode_tmap_3d(&a.tm_q[1], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt2) ||
-      !pkv_host::encode_tmap_3d(&a.tm_q[2], q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt4) ||
+  if (!pkv_host::encode_tmap_3d(&a.tm_q, q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt) ||
       !(rows_path ? pkv_host::encode_tmap_rows(&a.tm_k, pool->k, Hkv * D, rows, D) &&
                         pkv_host::encode_tmap_rows(&a.tm_v, pool->v, Hkv * D, rows, D)
                   : pkv_host::encode_tmap_head(&a.tm_k, pool->k, D, Hkv, rows, a.box_rows) &&
@@ -1347,7 +1076,6 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   a.cut = (Cut*)ws;
   a.part_lse = (float*)(ws + p.off_lse);
   a.part_o = (float*)(ws + p.off_o);
-  a.part_rows = p.part_rows;
   cudaStream_t st = (cudaStream_t)stream;
   if (rows_path) return D == 128 ? launch<128, true>(p, a, st) : launch<64, true>(p, a, st);
   return D == 128 ? launch<128, false>(p, a, st) : launch<64, false>(p, a, st);
