@@ -13,6 +13,9 @@
 //    as well as many trees do.  A unit cut by a share's border leaves fp32 partial states, merged by
 //    log-sum-exp in a programmatic dependent launch.  The CTA takes its segments one after the other, with
 //    all warps meeting between them; the other CTA of the SM fills the gap.
+//  * Where a request may have more rows than a Q tile, CTAs 2 c and 2 c + 1 take the same share with a Q
+//    tile each, so that K and V come from DRAM once for both (each its own share: 4 requests of 64
+//    tokens over 32700 positions 178 us, 127 so).
 //  * Only tiles that reach past the prefix are masked.  There the V rows behind the last position
 //    and the infinities and NaNs of drafted tokens become 0 in shared memory (weight 0 times them
 //    would be NaN for rows that do not see them); rows that do see them get them added when they are
@@ -80,7 +83,7 @@ struct Ctl {
 static_assert(kMaxNodes / 32 == 32, "a warp clears the notes");
 
 // The unit that a CTA's share ends in the middle of, for the merge: its parts are the slots
-// 2c + 1, 2(c + 1), 2(c + 2), ...
+// 2c + 1, 2(c + 1), 2(c + 2), ... (paired: 2c + 1, 2(c + 2), 2(c + 4), ...)
 struct Cut {
   int32_t parts;  // 0: none
   int32_t q0, T, t0, h;
@@ -104,6 +107,7 @@ struct TreeArgs {
   FastDiv page_div;  // by page_size
   int32_t num_kv_heads, num_q_heads, group;
   int32_t tpt;       // tokens per Q tile
+  int32_t paired;    // CTAs 2 c and 2 c + 1 take the same share, a Q tile each
   int32_t batch, num_q_tokens, max_nodes;
   float scale_log2;
   Cut* cut;          // [CTAs]
@@ -117,7 +121,7 @@ struct TreeArgs {
 // What a request asks for: its rows, its KV, its units and their tiles.
 struct Req {
   int32_t q0, T, P, p0, np;
-  int32_t qtiles, tiles;  // Q tiles, KV tiles (0: nothing to do)
+  int32_t passes, tiles;  // over its KV by a head's Q tiles, KV tiles (0: nothing to do)
   int32_t cost;           // of a unit in the stream: its tiles and what an epilogue costs
 };
 
@@ -129,13 +133,14 @@ __device__ Req load_req(const TreeArgs& a, int b, bool check) {
   r.p0 = ld(a.kv_indptr + b);
   r.np = ld(a.kv_indptr + b + 1) - r.p0;
   r.T = min(max(rows, 0), a.max_nodes);
-  r.qtiles = r.tiles = r.cost = 0;
+  r.passes = r.tiles = r.cost = 0;
   uint32_t bad = 0;
   if (rows < 0 || rows > a.max_nodes || r.P < 0 || r.P > 0x7fffffff - kMaxNodes - kBN) bad = PKV_DEVERR_LENGTH;
   if (rows > 0 && (r.q0 < 0 || r.q0 > a.num_q_tokens - rows)) bad |= PKV_DEVERR_ROW_OOB;
   if (bad && check) report(a.err_word, bad);
   if (r.T > 0 && r.P >= 0 && r.P <= 0x7fffffff - kMaxNodes - kBN && !(bad & PKV_DEVERR_ROW_OOB)) {
-    r.qtiles = (r.T + a.tpt - 1) / a.tpt;
+    const int per = a.paired ? 2 * a.tpt : a.tpt;  // tokens of a pass
+    r.passes = (r.T + per - 1) / per;
     r.tiles = (r.P + r.T + kBN - 1) / kBN;
     r.cost = r.tiles + kUnitCost;
   }
@@ -153,7 +158,7 @@ struct Walk {
 };
 
 __device__ void walk_scan(const TreeArgs& a, Walk& w) {
-  w.len = (int64_t)w.r.qtiles * w.r.cost * a.num_kv_heads;
+  w.len = (int64_t)w.r.passes * w.r.cost * a.num_kv_heads;
   w.incl = w.len;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -166,20 +171,21 @@ __device__ void walk_start(const TreeArgs& a, Walk& w) {
   const int lane = threadIdx.x & 31;
   w.r = Req{};
   if (lane < a.batch) w.r = load_req(a, lane, blockIdx.x == 0);
-  int64_t total = (int64_t)w.r.qtiles * w.r.cost;
+  int64_t total = (int64_t)w.r.passes * w.r.cost;
   for (int i = 32 + lane; i < a.batch; i += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {  // four requests' loads in flight
       if (i + 32 * u < a.batch) {
         const Req r = load_req(a, i + 32 * u, blockIdx.x == 0);
-        total += (int64_t)r.qtiles * r.cost;
+        total += (int64_t)r.passes * r.cost;
       }
     }
   }
   total = warp_sum(total) * a.num_kv_heads;
-  w.share = (total + gridDim.x - 1) / gridDim.x;
+  const int shares = gridDim.x >> a.paired;
+  w.share = (total + shares - 1) / shares;
   if (w.share < 1) w.share = 1;
-  w.c = (int64_t)blockIdx.x * w.share;
+  w.c = (int64_t)(blockIdx.x >> a.paired) * w.share;
   w.c1 = min(total, w.c + w.share);
   w.base = 0;
   w.b0 = 0;
@@ -209,27 +215,34 @@ __device__ Seg walk_next(const TreeArgs& a, Walk& w) {
     const int64_t r0 = __shfl_sync(0xffffffffu, rs, src);
     const int tiles = __shfl_sync(0xffffffffu, w.r.tiles, src);
     const int cost = __shfl_sync(0xffffffffu, w.r.cost, src);
-    const int qtiles = __shfl_sync(0xffffffffu, w.r.qtiles, src);
+    const int passes = __shfl_sync(0xffffffffu, w.r.passes, src);
     s.q0 = __shfl_sync(0xffffffffu, w.r.q0, src);
     s.T = __shfl_sync(0xffffffffu, w.r.T, src);
     s.P = __shfl_sync(0xffffffffu, w.r.P, src);
     s.p0 = __shfl_sync(0xffffffffu, w.r.p0, src);
     s.np = __shfl_sync(0xffffffffu, w.r.np, src);
-    const int u = (int)((w.c - r0) / cost);  // units in the order (KV head, Q tile)
+    const int u = (int)((w.c - r0) / cost);  // units in the order (KV head, pass)
     const int64_t us = r0 + (int64_t)u * cost;
     const int off = (int)(w.c - us);
     if (off >= tiles) {  // the rest of the unit is its epilogue's time
       w.c = us + cost;
       continue;
     }
-    s.h = u / qtiles;
-    s.t0 = (u % qtiles) * a.tpt;
+    s.h = u / passes;
     s.j0 = off;
     s.n = (int)min((int64_t)(tiles - off), w.c1 - w.c);
+    w.c += s.n;
+    s.t0 = (u % passes) * a.tpt << a.paired;
+    if (a.paired) {  // the pass's only Q tile goes to one CTA of the pair, taking turns
+      const int parity = blockIdx.x & 1;
+      if (s.t0 + a.tpt < s.T)
+        s.t0 += parity * a.tpt;
+      else if ((u & 1) != parity)
+        continue;
+    }
     s.part = s.n == tiles ? -1 : 2 * (int)blockIdx.x + (off == 0 ? 1 : 0);
     if (off == 0 && s.n < tiles)
-      w.cut = Cut{(int32_t)((us + tiles - 1) / w.share) - (int)blockIdx.x + 1, s.q0, s.T, s.t0, s.h, {0, 0, 0}};
-    w.c += s.n;
+      w.cut = Cut{(int32_t)((us + tiles - 1) / w.share) - (int)(blockIdx.x >> a.paired) + 1, s.q0, s.T, s.t0, s.h, {0, 0, 0}};
     return s;
   }
   s.n = 0;
@@ -875,7 +888,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   const int prow = blockIdx.y * 32 + lane;
   const int tok = cut.t0 + prow / a.group;
   if (prow >= a.group * a.tpt || tok >= cut.T) return;
-  auto slot = [&](int p) -> int64_t { return (int64_t)2 * (c + p) + (p == 0 ? 1 : 0); };
+  auto slot = [&](int p) -> int64_t { return (int64_t)2 * (c + (p << a.paired)) + (p == 0 ? 1 : 0); };
   float mx = -INFINITY, tot = 0.f;
   float acc[kGroups][4] = {};
   for (int p0 = 0; p0 < cut.parts; p0 += 4) {
@@ -1046,6 +1059,7 @@ pkv_status pkv_paged_tree_attention(const pkv_pool* pool, const void* q, int32_t
   const uint64_t Db = (uint64_t)D * 2;
   a.box_rows = rows_path ? 8 : (ps < kBN ? ps : kBN);
   a.tpt = p.tpt;
+  a.paired = max_tree_len > p.tpt ? 1 : 0;
   if (!pkv_host::encode_tmap_3d(&a.tm_q, q, D, Hq, (uint64_t)num_q_tokens, Db, Hq * Db, 64, p.G, a.tpt) ||
       !(rows_path ? pkv_host::encode_tmap_rows(&a.tm_k, pool->k, Hkv * D, rows, D) &&
                         pkv_host::encode_tmap_rows(&a.tm_v, pool->v, Hkv * D, rows, D)
