@@ -20,6 +20,12 @@
 //    and the infinities and NaNs of drafted tokens become 0 in shared memory (weight 0 times them
 //    would be NaN for rows that do not see them); rows that do see them get them added when they are
 //    written, which is what a sum with a non-zero weight would give.
+// Measured with 32/8 heads of 128 at page size 16: 64 requests of 1 to 16 tokens over 512 to 4096 positions
+// 108 us, 5.7 TB/s, 84 % of what a device copy reaches (K and V once from DRAM; the rest is the start, the
+// shares' uneven ends and the merge); 4 requests of 64 tokens over 32700 positions 124 to 136 us, 1.0 to 1.1
+// PFLOP/s, 59 to 64 % of the bytes' floor (two slots of product, softmax, product an SM; the tensor pipe is 55 %
+// busy and half of the issue slots are used); one request of 8 tokens over 1000 positions 12 us, all
+// latency.  Page size 1 (29 requests of about 6000 positions, 8 heads): 138 us at D 128, 93 at D 64.
 #include <atomic>
 
 #include "quant.cuh"
@@ -855,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tree_kernel(const __grid_co
 // Merge: block (c, y) joins rows 32 y .. 32 y + 31 of the unit that CTA c began and did not finish.  A
 // lane is a row, a warp every eighth group of four dims, so a part's rows are read as whole lines; the
 // states are joined in one pass with a running maximum, the loads of four parts in flight.  5 us after
-// 64 requests of up to 16 tokens, 9 after 4 of 64 (23 MB of states, which L2 holds).
+// 64 requests of up to 16 tokens, about 9 after 4 of 64 (23 MB of states, which L2 holds).
 // ---------------------------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
