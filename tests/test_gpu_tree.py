@@ -356,3 +356,25 @@ def test_scores_that_jump_within_a_tile(lib, nodes, Hq, Hkv, D):
     out, lse, err = call(lib, s)
     assert err == 0
     verify(s, out, lse)
+
+
+def test_many_launches_back_to_back(lib):
+    """A full queue of launches over ragged trees, eager: every one gives the first one's bits."""
+    rng = np.random.default_rng(3)
+    prefix, nodes = rng.integers(200, 1500, 48), rng.integers(1, 40, 48)
+    s = make(12, [int(p) for p in prefix], [int(n) for n in nodes], 16, 4, 128, 16)
+    want, lse, err = call(lib, s)
+    assert err == 0
+    ws = torch.empty(lib.tree_workspace_size(48, 16, 4, 128, s["most"]), dtype=torch.uint8, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    wrong = torch.zeros(1, dtype=torch.int64, device="cuda")
+    out, l = torch.empty_like(want), torch.empty_like(lse)
+    for _ in range(40):
+        for _ in range(50):
+            lib.paged_tree_attention(s["q"], s["k"], s["v"], s["qo"], s["indptr"], s["pages"], s["prefix"], s["mask"],
+                                     s["most"], s["sm"], out=out, lse=l, workspace=ws, err_word=word)
+        wrong += (out != want).sum() + (l != lse).sum()
+        out.zero_()
+        l.zero_()
+    assert int(wrong) == 0 and int(word) == 0
+    verify(s, want, lse, requests=[0, 7])
