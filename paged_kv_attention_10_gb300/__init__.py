@@ -11,6 +11,7 @@ Names follow the C ABI in ``include/pagedkv.h`` (``pkv_kv_append`` -> ``kv_appen
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib
 import math
@@ -243,6 +244,15 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream_ptr(stream, device):
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on_stream(stream, device):
+    """Makes a call's own stream current, for what the call allocates or fills itself."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    return torch.cuda.stream(stream)
 
 
 def _pool(k_pool: torch.Tensor, v_pool: torch.Tensor) -> Pool:
@@ -881,7 +891,8 @@ def tree_mask_from_parents(parents, qo_indptr, max_tree_len: int, out=None, err_
         raise ValueError("parents must be [num_tokens] and qo_indptr [batch_size + 1]")
     N = parents.numel()
     if out is None:
-        out = torch.zeros((N, -(-int(max_tree_len) // 32)), dtype=_I32, device=parents.device)
+        with _on_stream(stream, parents.device):  # the kernel fills rows that the zeroing has to come before
+            out = torch.zeros((N, -(-int(max_tree_len) // 32)), dtype=_I32, device=parents.device)
     mask, words = _mask_words(out, index, N, max_tree_len)
     _run(index, stream, "pkv_tree_mask_from_parents", at, qo, qo_indptr.numel() - 1, N, max_tree_len, words, mask,
          _addr_or_none(err_word, "err_word", _I32, index))
