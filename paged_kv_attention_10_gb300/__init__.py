@@ -7,6 +7,10 @@ All computation happens in the library's CUDA kernels; there is no CPU or PyTorc
 a missing library is an error.
 
 Names follow the C ABI in ``include/pagedkv.h`` (``pkv_kv_append`` -> ``kv_append`` ...).
+
+A call with ``stream=s`` is the call under ``torch.cuda.stream(s)``: the results and workspaces that
+it makes itself are allocated there, since the caching allocator orders the uses of a block by the
+stream that it came from.  Inputs, and what the caller passes in, the caller orders against ``s``.
 """
 
 from __future__ import annotations
@@ -255,6 +259,25 @@ def _on_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _scratch(nbytes, device, stream):
+    """A workspace that the caller did not bring.  It goes back to the allocator when the call returns, which
+    may hand it on only behind the call: a block of the call's own stream."""
+    with _on_stream(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _result(shape, dtype, device, stream, make=None):
+    """A result that the caller did not bring (its values from `make`, torch.empty by default): of the call's
+    stream, and read on the caller's current one."""
+    make = make or torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _on_stream(stream, device):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _pool(k_pool: torch.Tensor, v_pool: torch.Tensor) -> Pool:
     _need(k_pool, "k_pool", torch.bfloat16)
     _need(v_pool, "v_pool", torch.bfloat16, k_pool.device)
@@ -299,7 +322,7 @@ def rope_cos_sin_table(max_position: int, head_dim: int, theta: float, device=No
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     if out is None:
-        out = torch.empty((max_position, head_dim), dtype=torch.float32, device=dev)
+        out = _result((max_position, head_dim), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev)
     if out.shape != (max_position, head_dim):
         raise ValueError("out must be [max_position, head_dim]")
@@ -348,8 +371,8 @@ def paged_gather(k_pool, v_pool, kv_indptr, kv_indices, kv_lens, total_len: int,
     if err_word is not None:
         _need(err_word, "err_word", torch.int32, dev)
     B = kv_lens.numel()
-    k_out = torch.empty((total_len, pool.num_kv_heads, pool.head_dim), dtype=torch.bfloat16, device=dev)
-    v_out = torch.empty_like(k_out)
+    k_out, v_out = (_result((total_len, pool.num_kv_heads, pool.head_dim), torch.bfloat16, dev, stream)
+                    for _ in range(2))
     with torch.cuda.device(dev):
         _call("pkv_paged_gather", ctypes.byref(pool), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_lens),
               B, _ptr(k_out), _ptr(v_out), _ptr(err_word), _stream_ptr(stream, dev))
@@ -376,10 +399,10 @@ def paged_decode(q, k_pool, v_pool, kv_indptr, kv_indices, kv_lens, sm_scale: fl
         _need(t, n, torch.int32, dev)
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _result((B, Hq), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if err_word is not None:
@@ -387,7 +410,7 @@ def paged_decode(q, k_pool, v_pool, kv_indptr, kv_indices, kv_lens, sm_scale: fl
     with torch.cuda.device(dev):
         need = int(load().pkv_decode_workspace_size(B, Hq, pool.num_kv_heads, D))
         if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            workspace = _scratch(max(need, 256), dev, stream)
         _need(workspace, "workspace", torch.uint8, dev)
         if l2_keep_tokens is not None:
             _need(l2_keep_tokens, "l2_keep_tokens", torch.int32, dev)
@@ -420,10 +443,10 @@ def paged_decode_noalloc(q, k_pool, v_pool, kv_indptr, kv_indices, kv_lens, sm_s
         _need(t, n, torch.int32, dev)
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _result((B, Hq), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if err_word is not None:
@@ -455,10 +478,10 @@ def paged_extend(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, prefix_len
     N, Hq, D = q.shape
     B = prefix_lens.numel()
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        lse = _result((N, Hq), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if err_word is not None:
@@ -466,7 +489,7 @@ def paged_extend(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, prefix_len
     with torch.cuda.device(dev):
         need = int(load().pkv_extend_workspace_size(B, Hq, pool.num_kv_heads, D, max_extend_len))
         if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _scratch(need, dev, stream)
         if workspace is not None:
             _need(workspace, "workspace", torch.uint8, dev)
         _call("pkv_paged_extend", ctypes.byref(pool), _ptr(q), N, _ptr(qo_indptr), B, Hq, _ptr(kv_indptr),
@@ -487,9 +510,9 @@ def merge_states(o_parts, lse_parts, out=None, lse=None, stream=None):
     if lse_parts.shape != (S, N, H):
         raise ValueError("lse_parts must be [S, N, H]")
     if out is None:
-        out = torch.empty((N, H, D), dtype=torch.bfloat16, device=dev)
+        out = _result((N, H, D), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((N, H), dtype=torch.float32, device=dev)
+        lse = _result((N, H), torch.float32, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     _need(lse, "lse", torch.float32, dev)
     with torch.cuda.device(dev):
@@ -531,7 +554,7 @@ def shared_prefix_attention(q, k_pool, v_pool, q_start, q_len, o_start, kv_indpt
     with torch.cuda.device(dev):
         need = int(load().pkv_shared_prefix_workspace_size(P, Hq, pool.num_kv_heads, D, max_part_rows))
         if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _scratch(need, dev, stream)
         if workspace is not None:
             _need(workspace, "workspace", torch.uint8, dev)
         _call("pkv_shared_prefix_attention", ctypes.byref(pool), _ptr(q), Nq, _ptr(q_start), _ptr(q_len),
@@ -550,10 +573,11 @@ def cascade_decode(q, k_pool, v_pool, plan, sm_scale: float, out=None, lse=None,
     dev = q.device
     B, Hq, D = q.shape
     S = plan.num_splits
-    if o_parts is None:
-        o_parts = torch.empty((S + 1, B, Hq, D), dtype=torch.bfloat16, device=dev)
-    if lse_parts is None:
-        lse_parts = torch.empty((S + 1, B, Hq), dtype=torch.float32, device=dev)
+    with _on_stream(stream, dev):
+        if o_parts is None:
+            o_parts = torch.empty((S + 1, B, Hq, D), dtype=torch.bfloat16, device=dev)
+        if lse_parts is None:
+            lse_parts = torch.empty((S + 1, B, Hq), dtype=torch.float32, device=dev)
     if o_parts.shape != (S + 1, B, Hq, D) or lse_parts.shape != (S + 1, B, Hq):
         raise ValueError("o_parts / lse_parts must be [num_splits + 1, B, Hq, (D)]")
     shared_prefix_attention(q, k_pool, v_pool, plan.part_q_start, plan.part_q_len, plan.part_o_start,
@@ -734,7 +758,7 @@ def rotary_cos_sin_table(max_position: int, rotary_dim: int, theta: float, scali
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     if out is None:
-        out = torch.empty((max_position, rotary_dim), dtype=torch.float32, device=dev)
+        out = _result((max_position, rotary_dim), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev)
     if out.shape != (max_position, rotary_dim):
         raise ValueError("out must be [max_position, rotary_dim]")
@@ -783,19 +807,19 @@ def decode_fp8_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim, d
         return int(load().pkv_decode_fp8_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim))
 
 
-def _attention_io(q, index, head_dim, out, lse, return_lse):
+def _attention_io(q, index, head_dim, out, lse, return_lse, stream):
     """Check (or make) the outputs of an attention call over q [N, Hq, D]: (out, lse, the addresses of
     q, out and lse)."""
     at = _addr(q, "q", _BF16, index)
     if q.dim() != 3 or q.shape[2] != head_dim:
         raise ValueError("q must be [num_rows, num_q_heads, head_dim], with the pool's head_dim")
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(q.shape, _BF16, q.device, stream)
     o_at = _addr(out, "out", _BF16, index)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+        lse = _result(q.shape[:2], _F32, q.device, stream)
     l_at = _addr_or_none(lse, "lse", _F32, index)
     if lse is not None and lse.shape != q.shape[:2]:
         raise ValueError("lse must be [num_rows, num_q_heads]")
@@ -822,13 +846,13 @@ def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices,
     lens = _addr(kv_lens, "kv_lens", _I32, index)
     B = kv_lens.numel()
     indptr, indices = _page_table(index, kv_indptr, kv_indices, B)
-    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse)
+    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse, stream)
     if q.shape[0] != B:
         raise ValueError("q must have one row per request")
     Hq = q.shape[1]
     if workspace is None:
         need = decode_fp8_workspace_size(B, Hq, shape[2], shape[3], index)
-        workspace = torch.empty(max(need, 256), dtype=_U8, device=q.device)
+        workspace = _scratch(max(need, 256), q.device, stream)
     _run(index, stream, "pkv_paged_decode_fp8", pool, q_at, B, Hq, indptr, indices, lens, sm_scale, o_at, l_at,
          _addr(workspace, "workspace", _U8, index), workspace.numel(), _addr_or_none(err_word, "err_word", _I32, index),
          max_ctas)
@@ -869,12 +893,12 @@ def paged_tree_attention(q, k_pool, v_pool, qo_indptr, kv_indptr, kv_indices, pr
     indptr, indices = _page_table(index, kv_indptr, kv_indices, B)
     if qo_indptr.numel() != B + 1:
         raise ValueError("qo_indptr must have batch_size + 1 entries")
-    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse)
+    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse, stream)
     N, Hq, D = q.shape
     mask, words = _mask_words(tree_mask, index, N, max_tree_len)
     if workspace is None:
         need = tree_workspace_size(B, Hq, shape[2], D, max_tree_len, index)
-        workspace = torch.empty(max(need, 256), dtype=_U8, device=q.device)
+        workspace = _scratch(max(need, 256), q.device, stream)
     _run(index, stream, "pkv_paged_tree_attention", pool, q_at, N, qo, B, Hq, indptr, indices, prefix, mask, words,
          max_tree_len, sm_scale, o_at, l_at, _addr(workspace, "workspace", _U8, index), workspace.numel(),
          _addr_or_none(err_word, "err_word", _I32, index))
@@ -891,8 +915,8 @@ def tree_mask_from_parents(parents, qo_indptr, max_tree_len: int, out=None, err_
         raise ValueError("parents must be [num_tokens] and qo_indptr [batch_size + 1]")
     N = parents.numel()
     if out is None:
-        with _on_stream(stream, parents.device):  # the kernel fills rows that the zeroing has to come before
-            out = torch.zeros((N, -(-int(max_tree_len) // 32)), dtype=_I32, device=parents.device)
+        # zeroed on the call's stream, before the kernel
+        out = _result((N, -(-int(max_tree_len) // 32)), _I32, parents.device, stream, torch.zeros)
     mask, words = _mask_words(out, index, N, max_tree_len)
     _run(index, stream, "pkv_tree_mask_from_parents", at, qo, qo_indptr.numel() - 1, N, max_tree_len, words, mask,
          _addr_or_none(err_word, "err_word", _I32, index))
