@@ -7,8 +7,8 @@
 //
 //  * Scales never touch the matrix operands.  ks[j] multiplies a score after the product.  vs[j] goes
 //    into the softmax weights of the second product, w_j = p_j vs[j], which f16 must hold: they are
-//    formed as 2^(x_j + e_j - M) m_j with vs[j] = m_j 2^e_j and M a running maximum of x_j + e_j of its
-//    own, so that they stay in [0, 2) whatever the scales' range.  The softmax's own sum keeps its
+//    formed as 2^(x_j + e_j - M) m_j 2^14 with vs[j] = m_j 2^e_j and M a running maximum of x_j + e_j of its
+//    own, so that they stay in [0, 2^15) whatever the scales' range.  The softmax's own sum keeps its
 //    own running maximum, and the two meet when a segment ends.
 //  * Both products run as f16 m16n8k16 MMAs with fp32 accumulators: e4m3 converts to f16 exactly, two
 //    values per instruction.  Q, bf16, is scaled per head by a power of two into f16's range (largest
@@ -94,6 +94,10 @@ struct Decode8Args {
 constexpr int kMaxLen = 0x7fff0000;
 constexpr int kSlice = 32;  // positions of a warp's step, and the unit of the work split
 constexpr int kMaxStages = 8;
+// Weights of the second product stand in [0, 2^(kWeightExp + 1)), the top of f16's range: one as small as 2^-39 of
+// the largest is still counted.  (In [0, 2), what is below 2^-25 of it was not: 20000 positions with weights of
+// 2^-25.6 are 0.0004 of the sum.)
+constexpr int kWeightExp = 14;
 
 PKV_DEV void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -556,7 +560,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
       for (int i = 0; i < 4; ++i) {
         const uint32_t u = __float_as_uint(sc[(Ts + 8 * i) * HC]);
         ve[i] = (float)((int)(u >> 23) - 127);
-        vm[i] = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+        vm[i] = __uint_as_float((u & 0x7fffffu) | (uint32_t)(127 + kWeightExp) << 23);
       }
       uint32_t bp[2][2];
       float x[2][4];
@@ -700,6 +704,7 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
           lt += __shfl_xor_sync(0xffffffffu, lt, 16);
           const int col = head0 + 2 * c + k;  // query head within the group
           const float inv = ex2(mw[k] - m[k]) / lt;
+          const float unit = exp2i(-kWeightExp);  // first of the two: inv can be as small as fp32 goes
           const float lse_v = (m[k] + log2f(lt)) * kLn2;
           if (col < G) {
             const int qhl = hl * G + col;
@@ -707,12 +712,14 @@ __device__ void decode8_consumer(const Decode8Args& a, uint8_t* stages, StageHdr
               const int64_t qh = (int64_t)h.hg * HQU + qhl;
               uint32_t* op = reinterpret_cast<uint32_t*>(a.out + ((int64_t)h.b * a.num_q_heads + qh) * D) + g;
 #pragma unroll
-              for (int kc = 0; kc < NK; ++kc) op[8 * kc] = pack_bf16x2(o[kc][k] * inv, o[kc][2 + k] * inv);
+              for (int kc = 0; kc < NK; ++kc)
+                op[8 * kc] = pack_bf16x2(o[kc][k] * unit * inv, o[kc][2 + k] * unit * inv);
               if (g == 0 && a.lse) a.lse[(int64_t)h.b * a.num_q_heads + qh] = lse_v;
             } else {
               float2* pp = reinterpret_cast<float2*>(a.part_o + ((int64_t)h.part * HQU + qhl) * D) + g;
 #pragma unroll
-              for (int kc = 0; kc < NK; ++kc) pp[8 * kc] = make_float2(o[kc][k] * inv, o[kc][2 + k] * inv);
+              for (int kc = 0; kc < NK; ++kc)
+                pp[8 * kc] = make_float2(o[kc][k] * unit * inv, o[kc][2 + k] * unit * inv);
               if (g == 0) a.part_lse[(int64_t)h.part * HQU + qhl] = lse_v;
             }
           }
