@@ -85,7 +85,7 @@ struct Ctl {
   uint64_t s_full[2], s_free[2];  // S buffer b: QK written / its P consumed by PV
   uint64_t p_full[2];             // P written, V cleaned
   uint64_t qk_done, pv_done;      // every MMA of the issuing thread has completed (exit path)
-  float inv[kBM];                 // 1 / (sum of the weights) of each row, 0 for a row that saw nothing
+  float inv[kBM];                 // 1 / (sum of P) of each row, 0 for a row that saw nothing
 };
 static_assert(kMaxNodes / 32 == 32, "a warp clears the notes");
 
@@ -527,6 +527,18 @@ PKV_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// acc + (float)(low or high bf16 half of v), one rounding
+PKV_DEV float add_bf16_lo(uint32_t v, float acc) {
+  float r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, lo, %2;\n\t}" : "=f"(r) : "r"(v), "f"(acc));
+  return r;
+}
+PKV_DEV float add_bf16_hi(uint32_t v, float acc) {
+  float r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, hi, %2;\n\t}" : "=f"(r) : "r"(v), "f"(acc));
+  return r;
+}
+
 // A thread owns a row of the tile.
 template <int D>
 __device__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_t tmem, const Seg& s, uint32_t t) {
@@ -546,7 +558,8 @@ __device__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
   MaskRow mask{valid ? a.mask + (int64_t)(s.q0 + tok) * a.words : nullptr, a.words, {0u, 0u, 0u, 0u}};
   if ((s.j0 + s.n) * kBN > s.P) load_mask(mask);
   float m_used = -INFINITY;  // running max of the scaled (log2) scores
-  float l = 0.f;             // sum of the weights (in fp32; the PV MMA takes them as bf16)
+  float l = 0.f;             // sum of the weights (for the LSE)
+  float lr = 0.f;            // ... as rounded to bf16 for the PV MMA (for O: a rounding that they share cancels)
 
   for (int j = 0; j < s.n; ++j, ++t) {
     const int st = t & 1;
@@ -588,12 +601,13 @@ __device__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
       const float corr = resc ? ex2(m_used - m_ref) : 1.f;
       const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen so far: every weight is 0
       const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(neg, neg);
-      float tot = 0.f;
+      float tot = 0.f, rtot = 0.f;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const float(&sv)[32] = hf ? s1 : s0;
         uint32_t pk[16];
         uint64_t acc_a = f32x2(0.f, 0.f), acc_b = f32x2(0.f, 0.f);
+        float rs0 = 0.f, rs1 = 0.f, rs2 = 0.f, rs3 = 0.f;
 #pragma unroll
         for (int c = 0; c < 16; c += 2) {
           float x0, x1, x2, x3;
@@ -604,14 +618,20 @@ __device__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
           acc_b = add_f32x2(acc_b, f32x2(p2, p3));
           pk[c] = pack_bf16x2(p0, p1);
           pk[c + 1] = pack_bf16x2(p2, p3);
+          rs0 = add_bf16_lo(pk[c], rs0);
+          rs1 = add_bf16_hi(pk[c], rs1);
+          rs2 = add_bf16_lo(pk[c + 1], rs2);
+          rs3 = add_bf16_hi(pk[c + 1], rs3);
         }
         float e0, e1;
         split_f32x2(add_f32x2(acc_a, acc_b), e0, e1);
         tot += e0 + e1;
+        rtot += (rs0 + rs1) + (rs2 + rs3);
         // P (bf16 pairs) over the first 16 columns of each 32-column half of the S buffer
         tmem_st16(taddr + st * 64 + hf * 32, pk);
       }
       l = l * corr + tot;
+      lr = lr * corr + rtot;
       m_used = m_ref;
       if (j > 0 && __any_sync(0xffffffffu, resc)) {
         // O is rescaled only after the previous tile's PV is done
@@ -641,7 +661,7 @@ __device__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, Ctl* ctl, uint32_
   // the last PV is done
   const uint32_t last = t - 1;
   if (!__all_sync(0xffffffffu, mbar_wait(&ctl->s_free[last & 1], (last >> 1) & 1))) return false;
-  ctl->inv[r] = l == 0.f ? 0.f : 1.f / l;  // (NaN among the scores: in every dim)
+  ctl->inv[r] = l == 0.f ? 0.f : 1.f / lr;  // (NaN among the scores: in every dim)
   if (valid) {
     const float lse_v = (m_used + log2f(l)) * kLn2;
     if (s.part >= 0)

@@ -50,3 +50,59 @@ def test_small_weights_behind_a_large_one_count(lib, D, page, first):
     extra = 2.0 ** -38 * ref[4].max() * np.abs(v).sum(0)
     for h in range(H):
         check(oracle.as_f64(out)[0, h][None], oracle.as_f64(lse)[0, h: h + 1], ref, n, 2.0 ** -11, f"head {h}", extra)
+
+
+def _common_rounding(B, P, T, Hq, Hkv, D, v):
+    """B requests whose position 0 has the score 0 and all others ln 0.5057: weights that bf16 holds as
+    0.50390625, 0.36 % less.  v: values of all positions, [P + T, D]."""
+    page, n = 16, P + T
+    per = -(-n // page)
+    k = torch.zeros(per * page, Hkv, D)
+    k[1:, :, 0] = -1.0
+    vv = torch.zeros(per * page, Hkv, D)
+    vv[:n] = v[:, None]
+    k, vv = (x.to(torch.bfloat16).view(per, page, Hkv, D).cuda() for x in (k, vv))
+    q = torch.zeros(B * T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    qo = i32(np.arange(B + 1) * T)
+    return q, k, vv, qo, i32(np.arange(B + 1) * per), i32(np.tile(np.arange(per), B)), i32([P] * B), -math.log(0.5057)
+
+
+@pytest.mark.parametrize("B,P,T,Hq,Hkv,D", [(64, 500, 4, 32, 8, 128), (64, 900, 3, 8, 8, 64), (40, 700, 60, 32, 8, 128),
+                                            (1, 300, 2, 4, 4, 64)])
+def test_rounding_that_the_weights_share_cancels(lib, B, P, T, Hq, Hkv, D):
+    """Values that are all 1 give exactly 1, whatever the weights round to: products and their sum are off by
+    fp32's n 2^-24, far less than half a step of bf16 below 1, 2^-9.  So does the extend on the same chain."""
+    q, k, v, qo, indptr, pages, prefix, sm = _common_rounding(B, P, T, Hq, Hkv, D, torch.ones(P + T, D))
+    mask = lib.tree_mask_from_parents(i32(np.tile(np.arange(T) - 1, B)), qo, T)
+    out, _ = lib.paged_tree_attention(q, k, v, qo, indptr, pages, prefix, mask, T, sm)
+    ext, _ = lib.paged_extend(q, k, v, qo, indptr, pages, prefix, T, sm)
+    assert torch.all(ext == 1.0)
+    assert torch.all(out == 1.0), f"{float(out.min())} to {float(out.max())}"
+
+
+@pytest.mark.parametrize("B,P,T,Hq,Hkv,D", [(64, 500, 4, 32, 8, 128), (40, 700, 60, 8, 2, 64)])
+def test_rounding_reaches_a_result_by_the_values_spread_only(lib, B, P, T, Hq, Hkv, D):
+    """Weights p_j (1 + d_j), |d_j| <= 2^-8, over their own sum are off by sum p_j d_j (v_j - o) / sum p_j (1 + d_j):
+    at most 2^-8 (1 + 2^-7) sum p_j |v_j - o|, twice that where the row is put together from parts (whose own
+    results differ from o by no more on average).  The rest is _attention64's, the output's half step
+    2^(e - 8) with 2^e <= |o|."""
+    gen = torch.Generator().manual_seed(P)
+    vals = (1.9 + 0.03 * torch.randn(P + T, D, generator=gen)).to(torch.bfloat16)
+    q, k, v, qo, indptr, pages, prefix, sm = _common_rounding(B, P, T, Hq, Hkv, D, vals.float())
+    mask = lib.tree_mask_from_parents(i32(np.tile(np.arange(T) - 1, B)), qo, T)
+    out, lse = lib.paged_tree_attention(q, k, v, qo, indptr, pages, prefix, mask, T, sm)
+    kk = np.zeros((P + T, D))
+    kk[1:, 0] = -1.0
+    one = np.zeros((T, D))
+    one[:, 0] = 1.0
+    seen = np.concatenate([np.ones((T, P), dtype=bool), np.tril(np.ones((T, T), dtype=bool))], 1)
+    o, l, A, delta, w = attend(one, kk, oracle.as_f64(vals), sm, seen)
+    vd = oracle.as_f64(vals)
+    spread = np.stack([w[t] @ np.abs(vd - o[t]) for t in range(T)])
+    tol = 2.0 ** (np.floor(np.log2(np.abs(o))) - 8) + 2 * 2.0 ** -8 * (1 + 2.0 ** -7) * spread \
+        + A * (2 * delta[:, None] + 2.0 ** -20 + (P + T) * 2.0 ** -24)
+    off = np.abs(oracle.as_f64(out).reshape(B, T, Hq, D) - o[None, :, None])
+    assert np.all(off <= tol[None, :, None]), f"off by {off.max():.4g}, bound {tol.min():.4g}"
+    ltol = delta + 2.0 ** -20 + (P + T) * 2.0 ** -24 + 2.0 ** -22 * np.abs(l)
+    assert np.all(np.abs(oracle.as_f64(lse).reshape(B, T, Hq) - l[None, :, None]) <= ltol[None, :, None])
