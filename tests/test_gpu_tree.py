@@ -378,3 +378,26 @@ def test_many_launches_back_to_back(lib):
         l.zero_()
     assert int(wrong) == 0 and int(word) == 0
     verify(s, want, lse, requests=[0, 7])
+
+
+def test_every_launch_of_a_full_queue(lib):
+    """2000 launches over ragged trees, 50 in the queue at a time with an output each: all have the first one's
+    bits."""
+    rng = np.random.default_rng(3)
+    prefix, nodes = rng.integers(200, 1500, 48), rng.integers(1, 40, 48)
+    s = make(12, [int(p) for p in prefix], [int(n) for n in nodes], 16, 4, 128, 16)
+    want, lse, err = call(lib, s)
+    assert err == 0
+    verify(s, want, lse, requests=[0, 7])
+    ws = torch.empty(lib.tree_workspace_size(48, 16, 4, 128, s["most"]), dtype=torch.uint8, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    wrong = torch.zeros(1, dtype=torch.int64, device="cuda")
+    outs, lses = want.new_empty((50,) + want.shape), lse.new_empty((50,) + lse.shape)
+    for _ in range(40):
+        outs.zero_()
+        lses.zero_()
+        for i in range(50):
+            lib.paged_tree_attention(s["q"], s["k"], s["v"], s["qo"], s["indptr"], s["pages"], s["prefix"], s["mask"],
+                                     s["most"], s["sm"], out=outs[i], lse=lses[i], workspace=ws, err_word=word)
+        wrong += (outs != want).sum() + (lses != lse).sum()
+    assert int(wrong) == 0 and int(word) == 0
