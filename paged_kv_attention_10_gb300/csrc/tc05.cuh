@@ -164,11 +164,6 @@ PKV_DEV void tmem_fetch32(uint32_t taddr, float (&v)[32]) {
         "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
 }
-PKV_DEV void tmem_fetch8(uint32_t taddr, float* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-               : "r"(taddr));
-}
 
 PKV_DEV void tmem_st32(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
