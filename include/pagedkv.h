@@ -445,8 +445,8 @@ pkv_status pkv_rotary_kv_append(const pkv_pool* pool, const void* k_new, const v
  *                    scaling: low 1, high 4)
  *   PKV_ROPE_YARN    (Peng et al., "YaRN", 2023; theta > 1) with dim(b) = R ln(original_max_position /
  *                    (2 pi b)) / (2 ln theta), lo = max(floor(dim(high)), 0), hi = min(ceil(dim(low)),
- *                    R - 1): ramp_i = clamp((i - lo) / (hi - lo), 0, 1), f' = f / factor ramp_i +
- *                    f (1 - ramp_i); low and high are its beta_slow and beta_fast (1 and 32);
+ *                    R - 1), and 0.001 more than that where it is lo: ramp_i = clamp((i - lo) / (hi - lo),
+ *                    0, 1), f' = f / factor ramp_i + f (1 - ramp_i); low and high are its beta_slow and beta_fast (1 and 32);
  *                    m = attention_factor (0.1 ln(factor) + 1 in the paper)
  * factor >= 1, 0 < low < high, original_max_position > 0, attention_factor > 0 where they are used.
  */
@@ -524,7 +524,7 @@ pkv_status pkv_paged_gather_fp8(const pkv_pool_fp8* pool, const int32_t* kv_indp
  * Paged decode over an 8-bit cache: pkv_paged_decode_ctas with the values k8 k_scale and v8 v_scale.
  * Page lists, q, out, lse, max_ctas, errors and the treatment of kv_lens[b] == 0 as there;
  * head_dim 64 or 128, num_q_heads / num_kv_heads <= 16.  The softmax weights (times v_scale) are
- * rounded to f16 for the second product; sums are fp32.
+ * rounded to f16 for the second product (11 bits; one below 2^-39 of the largest is 0); sums are fp32.
  *   workspace  device, 256-byte aligned, at least pkv_decode_fp8_workspace_size(...) bytes; needs no
  *              initialisation, and is not shared with a call in flight on another stream
  */
@@ -548,12 +548,17 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
  *   tree_mask  uint32 [num_q_tokens, mask_words] (device), 32 * mask_words >= max_tree_len; bits of
  *              tokens the request does not have are ignored
  *   max_tree_len  an upper bound of qo_indptr[b+1] - qo_indptr[b], at most 1024; rows of a request past
- *              it are reported (PKV_DEVERR_LENGTH) and left unwritten
+ *              it are reported (PKV_DEVERR_LENGTH) and left unwritten.  A bound above 128 / (num_q_heads /
+ *              num_kv_heads), rounded down, lays the work out for trees that large: over smaller ones the call
+ *              can take up to 1.4 times as long as with their own bound
  *   out, lse   as for pkv_paged_extend; a row that sees nothing gets out = 0, lse = -inf
- *   workspace  device, 256-byte aligned, at least pkv_tree_workspace_size(...) bytes; needs no
- *              initialisation, and is not shared with a call in flight on another stream
+ *   workspace  device, 256-byte aligned, at least pkv_tree_workspace_size(...) bytes (partial states of every
+ *              CTA: 40 MB at head_dim 128 on 152 SMs, whatever the batch); needs no initialisation, and is not
+ *              shared with a call in flight on another stream
  *   err_word   nullable; PKV_DEVERR_LENGTH, PKV_DEVERR_PAGE_OOB, PKV_DEVERR_ROW_OOB (a request whose rows
  *              lie outside q is skipped)
+ * The softmax weights are rounded to bf16 for the second product; out is divided by their rounded sum, lse
+ * is of the sum before the rounding, in fp32.
  * What a drafted token's K and V hold does not reach rows that do not see it, infinities and NaNs
  * included.  An infinity in the V of a cached position, which every row sees, makes that dimension an
  * infinity or a NaN.  head_dim 64 or 128, any page_size, num_q_heads / num_kv_heads from 1 to 16.

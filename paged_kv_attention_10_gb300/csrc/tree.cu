@@ -15,17 +15,24 @@
 //    all warps meeting between them; the other CTA of the SM fills the gap.
 //  * Where a request may have more rows than a Q tile, CTAs 2 c and 2 c + 1 take the same share with a Q
 //    tile each, so that K and V come from DRAM once for both (each its own share: 4 requests of 64
-//    tokens over 32700 positions 178 us, 127 so).
+//    tokens over 32700 positions 178 us, 127 so).  Whether it may have follows from max_tree_len, not from the
+//    trees: a pass of one Q tile is then one CTA's of the pair (in turn over a request's units), the other
+//    passes it by.  A bound above a Q tile over smaller trees so costs 64 requests of 1 to 16 tokens 119 us for
+//    109, 16 of 8 tokens over 4000 positions 64 for 51, and 64 of 8 over 4000 with one KV head (where every
+//    second CTA is left without work) 46 for 39, at D 64 and group 8 37 for 27.
+//  * P goes to the second product in bf16 (the type of V, which the MMA asks for), so a result is divided by the
+//    sum of the rounded weights: a rounding that a row's weights share cancels (values of 1 give 1; 0.996
+//    with the fp32 sum, which the LSE keeps).  The second sum costs 4 requests of 64 tokens 3 to 5 %.
 //  * Only tiles that reach past the prefix are masked.  There the V rows behind the last position
 //    and the infinities and NaNs of drafted tokens become 0 in shared memory (weight 0 times them
 //    would be NaN for rows that do not see them); rows that do see them get them added when they are
 //    written, which is what a sum with a non-zero weight would give.
 // Measured with 32/8 heads of 128 at page size 16: 64 requests of 1 to 16 tokens over 512 to 4096 positions
-// 108 us, 5.7 TB/s, 84 % of what a device copy reaches (K and V once from DRAM; the rest is the start, the
-// shares' uneven ends and the merge); 4 requests of 64 tokens over 32700 positions 124 to 136 us, 1.0 to 1.1
-// PFLOP/s, 59 to 64 % of the bytes' floor (two slots of product, softmax, product an SM; the tensor pipe is 55 %
-// busy and half of the issue slots are used); one request of 8 tokens over 1000 positions 12 us, all
-// latency.  Page size 1 (29 requests of about 6000 positions, 8 heads): 138 us at D 128, 93 at D 64.
+// 109 us, 5.6 TB/s, 83 % of what a device copy reaches (K and V once from DRAM; the rest is the start, the
+// shares' uneven ends and the merge); 4 requests of 64 tokens over 32700 positions 129 to 144 us, 0.95 to 1.07
+// PFLOP/s, 55 to 62 % of the bytes' floor (two slots of product, softmax, product an SM; the tensor pipe is 51 %
+// busy and 58 % of the issue slots are used); one request of 8 tokens over 1000 positions 12 us, all
+// latency.  Page size 1 (29 requests of 8 tokens over 6000 positions, 8 heads): 146 us at D 128, 92 at D 64.
 #include <atomic>
 
 #include "quant.cuh"
