@@ -30,7 +30,7 @@
 //    scales come into the same stage: by bulk copies beside the boxes where the CTA takes every KV
 //    head (a box's lie side by side then), by cp.async otherwise.
 // Measured with 32/8 heads of 128 at page size 16: 8 requests of 32768 positions 90 us, 6.1 TB/s, 90 % of
-// what a device copy reaches; 256 requests of 512 to 4096 positions 196 to 197 us, 93 %.  DRAM reads are the cache's
+// what a device copy reaches; 256 requests of 512 to 4096 positions 196 to 198 us, 93 %.  DRAM reads are the cache's
 // bytes (554 MB of 554), the tensor pipe is 18 % busy, 43 % of the issue slots are used.  Small KV head counts are
 // bound by the producers' issue instead: one head of 128, 720000 positions, 50 us at page size 16, 41 at
 // 64 and 151 at 1 of the 28 that the bytes take; two heads at page size 1 118 of 28.
