@@ -1,0 +1,688 @@
+// Paged decode attention over a quantised cache (one query per request): what the 8-bit and the 4-bit kernels
+// share, which is all but a consumer warp's arithmetic on its 32 positions.
+//
+//  * One persistent CTA per SM over an equal share of the stream of slices of 32 positions of all (request,
+//    head group) units; a producer warp each for K and V fills a ring of stages, eight or sixteen consumer warps read
+//    them, a second kernel merges the units that the shares cut.
+//  * K and V come in TMA boxes of 32, 16 or 8 rows (the largest that divides the page size), by copies of single
+//    rows for other page sizes.  The scales come into the same stage: by bulk copies beside the boxes where the
+//    CTA takes every KV head (a box's lie side by side then), by cp.async otherwise.
+//
+// A format F is a struct with kDim (head_dim), kRowBytes and kScaleBytes (of one head of one position), kWarps
+// (consumer warps), kMergeFloats (of a lane's state, see consume), row_stride(bytes of a row) in shared memory for
+// the row copies, and consume<TMA>, a consumer warp.
+#pragma once
+
+#include <atomic>
+
+#include "quant.cuh"
+#include "tc05.cuh"
+
+namespace pkv {
+
+constexpr int kSegFirst = 1;    // first stage of this CTA's segment of the unit
+constexpr int kSegLast = 2;     // last stage of the segment
+constexpr int kStartsUnit = 4;  // the segment starts at position 0 of the unit
+constexpr int kEndsUnit = 8;    // the segment ends at the unit's last position
+
+struct StageHdr {
+  int32_t unit;  // -1: no more work
+  int32_t b, hg, ntok, flags, part, pad0, pad1;
+};
+
+struct QuantDecodeArgs {
+  CUtensorMap tm_k;  // pool bytes as (byte of a head, row, head), box [row bytes x box_rows x HC]; TMA instance only
+  CUtensorMap tm_v;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int64_t num_pages;
+  int32_t page_size, num_kv_heads;
+  FastDiv page_div;  // by page_size
+  const __nv_bfloat16* q;
+  int32_t batch, num_q_heads;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* kv_lens;
+  float scale_log2;
+  float out_scale;       // of the values of V, for the whole cache
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;
+  float* part_lse;
+  int32_t* unit_first;
+  int32_t* unit_last;
+  uint32_t* err_word;
+  int32_t HC;            // KV heads per CTA
+  int32_t nhg;           // head groups = num_kv_heads / HC
+  int32_t W;             // consumer warps per KV head
+  int32_t group;         // query heads per KV head
+  int32_t nt;            // warps that share a KV head's rows, eight of its query heads each
+  int32_t box_rows;      // TMA instance: rows of a box (32, 16 or 8)
+  int32_t row_stride;    // row-copy instance: shared-memory bytes per token row
+  int32_t stage_tokens;  // 32 * W
+  int32_t num_stages, num_parts;
+  uint32_t kv_region;    // bytes of the K (or V) part of one stage
+  uint32_t stage_bytes;  // K, V and the scales
+};
+
+// No request has more positions than the pool has rows; a longer kv_lens[b] (reported, its pages run
+// out) must not take the token counter past 31 bits.
+constexpr int kMaxLen = 0x7fff0000;
+constexpr int kSlice = 32;  // positions of a warp's step, and the unit of the work split
+constexpr int kMaxStages = 8;
+
+PKV_DEV void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+PKV_DEV void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+PKV_DEV void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on the barrier when every cp.async of this thread so far has landed.
+PKV_DEV void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// D = A * B + D, A 16x16 f16 (row), B 16x8 f16 (col), D 16x8 fp32.
+PKV_DEV void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                           uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Producer warps, one for K and one for V: each walks the CTA's share of the slice stream and fills
+// its part of the stages; K's also writes the headers.  A stage is a few hundred cycles of address work
+// for a warp and about 1400 of memory time, so one warp for both held the stream back (8 x 32768
+// positions, D 128: 105 us, 96 with two).
+// ---------------------------------------------------------------------------------------------
+template <class F, bool TMA>
+__device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
+                                 uint64_t* full, uint64_t* empty, bool v) {
+  constexpr int D = F::kDim, RH = F::kRowBytes, SH = F::kScaleBytes;  // bytes of a head's row and of its scales
+  const int lane = threadIdx.x & 31;
+  const int NS = a.num_stages, Ts = a.stage_tokens, W = a.W, HC = a.HC, nhg = a.nhg;
+  const uint32_t region = a.kv_region;
+  const CUtensorMap* tm = v ? &a.tm_v : &a.tm_k;
+  const uint8_t* pool = v ? a.v_pool : a.k_pool;
+  const uint8_t* scale = v ? a.v_scale : a.k_scale;
+  // Page indices come from a register window of 96 consecutive entries (three 32-lane slices), its
+  // last third loaded 32 pages before a stage can need it.  Usable while one stage spans at most
+  // 33 pages.
+  const bool windowed = (Ts - 1) / a.page_size + 1 <= 32;
+
+  // the first 32 requests' numbers in one round of loads, which the walk below starts with
+  const bool in0 = lane < a.batch;
+  const int32_t first_len = in0 ? min(max(0, ld(a.kv_lens + lane)), kMaxLen) : 0;
+  const int32_t first_p0 = in0 ? ld(a.kv_indptr + lane) : 0;
+  const int32_t first_p1 = in0 ? ld(a.kv_indptr + lane + 1) : 0;
+  int64_t sumS = ((int64_t)first_len + kSlice - 1) / kSlice;  // slices over all requests
+  for (int i = 32 + lane; i < a.batch; i += 128) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)  // four loads in flight
+      if (i + 32 * u < a.batch) sumS += (min(max(0, ld(a.kv_lens + i + 32 * u)), kMaxLen) + kSlice - 1) / kSlice;
+  }
+  sumS = warp_sum(sumS);
+  const int64_t T = sumS * nhg;
+  int64_t share = (T + gridDim.x - 1) / gridDim.x;
+  if (share < 1) share = 1;
+  const int64_t c0 = (int64_t)blockIdx.x * share;
+  const int64_t c1 = min(T, c0 + share);
+
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  int32_t cur_p0 = 0, cur_np = 0;  // page list of the request being streamed
+  int win_b = -1, wbase = 0;
+  int32_t w0 = -1, w1 = -1, w2 = -1;
+  auto entry = [&](int pidx) -> int32_t {  // page-list entry of the current request; -1 past its end
+    return pidx < cur_np ? ld(a.kv_indices + cur_p0 + pidx) : -1;
+  };
+  int nissued = 0;
+  auto next_stage = [&]() {
+    ++nissued;
+    if (++stage == NS) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+
+  auto emit = [&](int unit, int b, int hg, int tok0, int ntok, int flags) -> bool {
+    if (unit >= 0 && !v && (flags & kSegFirst)) {
+      const int hqu = HC * a.group;  // the unit's queries, on their way to L2 before they are read
+      const char* qb = reinterpret_cast<const char*>(a.q + ((int64_t)b * a.num_q_heads + (int64_t)hg * hqu) * D);
+      for (int off = lane * 128; off < hqu * D * 2; off += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(qb + off));
+    }
+    if (unit >= 0 && windowed) {
+      const int first_page = a.page_div.quot(tok0);
+      if (b != win_b || first_page < wbase) {
+        win_b = b;
+        wbase = first_page;
+        w0 = entry(wbase + lane);
+        w1 = entry(wbase + 32 + lane);
+        w2 = entry(wbase + 64 + lane);
+      }
+      while (first_page >= wbase + 32) {
+        w0 = w1;
+        w1 = w2;
+        wbase += 32;
+        w2 = entry(wbase + 64 + lane);
+      }
+    }
+    uint64_t* bar = &full[stage];
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) return false;
+    if (!v && lane == 0) {  // the consumers read the header, and a new unit's queries, while the stage is on its way
+      hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, 0, 0};
+      mbar_arrive(&hdr_full[stage]);
+    }
+    if (unit >= 0) {
+      uint8_t* dst = stages + (size_t)stage * a.stage_bytes + (v ? region : 0u);
+      uint8_t* sdst = stages + (size_t)stage * a.stage_bytes + 2 * region + (v ? (size_t)Ts * HC * SH : 0);
+      uint32_t bad = 0;
+      auto window_page = [&](uint32_t pidx) -> int32_t {  // all lanes call
+        const int k = (int)pidx - wbase;  // < 64
+        const int32_t v0 = __shfl_sync(0xffffffffu, w0, k & 31);
+        const int32_t v1 = __shfl_sync(0xffffffffu, w1, k & 31);
+        return k < 32 ? v0 : v1;
+      };
+      auto row_at = [&](uint32_t pidx, uint32_t in_page, int32_t page, bool in) -> int64_t {
+        if (!in) return -1;
+        if ((int)pidx >= cur_np) {
+          bad |= PKV_DEVERR_LENGTH;
+          return -1;
+        }
+        if (page < 0 || page >= a.num_pages) {
+          bad |= PKV_DEVERR_PAGE_OOB;
+          return -1;
+        }
+        return (int64_t)page * a.page_size + in_page;
+      };
+      auto copy_scales = [&](int64_t row, int j) {  // token j's scales of HC heads, in pieces of up to 16 bytes
+        const int n = HC * SH;
+        const uint8_t* src = scale + (row * a.num_kv_heads + hg * HC) * SH;
+        const uint32_t sd = smem_u32(sdst) + (uint32_t)(j * n);
+        if ((n & 15) == 0) {
+          for (int i = 0; i < n; i += 16) cp_async16(sd + i, src + i);
+        } else if (SH == 8) {
+          for (int i = 0; i < n; i += 8) cp_async8(sd + i, src + i);
+        } else {
+          for (int i = 0; i < n; i += 4) cp_async4(sd + i, src + i);
+        }
+      };
+      if constexpr (TMA) {
+        // Lane i fetches box i, box_rows tokens inside one page, and their scales, which lie side by side when
+        // the CTA takes all KV heads.  (One lookup a stage: with one per 32 tokens the eight of a stage of
+        // one KV head took 4 us, and 720000 positions of it 96 us; 48 now, of the 28 that their bytes take.)
+        // Only boxes of 8 rows in a stage of 512 positions are more than the lanes.
+        const int sh = 31 - __clz(a.box_rows), nbox = Ts >> sh;
+        const bool side_by_side = nhg == 1;
+        const uint32_t box = (uint32_t)(HC * RH) << sh, sbox = (uint32_t)(HC * SH) << sh;
+#pragma unroll 1
+        for (int i0 = 0; i0 < (F::kWarps > 8 ? nbox : 1); i0 += 32) {
+          const int tok = tok0 + ((i0 + lane) << sh);
+          const bool in = i0 + lane < nbox && tok < tok0 + ntok;
+          uint32_t pidx, in_page;
+          a.page_div.divmod((uint32_t)(in ? tok : tok0), pidx, in_page);
+          const int32_t page = windowed ? window_page(pidx) : in ? entry((int)pidx) : -1;
+          const int64_t row = row_at(pidx, in_page, page, in);
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+          if (lane == 0) mbar_expect_tx(bar, n * (box + (side_by_side ? sbox : 0u)));
+          __syncwarp();
+          if (row >= 0) {
+            tma_load_3d(smem_u32(dst) + (i0 + lane) * box, tm, 0, (int)row, hg * HC, bar);
+            if (side_by_side) bulk_g2s(sdst + (i0 + lane) * sbox, scale + row * a.num_kv_heads * SH, sbox, bar);
+          }
+          if (!side_by_side) {
+            const int rounds = F::kWarps > 8 ? min(W - (i0 << sh) / 32, 1 << sh) : W;
+            for (int r = 0; r < rounds; ++r) {
+              const int j = (i0 << sh) + lane + 32 * r;
+              const int first = __shfl_sync(0xffffffffu, (int)row, (j >> sh) & 31);
+              if (j < ntok && first >= 0) copy_scales(first + (j & (a.box_rows - 1)), j);
+            }
+          }
+        }
+      } else {
+        // One bulk copy per token row, or, for rows of 64 or 128 bytes, 16 bytes a lane: a bulk copy takes
+        // about 80 cycles to issue whatever it brings.  24 requests at page size 1, D 128: one KV head and 20000
+        // to 40000 positions 162 us so and 200 by bulk copies, two heads and half as many positions
+        // (rows of 256 bytes) 144 and 116.  Page indices that are not in the window are loaded four rounds
+        // ahead.
+        const uint32_t RB = (uint32_t)(HC * RH);
+        const bool short_rows = RB <= 128 && (RB & (RB - 1)) == 0;
+        const int csh = 27 - __clz(RB);  // log2 of the 16-byte chunks of a short row
+        auto ahead = [&](int r) -> int32_t {
+          const int j = lane + 32 * r;
+          return !windowed && j < ntok ? entry((int)a.page_div.quot((uint32_t)(tok0 + j))) : -1;
+        };
+        int32_t p0 = ahead(0), p1 = ahead(1), p2 = ahead(2), p3 = ahead(3);
+#pragma unroll 1
+        for (int r = 0; r < W; ++r) {
+          const int j = lane + 32 * r;
+          const bool in = j < ntok;
+          uint32_t pidx, in_page;
+          a.page_div.divmod((uint32_t)(tok0 + (in ? j : 0)), pidx, in_page);
+          int32_t page = p0;
+          if (windowed) page = window_page(pidx);
+          p0 = p1, p1 = p2, p2 = p3, p3 = ahead(r + 4);
+          const int64_t row = row_at(pidx, in_page, page, in);
+          if (short_rows) {
+            const uint32_t to = smem_u32(dst) + 32 * r * a.row_stride;
+#pragma unroll 1
+            for (int it = lane; it < 32 << csh; it += 32) {
+              const int tk = it >> csh, ch = it & ((1 << csh) - 1);
+              const int64_t from = __shfl_sync(0xffffffffu, row, tk);
+              if (from >= 0)
+                cp_async16(to + tk * a.row_stride + ch * 16, pool + (from * a.num_kv_heads + hg * HC) * RH + ch * 16);
+            }
+            if (row >= 0) copy_scales(row, j);
+          } else {
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) mbar_expect_tx(bar, n * RB);
+            __syncwarp();
+            if (row >= 0) {
+              bulk_g2s(dst + (size_t)j * a.row_stride, pool + (row * a.num_kv_heads + hg * HC) * RH, RB, bar);
+              copy_scales(row, j);
+            }
+          }
+        }
+      }
+      if (bad && !v) report(a.err_word, bad);
+    }
+    // the arrival that lets the stage complete comes after every byte count
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    cp_async_arrive(bar);
+    next_stage();
+    return true;
+  };
+
+  if (c0 < c1) {
+    int64_t base = 0;  // stream offset (in slices) of request b0
+    for (int b0 = 0; b0 < a.batch && base < c1 && ok; b0 += 32) {
+      const int b = b0 + lane;
+      const bool in = b < a.batch;
+      int64_t L = first_len;
+      int32_t ip0 = first_p0, ip1 = first_p1;
+      if (b0 > 0) {
+        L = in ? min(max(0, ld(a.kv_lens + b)), kMaxLen) : 0;
+        ip0 = in ? ld(a.kv_indptr + b) : 0;
+        ip1 = in ? ld(a.kv_indptr + b + 1) : 0;
+      }
+      const int64_t S = (L + kSlice - 1) / kSlice;
+      int64_t incl = S;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const int64_t rs = base + nhg * (incl - S);
+      const int64_t re = base + nhg * incl;
+      uint32_t mask = __ballot_sync(0xffffffffu, in && S > 0 && re > c0 && rs < c1);
+      while (mask && ok) {
+        const int src_lane = __ffs(mask) - 1;
+        mask &= mask - 1;
+        const int bb = b0 + src_lane;
+        const int64_t Lb = __shfl_sync(0xffffffffu, L, src_lane);
+        const int64_t Sb = __shfl_sync(0xffffffffu, S, src_lane);
+        const int64_t rsb = __shfl_sync(0xffffffffu, rs, src_lane);
+        cur_p0 = __shfl_sync(0xffffffffu, ip0, src_lane);
+        cur_np = __shfl_sync(0xffffffffu, ip1, src_lane) - cur_p0;
+        for (int hg = 0; hg < nhg && ok; ++hg) {
+          const int64_t us = rsb + (int64_t)hg * Sb, ue = us + Sb;
+          const int64_t s0 = max(us, c0), s1 = min(ue, c1);
+          if (s0 >= s1) continue;
+          const int t0 = (int)(s0 - us) * kSlice;
+          const int t1 = (int)min((s1 - us) * kSlice, Lb);
+          for (int t = t0; t < t1 && ok; t += Ts) {
+            int flags = 0;
+            if (t == t0) flags |= kSegFirst;
+            if (t + Ts >= t1) flags |= kSegLast;
+            if (s0 == us) flags |= kStartsUnit;
+            if (s1 == ue) flags |= kEndsUnit;
+            ok = emit(bb * nhg + hg, bb, hg, t, min(Ts, t1 - t), flags);
+          }
+        }
+      }
+      base += nhg * __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  ok = ok && emit(-1, 0, 0, 0, 0, 0);
+  // The merge may be scheduled once every CTA has issued its last copies (it waits for this grid's
+  // completion before it reads): early enough to hide its launch, late enough not to hold thread
+  // slots that kernels on other streams could use.
+  if (!v) pdl_trigger();
+  if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+  // No copy into this CTA's shared memory is in flight when it exits (bounded waits; immediate on
+  // the normal path, where the consumers have seen every stage complete).
+  for (int k = 0; k < min(nissued, NS); ++k) {
+    if (--stage < 0) {
+      stage = NS - 1;
+      phase ^= 1;
+    }
+    mbar_wait(&full[stage], phase);
+  }
+}
+
+template <class F, bool TMA>
+__global__ void __launch_bounds__((F::kWarps + 2) * 32, 1) quant_decode_kernel(const __grid_constant__ QuantDecodeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int NS = a.num_stages;
+  const int NC = a.HC * a.nt * a.W;
+  if (TMA && (smem_u32(smem) & 1023u)) {  // the swizzled stage layout needs a 1024-byte base
+    if (threadIdx.x == 0) {
+      pdl_wait();
+      report(a.err_word, PKV_DEVERR_INTERNAL);
+    }
+    return;
+  }
+  uint8_t* stages = smem;
+  StageHdr* hdr = reinterpret_cast<StageHdr*>(smem + (size_t)NS * a.stage_bytes);
+  uint64_t* hdr_full = reinterpret_cast<uint64_t*>(hdr + NS);
+  uint64_t* full = hdr_full + NS;
+  uint64_t* empty = full + 2 * NS;  // K's barriers, then V's
+  uint64_t* meet_bar = empty + 2 * NS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(&hdr_full[s], 1);
+    mbar_init(meet_bar, NC);
+    for (int s = 0; s < 2 * NS; ++s) {
+      mbar_init(&full[s], 1 + 32);  // a producer's go-ahead, and every lane's scale copies
+      mbar_init(&empty[s], NC);
+    }
+    fence_mbar_init();
+    if (TMA) {
+      prefetch_tmap(&a.tm_k);
+      prefetch_tmap(&a.tm_v);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  pdl_wait();
+
+  const int warp = threadIdx.x >> 5;
+  if (warp == NC) {
+    quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, full, empty, false);
+  } else if (warp == NC + 1) {
+    quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, full + NS, empty + NS, true);
+  } else if (warp < NC) {
+    F::template consume<TMA>(a, stages, hdr, hdr_full, full, empty, meet_bar);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Merge of the split partials: one warp per (unit, query head), a programmatic dependent of the
+// decode kernel.  Bound by latency: 4 us after 8 requests of 32768 positions, 7 after 256 requests.
+// ---------------------------------------------------------------------------------------------
+template <class F>
+__global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_constant__ QuantDecodeArgs a) {
+  constexpr int D = F::kDim;
+  pdl_trigger();
+  pdl_wait();
+  const int u = blockIdx.x;
+  const int b = u / a.nhg, hg = u % a.nhg;
+  const int HQU = a.HC * a.group;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qhl = blockIdx.y * 8 + warp;
+  if (qhl >= HQU) return;
+  constexpr int VPL = D / 32;  // values per lane
+  const int64_t row = (int64_t)b * a.num_q_heads + (int64_t)hg * HQU + qhl;
+  __nv_bfloat16* op = a.out + row * D + lane * VPL;
+  auto store = [&](const float (&v)[VPL]) {
+    if constexpr (VPL == 4)
+      *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(v[0], v[1]);
+  };
+  if (ld(a.kv_lens + b) <= 0) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, PKV_DEVERR_LENGTH);
+    const float zero[VPL] = {};
+    store(zero);
+    if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
+    return;
+  }
+  const int first = a.unit_first[u], last = a.unit_last[u];
+  if (first == last) return;  // written directly
+  if (first < 0 || last >= a.num_parts || last < first) {  // a wait gave up somewhere
+    if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+    return;
+  }
+  // One pass: the partials' LSEs (one per lane) and the first sixteen partial rows are loaded together,
+  // so up to 32 partials cost one trip to L2; more rescale what they found.
+  const float* plse = a.part_lse + qhl;
+  const float* po = a.part_o + (int64_t)qhl * D + lane * VPL;
+  float mx = -INFINITY, tot = 0.f;
+  float acc[VPL] = {};
+  for (int base = first; base <= last; base += 32) {
+    const int n = min(32, last - base + 1);
+    const float pl = lane < n ? ld(plse + (int64_t)(base + lane) * HQU) : -INFINITY;
+    float x[16][VPL];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float* src = po + (int64_t)(base + i0 + k) * HQU * D;
+        if (i0 + k < n) {
+          if constexpr (VPL == 4)
+            *reinterpret_cast<float4*>(x[k]) = ld(reinterpret_cast<const float4*>(src));
+          else
+            *reinterpret_cast<float2*>(x[k]) = ld(reinterpret_cast<const float2*>(src));
+        } else {
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) x[k][v] = 0.f;
+        }
+      }
+    };
+    load(0);
+    float mn = pl;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
+    mn = fmaxf(mx, mn);
+    const float corr = __expf(mx - mn);  // 0 on the first round
+    mx = mn;
+    const float w = lane < n ? __expf(pl - mx) : 0.f;
+    tot = tot * corr + w;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) acc[v] *= corr;
+    for (int i0 = 0; i0 < n; i0 += 16) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (i0 + k) & 31);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) acc[v] += wk * x[k][v];
+      }
+    }
+  }
+  tot = warp_sum(tot);
+  const float inv = 1.f / tot;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) acc[v] *= inv;
+  store(acc);
+  if (lane == 0 && a.lse) a.lse[row] = mx + logf(tot);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------------------------
+struct QuantDecodePlan {
+  int HC, nhg, W, G, NT, Ts, RS, R, NS, ncta;
+  bool tma;
+  uint32_t region, stage;
+  size_t smem;
+  int64_t nunits, nparts;
+  size_t off_first, off_last, off_plse, off_po, ws_bytes;
+};
+
+// page_size 0: the workspace's part of the plan only.
+template <class F>
+bool make_plan(int B, int Hq, int Hkv, int ncta, QuantDecodePlan& p, int page_size = 0, int64_t num_pages = 0) {
+  constexpr size_t kSmemBudget = 225 * 1024;
+  auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return false;
+  p.G = Hq / Hkv;
+  if (p.G > 16) return false;
+  p.NT = (p.G + 7) / 8;
+  p.HC = 1;
+  for (int d = 1; d <= 8 / p.NT; ++d)
+    if (Hkv % d == 0) p.HC = d;
+  p.nhg = Hkv / p.HC;
+  p.W = F::kWarps / (p.HC * p.NT);
+  p.Ts = kSlice * p.W;
+  const int RB = p.HC * F::kRowBytes;
+  p.RS = F::row_stride(RB);
+  p.R = page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 8;
+  p.tma = page_size > 0 && page_size % 8 == 0 && num_pages * (int64_t)page_size < 0x7fffffffLL;
+  p.region = p.tma ? (uint32_t)(p.Ts * RB) : (uint32_t)(p.Ts * p.RS);
+  p.stage = (2 * p.region + (uint32_t)(2 * p.Ts * p.HC * F::kScaleBytes) + 1023u) & ~1023u;
+  if (p.W > 1) {
+    // the stage carries the merge of a head's warps, at least one of them at a time
+    const uint32_t state = (uint32_t)(p.HC * p.NT * F::kMergeFloats * 128);
+    if (state > p.stage) p.stage = (state + 1023u) & ~1023u;
+  }
+  const size_t per_stage = p.stage + sizeof(StageHdr) + 40;
+  if (2 * per_stage + 8 > kSmemBudget) return false;
+  p.NS = (int)((kSmemBudget - 8) / per_stage);
+  if (p.NS > kMaxStages) p.NS = kMaxStages;
+  p.smem = (size_t)p.NS * per_stage + 8;
+  p.ncta = ncta;
+  p.nunits = (int64_t)B * p.nhg;
+  p.nparts = p.ncta + p.nunits;
+  const int HQU = p.HC * p.G;
+  p.off_first = 0;
+  p.off_last = align256(p.off_first + (size_t)p.nunits * 4);
+  p.off_plse = align256(p.off_last + (size_t)p.nunits * 4);
+  p.off_po = align256(p.off_plse + (size_t)p.nparts * HQU * 4);
+  p.ws_bytes = align256(p.off_po + (size_t)p.nparts * HQU * F::kDim * 4);
+  return true;
+}
+
+// What a call gives besides the pool.
+struct QuantDecodeCall {
+  const void* q;
+  int32_t batch, num_q_heads;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* kv_lens;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* err_word;
+  int32_t max_ctas;
+  cudaStream_t stream;
+};
+
+template <class F, bool TMA>
+pkv_status launch_quant_decode(const QuantDecodePlan& p, const QuantDecodeArgs& a, cudaStream_t st) {
+  auto kern = quant_decode_kernel<F, TMA>;
+  // whether this instance's dynamic shared-memory limit was raised on this device (any host thread)
+  static std::atomic<bool> configured[64];
+  const int dev = pkv_host::current_device();
+  if (dev < 0) return PKV_ERR_CUDA;
+  if (dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) {
+      cudaGetLastError();  // not left for a later call's check to find
+      return PKV_ERR_CUDA;
+    }
+    if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
+  }
+  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2) * 32, p.smem, st, a);
+  if (s != PKV_OK) return s;
+  return pkv_host::launch_after(quant_decode_merge_kernel<F>, dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8)),
+                                256, 0, st, a);
+}
+
+// The checks that the entry points of both formats share, before head_dim chooses the instance.
+inline pkv_status check_quant_decode(const QuantDecodeCall& c, int32_t num_kv_heads, int32_t head_dim) {
+  if (c.batch < 0 || c.num_q_heads <= 0 || c.max_ctas < 0) return PKV_ERR_INVALID_ARG;
+  if (c.batch == 0) return PKV_OK;
+  if (!c.q || !c.kv_indptr || !c.kv_indices || !c.kv_lens || !c.out) return PKV_ERR_INVALID_ARG;
+  if (!pkv_host::aligned16(c.q) || !pkv_host::aligned16(c.out)) return PKV_ERR_INVALID_ARG;
+  if (c.num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+  if (c.batch > 0x7fffffff / 64) return PKV_ERR_UNSUPPORTED;
+  if ((head_dim != 64 && head_dim != 128) || c.num_q_heads / num_kv_heads > 16) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+
+// pool: any of the quantised pools; score_scale multiplies q . k, out_scale the result.
+template <class F, class Pool>
+pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float score_scale, float out_scale) {
+  int ncta = pkv_host::sm_count();
+  if (ncta <= 0) return PKV_ERR_CUDA;
+  if (c.max_ctas > 0 && c.max_ctas < ncta) ncta = c.max_ctas;  // fewer partials: the workspace still fits
+  QuantDecodePlan p;
+  if (!make_plan<F>(c.batch, c.num_q_heads, pool->num_kv_heads, ncta, p, pool->page_size, pool->num_pages))
+    return PKV_ERR_UNSUPPORTED;
+  if (p.nparts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // 31-bit numbers of units and partials
+  if (!c.workspace || c.workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(c.workspace) & 255u) != 0) return PKV_ERR_INVALID_ARG;
+
+  QuantDecodeArgs a;
+  a.k_pool = (const uint8_t*)pool->k;
+  a.v_pool = (const uint8_t*)pool->v;
+  a.k_scale = (const uint8_t*)pool->k_scale;
+  a.v_scale = (const uint8_t*)pool->v_scale;
+  a.num_pages = pool->num_pages;
+  a.page_size = pool->page_size;
+  a.page_div = FastDiv((uint32_t)pool->page_size);
+  a.num_kv_heads = pool->num_kv_heads;
+  a.q = (const __nv_bfloat16*)c.q;
+  a.batch = c.batch;
+  a.num_q_heads = c.num_q_heads;
+  a.kv_indptr = c.kv_indptr;
+  a.kv_indices = c.kv_indices;
+  a.kv_lens = c.kv_lens;
+  a.scale_log2 = score_scale * kLog2e;
+  a.out_scale = out_scale;
+  a.out = (__nv_bfloat16*)c.out;
+  a.lse = c.lse;
+  uint8_t* ws = (uint8_t*)c.workspace;
+  a.unit_first = (int32_t*)(ws + p.off_first);
+  a.unit_last = (int32_t*)(ws + p.off_last);
+  a.part_lse = (float*)(ws + p.off_plse);
+  a.part_o = (float*)(ws + p.off_po);
+  a.err_word = c.err_word;
+  a.HC = p.HC;
+  a.nhg = p.nhg;
+  a.W = p.W;
+  a.group = p.G;
+  a.nt = p.NT;
+  a.box_rows = p.R;
+  a.row_stride = p.RS;
+  a.stage_tokens = p.Ts;
+  a.num_stages = p.NS;
+  a.num_parts = (int32_t)p.nparts;
+  a.kv_region = p.region;
+  a.stage_bytes = p.stage;
+  if (p.tma) {
+    const uint64_t Hkv = pool->num_kv_heads, RH = F::kRowBytes;
+    const uint64_t rows = (uint64_t)pool->num_pages * pool->page_size;
+    if (!pkv_host::encode_tmap_3d_u8(&a.tm_k, pool->k, RH, rows, Hkv, Hkv * RH, RH, RH, p.R, p.HC) ||
+        !pkv_host::encode_tmap_3d_u8(&a.tm_v, pool->v, RH, rows, Hkv, Hkv * RH, RH, RH, p.R, p.HC))
+      return PKV_ERR_CUDA;
+  }
+  return p.tma ? launch_quant_decode<F, true>(p, a, c.stream) : launch_quant_decode<F, false>(p, a, c.stream);
+}
+
+template <class F>
+size_t quant_decode_workspace(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads) {
+  QuantDecodePlan p;
+  const int n = pkv_host::sm_count();
+  if (n <= 0 || !make_plan<F>(batch_size, num_q_heads, num_kv_heads, n, p)) return 0;
+  return p.ws_bytes;
+}
+
+}  // namespace pkv
