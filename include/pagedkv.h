@@ -537,6 +537,117 @@ pkv_status pkv_paged_decode_fp8(const pkv_pool_fp8* pool, const void* q, int32_t
                                 int32_t max_ctas, void* stream);
 
 /*
+ * The 4-bit cache.  K and V are held as e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with an e4m3 scale
+ * for every 16 values of a head's row, and one fp32 scale each for all of K and all of V: the value at (slot, head, d)
+ * is k4[slot, head, d] * k_scale[slot, head, d / 16] * k_global.  4.5 bits a value.  What the appends write, for the
+ * values x of a block, g = k_global (v_global), all in fp32 and each conversion to the nearest, ties to even:
+ *   scale = e4m3(max |x| / (6 g)), at most 448;  code = e2m1(x / (scale g)), at most 6 in size.
+ * A block whose largest |x| is at most 6 g 2^-10 has the scale 0 and reads as zeros, and one with values above 2688 g is
+ * held at 2688 g: choose g near the largest value that the cache will hold over 2688 (a calibration's result; it is a
+ * constant of the cache, every call gets the same).  A block with a NaN or an infinity has the scale NaN and codes of 0:
+ * all of its 16 values read as NaN.  The attention and the read-back take any scale that is not negative.
+ */
+typedef struct {
+  void* k;              /* codes [num_pages, page_size, num_kv_heads, head_dim / 2], 16-byte aligned: byte j of a head's row
+                           holds value 2j in its low four bits and 2j + 1 in its high ones */
+  void* v;              /* same shape as k */
+  void* k_scale;        /* e4m3 [num_pages, page_size, num_kv_heads, head_dim / 16], 16-byte aligned */
+  void* v_scale;        /* same shape as k_scale */
+  int64_t num_pages;
+  int32_t page_size;    /* >= 1 */
+  int32_t num_kv_heads; /* >= 1 */
+  int32_t head_dim;     /* attention: 64 or 128; append and read-back: any multiple of 16 */
+  float k_global;       /* in [2^-64, 2^64] */
+  float v_global;
+} pkv_pool_fp4;
+
+/*
+ * pkv_kv_append and pkv_rotary_kv_append into a 4-bit cache.  K (rotated in fp32, not rounded in between) and V are
+ * quantised as they are written; Q, where given, is rotated to bf16.  Arguments, limits and errors as for
+ * pkv_rotary_kv_append; slots must be distinct within one call.
+ */
+pkv_status pkv_kv_append_fp4(const pkv_pool_fp4* pool, const void* k_new, const void* v_new,
+                             const int64_t* slot_mapping, int32_t num_tokens, uint32_t* err_word,
+                             void* stream);
+pkv_status pkv_rotary_kv_append_fp4(const pkv_pool_fp4* pool, const void* k_new, const void* v_new,
+                                    const int64_t* slot_mapping, const int32_t* positions,
+                                    const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                                    int32_t interleaved, const void* q, void* q_out, int32_t num_q_heads,
+                                    int32_t num_tokens, uint32_t* err_word, void* stream);
+
+/*
+ * Read-back of a 4-bit cache as bf16(k4 k_scale k_global), the products in fp32 from left to right.  Arguments and errors
+ * as for pkv_paged_gather_fp8.
+ */
+pkv_status pkv_paged_gather_fp4(const pkv_pool_fp4* pool, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, const int32_t* kv_lens, int32_t batch_size,
+                                const int32_t* out_indptr, int32_t num_out_rows, void* k_out, void* v_out,
+                                uint32_t* err_word, void* stream);
+
+/*
+ * Paged decode over a 4-bit cache: pkv_paged_decode_fp8 over its values.  Arguments, limits and errors as there.  The
+ * softmax weights are rounded to f16 for the second product (11 bits; one below 2^-40 of the largest is 0); sums are
+ * fp32.  A NaN in K makes the rows of its KV head's queries NaN, one in V the sixteen values of its block.
+ */
+size_t pkv_decode_fp4_workspace_size(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim);
+pkv_status pkv_paged_decode_fp4(const pkv_pool_fp4* pool, const void* q, int32_t batch_size,
+                                int32_t num_q_heads, const int32_t* kv_indptr, const int32_t* kv_indices,
+                                const int32_t* kv_lens, float sm_scale, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                                int32_t max_ctas, void* stream);
+
+/*
+ * Movements of rows within a cache, in several tensors at once: the K, V and scale tensors of one layer or of all of them,
+ * of any of the formats above.  Every tensor is [num_pages, page_size, ...], contiguous, and holds slot_bytes bytes for
+ * a slot (a bf16 K: num_kv_heads * head_dim * 2).  At most 256 tensors a call.
+ */
+typedef struct {
+  void* base;         /* device, 16-byte aligned */
+  int64_t slot_bytes; /* > 0 */
+} pkv_plane;
+
+/*
+ * Copies the first rows[i] rows (all of them where rows is NULL) of page src_pages[i] to page dst_pages[i] in every
+ * tensor: a sequence that forks in the middle of a page gets one of its own.  A negative dst_pages[i] is padding.  A page may
+ * be copied several times; it must not be a target twice, nor be a target and a (different) copy's source in one call
+ * (pkv_validate_page_copies checks that on the host).
+ *   planes     host array [num_planes], read before the call returns
+ *   src_pages, dst_pages, rows (nullable)  int32 [num_copies] (device)
+ *   err_word   nullable; PKV_DEVERR_PAGE_OOB, PKV_DEVERR_LENGTH for rows[i] outside [0, page_size]: the copy is skipped
+ */
+pkv_status pkv_copy_pages(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size,
+                          const int32_t* src_pages, const int32_t* dst_pages, const int32_t* rows,
+                          int32_t num_copies, uint32_t* err_word, void* stream);
+
+/*
+ * Host-side check of a call of pkv_copy_pages, on HOST copies: pages in [0, num_pages) (negative targets are padding),
+ * no target twice, no target that is another copy's source.  PKV_OK, or PKV_ERR_INVALID_ARG with the first offending copy in
+ * *bad_copy (nullable; -1 when none).
+ */
+pkv_status pkv_validate_page_copies(const int32_t* src_pages, const int32_t* dst_pages, int32_t num_copies,
+                                    int64_t num_pages, int32_t* bad_copy);
+
+/*
+ * Moves the accepted tokens of drafted trees (pkv_paged_tree_attention) behind their prefix in every tensor: the row at
+ * position prefix_lens[b] + accepted[accepted_indptr[b] + k] of request b goes to position prefix_lens[b] + k.  The
+ * request's length is then prefix_lens[b] plus the number of its accepted tokens; what its other drafted positions hold is
+ * not said.
+ *   planes     host array [num_planes], read before the call returns
+ *   kv_indptr, kv_indices  the page lists (device); a page with drafted positions belongs to one request alone
+ *   prefix_lens       int32 [batch_size], >= 0 (device)
+ *   accepted_indptr   int32 [batch_size+1], non-decreasing, within [0, num_accepted] (device)
+ *   accepted          int32 [num_accepted] (device): indices within the request's tree, >= 0, each larger than the one before
+ *   err_word   nullable; PKV_DEVERR_LENGTH for a position past the request's pages, a negative prefix or an accepted index
+ *              that is not larger than the one before, PKV_DEVERR_ROW_OOB for an accepted_indptr outside its range,
+ *              PKV_DEVERR_PAGE_OOB: the rows concerned are not moved
+ */
+pkv_status pkv_compact_accepted(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size,
+                                const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* prefix_lens,
+                                int32_t batch_size, const int32_t* accepted_indptr, const int32_t* accepted,
+                                int32_t num_accepted, uint32_t* err_word, void* stream);
+
+/*
  * Attention of trees of drafted tokens over a paged cache (speculative decoding: one pass verifies
  * every branch).  Request b's drafted tokens are rows qo_indptr[b] .. qo_indptr[b+1] of q; token t of
  * the request is at pool position prefix_lens[b] + t of its page list (append their K/V first).  Token

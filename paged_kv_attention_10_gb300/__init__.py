@@ -32,6 +32,8 @@ __all__ = [
     "rope_cos_sin_table", "rope_kv_append", "rotary_kv_append", "rotary_cos_sin_table",
     "kv_append_fp8", "rotary_kv_append_fp8", "paged_gather_fp8",
     "decode_fp8_workspace_size", "paged_decode_fp8",
+    "kv_append_fp4", "rotary_kv_append_fp4", "paged_gather_fp4", "decode_fp4_workspace_size", "paged_decode_fp4",
+    "copy_pages", "validate_page_copies", "compact_accepted",
     "tree_workspace_size", "paged_tree_attention", "tree_mask_from_parents", "DEVERR_PAGE_OOB", "DEVERR_SLOT_OOB", "DEVERR_LENGTH",
     "DEVERR_TIMEOUT", "DEVERR_INTERNAL", "DEVERR_ROW_OOB",
 ]
@@ -65,6 +67,16 @@ class PoolFP8(ctypes.Structure):
                 ("page_size", _c_i32), ("num_kv_heads", _c_i32), ("head_dim", _c_i32)]
 
 
+class PoolFP4(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _c_i64),
+                ("page_size", _c_i32), ("num_kv_heads", _c_i32), ("head_dim", _c_i32), ("k_global", _c_f32),
+                ("v_global", _c_f32)]
+
+
+class Plane(ctypes.Structure):
+    _fields_ = [("base", _vp), ("slot_bytes", _c_i64)]
+
+
 class RopeScaling(ctypes.Structure):
     _fields_ = [("kind", _c_i32), ("factor", ctypes.c_double), ("original_max_position", ctypes.c_double),
                 ("low", ctypes.c_double), ("high", ctypes.c_double), ("attention_factor", ctypes.c_double)]
@@ -90,6 +102,8 @@ def load():
     lib = ctypes.CDLL(_LIB_PATH)
     P = ctypes.POINTER(Pool)
     P8 = ctypes.POINTER(PoolFP8)
+    P4 = ctypes.POINTER(PoolFP4)
+    PL = ctypes.POINTER(Plane)
     sig = {
         "pkv_status_string": (ctypes.c_char_p, [_c_i32]),
         "pkv_version": (_c_i32, []),
@@ -137,6 +151,17 @@ def load():
                                               _c_i32, _c_i32, _c_f32, _vp, _vp, _vp, _c_sz, _vp, _vp]),
         "pkv_tree_mask_from_parents": (_c_i32, [_vp, _vp, _c_i32, _c_i32, _c_i32, _c_i32, _vp, _vp, _vp]),
         "pkv_paged_gather_fp8": (_c_i32, [P8, _vp, _vp, _vp, _c_i32, _vp, _c_i32, _vp, _vp, _vp, _vp]),
+        "pkv_kv_append_fp4": (_c_i32, [P4, _vp, _vp, _vp, _c_i32, _vp, _vp]),
+        "pkv_rotary_kv_append_fp4": (_c_i32, [P4, _vp, _vp, _vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _vp,
+                                              _vp, _c_i32, _c_i32, _vp, _vp]),
+        "pkv_paged_gather_fp4": (_c_i32, [P4, _vp, _vp, _vp, _c_i32, _vp, _c_i32, _vp, _vp, _vp, _vp]),
+        "pkv_decode_fp4_workspace_size": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
+        "pkv_paged_decode_fp4": (_c_i32, [P4, _vp, _c_i32, _c_i32, _vp, _vp, _vp, _c_f32, _vp, _vp, _vp,
+                                          _c_sz, _vp, _c_i32, _vp]),
+        "pkv_copy_pages": (_c_i32, [PL, _c_i32, _c_i64, _c_i32, _vp, _vp, _vp, _c_i32, _vp, _vp]),
+        "pkv_validate_page_copies": (_c_i32, [_vp, _vp, _c_i32, _c_i64, _vp]),
+        "pkv_compact_accepted": (_c_i32, [PL, _c_i32, _c_i64, _c_i32, _vp, _vp, _vp, _c_i32, _vp, _vp,
+                                          _c_i32, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -203,6 +228,22 @@ def validate_slots(slot_mapping, num_slots: int) -> None:
                                    ctypes.byref(bad))
     if st != 0:
         e = PagedKVError(f"pkv_validate_slots (token {bad.value})", st)
+        e.bad = bad.value
+        raise e
+
+
+def validate_page_copies(src_pages, dst_pages, num_pages: int) -> None:
+    """Check host lists of page copies (in range, no page a target twice or a target and another copy's source);
+    raises PagedKVError naming the first bad copy (``.bad``)."""
+    _host_i(src_pages, "src_pages", torch.int32)
+    _host_i(dst_pages, "dst_pages", torch.int32)
+    if src_pages.numel() != dst_pages.numel():
+        raise ValueError("src_pages and dst_pages must have as many entries")
+    bad = ctypes.c_int32(-1)
+    st = load().pkv_validate_page_copies(_ptr(src_pages), _ptr(dst_pages), dst_pages.numel(), int(num_pages),
+                                         ctypes.byref(bad))
+    if st != 0:
+        e = PagedKVError(f"pkv_validate_page_copies (copy {bad.value})", st)
         e.bad = bad.value
         raise e
 
@@ -601,6 +642,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current = torch._C._cuda_getDevice
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 _E4M3 = torch.float8_e4m3fn
+_CODES = tuple(t for t in (_U8, getattr(torch, "float4_e2m1fn_x2", None)) if t is not None)
 
 
 def _addr(t, name, dtype, index):
@@ -668,6 +710,25 @@ def _pool_fp8(k_pool, v_pool, k_scale, v_scale):
     if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
         raise ValueError("k_scale and v_scale must both be [num_pages, page_size, num_kv_heads]")
     return PoolFP8(k, v, ks, vs, *shape), index, shape
+
+
+def _pool_fp4(k_pool, v_pool, k_scale, v_scale, k_global, v_global):
+    """(pool, its device index, its shape in values) of a 4-bit cache."""
+    for t, name, types, what in ((k_pool, "k_pool", _CODES, "torch.uint8 (two codes a byte)"),
+                                 (k_scale, "k_scale", (_E4M3, _U8), "torch.float8_e4m3fn (or its bytes as torch.uint8)")):
+        if isinstance(t, torch.Tensor) and t.dtype not in types:
+            raise TypeError(f"{name} must be {what}, got {t.dtype}")
+    index = _device_index(k_pool, "k_pool")
+    k, v = _addr(k_pool, "k_pool", k_pool.dtype, index), _addr(v_pool, "v_pool", k_pool.dtype, index)
+    _device_index(k_scale, "k_scale")
+    ks, vs = _addr(k_scale, "k_scale", k_scale.dtype, index), _addr(v_scale, "v_scale", k_scale.dtype, index)
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape:
+        raise ValueError("k_pool and v_pool must both be [num_pages, page_size, num_kv_heads, head_dim / 2]")
+    if k_scale.shape != (*shape[:3], shape[3] // 8) or v_scale.shape != k_scale.shape or shape[3] % 8:
+        raise ValueError("k_scale and v_scale must both be [num_pages, page_size, num_kv_heads, head_dim / 16]")
+    shape = (*shape[:3], 2 * shape[3])
+    return PoolFP4(k, v, ks, vs, *shape, k_global, v_global), index, shape
 
 
 def _new_rows(index, shape, k_new, v_new, slot_mapping):
@@ -789,16 +850,8 @@ def paged_gather_fp8(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv
             None if stream is None else stream.cuda_stream), "pkv_paged_gather_fp8"):
         return k_out, v_out
     pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
-    at = [_addr(t, n, _I32, index) for t, n in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"),
-                                                (kv_lens, "kv_lens"), (out_indptr, "out_indptr"))]
-    ko, vo = _addr(k_out, "k_out", _BF16, index), _addr(v_out, "v_out", _BF16, index)
-    B = kv_lens.numel()
-    if kv_indptr.numel() != B + 1 or out_indptr.numel() != B + 1:
-        raise ValueError("kv_indptr and out_indptr must have batch_size + 1 entries")
-    if k_out.dim() != 3 or k_out.shape[1:] != shape[2:] or v_out.shape != k_out.shape:
-        raise ValueError("k_out/v_out must be [num_out_rows, num_kv_heads, head_dim]")
-    _run(index, stream, "pkv_paged_gather_fp8", pool, *at[:3], B, at[3], k_out.shape[0], ko, vo,
-         _addr_or_none(err_word, "err_word", _I32, index))
+    _gather("pkv_paged_gather_fp8", pool, index, shape, kv_indptr, kv_indices, kv_lens, out_indptr, k_out, v_out,
+            err_word, stream)
     return k_out, v_out
 
 
@@ -832,6 +885,24 @@ def _page_table(index, kv_indptr, kv_indices, B):
     return _addr(kv_indptr, "kv_indptr", _I32, index), _addr(kv_indices, "kv_indices", _I32, index)
 
 
+def _decode_quant(fn, workspace_size, pool, index, shape, q, kv_indptr, kv_indices, kv_lens, sm_scale, out, lse, workspace,
+                  err_word, stream, return_lse, max_ctas):
+    lens = _addr(kv_lens, "kv_lens", _I32, index)
+    B = kv_lens.numel()
+    indptr, indices = _page_table(index, kv_indptr, kv_indices, B)
+    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse, stream)
+    if q.shape[0] != B:
+        raise ValueError("q must have one row per request")
+    Hq = q.shape[1]
+    if workspace is None:
+        need = workspace_size(B, Hq, shape[2], shape[3], index)
+        workspace = _scratch(max(need, 256), q.device, stream)
+    _run(index, stream, fn, pool, q_at, B, Hq, indptr, indices, lens, sm_scale, o_at, l_at,
+         _addr(workspace, "workspace", _U8, index), workspace.numel(), _addr_or_none(err_word, "err_word", _I32, index),
+         max_ctas)
+    return out, lse
+
+
 def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, sm_scale: float,
                      out=None, lse=None, workspace=None, err_word=None, stream=None, return_lse=True,
                      max_ctas=0):
@@ -843,20 +914,140 @@ def paged_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices,
                 err_word, max_ctas, None if stream is None else stream.cuda_stream), "pkv_paged_decode_fp8"):
         return out, lse
     pool, index, shape = _pool_fp8(k_pool, v_pool, k_scale, v_scale)
-    lens = _addr(kv_lens, "kv_lens", _I32, index)
+    return _decode_quant("pkv_paged_decode_fp8", decode_fp8_workspace_size, pool, index, shape, q, kv_indptr,
+                         kv_indices, kv_lens, sm_scale, out, lse, workspace, err_word, stream, return_lse, max_ctas)
+
+
+def kv_append_fp4(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, k_global: float = 1.0,
+                  v_global: float = 1.0, err_word=None, stream=None) -> None:
+    """Quantise k_new[t], v_new[t] to e2m1 with an e4m3 scale for every 16 values (and the cache's own scales k_global,
+    v_global) and write them into pool slot slot_mapping[t] (negative = skip).  k_pool and v_pool are
+    uint8 [num_pages, page_size, num_kv_heads, head_dim / 2], k_scale and v_scale float8_e4m3fn [..., head_dim / 16]."""
+    if _done((_checked or _load_checked()).kv_append_fp4(
+            k_pool, v_pool, k_scale, v_scale, k_global, v_global, k_new, v_new, slot_mapping, err_word,
+            None if stream is None else stream.cuda_stream), "pkv_kv_append_fp4"):
+        return
+    pool, index, shape = _pool_fp4(k_pool, v_pool, k_scale, v_scale, k_global, v_global)
+    rows, T = _new_rows(index, shape, k_new, v_new, slot_mapping)
+    _run(index, stream, "pkv_kv_append_fp4", pool, *rows, T, _addr_or_none(err_word, "err_word", _I32, index))
+
+
+def rotary_kv_append_fp4(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, positions, cos_sin,
+                         q=None, q_out=None, interleaved: bool = False, k_global: float = 1.0, v_global: float = 1.0,
+                         err_word=None, stream=None) -> None:
+    """rotary_kv_append into a 4-bit cache: K (rotated) and V quantised as by kv_append_fp4."""
+    if _done((_checked or _load_checked()).rotary_kv_append_fp4(
+            k_pool, v_pool, k_scale, v_scale, k_global, v_global, k_new, v_new, slot_mapping, positions, cos_sin, q,
+            q_out, bool(interleaved), err_word, None if stream is None else stream.cuda_stream),
+            "pkv_rotary_kv_append_fp4"):
+        return
+    pool, index, shape = _pool_fp4(k_pool, v_pool, k_scale, v_scale, k_global, v_global)
+    _rotary("pkv_rotary_kv_append_fp4", pool, index, shape, k_new, v_new, slot_mapping, positions, cos_sin, q,
+            q_out, interleaved, err_word, stream)
+
+
+def _gather(fn, pool, index, shape, kv_indptr, kv_indices, kv_lens, out_indptr, k_out, v_out, err_word, stream):
+    at = [_addr(t, n, _I32, index) for t, n in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"),
+                                                (kv_lens, "kv_lens"), (out_indptr, "out_indptr"))]
+    ko, vo = _addr(k_out, "k_out", _BF16, index), _addr(v_out, "v_out", _BF16, index)
     B = kv_lens.numel()
+    if kv_indptr.numel() != B + 1 or out_indptr.numel() != B + 1:
+        raise ValueError("kv_indptr and out_indptr must have batch_size + 1 entries")
+    if k_out.dim() != 3 or k_out.shape[1:] != shape[2:] or v_out.shape != k_out.shape:
+        raise ValueError("k_out/v_out must be [num_out_rows, num_kv_heads, head_dim]")
+    _run(index, stream, fn, pool, *at[:3], B, at[3], k_out.shape[0], ko, vo,
+         _addr_or_none(err_word, "err_word", _I32, index))
+
+
+def paged_gather_fp4(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, out_indptr, k_out,
+                     v_out, k_global: float = 1.0, v_global: float = 1.0, err_word=None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Read a 4-bit cache back as bf16: position j of request b goes to row out_indptr[b] + j of
+    k_out/v_out [num_out_rows, num_kv_heads, head_dim]; other rows are left as they were."""
+    if _done((_checked or _load_checked()).paged_gather_fp4(
+            k_pool, v_pool, k_scale, v_scale, k_global, v_global, kv_indptr, kv_indices, kv_lens, out_indptr, k_out,
+            v_out, err_word, None if stream is None else stream.cuda_stream), "pkv_paged_gather_fp4"):
+        return k_out, v_out
+    pool, index, shape = _pool_fp4(k_pool, v_pool, k_scale, v_scale, k_global, v_global)
+    _gather("pkv_paged_gather_fp4", pool, index, shape, kv_indptr, kv_indices, kv_lens, out_indptr, k_out, v_out,
+            err_word, stream)
+    return k_out, v_out
+
+
+def decode_fp4_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim, device=None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(load().pkv_decode_fp4_workspace_size(batch_size, num_q_heads, num_kv_heads, head_dim))
+
+
+def paged_decode_fp4(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv_lens, sm_scale: float,
+                     out=None, lse=None, workspace=None, k_global: float = 1.0, v_global: float = 1.0, err_word=None,
+                     stream=None, return_lse=True, max_ctas=0):
+    """Decode attention of q [B, Hq, D] over each request's pages of a 4-bit cache.  Returns
+    (out, lse); arguments as for paged_decode, and the cache's own scales."""
+    if out is not None and workspace is not None and (lse is not None or not return_lse) and _done(
+            (_checked or _load_checked()).paged_decode_fp4(
+                k_pool, v_pool, k_scale, v_scale, k_global, v_global, q, out, lse, kv_indptr, kv_indices, kv_lens,
+                sm_scale, workspace, err_word, max_ctas, None if stream is None else stream.cuda_stream),
+            "pkv_paged_decode_fp4"):
+        return out, lse
+    pool, index, shape = _pool_fp4(k_pool, v_pool, k_scale, v_scale, k_global, v_global)
+    return _decode_quant("pkv_paged_decode_fp4", decode_fp4_workspace_size, pool, index, shape, q, kv_indptr,
+                         kv_indices, kv_lens, sm_scale, out, lse, workspace, err_word, stream, return_lse, max_ctas)
+
+
+# ---------------------------------------------------------------------------------------------
+# movements of rows within a cache
+# ---------------------------------------------------------------------------------------------
+def _planes(tensors):
+    """(planes, how many, the device index, num_pages, page_size) of a cache's tensors [num_pages, page_size, ...]."""
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("tensors must name at least one tensor of the cache")
+    index = _device_index(tensors[0], "tensors[0]")
+    planes = (Plane * len(tensors))()
+    for i, t in enumerate(tensors):
+        at = _addr(t, f"tensors[{i}]", t.dtype if isinstance(t, torch.Tensor) else None, index)
+        if t.dim() < 2 or t.shape[:2] != tensors[0].shape[:2] or not t.numel():
+            raise ValueError("tensors must all be [num_pages, page_size, ...], with the same num_pages and page_size")
+        planes[i] = Plane(at, t.numel() * t.element_size() // (t.shape[0] * t.shape[1]))
+    return planes, len(tensors), index, tensors[0].shape[0], tensors[0].shape[1]
+
+
+def copy_pages(tensors, src_pages, dst_pages, rows=None, err_word=None, stream=None) -> None:
+    """Copy page src_pages[i] (its first rows[i] rows where rows is given) to page dst_pages[i] (negative = skip) in
+    every one of the cache's tensors [num_pages, page_size, ...]: K, V and scales of a layer or of all layers, of any type, at
+    most 256.  No page may be a target twice, or a target and another copy's source (validate_page_copies)."""
+    if _done((_checked or _load_checked()).copy_pages(
+            tensors, src_pages, dst_pages, rows, err_word, None if stream is None else stream.cuda_stream),
+            "pkv_copy_pages"):
+        return
+    planes, count, index, num_pages, page_size = _planes(tensors)
+    src, dst = _addr(src_pages, "src_pages", _I32, index), _addr(dst_pages, "dst_pages", _I32, index)
+    n = dst_pages.numel()
+    if src_pages.numel() != n or (rows is not None and rows.numel() != n):
+        raise ValueError("src_pages, dst_pages and rows must have as many entries")
+    _run(index, stream, "pkv_copy_pages", planes, count, num_pages, page_size, src, dst,
+         _addr_or_none(rows, "rows", _I32, index), n, _addr_or_none(err_word, "err_word", _I32, index))
+
+
+def compact_accepted(tensors, kv_indptr, kv_indices, prefix_lens, accepted_indptr, accepted, err_word=None,
+                     stream=None) -> None:
+    """Move the accepted tokens of drafted trees behind their prefix in every one of the cache's tensors (as for
+    copy_pages): the row at position prefix_lens[b] + accepted[accepted_indptr[b] + k] of request b goes to position
+    prefix_lens[b] + k.  A request's accepted indices ascend."""
+    if _done((_checked or _load_checked()).compact_accepted(
+            tensors, kv_indptr, kv_indices, prefix_lens, accepted_indptr, accepted, err_word,
+            None if stream is None else stream.cuda_stream), "pkv_compact_accepted"):
+        return
+    planes, count, index, num_pages, page_size = _planes(tensors)
+    prefix = _addr(prefix_lens, "prefix_lens", _I32, index)
+    B = prefix_lens.numel()
     indptr, indices = _page_table(index, kv_indptr, kv_indices, B)
-    out, lse, q_at, o_at, l_at = _attention_io(q, index, shape[3], out, lse, return_lse, stream)
-    if q.shape[0] != B:
-        raise ValueError("q must have one row per request")
-    Hq = q.shape[1]
-    if workspace is None:
-        need = decode_fp8_workspace_size(B, Hq, shape[2], shape[3], index)
-        workspace = _scratch(max(need, 256), q.device, stream)
-    _run(index, stream, "pkv_paged_decode_fp8", pool, q_at, B, Hq, indptr, indices, lens, sm_scale, o_at, l_at,
-         _addr(workspace, "workspace", _U8, index), workspace.numel(), _addr_or_none(err_word, "err_word", _I32, index),
-         max_ctas)
-    return out, lse
+    starts, taken = _addr(accepted_indptr, "accepted_indptr", _I32, index), _addr(accepted, "accepted", _I32, index)
+    if accepted_indptr.numel() != B + 1:
+        raise ValueError("accepted_indptr must have batch_size + 1 entries")
+    _run(index, stream, "pkv_compact_accepted", planes, count, num_pages, page_size, indptr, indices, prefix, B, starts,
+         taken, accepted.numel(), _addr_or_none(err_word, "err_word", _I32, index))
 
 
 # ---------------------------------------------------------------------------------------------

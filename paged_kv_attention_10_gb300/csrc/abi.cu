@@ -53,6 +53,15 @@ bool valid_pool8(const pkv_pool_fp8* p) {
   return aligned16(p->k) && aligned16(p->v) && aligned16(p->k_scale) && aligned16(p->v_scale);
 }
 
+bool valid_pool4(const pkv_pool_fp4* p) {
+  if (!p || !p->k || !p->v || !p->k_scale || !p->v_scale) return false;
+  if (p->num_pages <= 0 || p->page_size <= 0 || p->num_kv_heads <= 0 || p->head_dim <= 0) return false;
+  if ((p->head_dim % 16) != 0) return false;
+  for (const float g : {p->k_global, p->v_global})  // with a block's scale 2^-9 .. 448 all products stay normal numbers
+    if (!(g >= 0x1p-64f && g <= 0x1p64f)) return false;
+  return aligned16(p->k) && aligned16(p->v) && aligned16(p->k_scale) && aligned16(p->v_scale);
+}
+
 namespace {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
@@ -146,13 +155,16 @@ bool encode_tmap_head(CUtensorMap* m, const void* base, uint64_t D, uint64_t hea
 bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                        uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2) {
   auto fn = encode_fn();
-  if (!fn || (b0 != 64 && b0 != 128)) return false;
+  if (!fn || (b0 != 32 && b0 != 64 && b0 != 128)) return false;
   cuuint64_t dims[3] = {d0, d1, d2};
   cuuint64_t strides[2] = {s1, s2};
   cuuint32_t box[3] = {b0, b1, b2};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, b0 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            b0 == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+            : b0 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                       : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -240,6 +252,34 @@ pkv_status pkv_validate_slots(const int64_t* slot_mapping, int32_t num_tokens, i
     return PKV_ERR_INVALID_ARG;
   }
   return PKV_OK;
+}
+
+pkv_status pkv_validate_page_copies(const int32_t* src_pages, const int32_t* dst_pages, int32_t num_copies,
+                                    int64_t num_pages, int32_t* bad_copy) {
+  if (bad_copy) *bad_copy = -1;
+  if (num_copies < 0 || num_pages < 0) return PKV_ERR_INVALID_ARG;
+  if (num_copies == 0) return PKV_OK;
+  if (!src_pages || !dst_pages) return PKV_ERR_INVALID_ARG;
+  std::vector<std::pair<int32_t, int32_t>> to;  // (target, copy), without padding
+  to.reserve((size_t)num_copies);
+  int32_t bad = num_copies;  // the first offending copy
+  for (int32_t i = 0; i < num_copies; ++i) {
+    if (dst_pages[i] < 0) continue;
+    if (src_pages[i] < 0 || src_pages[i] >= num_pages || dst_pages[i] >= num_pages) bad = std::min(bad, i);
+    to.emplace_back(dst_pages[i], i);
+  }
+  std::sort(to.begin(), to.end());
+  for (size_t k = 1; k < to.size(); ++k)
+    if (to[k].first == to[k - 1].first) bad = std::min(bad, to[k].second);
+  for (int32_t i = 0; i < num_copies; ++i) {
+    if (dst_pages[i] < 0) continue;
+    auto hit = std::lower_bound(to.begin(), to.end(), std::make_pair(src_pages[i], INT32_MIN));
+    if (hit != to.end() && hit->first == src_pages[i] && (hit->second != i || src_pages[i] != dst_pages[i]))
+      bad = std::min(bad, i);
+  }
+  if (bad == num_copies) return PKV_OK;
+  if (bad_copy) *bad_copy = bad;
+  return PKV_ERR_INVALID_ARG;
 }
 
 pkv_status pkv_selftest_bounded_wait(uint32_t* err_word, void* stream) {

@@ -1,0 +1,320 @@
+// Movements of rows within a paged cache of any format, in many tensors (the K, V and scale tensors of all layers) at
+// once: copies of whole or begun pages, and the accepted tokens of drafted trees moved behind their prefix.
+//
+// Nothing is computed: bytes move, in pieces of the largest power of two up to 16 that divides a tensor's bytes per
+// slot.  Bound by HBM for many pages, by latency for a few.
+#include "quant.cuh"
+
+namespace {
+
+using namespace pkv;
+
+// The tensors of a call.  N: how many it has room for; a call of a few (one layer) does not carry the room of all layers
+// through its launch.
+template <int N>
+struct Planes {
+  void* base[N];
+  uint32_t slot_bytes[N];
+  uint32_t first[N];  // of the plane's work items, counted from those of plane 0 (see each kernel)
+  int32_t count;
+};
+constexpr int kFewPlanes = 8, kMaxPlanes = 256;
+
+// The plane of work item r: the last whose first item is not behind r.
+template <int N>
+PKV_DEV int plane_of(const Planes<N>& p, uint32_t r) {
+  int lo = 0, hi = p.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.first[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Pieces that a lane has in flight.
+constexpr int kFlight = 8;
+
+// ---------------------------------------------------------------------------------------------
+// Copies of pages.  A warp takes a tile of one page of one tensor: 32 lanes times kFlight pieces.
+// ---------------------------------------------------------------------------------------------
+template <int N>
+struct CopyArgs {
+  Planes<N> planes;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* rows;
+  int64_t num_pages;
+  int32_t page_size;
+  FastDiv tile_div;  // by the tiles of a page in all tensors
+  uint32_t items;
+  uint32_t* err_word;
+};
+
+template <typename V>
+PKV_DEV void copy_tile(const char* from, char* to, uint32_t bytes, uint32_t tile) {
+  const uint32_t n = bytes / sizeof(V), at = tile * 32 * kFlight + (threadIdx.x & 31);
+  const V* s = reinterpret_cast<const V*>(from);
+  V* d = reinterpret_cast<V*>(to);
+  V v[kFlight];
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u)
+    if (at + 32 * u < n) v[u] = ld(s + at + 32 * u);
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u)
+    if (at + 32 * u < n) d[at + 32 * u] = v[u];
+}
+
+template <int N>
+__global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ CopyArgs<N> a) {
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (item >= a.items) return;
+  uint32_t i, r;
+  a.tile_div.divmod(item, i, r);
+  const int32_t dst = ld(a.dst + i), src = ld(a.src + i);
+  const int32_t rows = a.rows ? ld(a.rows + i) : a.page_size;
+  if (dst < 0) return;  // padding
+  const bool pages_ok = src >= 0 && src < a.num_pages && dst < a.num_pages, rows_ok = rows >= 0 && rows <= a.page_size;
+  if (!pages_ok || !rows_ok) {
+    if (r == 0 && (threadIdx.x & 31) == 0)
+      report(a.err_word, (pages_ok ? 0u : PKV_DEVERR_PAGE_OOB) | (rows_ok ? 0u : PKV_DEVERR_LENGTH));
+    return;
+  }
+  if (src == dst) return;
+  const int p = plane_of(a.planes, r);
+  const uint32_t tile = r - a.planes.first[p], slot = a.planes.slot_bytes[p], bytes = rows * slot;
+  const int64_t page = (int64_t)slot * a.page_size;
+  const char* from = (const char*)a.planes.base[p] + src * page;
+  char* to = (char*)a.planes.base[p] + dst * page;
+  if (slot % 16 == 0) copy_tile<uint4>(from, to, bytes, tile);
+  else if (slot % 8 == 0) copy_tile<uint2>(from, to, bytes, tile);
+  else if (slot % 4 == 0) copy_tile<uint32_t>(from, to, bytes, tile);
+  else if (slot % 2 == 0) copy_tile<uint16_t>(from, to, bytes, tile);
+  else copy_tile<uint8_t>(from, to, bytes, tile);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Compaction.  Row k of a request's accepted tokens moves from position prefix + accepted[k] to prefix + k.  With
+// accepted ascending, no row is written before it is read as long as rows are taken in order: what row k writes
+// (prefix + k) is not the source of a later row j (prefix + accepted[j], accepted[j] >= j > k).  A warp takes up to 32
+// pieces side by side of one request's rows in one tensor; of narrow rows it takes several at a time.  It reads a
+// group of rows, then writes it.
+// ---------------------------------------------------------------------------------------------
+template <int N>
+struct CompactArgs {
+  Planes<N> planes;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* prefix_lens;
+  const int32_t* accepted_indptr;
+  const int32_t* accepted;
+  int64_t num_pages;
+  int32_t page_size, num_accepted;
+  FastDiv item_div;  // by the warps of a request in all tensors
+  FastDiv page_div;
+  uint32_t items;
+  uint32_t* err_word;
+};
+
+// The slot of position `pos` of a request with np pages from p0 on; -1 and a bit in bad where there is none.
+template <int N>
+PKV_DEV int64_t slot_at(const CompactArgs<N>& a, int32_t p0, int32_t np, int64_t pos, uint32_t& bad) {
+  uint32_t pidx = 0, in_page = 0;
+  if (pos <= 0x7fffffff) a.page_div.divmod((uint32_t)pos, pidx, in_page);
+  if (pos > 0x7fffffff || (int64_t)pidx >= np) {
+    bad |= PKV_DEVERR_LENGTH;
+    return -1;
+  }
+  const int32_t page = ld(a.kv_indices + p0 + pidx);
+  if (page < 0 || page >= a.num_pages) {
+    bad |= PKV_DEVERR_PAGE_OOB;
+    return -1;
+  }
+  return (int64_t)page * a.page_size + in_page;
+}
+
+// A warp's pieces `chunk` (32 side by side) of the n rows of lane l's (source, target) slots.
+template <typename V>
+PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, int64_t src, int64_t dst, int n) {
+  const int lane = threadIdx.x & 31;
+  const int cols = min(32, (int)(slot_bytes / sizeof(V)) - 32 * (int)chunk);
+  const int sh = 32 - __clz(cols - 1);  // lanes of a row: the power of two at or above cols
+  const int col = lane & ((1 << sh) - 1), sub = lane >> sh, step = 32 >> sh;
+  char* at = base + (32 * (int64_t)chunk + col) * sizeof(V);
+  for (int k0 = 0; k0 < n; k0 += step * kFlight) {
+    V v[kFlight];
+    int64_t to[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int k = k0 + u * step + sub;
+      const int64_t s = __shfl_sync(0xffffffffu, src, k & 31), d = __shfl_sync(0xffffffffu, dst, k & 31);
+      to[u] = k < n && col < cols && s >= 0 ? d : -1;
+      if (to[u] >= 0) v[u] = ld(reinterpret_cast<const V*>(at + s * slot_bytes));
+    }
+    __syncwarp();  // read by every lane before any writes
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (to[u] >= 0) *reinterpret_cast<V*>(at + to[u] * slot_bytes) = v[u];
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(256) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (item >= a.items) return;
+  uint32_t b, r;
+  a.item_div.divmod(item, b, r);
+  const int32_t i0 = ld(a.accepted_indptr + b), i1 = ld(a.accepted_indptr + b + 1), prefix = ld(a.prefix_lens + b);
+  const int32_t p0 = ld(a.kv_indptr + b), np = ld(a.kv_indptr + b + 1) - p0;
+  if (i0 < 0 || i1 > a.num_accepted || prefix < 0) {
+    if (r == 0 && lane == 0) report(a.err_word, prefix < 0 ? PKV_DEVERR_LENGTH : PKV_DEVERR_ROW_OOB);
+    return;
+  }
+  const int p = plane_of(a.planes, r);
+  const uint32_t chunk = r - a.planes.first[p], slot = a.planes.slot_bytes[p];
+  char* base = (char*)a.planes.base[p];
+  for (int k0 = 0; k0 < i1 - i0; k0 += 32) {
+    const int k = k0 + lane, n = min(32, i1 - i0 - k0);
+    int64_t src = -1, dst = -1;
+    if (lane < n) {
+      const int32_t node = ld(a.accepted + i0 + k), before = k > 0 ? ld(a.accepted + i0 + k - 1) : -1;
+      uint32_t bad = node <= before ? PKV_DEVERR_LENGTH : 0u;
+      if (!bad && node > k) {  // else it is in its place
+        src = slot_at(a, p0, np, (int64_t)prefix + node, bad);
+        dst = slot_at(a, p0, np, (int64_t)prefix + k, bad);
+        if (dst < 0) src = -1;
+      }
+      if (bad && r == 0) report(a.err_word, bad);
+    }
+    if (slot % 16 == 0) move_rows<uint4>(base, slot, chunk, src, dst, n);
+    else if (slot % 8 == 0) move_rows<uint2>(base, slot, chunk, src, dst, n);
+    else if (slot % 4 == 0) move_rows<uint32_t>(base, slot, chunk, src, dst, n);
+    else if (slot % 2 == 0) move_rows<uint16_t>(base, slot, chunk, src, dst, n);
+    else move_rows<uint8_t>(base, slot, chunk, src, dst, n);
+    __syncwarp();  // a group's rows are written before the next group's are read
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------------------------
+uint32_t piece_bytes(int64_t slot_bytes) {
+  uint32_t v = 16;
+  while (slot_bytes % v) v >>= 1;
+  return v;
+}
+
+pkv_status check_planes(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size) {
+  if (num_planes < 0 || num_pages <= 0 || page_size <= 0 || (num_planes > 0 && !planes)) return PKV_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_planes; ++i) {
+    if (!planes[i].base || planes[i].slot_bytes <= 0 || !pkv_host::aligned16(planes[i].base)) return PKV_ERR_INVALID_ARG;
+    // 31-bit numbers of the bytes and pieces of a page
+    if (planes[i].slot_bytes > 0x7fffffff / page_size) return PKV_ERR_UNSUPPORTED;
+  }
+  return num_planes > kMaxPlanes ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+// Fills the planes, items(i) of each; the sum of those, or -1 where it passes 31 bits.
+template <int N, typename Items>
+int64_t fill_planes(Planes<N>& to, const pkv_plane* planes, int32_t num_planes, Items items) {
+  int64_t sum = 0;
+  to.count = num_planes;
+  for (int32_t i = 0; i < num_planes; ++i) {
+    to.base[i] = planes[i].base;
+    to.slot_bytes[i] = (uint32_t)planes[i].slot_bytes;
+    to.first[i] = (uint32_t)sum;
+    sum += items(planes[i]);
+    if (sum > 0x7fffffffLL) return -1;
+  }
+  return sum;
+}
+
+template <int N>
+pkv_status copy_pages(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size,
+                      const int32_t* src, const int32_t* dst, const int32_t* rows, int32_t num_copies,
+                      uint32_t* err_word, cudaStream_t st) {
+  CopyArgs<N> a;
+  const int64_t tiles = fill_planes(a.planes, planes, num_planes, [&](const pkv_plane& p) {
+    const int64_t tile = 32 * kFlight * piece_bytes(p.slot_bytes);
+    return (p.slot_bytes * page_size + tile - 1) / tile;
+  });
+  if (tiles < 0 || tiles * num_copies > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  a.src = src;
+  a.dst = dst;
+  a.rows = rows;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.tile_div = FastDiv((uint32_t)tiles);
+  a.items = (uint32_t)(tiles * num_copies);
+  a.err_word = err_word;
+  return pkv_host::launch_after(copy_pages_kernel<N>, dim3((a.items + 7) / 8), 256, 0, st, a);
+}
+
+template <int N>
+pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size,
+                   const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* prefix_lens, int32_t batch,
+                   const int32_t* accepted_indptr, const int32_t* accepted, int32_t num_accepted, uint32_t* err_word,
+                   cudaStream_t st) {
+  CompactArgs<N> a;
+  const int64_t warps = fill_planes(a.planes, planes, num_planes, [&](const pkv_plane& p) {
+    return (p.slot_bytes / piece_bytes(p.slot_bytes) + 31) / 32;
+  });
+  if (warps < 0 || warps * batch > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.prefix_lens = prefix_lens;
+  a.accepted_indptr = accepted_indptr;
+  a.accepted = accepted;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.num_accepted = num_accepted;
+  a.item_div = FastDiv((uint32_t)warps);
+  a.page_div = FastDiv((uint32_t)page_size);
+  a.items = (uint32_t)(warps * batch);
+  a.err_word = err_word;
+  return pkv_host::launch_after(compact_accepted_kernel<N>, dim3((a.items + 7) / 8), 256, 0, st, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_copy_pages(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size,
+                          const int32_t* src_pages, const int32_t* dst_pages, const int32_t* rows,
+                          int32_t num_copies, uint32_t* err_word, void* stream) {
+  pkv_host::NvtxRange nvtx_range("pkv_copy_pages");
+  const pkv_status s = check_planes(planes, num_planes, num_pages, page_size);
+  if (s != PKV_OK) return s;
+  if (num_copies < 0) return PKV_ERR_INVALID_ARG;
+  if (num_copies == 0 || num_planes == 0) return PKV_OK;
+  if (!src_pages || !dst_pages) return PKV_ERR_INVALID_ARG;
+  return num_planes <= kFewPlanes
+             ? copy_pages<kFewPlanes>(planes, num_planes, num_pages, page_size, src_pages, dst_pages, rows, num_copies,
+                                      err_word, (cudaStream_t)stream)
+             : copy_pages<kMaxPlanes>(planes, num_planes, num_pages, page_size, src_pages, dst_pages, rows, num_copies,
+                                      err_word, (cudaStream_t)stream);
+}
+
+pkv_status pkv_compact_accepted(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size,
+                                const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* prefix_lens,
+                                int32_t batch_size, const int32_t* accepted_indptr, const int32_t* accepted,
+                                int32_t num_accepted, uint32_t* err_word, void* stream) {
+  pkv_host::NvtxRange nvtx_range("pkv_compact_accepted");
+  const pkv_status s = check_planes(planes, num_planes, num_pages, page_size);
+  if (s != PKV_OK) return s;
+  if (batch_size < 0 || num_accepted < 0) return PKV_ERR_INVALID_ARG;
+  if (batch_size == 0 || num_accepted == 0 || num_planes == 0) return PKV_OK;
+  if (!kv_indptr || !kv_indices || !prefix_lens || !accepted_indptr || !accepted) return PKV_ERR_INVALID_ARG;
+  return num_planes <= kFewPlanes
+             ? compact<kFewPlanes>(planes, num_planes, num_pages, page_size, kv_indptr, kv_indices, prefix_lens,
+                                   batch_size, accepted_indptr, accepted, num_accepted, err_word, (cudaStream_t)stream)
+             : compact<kMaxPlanes>(planes, num_planes, num_pages, page_size, kv_indptr, kv_indices, prefix_lens,
+                                   batch_size, accepted_indptr, accepted, num_accepted, err_word, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,11 +1,16 @@
-// e4m3 with a power-of-two scale per row and head, and small host/device helpers the 8-bit cache's
-// kernels share.
+// The quantised caches' number formats, and small host/device helpers their kernels share.
 //
-// A cache row (one slot, one head) x holds x8 = e4m3(x * 2^-k) and the scale 2^k, with the smallest
+// 8 bits: e4m3 with a power-of-two scale per row and head.  A cache row (one slot, one head) x holds x8 = e4m3(x * 2^-k) and the scale 2^k, with the smallest
 // k >= -126 for which max |x| <= 448 * 2^k.  The scale is a power of two so that scaling is exact
 // both ways: a row is rounded once, when it is written, and bf16(x8 * 2^k) reads it back without a
 // second rounding.  A free (not power-of-two) scale would not make e4m3 more accurate: its relative
 // step is the same in every binade.
+//
+// 4 bits: e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with an e4m3 scale s for every 16 values of a head's
+// row and one fp32 scale g for the whole cache: x is held as e2m1(x / (s g)), s = e4m3(max |x| / (6 g)) over the
+// block.  With two significant bits the place of a block's largest value within its binade matters (a power of two
+// would waste up to half of the codes), so s has three bits of mantissa; the product of a code and s has at most six
+// significant bits and is exact in f16, which is what the attention multiplies.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -54,6 +59,58 @@ PKV_DEV void unpack_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
       : "r"(v));
 }
 
+// Eight values to e2m1, round to nearest even, at most 6 in size: x[i] in bits 4i .. 4i + 3.
+PKV_DEV uint32_t pack_e2m1x8(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// Eight e2m1 values as f16 pairs, h[i] from byte i; exact.
+PKV_DEV void unpack_e2m1x8(uint32_t v, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(v));
+}
+
+// The two e4m3 values in the low bytes of v as an f16 pair; exact.
+PKV_DEV uint32_t unpack_e4m3x2(uint32_t v) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(v));
+  return h;
+}
+
+// One value to e4m3, round to nearest even, at most 448; x >= 0.
+PKV_DEV uint8_t pack_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(x), "f"(0.f));
+  return (uint8_t)r;
+}
+
+PKV_DEV float e4m3_value(uint8_t b) {
+  const uint32_t h = unpack_e4m3x2(b);
+  return __half2float(__ushort_as_half((unsigned short)h));
+}
+
+// The product of two f16 pairs.
+PKV_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Division of a 31-bit number by a number fixed at launch: multiply by the rounded-up reciprocal
 // and shift (Granlund and Montgomery, "Division by invariant integers using multiplication").
 struct FastDiv {
@@ -75,4 +132,5 @@ struct FastDiv {
 
 namespace pkv_host {
 bool valid_pool8(const pkv_pool_fp8* p);  // non-null, positive sizes, head_dim % 8 == 0, 16-byte aligned
+bool valid_pool4(const pkv_pool_fp4* p);  // the same with head_dim % 16 == 0 and cache scales within 2^-64 .. 2^64
 }  // namespace pkv_host

@@ -1,11 +1,12 @@
 // Rotary embedding of the step's new K and Q fused with the KV-cache write, for every pairing and
-// width, into a bf16 or an 8-bit cache; and the 8-bit cache write without a rotation.
+// width, into a bf16, an 8-bit or a 4-bit cache; and the quantised caches' write without a rotation.
 //
 // For pair i < R/2 of the first R = rotary_dim values of a head, at position p,
 //   x'[a] = x[a] cos(p, i) - x[b] sin(p, i),   x'[b] = x[b] cos(p, i) + x[a] sin(p, i),
 // with (a, b) = (i, i + R/2) (half-split pairs) or (2i, 2i + 1) (neighbouring pairs), in fp32 with
 // one rounding at the end; the values from R on pass through.  In the 8-bit cache a row is
-// quantised from those fp32 values (quant.cuh), so K is rounded once, to e4m3.
+// quantised from those fp32 values (quant.cuh), so K is rounded once, to e4m3.  In the 4-bit cache so is every
+// block of 16 values.
 //
 // Bound by HBM.  A row of a head is held by D/16 lanes, two 16-byte chunks each: for half-split
 // pairs the chunk and its partner R/2 further on, so that a pair never leaves its lane, for
@@ -24,13 +25,15 @@ namespace {
 
 using namespace pkv;
 
-enum { kNone = 0, kHalf = 1, kPairs = 2 };
+enum { kNone = 0, kHalf = 1, kPairs = 2 };        // the rotation's pairs
+enum { kBf16 = 0, kE4m3 = 1, kE2m1 = 2 };         // what the cache holds
 
 struct AppendArgs {
   void* k_pool;
   void* v_pool;
-  float* k_scale;
-  float* v_scale;
+  void* k_scale;
+  void* v_scale;
+  float k_global, v_global;  // 4 bits: the caches' scales
   const __nv_bfloat16* k_new;
   const __nv_bfloat16* v_new;
   const __nv_bfloat16* q;
@@ -84,6 +87,32 @@ PKV_DEV uint2 quantise8(float (&x)[8], int k) {
   return make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
 }
 
+// The e4m3 scale of a 4-bit block from the bits of its largest |x| (NaN and infinities included).
+PKV_DEV uint8_t block_scale(uint32_t amax_bits, float g) {
+  if (amax_bits >= 0x7f800000u) return 0x7f;
+  return pack_e4m3(__fdiv_rn(__uint_as_float(amax_bits), 6.f * g));
+}
+
+PKV_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// 8 values of a 4-bit block with scale s as codes: x / (s g), correctly rounded to fp32, then to e2m1.  The quotient
+// is x r with r = 1 / (s g) and one correction by its remainder (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990); x r alone is off the ties of e2m1 that x / (s g) meets (s = 1.875, x = 2.5 s).
+PKV_DEV uint32_t quantise_block8(float (&x)[8], uint8_t s, float g) {
+  if (s == 0 || s == 0x7f) return 0u;
+  const float step = e4m3_value(s) * g, r = __frcp_rn(step);
+  if (s == 0x7e) {  // the largest scale: x / step has no bound
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -7.f * step), 7.f * step);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = x[e] * r;
+    x[e] = fmaf(fmaf(-y, step, x[e]), r, y);
+  }
+  return pack_e2m1x8(x);
+}
+
 struct Row {
   const __nv_bfloat16* src;
   int kind;  // 0 K, 1 V, 2 Q
@@ -119,7 +148,7 @@ constexpr int kSteps = 2;
 
 // L lanes hold a row (the power of two at or above its units of two chunks); a warp takes kSteps
 // times 32 / L rows of one token.
-template <bool FP8, int ROT, int L>
+template <int FMT, int ROT, int L>
 __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kRows = 32 / L;
   pdl_trigger();
@@ -204,7 +233,35 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
         }
       }
     }
-    if (FP8 && !is_q) {
+    if (FMT == kE2m1 && !is_q) {
+      // A block is two chunks: the lane's own, or one of its and one of the next lane's.  (Half-split pairs: the
+      // launch sees to an even number of chunks in each half, so that both chunks have their partners in lane u ^ 1.)
+      uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m0 = max(m0, abs_bits(x0[e])), m1 = max(m1, abs_bits(x1[e]));
+      if constexpr (ROT == kHalf) {
+        const uint32_t n0 = __shfl_xor_sync(mask, m0, 1), n1 = __shfl_xor_sync(mask, m1, 1);
+        const uint32_t both = max(m0, m1);
+        m0 = paired ? max(m0, n0) : both;
+        m1 = paired ? max(m1, n1) : both;
+      } else {
+        m0 = m1 = max(m0, m1);
+      }
+      const int64_t dst = slot * a.Hkv + r.head;
+      const float glob = r.kind == 1 ? a.v_global : a.k_global;
+      const uint8_t s0 = block_scale(m0, glob), s1 = block_scale(m1, glob);
+      const uint32_t p0 = quantise_block8(x0, s0, glob), p1 = quantise_block8(x1, s1, glob);
+      uint8_t* out = (uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * (a.D / 2);
+      uint8_t* scale = (uint8_t*)(r.kind == 1 ? a.v_scale : a.k_scale) + dst * (a.D / 16);
+      if (ROT == kHalf ? paired : false) {
+        *reinterpret_cast<uint32_t*>(out + 4 * c0) = p0;
+        *reinterpret_cast<uint32_t*>(out + 4 * c1) = p1;
+        if (!(u & 1)) scale[c0 / 2] = s0, scale[c1 / 2] = s1;
+      } else if (has0) {
+        *reinterpret_cast<uint2*>(out + 4 * c0) = make_uint2(p0, p1);
+        scale[c0 / 2] = s0;
+      }
+    } else if (FMT == kE4m3 && !is_q) {
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = max(m, max(finite_abs_bits(x0[e]), finite_abs_bits(x1[e])));
@@ -214,7 +271,7 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
       const uint2 p0 = quantise8(x0, k), p1 = quantise8(x1, k);
       if (has0) *reinterpret_cast<uint2*>(out + 8 * c0) = p0;
       if (has1) *reinterpret_cast<uint2*>(out + 8 * c1) = p1;
-      if (u == 0) (r.kind == 1 ? a.v_scale : a.k_scale)[dst] = exp2i(k);
+      if (u == 0) ((float*)(r.kind == 1 ? a.v_scale : a.k_scale))[dst] = exp2i(k);
     } else {
       uint4* out = reinterpret_cast<uint4*>(is_q ? a.q_out + ((int64_t)t * a.Hq + r.head) * a.D
                                                  : (__nv_bfloat16*)(r.kind == 1 ? a.v_pool : a.k_pool) +
@@ -226,7 +283,7 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
 }
 
 // Any even width: one chunk per lane, L lanes per row, partners read one by one.
-template <bool FP8, int L>
+template <int FMT, int L>
 __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_constant__ AppendArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -264,7 +321,18 @@ __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_cons
     }
   }
   __syncwarp(mask);  // q may be rotated in place: every lane of the row has read its partners
-  if (FP8 && !is_q) {
+  if (FMT == kE2m1 && !is_q) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
+    m = max(m, __shfl_xor_sync(mask, m, 1));  // a block is the chunks of two lanes
+    const int64_t dst = slot * a.Hkv + r.head;
+    const float glob = r.kind == 1 ? a.v_global : a.k_global;
+    const uint8_t s = block_scale(m, glob);
+    const uint32_t p = quantise_block8(x, s, glob);
+    if (has) *reinterpret_cast<uint32_t*>((uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * (a.D / 2) + 4 * c) = p;
+    if (has && !(c & 1)) ((uint8_t*)(r.kind == 1 ? a.v_scale : a.k_scale))[dst * (a.D / 16) + c / 2] = s;
+  } else if (FMT == kE4m3 && !is_q) {
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = max(m, finite_abs_bits(x[e]));
@@ -272,7 +340,7 @@ __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_cons
     const int64_t dst = slot * a.Hkv + r.head;
     const uint2 p = quantise8(x, k);
     if (has) *reinterpret_cast<uint2*>((uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * a.D + 8 * c) = p;
-    if (c == 0) (r.kind == 1 ? a.v_scale : a.k_scale)[dst] = exp2i(k);
+    if (c == 0) ((float*)(r.kind == 1 ? a.v_scale : a.k_scale))[dst] = exp2i(k);
   } else if (has) {
     uint4* out = reinterpret_cast<uint4*>(is_q ? a.q_out + ((int64_t)t * a.Hq + r.head) * a.D
                                                : (__nv_bfloat16*)(r.kind == 1 ? a.v_pool : a.k_pool) +
@@ -287,7 +355,7 @@ int pow2_at_least(int n) {
   return p;
 }
 
-template <bool FP8, int ROT>
+template <int FMT, int ROT>
 pkv_status launch_rows(AppendArgs a, cudaStream_t st) {
   const int hc = a.R / 16;
   const int units = ROT == kHalf ? hc + (a.D - 16 * hc + 15) / 16 : (a.D + 15) / 16;
@@ -298,27 +366,27 @@ pkv_status launch_rows(AppendArgs a, cudaStream_t st) {
   a.item_div = FastDiv((uint32_t)parts);
   const unsigned g = (a.items + 7) / 8;
   switch (L) {
-    case 1: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 1>, dim3(g), 256, 0, st, a);
-    case 2: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 2>, dim3(g), 256, 0, st, a);
-    case 4: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 4>, dim3(g), 256, 0, st, a);
-    case 8: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 8>, dim3(g), 256, 0, st, a);
-    default: return pkv_host::launch_after(append_rows_kernel<FP8, ROT, 16>, dim3(g), 256, 0, st, a);
+    case 1: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 1>, dim3(g), 256, 0, st, a);
+    case 2: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 2>, dim3(g), 256, 0, st, a);
+    case 4: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 4>, dim3(g), 256, 0, st, a);
+    case 8: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 8>, dim3(g), 256, 0, st, a);
+    default: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 16>, dim3(g), 256, 0, st, a);
   }
 }
 
-template <bool FP8>
+template <int FMT>
 pkv_status launch_any_width(AppendArgs a, cudaStream_t st) {
   const int L = pow2_at_least(a.D / 8);
   a.items = (uint32_t)((int64_t)a.heads * a.T);
   a.row_div = FastDiv((uint32_t)a.heads);
   const unsigned per = 256 / L, g = (a.items + per - 1) / per;
   switch (L) {
-    case 1: return pkv_host::launch_after(append_any_width_kernel<FP8, 1>, dim3(g), 256, 0, st, a);
-    case 2: return pkv_host::launch_after(append_any_width_kernel<FP8, 2>, dim3(g), 256, 0, st, a);
-    case 4: return pkv_host::launch_after(append_any_width_kernel<FP8, 4>, dim3(g), 256, 0, st, a);
-    case 8: return pkv_host::launch_after(append_any_width_kernel<FP8, 8>, dim3(g), 256, 0, st, a);
-    case 16: return pkv_host::launch_after(append_any_width_kernel<FP8, 16>, dim3(g), 256, 0, st, a);
-    default: return pkv_host::launch_after(append_any_width_kernel<FP8, 32>, dim3(g), 256, 0, st, a);
+    case 1: return pkv_host::launch_after(append_any_width_kernel<FMT, 1>, dim3(g), 256, 0, st, a);
+    case 2: return pkv_host::launch_after(append_any_width_kernel<FMT, 2>, dim3(g), 256, 0, st, a);
+    case 4: return pkv_host::launch_after(append_any_width_kernel<FMT, 4>, dim3(g), 256, 0, st, a);
+    case 8: return pkv_host::launch_after(append_any_width_kernel<FMT, 8>, dim3(g), 256, 0, st, a);
+    case 16: return pkv_host::launch_after(append_any_width_kernel<FMT, 16>, dim3(g), 256, 0, st, a);
+    default: return pkv_host::launch_after(append_any_width_kernel<FMT, 32>, dim3(g), 256, 0, st, a);
   }
 }
 
@@ -328,7 +396,7 @@ bool disjoint_or_same(const void* a, const void* b, size_t bytes) {
 }
 
 // The checks and the launch every entry point of this file shares.  rotary: with positions and Q.
-template <bool FP8>
+template <int FMT>
 pkv_status append_rows(AppendArgs a, int64_t num_pages, int32_t page_size, bool rotary, cudaStream_t st) {
   if (a.T < 0 || a.Hq < 0) return PKV_ERR_INVALID_ARG;
   if (rotary && (a.max_position <= 0 || a.R <= 0 || a.R % 2 != 0 || a.R > a.D)) return PKV_ERR_INVALID_ARG;
@@ -346,9 +414,10 @@ pkv_status append_rows(AppendArgs a, int64_t num_pages, int32_t page_size, bool 
   if (heads * a.T > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // 31-bit row numbers
   a.heads = (int32_t)heads;
   a.num_slots = num_pages * page_size;
-  if (!rotary) return launch_rows<FP8, kNone>(a, st);
-  if (a.interleaved ? a.R % 8 != 0 : a.R % 16 != 0) return launch_any_width<FP8>(a, st);
-  return a.interleaved ? launch_rows<FP8, kPairs>(a, st) : launch_rows<FP8, kHalf>(a, st);
+  if (!rotary) return launch_rows<FMT, kNone>(a, st);
+  // half-split: whole chunks in each half, and for 4 bits whole blocks
+  if (a.interleaved ? a.R % 8 != 0 : a.R % (FMT == kE2m1 ? 32 : 16) != 0) return launch_any_width<FMT>(a, st);
+  return a.interleaved ? launch_rows<FMT, kPairs>(a, st) : launch_rows<FMT, kHalf>(a, st);
 }
 
 AppendArgs rotary_args(const void* k_new, const void* v_new, const int64_t* slots, const int32_t* positions,
@@ -372,7 +441,8 @@ AppendArgs rotary_args(const void* k_new, const void* v_new, const int64_t* slot
   return a;
 }
 
-void set_pool(AppendArgs& a, const pkv_pool_fp8* p) {
+template <typename Pool>
+void set_pool(AppendArgs& a, const Pool* p) {
   a.k_pool = p->k;
   a.v_pool = p->v;
   a.k_scale = p->k_scale;
@@ -398,7 +468,7 @@ pkv_status pkv_rotary_kv_append(const pkv_pool* pool, const void* k_new, const v
   a.v_pool = pool->v;
   a.Hkv = pool->num_kv_heads;
   a.D = pool->head_dim;
-  return append_rows<false>(a, pool->num_pages, pool->page_size, true, (cudaStream_t)stream);
+  return append_rows<kBf16>(a, pool->num_pages, pool->page_size, true, (cudaStream_t)stream);
 }
 
 pkv_status pkv_rotary_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new, const void* v_new,
@@ -411,7 +481,7 @@ pkv_status pkv_rotary_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new,
   AppendArgs a = rotary_args(k_new, v_new, slot_mapping, positions, cos_sin, max_position, rotary_dim,
                              interleaved, q, q_out, num_q_heads, num_tokens, err_word);
   set_pool(a, pool);
-  return append_rows<true>(a, pool->num_pages, pool->page_size, true, (cudaStream_t)stream);
+  return append_rows<kE4m3>(a, pool->num_pages, pool->page_size, true, (cudaStream_t)stream);
 }
 
 pkv_status pkv_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new, const void* v_new,
@@ -422,7 +492,35 @@ pkv_status pkv_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new, const 
   AppendArgs a = rotary_args(k_new, v_new, slot_mapping, nullptr, nullptr, 0, 0, 0, nullptr, nullptr, 0,
                              num_tokens, err_word);
   set_pool(a, pool);
-  return append_rows<true>(a, pool->num_pages, pool->page_size, false, (cudaStream_t)stream);
+  return append_rows<kE4m3>(a, pool->num_pages, pool->page_size, false, (cudaStream_t)stream);
+}
+
+pkv_status pkv_rotary_kv_append_fp4(const pkv_pool_fp4* pool, const void* k_new, const void* v_new,
+                                    const int64_t* slot_mapping, const int32_t* positions,
+                                    const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                                    int32_t interleaved, const void* q, void* q_out, int32_t num_q_heads,
+                                    int32_t num_tokens, uint32_t* err_word, void* stream) {
+  pkv_host::NvtxRange nvtx_range("pkv_rotary_kv_append_fp4");
+  if (!pkv_host::valid_pool4(pool)) return PKV_ERR_INVALID_ARG;
+  AppendArgs a = rotary_args(k_new, v_new, slot_mapping, positions, cos_sin, max_position, rotary_dim,
+                             interleaved, q, q_out, num_q_heads, num_tokens, err_word);
+  set_pool(a, pool);
+  a.k_global = pool->k_global;
+  a.v_global = pool->v_global;
+  return append_rows<kE2m1>(a, pool->num_pages, pool->page_size, true, (cudaStream_t)stream);
+}
+
+pkv_status pkv_kv_append_fp4(const pkv_pool_fp4* pool, const void* k_new, const void* v_new,
+                             const int64_t* slot_mapping, int32_t num_tokens, uint32_t* err_word,
+                             void* stream) {
+  pkv_host::NvtxRange nvtx_range("pkv_kv_append_fp4");
+  if (!pkv_host::valid_pool4(pool)) return PKV_ERR_INVALID_ARG;
+  AppendArgs a = rotary_args(k_new, v_new, slot_mapping, nullptr, nullptr, 0, 0, 0, nullptr, nullptr, 0,
+                             num_tokens, err_word);
+  set_pool(a, pool);
+  a.k_global = pool->k_global;
+  a.v_global = pool->v_global;
+  return append_rows<kE2m1>(a, pool->num_pages, pool->page_size, false, (cudaStream_t)stream);
 }
 
 }  // extern "C"
