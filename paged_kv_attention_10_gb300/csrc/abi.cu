@@ -164,7 +164,7 @@ bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d
             CU_TENSOR_MAP_INTERLEAVE_NONE,
             b0 == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
             : b0 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                       : CU_TENSOR_MAP_SWIZZLE_NONE,
+                       : CU_TENSOR_MAP_SWIZZLE_32B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -24,9 +24,10 @@ namespace {
 
 using namespace pkv;
 
-// Weights of the second product stand in [0, 2^kWeightExp], the top of f16's range: one as small as 2^-40 of the
-// largest is still counted.  (A value of V is below 2^12 and the sums are fp32.)
-constexpr int kWeightExp = 15;
+// The weights of a row are 2^(x - m + kWeightExp) with m a score near the largest so far: m moves only when a score is more
+// than kHeadroom above it, so that most steps need no maximum over lanes and no rescaling.  Weights then stand in [0, 2^15],
+// the top of f16's range; one as small as 2^-32 of m's own is still counted.
+constexpr int kWeightExp = 8, kHeadroom = 7;
 
 // The position, of eight consecutive ones, that row r of a score tile stands for.  K's loads of rows 2i and 2i + 1 and
 // V's of rows 0, 2, 4, 6 and of 1, 3, 5, 7 are then free of bank conflicts.  Rows of 64 bytes, 16-byte pieces p of row t at
@@ -37,10 +38,11 @@ PKV_DEV int position(int r) {
   return (0x57463120 >> (4 * r)) & 7;
 }
 
-template <int D>
+template <int D, bool FEW>
 struct Format4 {
   static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kWarps = 16;
-  static constexpr int kMergeFloats = 4 + D / 4;
+  static constexpr int kTiles = FEW ? D / 32 : D / 16;  // row tiles of O
+  static constexpr int kMergeFloats = 4 + 4 * kTiles;
   // an odd multiple of a head's bytes, so that neighbouring rows lie in other banks
   static int row_stride(int bytes) { return bytes / kRowBytes % 2 ? bytes : bytes + kRowBytes; }
   template <bool TMA>
@@ -58,15 +60,38 @@ PKV_DEV void lds(uint32_t addr, uint32_t (&w)[N]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
+PKV_DEV uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+PKV_DEV uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// D = A * B, as mma_f16_16816.
+PKV_DEV void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+PKV_DEV float half_to_float(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
+
 // ---------------------------------------------------------------------------------------------
 // Consumer warps: 32-position steps of one KV head with its G query heads.
 // ---------------------------------------------------------------------------------------------
-template <int D>
+template <int D, bool FEW>
 template <bool TMA>
-__device__ void Format4<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
-                                    uint64_t* full, uint64_t* empty, uint64_t* meet_bar) {
-  constexpr int RH = kRowBytes, SH = kScaleBytes;
-  constexpr int NM = D / 16;          // MMAs of a score tile, row tiles of O
+__device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
+                                         uint64_t* full, uint64_t* empty, uint64_t* meet_bar) {
+  constexpr int RH = kRowBytes, SH = kScaleBytes, NT = kTiles;
+  constexpr int NM = D / 16;          // MMAs of a score tile
   constexpr int KW = D / 32;          // words of a lane's share of a K row
   constexpr int VW = D / 64;          // ... of a V row
   constexpr int MF = kMergeFloats;    // floats per lane merged between the warps of a head
@@ -78,32 +103,40 @@ __device__ void Format4<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
   const int si = warp / HV;                         // slice within a stage
   const int g = lane >> 2, c = lane & 3;
   const int NS = a.num_stages;
-  const uint32_t region = a.kv_region;
   const int HQU = HC * G;  // query heads per unit
 
-  // Shared-memory places: of the four groups of eight positions of the slice, and of the lane's positions in a group.
-  // K: row g.  V: rows 2c and 2c + 1, the lane's eighth g.
-  uint32_t group_off[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = si * kSlice + 8 * i;
-    group_off[i] = TMA ? (uint32_t)(((t / a.box_rows) * HC + hl) * a.box_rows + t % a.box_rows) * RH
-                       : (uint32_t)(t * a.row_stride + hl * RH);
-  }
+  // Shared-memory places within a stage of the slice's first eight positions: of K, of V's rows 2c and 2c + 1 (the
+  // lane's eighth g), and of the scales of row g.
+  const int t0 = si * kSlice;
+  const uint32_t first = TMA ? (uint32_t)(((t0 / a.box_rows) * HC + hl) * a.box_rows + t0 % a.box_rows) * RH
+                             : (uint32_t)(t0 * a.row_stride + hl * RH);
   const int stride = TMA ? RH : a.row_stride;
-  auto piece = [&](int t, int p) -> uint32_t {  // 16-byte piece p of position t of a group
-    return (uint32_t)(t * stride + ((TMA && D == 128 ? p ^ ((t >> 1) & 3) : p) << 4));
+  auto piece = [&](int t, int p) -> uint32_t {  // 16-byte piece p of position t of eight
+    return first + (uint32_t)(t * stride + ((!TMA ? p : D == 128 ? p ^ ((t >> 1) & 3) : p ^ ((t >> 2) & 1)) << 4));
   };
   const int pk = position<D>(g), pa = position<D>(2 * c), pb = position<D>(2 * c + 1);
-  const uint32_t k_off = D == 128 ? piece(pk, c) : piece(pk, c >> 1) + (c & 1) * 8;
-  const uint32_t va_off = D == 128 ? piece(pa, g >> 1) + (g & 1) * 8 : piece(pa, g >> 2) + (g & 3) * 4;
-  const uint32_t vb_off = D == 128 ? piece(pb, g >> 1) + (g & 1) * 8 : piece(pb, g >> 2) + (g & 3) * 4;
-  const uint32_t stages_u32 = smem_u32(stages);
+  const uint32_t base = smem_u32(stages);
+  // FEW: the row that the lane addresses for ldmatrix, of piece lane / 8 of four (of two, of the next eight positions'
+  // row from lane 16 on).  Else its own bytes of row g.
+  const int pl = position<D>(lane & 7);
+  const uint32_t k_at =
+      base + (FEW ? D == 128 ? piece(pl, lane >> 3) : piece(pl, (lane >> 3) & 1) + (lane >= 16 ? a.eight : 0u)
+                  : D == 128 ? piece(pk, c) : piece(pk, c >> 1) + (c & 1) * 8);
+  const uint32_t v_at = base + a.kv_region;
+  const uint32_t va_at = v_at + (D == 128 ? piece(pa, g >> 1) + (g & 1) * 8 : piece(pa, g >> 2) + (g & 3) * 4);
+  const uint32_t vb_at = v_at + (D == 128 ? piece(pb, g >> 1) + (g & 1) * 8 : piece(pb, g >> 2) + (g & 3) * 4);
+  const uint32_t s_at = base + 2 * a.kv_region + (uint32_t)(((t0 + pk) * HC + hl) * SH);
+  const uint32_t s_eight = 8 * HC * SH;
+  // two scales of a row: of the blocks 2c and 2c + 1 of eight, or twice of block c of four
+  auto scales = [&](uint32_t at) -> uint32_t { return D == 128 ? lds_u16(at + 2 * c) : lds_u8(at + c) * 0x101u; };
+  // FEW: which bytes of a row's scales are those of the lane's blocks; where the halves of a pair of weights go in B
+  const uint32_t pick = c < 2 ? 0x6420u : 0x7531u;
+  const uint32_t put_a = g < 4 ? 0x4410u : 0x1044u, put_b = g < 4 ? 0x4432u : 0x3244u;
 
   uint32_t qf[NM][2];
-  float qs[2];        // score scale (log2 units) of the lane's heads head0 + 2c, + 1
-  float o[NM][4];
-  float m[2], l[2];   // running maximum of x and sum of the weights 2^(x - m + kWeightExp)
+  float qs[2];       // score scale (log2 units) of the lane's two heads, positive
+  float o[NT][4];
+  float m[2], l[2];  // what the weights are relative to, w = 2^(x - m + kWeightExp), and the sum of the lane's own
 
   int stage = 0;
   uint32_t phase = 0, met_phase = 0;
@@ -115,25 +148,28 @@ __device__ void Format4<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
     met_phase ^= 1;
     return ok;
   };
+  auto wait = [&](uint64_t* bar) -> bool {
+    if (__all_sync(0xffffffffu, mbar_wait(bar, phase))) return true;
+    if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+    return false;
+  };
   while (true) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&hdr_full[stage], phase))) {
-      if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      break;
-    }
-    const StageHdr h = hdr[stage];
-    if (h.unit < 0) break;
+    if (!wait(&hdr_full[stage])) return;
+    const StageHdr h = hdr[stage];  // the first stage of a segment, or the end
+    if (h.unit < 0) return;
 
-    if (h.flags & kSegFirst) {
-      // q fragments: lane (g, c) holds the dims of its quarter c, of head head0 + g
-      const int head = head0 + g;
-      const bool valid = head < G;
-      const uint4* qp = reinterpret_cast<const uint4*>(
-          a.q + ((int64_t)h.b * a.num_q_heads + (int64_t)(h.hg * HC + hl) * G + head) * D + c * (D / 4));
+    {
+      // q fragments.  Lane (g, c) holds head head0 + g's dims of its quarter c.  FEW: head g % 4's dims 8c .. 8c + 7 of
+      // every 32, and only where they lie in the block that column g is for: the even ones for columns 0 to 3.
+      const int head = FEW ? g & 3 : head0 + g;
+      const bool valid = head < G && (!FEW || (g < 4) == (c < 2));
+      const __nv_bfloat16* qp =
+          a.q + ((int64_t)h.b * a.num_q_heads + (int64_t)(h.hg * HC + hl) * G + head) * D + c * (FEW ? 8 : D / 4);
       uint32_t raw[2 * NM];
       uint32_t amax = 0;
 #pragma unroll
       for (int i = 0; i < NM / 2; ++i) {
-        const uint4 u = valid ? ld(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 u = valid ? ld(reinterpret_cast<const uint4*>(qp + i * (FEW ? 32 : 8))) : make_uint4(0u, 0u, 0u, 0u);
         raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
       }
 #pragma unroll
@@ -142,258 +178,331 @@ __device__ void Format4<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
                              finite_abs_bits(__uint_as_float(raw[i] & 0xffff0000u))));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      if (FEW) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
       // 2^e <= amax < 2^(e+1); q 2^(14 - e) goes into f16 and 2^(e - 14) into the score scale.  e is
-      // held at -100 and above so that both factors are normal numbers.
+      // held at -100 and above so that both factors are normal numbers.  The scale's sign goes into q; a scale of 0
+      // (or one that is too small to be told from it) makes q 0 instead.
       const int e = max((int)(amax >> 23) - 127, -100);
-      const float up = exp2i(14 - e);
-      const float down = a.scale_log2 * exp2i(e - 14);
+      const float down = fabsf(a.scale_log2) * exp2i(e - 14);
+      const float up = down == 0.f ? 0.f : copysignf(exp2i(14 - e), a.scale_log2);
+      const float pos = down == 0.f ? 1.f : down;
 #pragma unroll
       for (int i = 0; i < 2 * NM; ++i)
         qf[i / 2][i % 2] = pack_f16x2(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xffff0000u) * up);
-      // heads 2c and 2c + 1 of the tile live in lanes 8c and 8c + 4
-      qs[0] = __shfl_sync(0xffffffffu, down, 8 * c);
-      qs[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+      // columns 2c and 2c + 1 of the tile live in lanes 8c and 8c + 4
+      qs[0] = __shfl_sync(0xffffffffu, pos, 8 * c);
+      qs[1] = __shfl_sync(0xffffffffu, pos, 8 * c + 4);
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
 #pragma unroll
-      for (int t = 0; t < NM; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     }
 
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
-      if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      break;
-    }
-    const int nv = min(kSlice, h.ntok - si * kSlice);
-    const uint32_t kb = stages_u32 + (uint32_t)stage * a.stage_bytes;
-    const uint32_t vb = kb + region;
-    // the scales of the slice's first position; V's lie Ts positions behind K's
-    const uint8_t* sc = stages + (size_t)stage * a.stage_bytes + 2 * region + (si * kSlice * HC + hl) * SH;
-    float s[2][2][4];  // [half][MMA parity]: four independent accumulation chains
-    if (nv > 0) {
+    int left = h.left;
+    while (true) {  // the segment's stages
+      if (!wait(&full[stage])) return;
+      const int nv = left - si * kSlice;  // positions of the slice, at least where it is below 32
+      // A segment's last stage is held when warps share a head: its memory carries their merge.
+      const bool last = left <= Ts, hold = last && W > 1;
+      const uint32_t at = (uint32_t)stage * a.stage_bytes;
+      float s[2][4];
+      if (nv > 0) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[hf][pr][i] = 0.f;
-        uint32_t w[2][KW], ks[2][2];  // rows g and g + 8: codes, and the scales of the two halves of the lane's quarter
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          lds<KW>(kb + group_off[2 * hf + i] + k_off, w[i]);
-          const uint8_t* p = sc + (16 * hf + 8 * i + pk) * HC * SH;
-          if (D == 128) {
-            const uint32_t pair = unpack_e4m3x2(*reinterpret_cast<const uint16_t*>(p + 2 * c));
-            ks[i][0] = __byte_perm(pair, 0, 0x1010);
-            ks[i][1] = __byte_perm(pair, 0, 0x3232);
-          } else {
-            const uint32_t one = unpack_e4m3x2(p[c]);
-            ks[i][0] = ks[i][1] = __byte_perm(one, 0, 0x1010);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < KW; ++j) {
-          uint32_t x[4], y[4];
-          unpack_e2m1x8(w[0][j], x);
-          unpack_e2m1x8(w[1][j], y);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = mul_f16x2(x[i], ks[0][2 * j / KW]);
-            y[i] = mul_f16x2(y[i], ks[1][2 * j / KW]);
-          }
-          mma_f16_16816(s[hf][0], x[0], y[0], x[1], y[1], qf[2 * j][0], qf[2 * j][1]);
-          mma_f16_16816(s[hf][1], x[2], y[2], x[3], y[3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
-        }
-      }
-    }
-    // A segment's last stage is held when warps share a head: its memory carries their merge.
-    const bool hold = (h.flags & kSegLast) && W > 1;
-    __syncwarp();
-    if (!hold && lane == 0) mbar_arrive(&empty[stage]);  // K is read: its buffer is free while V is still in use
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[NS + stage], phase))) {
-      if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-      break;
-    }
-    if (nv > 0) {
-      uint32_t bp[2][2];
-      float x[2][4];
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = (s[hf][0][i] + s[hf][1][i]) * qs[i & 1];
-          x[hf][i] = 16 * hf + 8 * (i >> 1) + pk < nv ? v : -INFINITY;
-          mx[i & 1] = fmaxf(mx[i & 1], x[hf][i]);
-        }
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
-      }
-      float corr[2], base[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float mn = fmaxf(m[k], mx[k]);
-        // nothing but NaN so far: any finite maximum will do
-        corr[k] = mn == -INFINITY ? 1.f : ex2(m[k] - mn);
-        base[k] = (mn == -INFINITY ? 0.f : mn) - (float)kWeightExp;
-        m[k] = mn;
-        l[k] *= corr[k];
-      }
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = ex2(x[hf][i] - base[i & 1]);
-          l[i & 1] += w[i];
-        }
-        bp[hf][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
-        bp[hf][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
-      }
-      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-        for (int t = 0; t < NM; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[t][i] *= corr[i & 1];
-      }
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        // Rows past the request's end hold unused pool slots (the boxes bring them) or what shared memory held
-        // before, NaN scales among them: with a scale of 0 their values are 0, and 0 times their weight 0 stays 0.
-        uint32_t va[2][VW], vo[2][VW], vs[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t wa[VW], wb[VW];
-          lds<VW>(vb + group_off[2 * hf + i] + va_off, wa);
-          lds<VW>(vb + group_off[2 * hf + i] + vb_off, wb);
-          const int t0 = 16 * hf + 8 * i;
-          const uint8_t* p = sc + (Ts + t0) * HC * SH + (D == 128 ? g : g >> 1);
-          const uint32_t sa = t0 + pa < nv ? p[pa * HC * SH] : 0u, sb = t0 + pb < nv ? p[pb * HC * SH] : 0u;
-          vs[i] = unpack_e4m3x2(sa | sb << 8);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            va[i][j] = (wa[j] & 0x0f0f0f0fu) | ((wb[j] << 4) & 0xf0f0f0f0u);  // even dims: byte = (position a, position b)
-            vo[i][j] = ((wa[j] >> 4) & 0x0f0f0f0fu) | (wb[j] & 0xf0f0f0f0u);  // odd dims
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          uint32_t e0[4], e1[4], f0[4], f1[4];
-          unpack_e2m1x8(va[0][j], e0);
-          unpack_e2m1x8(vo[0][j], f0);
-          unpack_e2m1x8(va[1][j], e1);
-          unpack_e2m1x8(vo[1][j], f1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_f16_16816(o[4 * j + i], mul_f16x2(e0[i], vs[0]), mul_f16x2(f0[i], vs[0]), mul_f16x2(e1[i], vs[1]),
-                          mul_f16x2(f1[i], vs[1]), bp[hf][0], bp[hf][1]);
-        }
-      }
-    }
-    __syncwarp();
-    if (!hold && lane == 0) mbar_arrive(&empty[NS + stage]);
-
-    if (h.flags & kSegLast) {
-      if (W > 1) {
-        // Combine the W warps that split this head's positions (all consumer warps reach the segment end on
-        // the same stage).  A warp without a position in the segment holds a maximum of -inf and sums of 0.
-        bool met = meet();
-        float* buf = reinterpret_cast<float*>(stages + (size_t)stage * a.stage_bytes) + lane;
-        // all but one at once where their states fit into the stage, else half of them, or as many as do, at a time
-        const int room = (int)(a.stage_bytes / (uint32_t)(HV * MF * 128));
-        for (int left = W; met && left > 1;) {
-          const int keep = left - 1 <= room ? 1 : max(left / 2, left - room);
-          if (si >= keep && si < left) {
-            float* to = buf + ((si - keep) * HV + hv) * MF * 32;
-            int e = 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              to[(e++) * 32] = m[k];
-              to[(e++) * 32] = l[k];
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t ka = k_at + at + hf * a.sixteen, sa = s_at + at + 2 * hf * s_eight;
+          if constexpr (FEW) {
+            uint32_t w[2][KW];  // rows g and g + 8: word c of each 16-byte piece
+            float ks[2][KW];    // ... and the scale of its block
+            if constexpr (D == 128) {
+              ldsm_x4(ka, w[0][0], w[0][1], w[0][2], w[0][3]);
+              ldsm_x4(ka + a.eight, w[1][0], w[1][1], w[1][2], w[1][3]);
+            } else {
+              ldsm_x4(ka, w[0][0], w[0][1], w[1][0], w[1][1]);
             }
 #pragma unroll
-            for (int t = 0; t < NM; ++t)
+            for (int i = 0; i < 2; ++i) {
+              uint32_t b[VW];
+              lds<VW>(sa + i * s_eight, b);
+              const uint32_t four = __byte_perm(b[0], VW == 2 ? b[VW - 1] : 0u, pick);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) to[(e++) * 32] = o[t][i];
-          }
-          met = meet();
-          if (!met) break;
-          if (si < keep) {
-            for (int w = si; w < left - keep; w += keep) {
-              const float* ob = buf + (w * HV + hv) * MF * 32;
-              // one that has seen only NaN (or nothing) keeps its sums: they are NaN or 0
-              auto weight = [](float x, float top) { return x == -INFINITY ? 1.f : ex2(x - top); };
-              int e = 0;
-              float fa[2], fb[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float om = ob[(e++) * 32], ol = ob[(e++) * 32];
-                const float mn = fmaxf(m[k], om);
-                fa[k] = weight(m[k], mn);
-                fb[k] = weight(om, mn);
-                l[k] = l[k] * fa[k] + ol * fb[k];
-                m[k] = mn;
+              for (int j = 0; j < KW / 2; ++j) {
+                const uint32_t two = unpack_e4m3x2(four >> (16 * j));
+                ks[i][2 * j] = half_to_float(two);
+                ks[i][2 * j + 1] = half_to_float(two >> 16);
               }
+            }
 #pragma unroll
-              for (int t = 0; t < NM; ++t)
+            for (int j = 0; j < KW; ++j) {
+              uint32_t x[4], y[4];
+              float d[4];
+              unpack_e2m1x8(w[0][j], x);
+              unpack_e2m1x8(w[1][j], y);
+              mma_f16_16816_zero(d, x[0], y[0], x[1], y[1], qf[2 * j][0], qf[2 * j][1]);
+              mma_f16_16816(d, x[2], y[2], x[3], y[3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[t][i] = o[t][i] * fa[i & 1] + ob[(e++) * 32] * fb[i & 1];
+              for (int i = 0; i < 4; ++i) s[hf][i] = j == 0 ? d[i] * ks[i / 2][0] : fmaf(d[i], ks[i / 2][j], s[hf][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[hf][i] += __shfl_xor_sync(0xffffffffu, s[hf][i], 2);
+          } else {
+            uint32_t w[2][KW];  // rows g and g + 8: codes, and the scales of the two halves of the lane's quarter
+            lds<KW>(ka, w[0]);
+            lds<KW>(ka + a.eight, w[1]);
+            uint32_t ks[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t pair = unpack_e4m3x2(scales(sa + i * s_eight));
+              ks[i][0] = D == 128 ? __byte_perm(pair, 0, 0x1010) : pair;
+              ks[i][1] = D == 128 ? __byte_perm(pair, 0, 0x3232) : pair;
+            }
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+              uint32_t x[4], y[4];
+              unpack_e2m1x8(w[0][j], x);
+              unpack_e2m1x8(w[1][j], y);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[i] = mul_f16x2(x[i], ks[0][2 * j / KW]);
+                y[i] = mul_f16x2(y[i], ks[1][2 * j / KW]);
+              }
+              if (j == 0)
+                mma_f16_16816_zero(s[hf], x[0], y[0], x[1], y[1], qf[0][0], qf[0][1]);
+              else
+                mma_f16_16816(s[hf], x[0], y[0], x[1], y[1], qf[2 * j][0], qf[2 * j][1]);
+              mma_f16_16816(s[hf], x[2], y[2], x[3], y[3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
             }
           }
-          left = keep;
-          if (left > 1) met = meet();  // read before the next writes
-        }
-        if (!met) {
-          if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
-          break;
-        }
-        fence_proxy_async_smem();  // the merge's accesses, before the next async fill
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&empty[stage]);
-          mbar_arrive(&empty[NS + stage]);
         }
       }
-      if (si == 0) {
-        const bool whole = (h.flags & kStartsUnit) && (h.flags & kEndsUnit);
+      __syncwarp();
+      if (!hold && lane == 0) mbar_arrive(&empty[stage]);  // K is read: its buffer is free while V is still in use
+      uint32_t bp[2][2];
+      if (nv > 0) {
+        if (nv < kSlice) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * hf + 8 * (i >> 1) + pk >= nv) s[hf][i] = -INFINITY;
+        }
+        float top[2];
+        bool far = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float lt = l[k];
-          lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-          lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-          lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-          const int col = head0 + 2 * c + k;  // query head within the group
-          const float inv = a.out_scale / lt;
-          const float lse_v = (m[k] + log2f(lt) - (float)kWeightExp) * kLn2;
-          if (col < G) {
-            // tile t of O: row g is dim D / 8 g + 2t, row g + 8 the next one
-            const int qhl = hl * G + col;
-            if (whole) {
-              const int64_t qh = (int64_t)h.hg * HQU + qhl;
-              uint4* op = reinterpret_cast<uint4*>(a.out + ((int64_t)h.b * a.num_q_heads + qh) * D + g * (D / 8));
+          top[k] = fmaxf(fmaxf(s[0][k], s[0][2 + k]), fmaxf(s[1][k], s[1][2 + k]));
+          far |= fmaf(top[k], qs[k], -m[k]) > (float)kHeadroom;
+        }
+        if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
-              for (int t = 0; t < NM; t += 4)
-                op[t / 4] = make_uint4(pack_bf16x2(o[t][k] * inv, o[t][2 + k] * inv),
-                                       pack_bf16x2(o[t + 1][k] * inv, o[t + 1][2 + k] * inv),
-                                       pack_bf16x2(o[t + 2][k] * inv, o[t + 2][2 + k] * inv),
-                                       pack_bf16x2(o[t + 3][k] * inv, o[t + 3][2 + k] * inv));
-              if (g == 0 && a.lse) a.lse[(int64_t)h.b * a.num_q_heads + qh] = lse_v;
-            } else {
-              float4* pp = reinterpret_cast<float4*>(a.part_o + ((int64_t)h.part * HQU + qhl) * D + g * (D / 8));
+          for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-              for (int t = 0; t < NM; t += 2)
-                pp[t / 2] = make_float4(o[t][k] * inv, o[t][2 + k] * inv, o[t + 1][k] * inv, o[t + 1][2 + k] * inv);
-              if (g == 0) a.part_lse[(int64_t)h.part * HQU + qhl] = lse_v;
+            for (int k = 0; k < 2; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], off));
+          float corr[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float mn = fmaxf(m[k], top[k] * qs[k]);
+            corr[k] = m[k] == -INFINITY ? 1.f : ex2(m[k] - mn);  // nothing so far, or NaN: sums that stay what they are
+            m[k] = mn;
+            l[k] *= corr[k];
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[t][i] *= corr[i & 1];
+        }
+        const float b0 = (float)kWeightExp - m[0], b1 = (float)kWeightExp - m[1];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float w0 = ex2(fmaf(s[hf][2 * i], qs[0], b0)), w1 = ex2(fmaf(s[hf][2 * i + 1], qs[1], b1));
+            l[0] += w0;
+            l[1] += w1;
+            bp[hf][i] = movmatrix_t(pack_f16x2(w0, w1));
+          }
+      }
+      if (!wait(&full[NS + stage])) return;
+      if (nv > 0) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t aa = va_at + at + hf * a.sixteen, ab = vb_at + at + hf * a.sixteen;
+          const uint32_t sa = s_at + at + (uint32_t)(Ts * HC * SH) + 2 * hf * s_eight;
+          uint32_t wa[2][VW], wb[2][VW], vs[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            lds<VW>(aa + i * a.eight, wa[i]);
+            lds<VW>(ab + i * a.eight, wb[i]);
+            uint32_t two = scales(sa + i * s_eight);
+            // Rows past the request's end hold unused pool slots (the boxes bring them) or what shared memory held
+            // before, NaN scales among them: with a scale of 0 their values are 0, and 0 times their weight 0 stays 0.
+            if (nv < kSlice && 16 * hf + 8 * i + pk >= nv) two = 0;
+            // position g's scales of two blocks become block g's (g / 2's) scales of two positions
+            vs[i] = movmatrix_t(unpack_e4m3x2(two));
+          }
+          if constexpr (FEW) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              // row 2c's weight and row 2c + 1's, for the even dims in columns 0 to 3, for the odd ones in 4 to 7
+              const uint32_t b0 = __byte_perm(bp[hf][i], 0, put_a), b1 = __byte_perm(bp[hf][i], 0, put_b);
+              const uint32_t sa2 = __byte_perm(vs[i], 0, 0x1010), sb2 = __byte_perm(vs[i], 0, 0x3232);
+#pragma unroll
+              for (int j = 0; j < VW; ++j) {
+                uint32_t x[4], y[4];
+                unpack_e2m1x8(wa[i][j], x);
+                unpack_e2m1x8(wb[i][j], y);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                  mma_f16_16816(o[2 * j + u], mul_f16x2(x[2 * u], sa2), mul_f16x2(x[2 * u + 1], sa2),
+                                mul_f16x2(y[2 * u], sb2), mul_f16x2(y[2 * u + 1], sb2), b0, b1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              uint32_t e[2][4], f[2][4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                // even and odd dims: byte = (row 2c, row 2c + 1)
+                unpack_e2m1x8((wa[i][j] & 0x0f0f0f0fu) | ((wb[i][j] << 4) & 0xf0f0f0f0u), e[i]);
+                unpack_e2m1x8(((wa[i][j] >> 4) & 0x0f0f0f0fu) | (wb[i][j] & 0xf0f0f0f0u), f[i]);
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                mma_f16_16816(o[4 * j + u], mul_f16x2(e[0][u], vs[0]), mul_f16x2(f[0][u], vs[0]),
+                              mul_f16x2(e[1][u], vs[1]), mul_f16x2(f[1][u], vs[1]), bp[hf][0], bp[hf][1]);
             }
           }
         }
-        if (warp == 0 && lane == 0) {
-          if (h.flags & kStartsUnit) a.unit_first[h.unit] = h.part;
-          if (h.flags & kEndsUnit) a.unit_last[h.unit] = h.part;
+      }
+      __syncwarp();
+      if (!hold && lane == 0) mbar_arrive(&empty[NS + stage]);
+      if (last) break;
+      left -= Ts;
+      if (++stage == NS) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    if (W > 1) {
+      // Combine the W warps that split this head's positions (all consumer warps reach the segment end on
+      // the same stage).  A warp without a position in the segment holds a maximum of -inf and sums of 0.
+      bool met = meet();
+      float* buf = reinterpret_cast<float*>(stages + (size_t)stage * a.stage_bytes) + lane;
+      // all but one at once where their states fit into the stage, else half of them, or as many as do, at a time
+      const int room = (int)(a.stage_bytes / (uint32_t)(HV * MF * 128));
+      for (int some = W; met && some > 1;) {
+        const int keep = some - 1 <= room ? 1 : max(some / 2, some - room);
+        if (si >= keep && si < some) {
+          float* to = buf + ((si - keep) * HV + hv) * MF * 32;
+          int e = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            to[(e++) * 32] = m[k];
+            to[(e++) * 32] = l[k];
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[(e++) * 32] = o[t][i];
         }
+        met = meet();
+        if (!met) break;
+        if (si < keep) {
+          for (int w = si; w < some - keep; w += keep) {
+            const float* ob = buf + (w * HV + hv) * MF * 32;
+            // one that has seen only NaN (or nothing) keeps its sums: they are NaN or 0
+            auto weight = [](float x, float top) { return x == -INFINITY ? 1.f : ex2(x - top); };
+            int e = 0;
+            float fa[2], fb[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float om = ob[(e++) * 32], ol = ob[(e++) * 32];
+              const float mn = fmaxf(m[k], om);
+              fa[k] = weight(m[k], mn);
+              fb[k] = weight(om, mn);
+              l[k] = l[k] * fa[k] + ol * fb[k];
+              m[k] = mn;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[t][i] = o[t][i] * fa[i & 1] + ob[(e++) * 32] * fb[i & 1];
+          }
+        }
+        some = keep;
+        if (some > 1) met = meet();  // read before the next writes
+      }
+      if (!met) {
+        if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
+        return;
+      }
+      fence_proxy_async_smem();  // the merge's accesses, before the next async fill
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&empty[stage]);
+        mbar_arrive(&empty[NS + stage]);
+      }
+    }
+    if (si == 0) {
+      const bool whole = (h.flags & kStartsUnit) && (h.flags & kEndsUnit);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+      // Four consecutive dims g D/8 + 4j .. + 3 of query head `col` of the group, in r[j].
+      auto store = [&](int col, const float (&r)[D / 32][4], float sum, float top, bool one) {
+        if (col >= G) return;
+        const int qhl = hl * G + col;
+        const float inv = a.out_scale / sum, lse_v = (top + log2f(sum) - (float)kWeightExp) * kLn2;
+        if (whole) {
+          const int64_t qh = (int64_t)h.b * a.num_q_heads + (int64_t)h.hg * HQU + qhl;
+          uint4* op = reinterpret_cast<uint4*>(a.out + qh * D + g * (D / 8));
+#pragma unroll
+          for (int j = 0; j < D / 32; j += 2)
+            op[j / 2] = make_uint4(pack_bf16x2(r[j][0] * inv, r[j][1] * inv), pack_bf16x2(r[j][2] * inv, r[j][3] * inv),
+                                   pack_bf16x2(r[j + 1][0] * inv, r[j + 1][1] * inv),
+                                   pack_bf16x2(r[j + 1][2] * inv, r[j + 1][3] * inv));
+          if (one && a.lse) a.lse[qh] = lse_v;
+        } else {
+          const int64_t row = (int64_t)h.part * HQU + qhl;
+          float4* pp = reinterpret_cast<float4*>(a.part_o + row * D + g * (D / 8));
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) pp[j] = make_float4(r[j][0] * inv, r[j][1] * inv, r[j][2] * inv, r[j][3] * inv);
+          if (one) a.part_lse[row] = lse_v;
+        }
+      };
+      float r[D / 32][4];
+      if constexpr (FEW) {
+        // Tile j's rows g and g + 8 are dims 4j and 4j + 2 in columns 0 to 3, the ones behind them in 4 to 7: lanes c and
+        // c ^ 2 hold the even and the odd dims of the same two heads.  The lower takes the first head, the upper the second.
+        const bool up = c >= 2;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mine = up ? o[j][2 * i + 1] : o[j][2 * i], theirs = up ? o[j][2 * i] : o[j][2 * i + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, theirs, 2);
+            r[j][2 * i] = up ? other : mine;
+            r[j][2 * i + 1] = up ? mine : other;
+          }
+        store(2 * (c & 1) + (up ? 1 : 0), r, up ? l[1] : l[0], up ? m[1] : m[0], g == 0);
+      } else {
+        // tile t: row g is dim 2t, row g + 8 the one behind it
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[j][i] = o[2 * j + i / 2][2 * (i % 2) + k];
+          store(head0 + 2 * c + k, r, l[k], m[k], g == 0);
+        }
+      }
+      if (warp == 0 && lane == 0) {
+        if (h.flags & kStartsUnit) a.unit_first[h.unit] = h.part;
+        if (h.flags & kEndsUnit) a.unit_last[h.unit] = h.part;
       }
     }
     if (++stage == NS) {
@@ -409,8 +518,8 @@ extern "C" {
 
 size_t pkv_decode_fp4_workspace_size(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
                                      int32_t head_dim) {
-  if (head_dim == 128) return quant_decode_workspace<Format4<128>>(batch_size, num_q_heads, num_kv_heads);
-  if (head_dim == 64) return quant_decode_workspace<Format4<64>>(batch_size, num_q_heads, num_kv_heads);
+  if (head_dim == 128) return quant_decode_workspace<Format4<128, true>>(batch_size, num_q_heads, num_kv_heads);
+  if (head_dim == 64) return quant_decode_workspace<Format4<64, true>>(batch_size, num_q_heads, num_kv_heads);
   return 0;
 }
 
@@ -426,8 +535,12 @@ pkv_status pkv_paged_decode_fp4(const pkv_pool_fp4* pool, const void* q, int32_t
   const pkv_status s = check_quant_decode(c, pool->num_kv_heads, pool->head_dim);
   if (s != PKV_OK || batch_size == 0) return s;
   const float score_scale = sm_scale * pool->k_global;
-  return pool->head_dim == 128 ? run_quant_decode<Format4<128>>(pool, c, score_scale, pool->v_global)
-                               : run_quant_decode<Format4<64>>(pool, c, score_scale, pool->v_global);
+  const bool few = num_q_heads / pool->num_kv_heads <= 4;
+  if (pool->head_dim == 128)
+    return few ? run_quant_decode<Format4<128, true>>(pool, c, score_scale, pool->v_global)
+               : run_quant_decode<Format4<128, false>>(pool, c, score_scale, pool->v_global);
+  return few ? run_quant_decode<Format4<64, true>>(pool, c, score_scale, pool->v_global)
+             : run_quant_decode<Format4<64, false>>(pool, c, score_scale, pool->v_global);
 }
 
 }  // extern "C"

@@ -27,7 +27,9 @@ constexpr int kEndsUnit = 8;    // the segment ends at the unit's last position
 
 struct StageHdr {
   int32_t unit;  // -1: no more work
-  int32_t b, hg, ntok, flags, part, pad0, pad1;
+  int32_t b, hg, ntok, flags, part;
+  int32_t left;  // positions of the segment from this stage on
+  int32_t pad;
 };
 
 struct QuantDecodeArgs {
@@ -61,6 +63,7 @@ struct QuantDecodeArgs {
   int32_t nt;            // warps that share a KV head's rows, eight of its query heads each
   int32_t box_rows;      // TMA instance: rows of a box (32, 16 or 8)
   int32_t row_stride;    // row-copy instance: shared-memory bytes per token row
+  uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // 32 * W
   int32_t num_stages, num_parts;
   uint32_t kv_region;    // bytes of the K (or V) part of one stage
@@ -160,7 +163,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
     }
   };
 
-  auto emit = [&](int unit, int b, int hg, int tok0, int ntok, int flags) -> bool {
+  auto emit = [&](int unit, int b, int hg, int tok0, int ntok, int left, int flags) -> bool {
     if (unit >= 0 && !v && (flags & kSegFirst)) {
       const int hqu = HC * a.group;  // the unit's queries, on their way to L2 before they are read
       const char* qb = reinterpret_cast<const char*>(a.q + ((int64_t)b * a.num_q_heads + (int64_t)hg * hqu) * D);
@@ -186,7 +189,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
     uint64_t* bar = &full[stage];
     if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) return false;
     if (!v && lane == 0) {  // the consumers read the header, and a new unit's queries, while the stage is on its way
-      hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, 0, 0};
+      hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, left, 0};
       mbar_arrive(&hdr_full[stage]);
     }
     if (unit >= 0) {
@@ -353,14 +356,14 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
             if (t + Ts >= t1) flags |= kSegLast;
             if (s0 == us) flags |= kStartsUnit;
             if (s1 == ue) flags |= kEndsUnit;
-            ok = emit(bb * nhg + hg, bb, hg, t, min(Ts, t1 - t), flags);
+            ok = emit(bb * nhg + hg, bb, hg, t, min(Ts, t1 - t), t1 - t, flags);
           }
         }
       }
       base += nhg * __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  ok = ok && emit(-1, 0, 0, 0, 0, 0);
+  ok = ok && emit(-1, 0, 0, 0, 0, 0, 0);
   // The merge may be scheduled once every CTA has issued its last copies (it waits for this grid's
   // completion before it reads): early enough to hide its launch, late enough not to hold thread
   // slots that kernels on other streams could use.
@@ -662,6 +665,8 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   a.nt = p.NT;
   a.box_rows = p.R;
   a.row_stride = p.RS;
+  a.eight = p.tma ? (uint32_t)(8 * F::kRowBytes * (p.R == 8 ? p.HC : 1)) : (uint32_t)(8 * p.RS);
+  a.sixteen = p.tma ? (uint32_t)(16 * F::kRowBytes * (p.R <= 16 ? p.HC : 1)) : (uint32_t)(16 * p.RS);
   a.stage_tokens = p.Ts;
   a.num_stages = p.NS;
   a.num_parts = (int32_t)p.nparts;

@@ -221,7 +221,7 @@ bool encode_tmap_rows(CUtensorMap* m, const void* base, uint64_t d0, uint64_t ro
 // choice of fetch size.
 bool encode_tmap_head(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads, uint64_t rows, uint32_t box_rows);
 // encode_tmap_3d of bytes, with the 128-byte swizzle for rows of 128 bytes, the 64-byte one for 64 and
-// none for 32 (b0).
+// the 32-byte one for 32 (b0).
 bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                        uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
 }  // namespace pkv_host
