@@ -40,12 +40,12 @@ PKV_DEV int position(int r) {
 
 template <int D, bool FEW>
 struct Format4 {
-  static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kWarps = 16;
+  static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kWarps = 16, kParts = 2;
+  static constexpr bool kBoxedRows = true, kJoint = true;
   static constexpr int kTiles = FEW ? D / 32 : D / 16;  // row tiles of O
   static constexpr int kMergeFloats = 4 + 4 * kTiles;
-  // an odd multiple of a head's bytes, so that neighbouring rows lie in other banks
-  static int row_stride(int bytes) { return bytes / kRowBytes % 2 ? bytes : bytes + kRowBytes; }
-  template <bool TMA>
+  static int row_stride(int bytes) { return bytes; }
+  template <bool>
   static __device__ void consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                  uint64_t* full, uint64_t* empty, uint64_t* meet_bar);
 };
@@ -81,13 +81,29 @@ PKV_DEV void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-PKV_DEV float half_to_float(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
+PKV_DEV float2 half2_to_floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+
+// The product of an f16 pair with the low (high) half of another, which the instruction reads in place.
+PKV_DEV uint32_t mul_f16x2_low(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {l, l};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+      : "=r"(d)
+      : "r"(a), "r"(b));
+  return d;
+}
+PKV_DEV uint32_t mul_f16x2_high(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {h, h};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+      : "=r"(d)
+      : "r"(a), "r"(b));
+  return d;
+}
 
 // ---------------------------------------------------------------------------------------------
 // Consumer warps: 32-position steps of one KV head with its G query heads.
 // ---------------------------------------------------------------------------------------------
 template <int D, bool FEW>
-template <bool TMA>
+template <bool>
 __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                          uint64_t* full, uint64_t* empty, uint64_t* meet_bar) {
   constexpr int RH = kRowBytes, SH = kScaleBytes, NT = kTiles;
@@ -108,11 +124,9 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
   // Shared-memory places within a stage of the slice's first eight positions: of K, of V's rows 2c and 2c + 1 (the
   // lane's eighth g), and of the scales of row g.
   const int t0 = si * kSlice;
-  const uint32_t first = TMA ? (uint32_t)(((t0 / a.box_rows) * HC + hl) * a.box_rows + t0 % a.box_rows) * RH
-                             : (uint32_t)(t0 * a.row_stride + hl * RH);
-  const int stride = TMA ? RH : a.row_stride;
-  auto piece = [&](int t, int p) -> uint32_t {  // 16-byte piece p of position t of eight
-    return first + (uint32_t)(t * stride + ((!TMA ? p : D == 128 ? p ^ ((t >> 1) & 3) : p ^ ((t >> 2) & 1)) << 4));
+  const uint32_t first = (uint32_t)(((t0 / a.box_rows) * HC + hl) * a.box_rows + t0 % a.box_rows) * RH;
+  auto piece = [&](int t, int p) -> uint32_t {  // 16-byte piece p of position t of eight, in the boxes' swizzle
+    return first + (uint32_t)(t * RH + ((D == 128 ? p ^ ((t >> 1) & 3) : p ^ ((t >> 2) & 1)) << 4));
   };
   const int pk = position<D>(g), pa = position<D>(2 * c), pb = position<D>(2 * c + 1);
   const uint32_t base = smem_u32(stages);
@@ -226,11 +240,13 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
               uint32_t b[VW];
               lds<VW>(sa + i * s_eight, b);
               const uint32_t four = __byte_perm(b[0], VW == 2 ? b[VW - 1] : 0u, pick);
+              uint32_t two[2];
+              unpack_e4m3x4(four, two[0], two[1]);
 #pragma unroll
               for (int j = 0; j < KW / 2; ++j) {
-                const uint32_t two = unpack_e4m3x2(four >> (16 * j));
-                ks[i][2 * j] = half_to_float(two);
-                ks[i][2 * j + 1] = half_to_float(two >> 16);
+                const float2 f = half2_to_floats(two[j]);
+                ks[i][2 * j] = f.x;
+                ks[i][2 * j + 1] = f.y;
               }
             }
 #pragma unroll
@@ -250,13 +266,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             uint32_t w[2][KW];  // rows g and g + 8: codes, and the scales of the two halves of the lane's quarter
             lds<KW>(ka, w[0]);
             lds<KW>(ka + a.eight, w[1]);
-            uint32_t ks[2][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t pair = unpack_e4m3x2(scales(sa + i * s_eight));
-              ks[i][0] = D == 128 ? __byte_perm(pair, 0, 0x1010) : pair;
-              ks[i][1] = D == 128 ? __byte_perm(pair, 0, 0x3232) : pair;
-            }
+            const uint32_t ks[2] = {unpack_e4m3x2(scales(sa)), unpack_e4m3x2(scales(sa + s_eight))};
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
               uint32_t x[4], y[4];
@@ -264,8 +274,8 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
               unpack_e2m1x8(w[1][j], y);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                x[i] = mul_f16x2(x[i], ks[0][2 * j / KW]);
-                y[i] = mul_f16x2(y[i], ks[1][2 * j / KW]);
+                x[i] = 2 * j < KW ? mul_f16x2_low(x[i], ks[0]) : mul_f16x2_high(x[i], ks[0]);
+                y[i] = 2 * j < KW ? mul_f16x2_low(y[i], ks[1]) : mul_f16x2_high(y[i], ks[1]);
               }
               if (j == 0)
                 mma_f16_16816_zero(s[hf], x[0], y[0], x[1], y[1], qf[0][0], qf[0][1]);
@@ -276,8 +286,6 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
           }
         }
       }
-      __syncwarp();
-      if (!hold && lane == 0) mbar_arrive(&empty[stage]);  // K is read: its buffer is free while V is still in use
       uint32_t bp[2][2];
       if (nv > 0) {
         if (nv < kSlice) {
@@ -323,7 +331,6 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             bp[hf][i] = movmatrix_t(pack_f16x2(w0, w1));
           }
       }
-      if (!wait(&full[NS + stage])) return;
       if (nv > 0) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -346,7 +353,6 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             for (int i = 0; i < 2; ++i) {
               // row 2c's weight and row 2c + 1's, for the even dims in columns 0 to 3, for the odd ones in 4 to 7
               const uint32_t b0 = __byte_perm(bp[hf][i], 0, put_a), b1 = __byte_perm(bp[hf][i], 0, put_b);
-              const uint32_t sa2 = __byte_perm(vs[i], 0, 0x1010), sb2 = __byte_perm(vs[i], 0, 0x3232);
 #pragma unroll
               for (int j = 0; j < VW; ++j) {
                 uint32_t x[4], y[4];
@@ -354,8 +360,8 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
                 unpack_e2m1x8(wb[i][j], y);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                  mma_f16_16816(o[2 * j + u], mul_f16x2(x[2 * u], sa2), mul_f16x2(x[2 * u + 1], sa2),
-                                mul_f16x2(y[2 * u], sb2), mul_f16x2(y[2 * u + 1], sb2), b0, b1);
+                  mma_f16_16816(o[2 * j + u], mul_f16x2_low(x[2 * u], vs[i]), mul_f16x2_low(x[2 * u + 1], vs[i]),
+                                mul_f16x2_high(y[2 * u], vs[i]), mul_f16x2_high(y[2 * u + 1], vs[i]), b0, b1);
               }
             }
           } else {
@@ -377,7 +383,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
         }
       }
       __syncwarp();
-      if (!hold && lane == 0) mbar_arrive(&empty[NS + stage]);
+      if (!hold && lane == 0) mbar_arrive(&empty[stage]);
       if (last) break;
       left -= Ts;
       if (++stage == NS) {
@@ -441,10 +447,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
       }
       fence_proxy_async_smem();  // the merge's accesses, before the next async fill
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&empty[stage]);
-        mbar_arrive(&empty[NS + stage]);
-      }
+      if (lane == 0) mbar_arrive(&empty[stage]);
     }
     if (si == 0) {
       const bool whole = (h.flags & kStartsUnit) && (h.flags & kEndsUnit);

@@ -2,15 +2,17 @@
 // share, which is all but a consumer warp's arithmetic on its 32 positions.
 //
 //  * One persistent CTA per SM over an equal share of the stream of slices of 32 positions of all (request,
-//    head group) units; a producer warp each for K and V fills a ring of stages, eight or sixteen consumer warps read
+//    head group) units; producer warps for K and for V fill a ring of stages, eight or sixteen consumer warps read
 //    them, a second kernel merges the units that the shares cut.
 //  * K and V come in TMA boxes of 32, 16 or 8 rows (the largest that divides the page size), by copies of single
 //    rows for other page sizes.  The scales come into the same stage: by bulk copies beside the boxes where the
 //    CTA takes every KV head (a box's lie side by side then), by cp.async otherwise.
 //
 // A format F is a struct with kDim (head_dim), kRowBytes and kScaleBytes (of one head of one position), kWarps
-// (consumer warps), kMergeFloats (of a lane's state, see consume), row_stride(bytes of a row) in shared memory for
-// the row copies, and consume<TMA>, a consumer warp.
+// (consumer warps), kParts (most producer warps each for K and V), kJoint (whether K and V share a stage's barriers),
+// kMergeFloats (of a lane's state, see consume),
+// kBoxedRows (whether row copies make boxes of 32 rows of a head in the boxes' swizzle, or rows row_stride(their bytes)
+// apart), and consume<TMA>, a consumer warp.
 #pragma once
 
 #include <atomic>
@@ -63,6 +65,9 @@ struct QuantDecodeArgs {
   int32_t nt;            // warps that share a KV head's rows, eight of its query heads each
   int32_t box_rows;      // TMA instance: rows of a box (32, 16 or 8)
   int32_t row_stride;    // row-copy instance: shared-memory bytes per token row
+  FastDiv piece_div;     // boxed rows: by the 16-byte pieces of a row of HC heads
+  int32_t scale_piece;   // ... bytes of one copy of scales: 16, 8 or 4
+  int32_t parts;         // producer warps each for K and V
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // 32 * W
   int32_t num_stages, num_parts;
@@ -114,8 +119,9 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
 // ---------------------------------------------------------------------------------------------
 template <class F, bool TMA>
 __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
-                                 uint64_t* full, uint64_t* empty, bool v) {
+                                 uint64_t* full, uint64_t* empty, bool v, int part) {
   constexpr int D = F::kDim, RH = F::kRowBytes, SH = F::kScaleBytes;  // bytes of a head's row and of its scales
+  const int P = F::kParts == 1 ? 1 : a.parts;
   const int lane = threadIdx.x & 31;
   const int NS = a.num_stages, Ts = a.stage_tokens, W = a.W, HC = a.HC, nhg = a.nhg;
   const uint32_t region = a.kv_region;
@@ -154,6 +160,19 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
   auto entry = [&](int pidx) -> int32_t {  // page-list entry of the current request; -1 past its end
     return pidx < cur_np ? ld(a.kv_indices + cur_p0 + pidx) : -1;
   };
+  // boxed rows: the pages of the lane's positions in this warp's next four rounds of 32, and the round behind them
+  int32_t p0 = -1, p1 = -1, p2 = -1, p3 = -1;
+  int ahead_tok = 0, ahead_round = 0;
+  auto ahead_page = [&]() -> int32_t {
+    const int32_t page = entry((int)a.page_div.quot((uint32_t)(ahead_tok + 32 * ahead_round + lane)));
+    ahead_round += P;
+    if (ahead_round >= W) {
+      ahead_round = part;
+      ahead_tok += Ts;
+    }
+    return page;
+  };
+  const FastDiv pieces_div = a.piece_div;
   int nissued = 0;
   auto next_stage = [&]() {
     ++nissued;
@@ -164,13 +183,14 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
   };
 
   auto emit = [&](int unit, int b, int hg, int tok0, int ntok, int left, int flags) -> bool {
-    if (unit >= 0 && !v && (flags & kSegFirst)) {
+    const bool first = !v && part == 0;  // of the warps: the one that writes headers and reports
+    if (unit >= 0 && first && (flags & kSegFirst)) {
       const int hqu = HC * a.group;  // the unit's queries, on their way to L2 before they are read
       const char* qb = reinterpret_cast<const char*>(a.q + ((int64_t)b * a.num_q_heads + (int64_t)hg * hqu) * D);
       for (int off = lane * 128; off < hqu * D * 2; off += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(qb + off));
     }
-    if (unit >= 0 && windowed) {
+    if (unit >= 0 && (F::kBoxedRows && !TMA ? false : windowed)) {
       const int first_page = a.page_div.quot(tok0);
       if (b != win_b || first_page < wbase) {
         win_b = b;
@@ -188,7 +208,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
     }
     uint64_t* bar = &full[stage];
     if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) return false;
-    if (!v && lane == 0) {  // the consumers read the header, and a new unit's queries, while the stage is on its way
+    if (first && lane == 0) {  // the consumers read the header, and a new unit's queries, while the stage is on its way
       hdr[stage] = StageHdr{unit, b, hg, ntok, flags, (int32_t)blockIdx.x + unit, left, 0};
       mbar_arrive(&hdr_full[stage]);
     }
@@ -232,12 +252,14 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         // one KV head took 4 us, and 720000 positions of it 96 us; 48 now, of the 28 that their bytes take.)
         // Only boxes of 8 rows in a stage of 512 positions are more than the lanes.
         const int sh = 31 - __clz(a.box_rows), nbox = Ts >> sh;
-        const bool side_by_side = nhg == 1;
+        // Side by side, and enough of them for a bulk copy, which costs about 65 cycles of the copy unit whatever it
+        // brings (4 bits, one head of 128 at page size 16, 720000 positions: 42 us with 128-byte copies of them).
+        const bool side_by_side = nhg == 1 && (F::kParts == 1 || (HC * SH << (31 - __clz(a.box_rows))) >= 512);
         const uint32_t box = (uint32_t)(HC * RH) << sh, sbox = (uint32_t)(HC * SH) << sh;
 #pragma unroll 1
-        for (int i0 = 0; i0 < (F::kWarps > 8 ? nbox : 1); i0 += 32) {
-          const int tok = tok0 + ((i0 + lane) << sh);
-          const bool in = i0 + lane < nbox && tok < tok0 + ntok;
+        for (int i0 = 0; i0 < (F::kWarps > 8 ? nbox : 1); i0 += 32 * P) {
+          const int box_i = i0 + P * lane + part, tok = tok0 + (box_i << sh);
+          const bool in = box_i < nbox && tok < tok0 + ntok;
           uint32_t pidx, in_page;
           a.page_div.divmod((uint32_t)(in ? tok : tok0), pidx, in_page);
           const int32_t page = windowed ? window_page(pidx) : in ? entry((int)pidx) : -1;
@@ -246,15 +268,77 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           if (lane == 0) mbar_expect_tx(bar, n * (box + (side_by_side ? sbox : 0u)));
           __syncwarp();
           if (row >= 0) {
-            tma_load_3d(smem_u32(dst) + (i0 + lane) * box, tm, 0, (int)row, hg * HC, bar);
-            if (side_by_side) bulk_g2s(sdst + (i0 + lane) * sbox, scale + row * a.num_kv_heads * SH, sbox, bar);
+            tma_load_3d(smem_u32(dst) + box_i * box, tm, 0, (int)row, hg * HC, bar);
+            if (side_by_side) bulk_g2s(sdst + box_i * sbox, scale + row * a.num_kv_heads * SH, sbox, bar);
           }
           if (!side_by_side) {
-            const int rounds = F::kWarps > 8 ? min(W - (i0 << sh) / 32, 1 << sh) : W;
-            for (int r = 0; r < rounds; ++r) {
-              const int j = (i0 << sh) + lane + 32 * r;
-              const int first = __shfl_sync(0xffffffffu, (int)row, (j >> sh) & 31);
-              if (j < ntok && first >= 0) copy_scales(first + (j & (a.box_rows - 1)), j);
+            if (F::kParts > 1 && nhg == 1) {  // 16 bytes a lane of this warp's boxes' scales
+              const int psh = 27 - __clz(sbox);  // sbox is 16 times a power of two, or HC is not: see below
+              if ((sbox & (sbox - 1)) == 0) {
+                const int mine = min((nbox - i0 + P - 1) / P, 32);
+                for (int r = 0; r < mine << psh; r += 32) {
+                  const int k = r + lane, bi = k >> psh;
+                  const int first_row = __shfl_sync(0xffffffffu, (int)row, bi & 31);
+                  const uint32_t off = (uint32_t)(k & ((1 << psh) - 1)) * 16;
+                  if (bi < mine && first_row >= 0)
+                    cp_async16(smem_u32(sdst) + (i0 + P * bi + part) * sbox + off,
+                               scale + (int64_t)first_row * a.num_kv_heads * SH + off);
+                }
+                continue;
+              }
+            }
+            // lane by lane the rows of this warp's boxes
+            const int rounds = F::kWarps > 8 ? min((nbox - i0 + P - 1) / P, 32) << sh : Ts;
+            for (int r = 0; r < rounds; r += 32) {
+              const int k = r + lane, j = (i0 + P * (k >> sh) + part) * a.box_rows + (k & (a.box_rows - 1));
+              const int first_row = __shfl_sync(0xffffffffu, (int)row, (k >> sh) & 31);
+              if (k < rounds && j < ntok && first_row >= 0) copy_scales(first_row + (k & (a.box_rows - 1)), j);
+            }
+          }
+        }
+      } else if constexpr (F::kBoxedRows) {
+        // Single rows, 16 bytes a lane, into the places that a box of 32 rows has: [slice][head][row], pieces swizzled.
+        // Rows lie together in shared memory by head, so a warp's 32 pieces come from as few rows as hold them.
+        constexpr int HP = RH / 16;  // pieces of a head's row
+        if (flags & kSegFirst) {
+          ahead_tok = tok0;
+          ahead_round = part;
+          p0 = ahead_page(), p1 = ahead_page(), p2 = ahead_page(), p3 = ahead_page();
+        }
+        const int pieces = HC * HP, spieces = HC * SH / a.scale_piece;
+#pragma unroll 1
+        for (int r = part; r < W; r += P) {
+          const int j = lane + 32 * r;
+          const bool in = j < ntok;
+          uint32_t pidx, in_page;
+          a.page_div.divmod((uint32_t)(tok0 + (in ? j : 0)), pidx, in_page);
+          const int32_t page = p0;
+          p0 = p1, p1 = p2, p2 = p3, p3 = ahead_page();
+          const int64_t row = row_at(pidx, in_page, page, in);
+          const int64_t from = row * a.num_kv_heads + hg * HC;  // in heads; negative where there is no row
+          const uint32_t to = smem_u32(dst) + (uint32_t)(r * HC * 32) * RH;
+          const uint32_t sto = smem_u32(sdst) + (uint32_t)(r * 32 * HC) * SH;
+          const int rows = min(32, ntok - 32 * r);
+#pragma unroll 4
+          for (int it = lane; it < 32 * pieces; it += 32) {
+            uint32_t t, ch;
+            pieces_div.divmod((uint32_t)it, t, ch);
+            const int64_t src = __shfl_sync(0xffffffffu, from, t & 31);
+            const uint32_t hd = ch / HP, pc = ch % HP;
+            const uint32_t swz = RH == 64 ? pc ^ ((t >> 1) & 3) : pc ^ ((t >> 2) & 1);
+            if ((int)t < rows && src >= 0)
+              cp_async16(to + (hd * 32 + t) * RH + swz * 16, pool + src * RH + ch * 16);
+          }
+#pragma unroll 1
+          for (int it = lane; it < 32 * spieces; it += 32) {
+            const uint32_t t = (uint32_t)it / (uint32_t)spieces, ch = (uint32_t)it % (uint32_t)spieces;
+            const int64_t src = __shfl_sync(0xffffffffu, from, t & 31);
+            if ((int)t < rows && src >= 0) {
+              const uint32_t sd = sto + t * HC * SH + ch * a.scale_piece;
+              const uint8_t* sp = scale + src * SH + ch * a.scale_piece;
+              if (a.scale_piece == 16) cp_async16(sd, sp);
+              else if (a.scale_piece == 8) cp_async8(sd, sp);
+              else cp_async4(sd, sp);
             }
           }
         }
@@ -271,7 +355,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           const int j = lane + 32 * r;
           return !windowed && j < ntok ? entry((int)a.page_div.quot((uint32_t)(tok0 + j))) : -1;
         };
-        int32_t p0 = ahead(0), p1 = ahead(1), p2 = ahead(2), p3 = ahead(3);
+        p0 = ahead(0), p1 = ahead(1), p2 = ahead(2), p3 = ahead(3);
 #pragma unroll 1
         for (int r = 0; r < W; ++r) {
           const int j = lane + 32 * r;
@@ -303,7 +387,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           }
         }
       }
-      if (bad && !v) report(a.err_word, bad);
+      if (bad && !v) report(a.err_word, bad);  // K's warps see every row
     }
     // the arrival that lets the stage complete comes after every byte count
     __syncwarp();
@@ -367,7 +451,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
   // The merge may be scheduled once every CTA has issued its last copies (it waits for this grid's
   // completion before it reads): early enough to hide its launch, late enough not to hold thread
   // slots that kernels on other streams could use.
-  if (!v) pdl_trigger();
+  if (!v && part == 0) pdl_trigger();
   if (!ok && lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
   // No copy into this CTA's shared memory is in flight when it exits (bounded waits; immediate on
   // the normal path, where the consumers have seen every stage complete).
@@ -381,7 +465,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
 }
 
 template <class F, bool TMA>
-__global__ void __launch_bounds__((F::kWarps + 2) * 32, 1) quant_decode_kernel(const __grid_constant__ QuantDecodeArgs a) {
+__global__ void __launch_bounds__((F::kWarps + 2 * F::kParts) * 32, 1) quant_decode_kernel(const __grid_constant__ QuantDecodeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int NS = a.num_stages;
   const int NC = a.HC * a.nt * a.W;
@@ -396,14 +480,15 @@ __global__ void __launch_bounds__((F::kWarps + 2) * 32, 1) quant_decode_kernel(c
   StageHdr* hdr = reinterpret_cast<StageHdr*>(smem + (size_t)NS * a.stage_bytes);
   uint64_t* hdr_full = reinterpret_cast<uint64_t*>(hdr + NS);
   uint64_t* full = hdr_full + NS;
-  uint64_t* empty = full + 2 * NS;  // K's barriers, then V's
+  uint64_t* empty = full + 2 * NS;  // K's barriers, then V's (joint: those alone)
   uint64_t* meet_bar = empty + 2 * NS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) mbar_init(&hdr_full[s], 1);
     mbar_init(meet_bar, NC);
+    const int parts = F::kParts == 1 ? 1 : a.parts;
     for (int s = 0; s < 2 * NS; ++s) {
-      mbar_init(&full[s], 1 + 32);  // a producer's go-ahead, and every lane's scale copies
+      mbar_init(&full[s], 33 * parts * (F::kJoint ? 2 : 1));  // each producer's go-ahead, and every lane's copies
       mbar_init(&empty[s], NC);
     }
     fence_mbar_init();
@@ -417,11 +502,12 @@ __global__ void __launch_bounds__((F::kWarps + 2) * 32, 1) quant_decode_kernel(c
   pdl_wait();
 
   const int warp = threadIdx.x >> 5;
-  if (warp == NC) {
-    quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, full, empty, false);
-  } else if (warp == NC + 1) {
-    quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, full + NS, empty + NS, true);
-  } else if (warp < NC) {
+  if (warp >= NC) {
+    const int p = warp - NC;  // K's and V's in turn
+    const bool v = p & 1;
+    quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, v && !F::kJoint ? full + NS : full,
+                                  v && !F::kJoint ? empty + NS : empty, v, p >> 1);
+  } else {
     F::template consume<TMA>(a, stages, hdr, hdr_full, full, empty, meet_bar);
   }
 }
@@ -545,7 +631,7 @@ bool make_plan(int B, int Hq, int Hkv, int ncta, QuantDecodePlan& p, int page_si
   p.W = F::kWarps / (p.HC * p.NT);
   p.Ts = kSlice * p.W;
   const int RB = p.HC * F::kRowBytes;
-  p.RS = F::row_stride(RB);
+  p.RS = F::kBoxedRows ? RB : F::row_stride(RB);
   p.R = page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 8;
   p.tma = page_size > 0 && page_size % 8 == 0 && num_pages * (int64_t)page_size < 0x7fffffffLL;
   p.region = p.tma ? (uint32_t)(p.Ts * RB) : (uint32_t)(p.Ts * p.RS);
@@ -602,7 +688,7 @@ pkv_status launch_quant_decode(const QuantDecodePlan& p, const QuantDecodeArgs& 
     }
     if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
   }
-  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2) * 32, p.smem, st, a);
+  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2 * a.parts) * 32, p.smem, st, a);
   if (s != PKV_OK) return s;
   return pkv_host::launch_after(quant_decode_merge_kernel<F>, dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8)),
                                 256, 0, st, a);
@@ -665,8 +751,16 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   a.nt = p.NT;
   a.box_rows = p.R;
   a.row_stride = p.RS;
-  a.eight = p.tma ? (uint32_t)(8 * F::kRowBytes * (p.R == 8 ? p.HC : 1)) : (uint32_t)(8 * p.RS);
-  a.sixteen = p.tma ? (uint32_t)(16 * F::kRowBytes * (p.R <= 16 ? p.HC : 1)) : (uint32_t)(16 * p.RS);
+  a.piece_div = FastDiv((uint32_t)(p.HC * F::kRowBytes / 16));
+  // One warp each issues a few boxes and their scales in time, and more warps' walks would take issue slots from the
+  // consumers (4 bits, 256 requests of 32/8 heads: 140 us with one, 144 with two; copied row by row, 48/16 heads of 64: 47, 40).
+  a.parts = F::kParts == 1 || (p.tma && p.Ts / p.R <= 4 && p.nhg == 1) ? 1 : F::kParts;
+  const int scales = p.HC * F::kScaleBytes;
+  a.scale_piece = scales % 16 == 0 ? 16 : scales % 8 == 0 ? 8 : 4;
+  if (!p.tma && F::kBoxedRows) p.R = a.box_rows = kSlice;
+  const bool boxed = p.tma || F::kBoxedRows;
+  a.eight = boxed ? (uint32_t)(8 * F::kRowBytes * (p.R == 8 ? p.HC : 1)) : (uint32_t)(8 * p.RS);
+  a.sixteen = boxed ? (uint32_t)(16 * F::kRowBytes * (p.R <= 16 ? p.HC : 1)) : (uint32_t)(16 * p.RS);
   a.stage_tokens = p.Ts;
   a.num_stages = p.NS;
   a.num_parts = (int32_t)p.nparts;
