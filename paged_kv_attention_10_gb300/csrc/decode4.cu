@@ -40,7 +40,7 @@ PKV_DEV int position(int r) {
 
 template <int D, bool FEW>
 struct Format4 {
-  static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kWarps = 16, kParts = 2;
+  static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kWarps = 8, kStep = 64, kParts = 2;
   static constexpr bool kBoxedRows = true, kJoint = true;
   static constexpr int kTiles = FEW ? D / 32 : D / 16;  // row tiles of O
   static constexpr int kMergeFloats = 4 + 4 * kTiles;
@@ -107,6 +107,7 @@ template <bool>
 __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                          uint64_t* full, uint64_t* empty, uint64_t* meet_bar) {
   constexpr int RH = kRowBytes, SH = kScaleBytes, NT = kTiles;
+  constexpr int NH = kStep / 16;      // score tiles of a step
   constexpr int NM = D / 16;          // MMAs of a score tile
   constexpr int KW = D / 32;          // words of a lane's share of a K row
   constexpr int VW = D / 64;          // ... of a V row
@@ -123,7 +124,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
 
   // Shared-memory places within a stage of the slice's first eight positions: of K, of V's rows 2c and 2c + 1 (the
   // lane's eighth g), and of the scales of row g.
-  const int t0 = si * kSlice;
+  const int t0 = si * kStep;
   const uint32_t first = (uint32_t)(((t0 / a.box_rows) * HC + hl) * a.box_rows + t0 % a.box_rows) * RH;
   auto piece = [&](int t, int p) -> uint32_t {  // 16-byte piece p of position t of eight, in the boxes' swizzle
     return first + (uint32_t)(t * RH + ((D == 128 ? p ^ ((t >> 1) & 3) : p ^ ((t >> 2) & 1)) << 4));
@@ -141,6 +142,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
   const uint32_t vb_at = v_at + (D == 128 ? piece(pb, g >> 1) + (g & 1) * 8 : piece(pb, g >> 2) + (g & 3) * 4);
   const uint32_t s_at = base + 2 * a.kv_region + (uint32_t)(((t0 + pk) * HC + hl) * SH);
   const uint32_t s_eight = 8 * HC * SH;
+  auto tile_off = [&](int hf) -> uint32_t { return (hf & 1) * a.sixteen + (hf >> 1) * (uint32_t)(HC * 32 * RH); };
   // two scales of a row: of the blocks 2c and 2c + 1 of eight, or twice of block c of four
   auto scales = [&](uint32_t at) -> uint32_t { return D == 128 ? lds_u16(at + 2 * c) : lds_u8(at + c) * 0x101u; };
   // FEW: which bytes of a row's scales are those of the lane's blocks; where the halves of a pair of weights go in B
@@ -217,15 +219,15 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
     int left = h.left;
     while (true) {  // the segment's stages
       if (!wait(&full[stage])) return;
-      const int nv = left - si * kSlice;  // positions of the slice, at least where it is below 32
+      const int nv = left - si * kStep;  // positions of the step, at least where it is below kStep
       // A segment's last stage is held when warps share a head: its memory carries their merge.
       const bool last = left <= Ts, hold = last && W > 1;
       const uint32_t at = (uint32_t)stage * a.stage_bytes;
-      float s[2][4];
+      float s[NH][4];
       if (nv > 0) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t ka = k_at + at + hf * a.sixteen, sa = s_at + at + 2 * hf * s_eight;
+        for (int hf = 0; hf < NH; ++hf) {
+          const uint32_t ka = k_at + at + tile_off(hf), sa = s_at + at + 2 * hf * s_eight;
           if constexpr (FEW) {
             uint32_t w[2][KW];  // rows g and g + 8: word c of each 16-byte piece
             float ks[2][KW];    // ... and the scale of its block
@@ -286,11 +288,11 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
           }
         }
       }
-      uint32_t bp[2][2];
+      uint32_t bp[NH][2];
       if (nv > 0) {
-        if (nv < kSlice) {
+        if (nv < kStep) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
+          for (int hf = 0; hf < NH; ++hf)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (16 * hf + 8 * (i >> 1) + pk >= nv) s[hf][i] = -INFINITY;
@@ -299,7 +301,9 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
         bool far = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          top[k] = fmaxf(fmaxf(s[0][k], s[0][2 + k]), fmaxf(s[1][k], s[1][2 + k]));
+          top[k] = fmaxf(s[0][k], s[0][2 + k]);
+#pragma unroll
+          for (int hf = 1; hf < NH; ++hf) top[k] = fmaxf(top[k], fmaxf(s[hf][k], s[hf][2 + k]));
           far |= fmaf(top[k], qs[k], -m[k]) > (float)kHeadroom;
         }
         if (__any_sync(0xffffffffu, far)) {
@@ -322,7 +326,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
         }
         const float b0 = (float)kWeightExp - m[0], b1 = (float)kWeightExp - m[1];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
+        for (int hf = 0; hf < NH; ++hf)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float w0 = ex2(fmaf(s[hf][2 * i], qs[0], b0)), w1 = ex2(fmaf(s[hf][2 * i + 1], qs[1], b1));
@@ -333,8 +337,8 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
       }
       if (nv > 0) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t aa = va_at + at + hf * a.sixteen, ab = vb_at + at + hf * a.sixteen;
+        for (int hf = 0; hf < NH; ++hf) {
+          const uint32_t aa = va_at + at + tile_off(hf), ab = vb_at + at + tile_off(hf);
           const uint32_t sa = s_at + at + (uint32_t)(Ts * HC * SH) + 2 * hf * s_eight;
           uint32_t wa[2][VW], wb[2][VW], vs[2];
 #pragma unroll
@@ -344,7 +348,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             uint32_t two = scales(sa + i * s_eight);
             // Rows past the request's end hold unused pool slots (the boxes bring them) or what shared memory held
             // before, NaN scales among them: with a scale of 0 their values are 0, and 0 times their weight 0 stays 0.
-            if (nv < kSlice && 16 * hf + 8 * i + pk >= nv) two = 0;
+            if (nv < kStep && 16 * hf + 8 * i + pk >= nv) two = 0;
             // position g's scales of two blocks become block g's (g / 2's) scales of two positions
             vs[i] = movmatrix_t(unpack_e4m3x2(two));
           }

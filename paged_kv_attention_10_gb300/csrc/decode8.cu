@@ -39,7 +39,7 @@ using namespace pkv;
 
 template <int D>
 struct Format8 {
-  static constexpr int kDim = D, kRowBytes = D, kScaleBytes = 4, kWarps = 8, kParts = 1;
+  static constexpr int kDim = D, kRowBytes = D, kScaleBytes = 4, kWarps = 8, kStep = 32, kParts = 1;
   static constexpr bool kBoxedRows = false, kJoint = false;
   static constexpr int kMergeFloats = 6 + D / 4;
   // the bytes of a row are a multiple of 64: rows 16 bytes off a multiple of 32 keep ldmatrix free of conflicts

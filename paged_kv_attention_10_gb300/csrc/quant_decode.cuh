@@ -9,8 +9,8 @@
 //    CTA takes every KV head (a box's lie side by side then), by cp.async otherwise.
 //
 // A format F is a struct with kDim (head_dim), kRowBytes and kScaleBytes (of one head of one position), kWarps
-// (consumer warps), kParts (most producer warps each for K and V), kJoint (whether K and V share a stage's barriers),
-// kMergeFloats (of a lane's state, see consume),
+// (consumer warps), kStep (positions of a warp's step), kParts (most producer warps each for K and V), kJoint (whether K
+// and V share a stage's barriers), kMergeFloats (of a lane's state, see consume),
 // kBoxedRows (whether row copies make boxes of 32 rows of a head in the boxes' swizzle, or rows row_stride(their bytes)
 // apart), and consume<TMA>, a consumer warp.
 #pragma once
@@ -69,7 +69,7 @@ struct QuantDecodeArgs {
   int32_t scale_piece;   // ... bytes of one copy of scales: 16, 8 or 4
   int32_t parts;         // producer warps each for K and V
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
-  int32_t stage_tokens;  // 32 * W
+  int32_t stage_tokens;  // kStep * W
   int32_t num_stages, num_parts;
   uint32_t kv_region;    // bytes of the K (or V) part of one stage
   uint32_t stage_bytes;  // K, V and the scales
@@ -123,7 +123,9 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
   constexpr int D = F::kDim, RH = F::kRowBytes, SH = F::kScaleBytes;  // bytes of a head's row and of its scales
   const int P = F::kParts == 1 ? 1 : a.parts;
   const int lane = threadIdx.x & 31;
-  const int NS = a.num_stages, Ts = a.stage_tokens, W = a.W, HC = a.HC, nhg = a.nhg;
+  const int NS = a.num_stages, Ts = a.stage_tokens, HC = a.HC, nhg = a.nhg;
+  const int W = Ts / kSlice;  // rounds of 32 positions
+  constexpr bool kManyBoxes = F::kWarps * F::kStep > 256;  // a stage may have more boxes than a warp has lanes
   const uint32_t region = a.kv_region;
   const CUtensorMap* tm = v ? &a.tm_v : &a.tm_k;
   const uint8_t* pool = v ? a.v_pool : a.k_pool;
@@ -257,7 +259,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         const bool side_by_side = nhg == 1 && (F::kParts == 1 || (HC * SH << (31 - __clz(a.box_rows))) >= 512);
         const uint32_t box = (uint32_t)(HC * RH) << sh, sbox = (uint32_t)(HC * SH) << sh;
 #pragma unroll 1
-        for (int i0 = 0; i0 < (F::kWarps > 8 ? nbox : 1); i0 += 32 * P) {
+        for (int i0 = 0; i0 < (kManyBoxes ? nbox : 1); i0 += 32 * P) {
           const int box_i = i0 + P * lane + part, tok = tok0 + (box_i << sh);
           const bool in = box_i < nbox && tok < tok0 + ntok;
           uint32_t pidx, in_page;
@@ -288,7 +290,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
               }
             }
             // lane by lane the rows of this warp's boxes
-            const int rounds = F::kWarps > 8 ? min((nbox - i0 + P - 1) / P, 32) << sh : Ts;
+            const int rounds = kManyBoxes ? min((nbox - i0 + P - 1) / P, 32) << sh : Ts;
             for (int r = 0; r < rounds; r += 32) {
               const int k = r + lane, j = (i0 + P * (k >> sh) + part) * a.box_rows + (k & (a.box_rows - 1));
               const int first_row = __shfl_sync(0xffffffffu, (int)row, (k >> sh) & 31);
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__((F::kWarps + 2 * F::kParts) * 32, 1) quant_dec
     const int p = warp - NC;  // K's and V's in turn
     const bool v = p & 1;
     quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, v && !F::kJoint ? full + NS : full,
-                                  v && !F::kJoint ? empty + NS : empty, v, p >> 1);
+                                  v && !F::kJoint ? empty + NS : empty, v, F::kParts == 1 ? 0 : p >> 1);
   } else {
     F::template consume<TMA>(a, stages, hdr, hdr_full, full, empty, meet_bar);
   }
@@ -629,7 +631,7 @@ bool make_plan(int B, int Hq, int Hkv, int ncta, QuantDecodePlan& p, int page_si
     if (Hkv % d == 0) p.HC = d;
   p.nhg = Hkv / p.HC;
   p.W = F::kWarps / (p.HC * p.NT);
-  p.Ts = kSlice * p.W;
+  p.Ts = F::kStep * p.W;
   const int RB = p.HC * F::kRowBytes;
   p.RS = F::kBoxedRows ? RB : F::row_stride(RB);
   p.R = page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 8;
