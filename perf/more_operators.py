@@ -442,7 +442,9 @@ def _own(s):
         pkv.compact_accepted(s["tensors"], s["kv_indptr"], s["kv_indices"], s["prefix_lens"], s["taken_indptr"],
                              s["taken"])
         return s["stacks"]
-    pool = (s["codes"][0], s["codes"][1], s["scales"][0], s["scales"][1])
+    if "pool" not in s:  # the cache's tensors, which a program holds
+        s["pool"] = (s["codes"][0], s["codes"][1], s["scales"][0], s["scales"][1])
+    pool = s["pool"]
     scales = dict(k_global=GLOBAL["k"], v_global=GLOBAL["v"])
     if op == "append4":
         out = {}
