@@ -60,19 +60,22 @@ struct Bits4 {
   // one per chunk
   static PKV_DEV int64_t scale_at(const GatherArgs& a, int64_t slot, uint32_t c) { return slot * a.cpr.d + c; }
   static PKV_DEV void store(uint4* to, uint2 u, uint8_t s8, float g) {
-    const float s = e4m3_value(s8);
-    const uint32_t w[2] = {u.x, u.y};
+    const uint32_t s = unpack_e4m3x2(s8 | s8 << 8);
+    uint32_t h[4], r[8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      uint32_t h[4], r[4];
-      unpack_e2m1x8(w[j], h);
+      unpack_e2m1x8(j ? u.y : u.x, h);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        r[i] = pack_bf16x2(f.x * s * g, f.y * s * g);  // f s is exact
+        const uint32_t v = mul_f16x2(h[i], s);  // exact
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        r[4 * j + i] = pack_bf16x2(f.x * g, f.y * g);
       }
-      to[j] = make_uint4(r[0], r[1], r[2], r[3]);
     }
+    // one store of 32 bytes: in two of 16, each instruction would fill half of every sector that it touches
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
   }
 };
 

@@ -3,6 +3,8 @@
 //
 // Nothing is computed: bytes move, in pieces of the largest power of two up to 16 that divides a tensor's bytes per
 // slot.  Bound by HBM for many pages, by latency for a few.
+#include <algorithm>
+
 #include "quant.cuh"
 
 namespace {
@@ -15,12 +17,12 @@ template <int N>
 struct Planes {
   void* base[N];
   uint32_t slot_bytes[N];
-  uint32_t first[N];  // of the plane's work items, counted from those of plane 0 (see each kernel)
+  uint32_t first[N];  // of the plane's tiles (chunks), counted from those of plane 0 (see each kernel)
   int32_t count;
 };
 constexpr int kFewPlanes = 8, kMaxPlanes = 256;
 
-// The plane of work item r: the last whose first item is not behind r.
+// The plane of tile (chunk) r: the last whose first is not behind r.
 template <int N>
 PKV_DEV int plane_of(const Planes<N>& p, uint32_t r) {
   int lo = 0, hi = p.count - 1;
@@ -98,9 +100,9 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------------------------
 // Compaction.  Row k of a request's accepted tokens moves from position prefix + accepted[k] to prefix + k.  With
 // accepted ascending, no row is written before it is read as long as rows are taken in order: what row k writes
-// (prefix + k) is not the source of a later row j (prefix + accepted[j], accepted[j] >= j > k).  A warp takes up to 32
-// pieces side by side of one request's rows in one tensor; of narrow rows it takes several at a time.  It reads a
-// group of rows, then writes it.
+// (prefix + k) is not the source of a later row j (prefix + accepted[j], accepted[j] >= j > k).  A warp takes a run of
+// chunks, 32 pieces side by side in one tensor, of one request's rows: it looks the rows' slots up once.  Of narrow rows it
+// takes several at a time.  It reads a group of rows, then writes it.
 // ---------------------------------------------------------------------------------------------
 template <int N>
 struct CompactArgs {
@@ -112,8 +114,9 @@ struct CompactArgs {
   const int32_t* accepted;
   int64_t num_pages;
   int32_t page_size, num_accepted;
-  FastDiv item_div;  // by the warps of a request in all tensors
+  FastDiv item_div;  // by the warps of a request
   FastDiv page_div;
+  uint32_t chunks, run;  // of a request in all tensors, and of a warp
   uint32_t items;
   uint32_t* err_word;
 };
@@ -135,7 +138,10 @@ PKV_DEV int64_t slot_at(const CompactArgs<N>& a, int32_t p0, int32_t np, int64_t
   return (int64_t)page * a.page_size + in_page;
 }
 
-// A warp's pieces `chunk` (32 side by side) of the n rows of lane l's (source, target) slots.
+// A warp's pieces `chunk` (32 side by side) of the n rows of lane l's (source, target) slots, kMoves pieces a lane in
+// flight.
+constexpr int kMoves = 4;
+
 template <typename V>
 PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, int64_t src, int64_t dst, int n) {
   const int lane = threadIdx.x & 31;
@@ -143,11 +149,12 @@ PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, int64_t 
   const int sh = 32 - __clz(cols - 1);  // lanes of a row: the power of two at or above cols
   const int col = lane & ((1 << sh) - 1), sub = lane >> sh, step = 32 >> sh;
   char* at = base + (32 * (int64_t)chunk + col) * sizeof(V);
-  for (int k0 = 0; k0 < n; k0 += step * kFlight) {
-    V v[kFlight];
-    int64_t to[kFlight];
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += step * kMoves) {
+    V v[kMoves];
+    int64_t to[kMoves];
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
+    for (int u = 0; u < kMoves; ++u) {
       const int k = k0 + u * step + sub;
       const int64_t s = __shfl_sync(0xffffffffu, src, k & 31), d = __shfl_sync(0xffffffffu, dst, k & 31);
       to[u] = k < n && col < cols && s >= 0 ? d : -1;
@@ -155,29 +162,29 @@ PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, int64_t 
     }
     __syncwarp();  // read by every lane before any writes
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u)
+    for (int u = 0; u < kMoves; ++u)
       if (to[u] >= 0) *reinterpret_cast<V*>(at + to[u] * slot_bytes) = v[u];
+    __syncwarp();  // a group's rows are written before the next group's are read
   }
 }
 
-template <int N>
-__global__ void __launch_bounds__(256) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
+// kWide: every tensor's bytes per slot are a multiple of 16.
+template <int N, bool kWide>
+__global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (item >= a.items) return;
-  uint32_t b, r;
-  a.item_div.divmod(item, b, r);
+  uint32_t b, part;
+  a.item_div.divmod(item, b, part);
   const int32_t i0 = ld(a.accepted_indptr + b), i1 = ld(a.accepted_indptr + b + 1), prefix = ld(a.prefix_lens + b);
   const int32_t p0 = ld(a.kv_indptr + b), np = ld(a.kv_indptr + b + 1) - p0;
   if (i0 < 0 || i1 > a.num_accepted || prefix < 0) {
-    if (r == 0 && lane == 0) report(a.err_word, prefix < 0 ? PKV_DEVERR_LENGTH : PKV_DEVERR_ROW_OOB);
+    if (part == 0 && lane == 0) report(a.err_word, prefix < 0 ? PKV_DEVERR_LENGTH : PKV_DEVERR_ROW_OOB);
     return;
   }
-  const int p = plane_of(a.planes, r);
-  const uint32_t chunk = r - a.planes.first[p], slot = a.planes.slot_bytes[p];
-  char* base = (char*)a.planes.base[p];
+  const uint32_t r0 = part * a.run, r1 = min(r0 + a.run, a.chunks);
   for (int k0 = 0; k0 < i1 - i0; k0 += 32) {
     const int k = k0 + lane, n = min(32, i1 - i0 - k0);
     int64_t src = -1, dst = -1;
@@ -189,14 +196,20 @@ __global__ void __launch_bounds__(256) compact_accepted_kernel(const __grid_cons
         dst = slot_at(a, p0, np, (int64_t)prefix + k, bad);
         if (dst < 0) src = -1;
       }
-      if (bad && r == 0) report(a.err_word, bad);
+      if (bad && part == 0) report(a.err_word, bad);
     }
-    if (slot % 16 == 0) move_rows<uint4>(base, slot, chunk, src, dst, n);
-    else if (slot % 8 == 0) move_rows<uint2>(base, slot, chunk, src, dst, n);
-    else if (slot % 4 == 0) move_rows<uint32_t>(base, slot, chunk, src, dst, n);
-    else if (slot % 2 == 0) move_rows<uint16_t>(base, slot, chunk, src, dst, n);
-    else move_rows<uint8_t>(base, slot, chunk, src, dst, n);
-    __syncwarp();  // a group's rows are written before the next group's are read
+    if (!__any_sync(0xffffffffu, src >= 0)) continue;
+    int p = plane_of(a.planes, r0);
+    for (uint32_t r = r0; r < r1; ++r) {
+      if (p + 1 < a.planes.count && a.planes.first[p + 1] <= r) ++p;
+      const uint32_t chunk = r - a.planes.first[p], slot = a.planes.slot_bytes[p];
+      char* base = (char*)a.planes.base[p];
+      if (kWide || slot % 16 == 0) move_rows<uint4>(base, slot, chunk, src, dst, n);
+      else if (slot % 8 == 0) move_rows<uint2>(base, slot, chunk, src, dst, n);
+      else if (slot % 4 == 0) move_rows<uint32_t>(base, slot, chunk, src, dst, n);
+      else if (slot % 2 == 0) move_rows<uint16_t>(base, slot, chunk, src, dst, n);
+      else move_rows<uint8_t>(base, slot, chunk, src, dst, n);
+    }
   }
 }
 
@@ -261,10 +274,14 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
                    const int32_t* accepted_indptr, const int32_t* accepted, int32_t num_accepted, uint32_t* err_word,
                    cudaStream_t st) {
   CompactArgs<N> a;
-  const int64_t warps = fill_planes(a.planes, planes, num_planes, [&](const pkv_plane& p) {
+  const int64_t chunks = fill_planes(a.planes, planes, num_planes, [&](const pkv_plane& p) {
     return (p.slot_bytes / piece_bytes(p.slot_bytes) + 31) / 32;
   });
-  if (warps < 0 || warps * batch > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (chunks < 0 || chunks * batch > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  // Longer runs once there are warps for all places of the GPU (32 an SM).
+  const int64_t most = (int64_t)std::max(1, pkv_host::sm_count()) * 32;
+  const int64_t run = std::min<int64_t>(16, std::max<int64_t>(1, chunks * batch / most));
+  const int64_t warps = (chunks + run - 1) / run;
   a.kv_indptr = kv_indptr;
   a.kv_indices = kv_indices;
   a.prefix_lens = prefix_lens;
@@ -275,9 +292,14 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
   a.num_accepted = num_accepted;
   a.item_div = FastDiv((uint32_t)warps);
   a.page_div = FastDiv((uint32_t)page_size);
+  a.chunks = (uint32_t)chunks;
+  a.run = (uint32_t)run;
   a.items = (uint32_t)(warps * batch);
   a.err_word = err_word;
-  return pkv_host::launch_after(compact_accepted_kernel<N>, dim3((a.items + 7) / 8), 256, 0, st, a);
+  bool wide = true;
+  for (int32_t i = 0; i < num_planes; ++i) wide = wide && planes[i].slot_bytes % 16 == 0;
+  return wide ? pkv_host::launch_after(compact_accepted_kernel<N, true>, dim3((a.items + 7) / 8), 256, 0, st, a)
+              : pkv_host::launch_after(compact_accepted_kernel<N, false>, dim3((a.items + 7) / 8), 256, 0, st, a);
 }
 
 }  // namespace

@@ -33,7 +33,9 @@ struct AppendArgs {
   void* v_pool;
   void* k_scale;
   void* v_scale;
-  float k_global, v_global;  // 4 bits: the caches' scales
+  float k_global, v_global;      // 4 bits: the caches' scales g,
+  float k_six, v_six;            // 6 g
+  float k_by_six, v_by_six;      // and 1 / (6 g)
   const __nv_bfloat16* k_new;
   const __nv_bfloat16* v_new;
   const __nv_bfloat16* q;
@@ -87,17 +89,29 @@ PKV_DEV uint2 quantise8(float (&x)[8], int k) {
   return make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
 }
 
-// The e4m3 scale of a 4-bit block from the bits of its largest |x| (NaN and infinities included).
-PKV_DEV uint8_t block_scale(uint32_t amax_bits, float g) {
-  if (amax_bits >= 0x7f800000u) return 0x7f;
-  return pack_e4m3(__fdiv_rn(__uint_as_float(amax_bits), 6.f * g));
+// The larger of m and |x|; NaN if either is.
+PKV_DEV float max_abs(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
 }
 
-PKV_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// x / d, correctly rounded where r = 1 / d is and nothing overflows or loses bits to underflow: a product with the reciprocal
+// and one correction by the remainder (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  x r alone is off the ties that x / d meets (1 / 1.875: 2.5 * 1.875 becomes 2.5000002).
+PKV_DEV float quotient(float x, float d, float r) {
+  const float y = x * r;
+  return fmaf(fmaf(-y, d, x), r, y);
+}
 
-// 8 values of a 4-bit block with scale s as codes: x / (s g), correctly rounded to fp32, then to e2m1.  The quotient
-// is x r with r = 1 / (s g) and one correction by its remainder (Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", 1990); x r alone is off the ties of e2m1 that x / (s g) meets (s = 1.875, x = 2.5 s).
+// The e4m3 scale of a 4-bit block: its largest |x| over 6 g (d, and r = 1 / d).
+PKV_DEV uint8_t block_scale(float amax, float d, float r) {
+  if (!(amax < INFINITY)) return 0x7f;
+  if (amax * r > 1024.f) return 0x7e;
+  return pack_e4m3(quotient(amax, d, r));  // below 2^-10, where bits can be lost, it is 0 either way
+}
+
+// 8 values of a 4-bit block with scale s as codes: x / (s g), rounded to fp32, then to e2m1.
 PKV_DEV uint32_t quantise_block8(float (&x)[8], uint8_t s, float g) {
   if (s == 0 || s == 0x7f) return 0u;
   const float step = e4m3_value(s) * g, r = __frcp_rn(step);
@@ -106,10 +120,7 @@ PKV_DEV uint32_t quantise_block8(float (&x)[8], uint8_t s, float g) {
     for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -7.f * step), 7.f * step);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float y = x[e] * r;
-    x[e] = fmaf(fmaf(-y, step, x[e]), r, y);
-  }
+  for (int e = 0; e < 8; ++e) x[e] = quotient(x[e], step, r);
   return pack_e2m1x8(x);
 }
 
@@ -236,20 +247,21 @@ __global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_consta
     if (FMT == kE2m1 && !is_q) {
       // A block is two chunks: the lane's own, or one of its and one of the next lane's.  (Half-split pairs: the
       // launch sees to an even number of chunks in each half, so that both chunks have their partners in lane u ^ 1.)
-      uint32_t m0 = 0, m1 = 0;
+      float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m0 = max(m0, abs_bits(x0[e])), m1 = max(m1, abs_bits(x1[e]));
+      for (int e = 0; e < 8; ++e) m0 = max_abs(m0, x0[e]), m1 = max_abs(m1, x1[e]);
       if constexpr (ROT == kHalf) {
-        const uint32_t n0 = __shfl_xor_sync(mask, m0, 1), n1 = __shfl_xor_sync(mask, m1, 1);
-        const uint32_t both = max(m0, m1);
-        m0 = paired ? max(m0, n0) : both;
-        m1 = paired ? max(m1, n1) : both;
+        const float n0 = __shfl_xor_sync(mask, m0, 1), n1 = __shfl_xor_sync(mask, m1, 1);
+        const float both = max_abs(m0, m1);
+        m0 = paired ? max_abs(m0, n0) : both;
+        m1 = paired ? max_abs(m1, n1) : both;
       } else {
-        m0 = m1 = max(m0, m1);
+        m0 = m1 = max_abs(m0, m1);
       }
       const int64_t dst = slot * a.Hkv + r.head;
-      const float glob = r.kind == 1 ? a.v_global : a.k_global;
-      const uint8_t s0 = block_scale(m0, glob), s1 = block_scale(m1, glob);
+      const bool is_v = r.kind == 1;
+      const float glob = is_v ? a.v_global : a.k_global, six = is_v ? a.v_six : a.k_six, by = is_v ? a.v_by_six : a.k_by_six;
+      const uint8_t s0 = block_scale(m0, six, by), s1 = ROT == kHalf ? block_scale(m1, six, by) : s0;
       const uint32_t p0 = quantise_block8(x0, s0, glob), p1 = quantise_block8(x1, s1, glob);
       uint8_t* out = (uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * (a.D / 2);
       uint8_t* scale = (uint8_t*)(r.kind == 1 ? a.v_scale : a.k_scale) + dst * (a.D / 16);
@@ -322,13 +334,14 @@ __global__ void __launch_bounds__(256) append_any_width_kernel(const __grid_cons
   }
   __syncwarp(mask);  // q may be rotated in place: every lane of the row has read its partners
   if (FMT == kE2m1 && !is_q) {
-    uint32_t m = 0;
+    float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
-    m = max(m, __shfl_xor_sync(mask, m, 1));  // a block is the chunks of two lanes
+    for (int e = 0; e < 8; ++e) m = max_abs(m, x[e]);
+    m = max_abs(m, __shfl_xor_sync(mask, m, 1));  // a block is the chunks of two lanes
     const int64_t dst = slot * a.Hkv + r.head;
-    const float glob = r.kind == 1 ? a.v_global : a.k_global;
-    const uint8_t s = block_scale(m, glob);
+    const bool is_v = r.kind == 1;
+    const float glob = is_v ? a.v_global : a.k_global;
+    const uint8_t s = block_scale(m, is_v ? a.v_six : a.k_six, is_v ? a.v_by_six : a.k_by_six);
     const uint32_t p = quantise_block8(x, s, glob);
     if (has) *reinterpret_cast<uint32_t*>((uint8_t*)(r.kind == 1 ? a.v_pool : a.k_pool) + dst * (a.D / 2) + 4 * c) = p;
     if (has && !(c & 1)) ((uint8_t*)(r.kind == 1 ? a.v_scale : a.k_scale))[dst * (a.D / 16) + c / 2] = s;
@@ -451,6 +464,15 @@ void set_pool(AppendArgs& a, const Pool* p) {
   a.D = p->head_dim;
 }
 
+void set_globals(AppendArgs& a, const pkv_pool_fp4* p) {
+  a.k_global = p->k_global;
+  a.v_global = p->v_global;
+  a.k_six = 6.f * p->k_global;
+  a.v_six = 6.f * p->v_global;
+  a.k_by_six = 1.f / a.k_six;
+  a.v_by_six = 1.f / a.v_six;
+}
+
 }  // namespace
 
 extern "C" {
@@ -505,8 +527,7 @@ pkv_status pkv_rotary_kv_append_fp4(const pkv_pool_fp4* pool, const void* k_new,
   AppendArgs a = rotary_args(k_new, v_new, slot_mapping, positions, cos_sin, max_position, rotary_dim,
                              interleaved, q, q_out, num_q_heads, num_tokens, err_word);
   set_pool(a, pool);
-  a.k_global = pool->k_global;
-  a.v_global = pool->v_global;
+  set_globals(a, pool);
   return append_rows<kE2m1>(a, pool->num_pages, pool->page_size, true, (cudaStream_t)stream);
 }
 
@@ -518,8 +539,7 @@ pkv_status pkv_kv_append_fp4(const pkv_pool_fp4* pool, const void* k_new, const 
   AppendArgs a = rotary_args(k_new, v_new, slot_mapping, nullptr, nullptr, 0, 0, 0, nullptr, nullptr, 0,
                              num_tokens, err_word);
   set_pool(a, pool);
-  a.k_global = pool->k_global;
-  a.v_global = pool->v_global;
+  set_globals(a, pool);
   return append_rows<kE2m1>(a, pool->num_pages, pool->page_size, false, (cudaStream_t)stream);
 }
 
