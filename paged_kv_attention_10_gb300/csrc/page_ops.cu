@@ -139,11 +139,11 @@ PKV_DEV int64_t slot_at(const CompactArgs<N>& a, int32_t p0, int32_t np, int64_t
 }
 
 // A warp's pieces `chunk` (32 side by side) of the n rows of lane l's (source, target) slots, kMoves pieces a lane in
-// flight.
+// flight: four, with four blocks an SM, since more spill (64 trees of 16 in 36 layers: eight 22.6 us, four 18.5).
 constexpr int kMoves = 4;
 
-template <typename V>
-PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, int64_t src, int64_t dst, int n) {
+template <typename V, typename Slot>
+PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, Slot src, Slot dst, int n) {
   const int lane = threadIdx.x & 31;
   const int cols = min(32, (int)(slot_bytes / sizeof(V)) - 32 * (int)chunk);
   const int sh = 32 - __clz(cols - 1);  // lanes of a row: the power of two at or above cols
@@ -152,23 +152,27 @@ PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, int64_t 
 #pragma unroll 1
   for (int k0 = 0; k0 < n; k0 += step * kMoves) {
     V v[kMoves];
-    int64_t to[kMoves];
+    uint32_t on = 0;
 #pragma unroll
     for (int u = 0; u < kMoves; ++u) {
       const int k = k0 + u * step + sub;
-      const int64_t s = __shfl_sync(0xffffffffu, src, k & 31), d = __shfl_sync(0xffffffffu, dst, k & 31);
-      to[u] = k < n && col < cols && s >= 0 ? d : -1;
-      if (to[u] >= 0) v[u] = ld(reinterpret_cast<const V*>(at + s * slot_bytes));
+      const Slot s = __shfl_sync(0xffffffffu, src, k & 31);
+      if (k < n && col < cols && s >= 0) {
+        v[u] = ld(reinterpret_cast<const V*>(at + (int64_t)s * slot_bytes));
+        on |= 1u << u;
+      }
     }
     __syncwarp();  // read by every lane before any writes
 #pragma unroll
-    for (int u = 0; u < kMoves; ++u)
-      if (to[u] >= 0) *reinterpret_cast<V*>(at + to[u] * slot_bytes) = v[u];
+    for (int u = 0; u < kMoves; ++u) {
+      const Slot d = __shfl_sync(0xffffffffu, dst, (k0 + u * step + sub) & 31);
+      if (on >> u & 1) *reinterpret_cast<V*>(at + (int64_t)d * slot_bytes) = v[u];
+    }
     __syncwarp();  // a group's rows are written before the next group's are read
   }
 }
 
-// kWide: every tensor's bytes per slot are a multiple of 16.
+// kWide: every tensor's bytes per slot are a multiple of 16, and slots have 31-bit numbers.
 template <int N, bool kWide>
 __global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
   pdl_trigger();
@@ -204,7 +208,8 @@ __global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(co
       if (p + 1 < a.planes.count && a.planes.first[p + 1] <= r) ++p;
       const uint32_t chunk = r - a.planes.first[p], slot = a.planes.slot_bytes[p];
       char* base = (char*)a.planes.base[p];
-      if (kWide || slot % 16 == 0) move_rows<uint4>(base, slot, chunk, src, dst, n);
+      if constexpr (kWide) move_rows<uint4, int32_t>(base, slot, chunk, (int32_t)src, (int32_t)dst, n);
+      else if (slot % 16 == 0) move_rows<uint4>(base, slot, chunk, src, dst, n);
       else if (slot % 8 == 0) move_rows<uint2>(base, slot, chunk, src, dst, n);
       else if (slot % 4 == 0) move_rows<uint32_t>(base, slot, chunk, src, dst, n);
       else if (slot % 2 == 0) move_rows<uint16_t>(base, slot, chunk, src, dst, n);
@@ -278,9 +283,9 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
     return (p.slot_bytes / piece_bytes(p.slot_bytes) + 31) / 32;
   });
   if (chunks < 0 || chunks * batch > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  // Longer runs once there are warps for all places of the GPU (32 an SM).
-  const int64_t most = (int64_t)std::max(1, pkv_host::sm_count()) * 32;
-  const int64_t run = std::min<int64_t>(16, std::max<int64_t>(1, chunks * batch / most));
+  // Runs of two chunks once there are more than warps for all places of the GPU, 32 an SM (64 trees in 36 layers: one
+  // 18.7 us, two 17.5, four 18.5).
+  const int64_t run = chunks * batch > (int64_t)pkv_host::sm_count() * 32 ? 2 : 1;
   const int64_t warps = (chunks + run - 1) / run;
   a.kv_indptr = kv_indptr;
   a.kv_indices = kv_indices;
@@ -296,7 +301,7 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
   a.run = (uint32_t)run;
   a.items = (uint32_t)(warps * batch);
   a.err_word = err_word;
-  bool wide = true;
+  bool wide = num_pages * page_size <= 0x7fffffffLL;
   for (int32_t i = 0; i < num_planes; ++i) wide = wide && planes[i].slot_bytes % 16 == 0;
   return wide ? pkv_host::launch_after(compact_accepted_kernel<N, true>, dim3((a.items + 7) / 8), 256, 0, st, a)
               : pkv_host::launch_after(compact_accepted_kernel<N, false>, dim3((a.items + 7) / 8), 256, 0, st, a);

@@ -154,13 +154,15 @@ PKV_DEV bool slot_ok(const AppendArgs& a, int64_t slot, bool reporter) {
 // Steps and blocks per SM, measured on 8191 tokens of 32/8 heads at D 128, R 64 (and quantising 2304 with
 // R 128): 2 steps and 4 blocks 39.0 us (15.3), 4 and 3 39.5 (16.8), 4 and 2 41.1 (17.3), 1 and 4 46.0
 // (17.1); more blocks spill.  All of these before the kernel started beside the one before it, with which the
-// chosen setting takes 35.9 us (12.2).  A device copy of the same bytes takes 37.1 us (16.5).
+// chosen setting takes 35.9 us (12.2).  A device copy of the same bytes takes 37.1 us (16.5).  The 4-bit write without a
+// rotation fits five blocks (8191 tokens of eight heads: 13.1 us with four, 12.2).
 constexpr int kSteps = 2;
+constexpr int blocks_of(int format, int rotation) { return format == kE2m1 && rotation == kNone ? 5 : 4; }
 
 // L lanes hold a row (the power of two at or above its units of two chunks); a warp takes kSteps
 // times 32 / L rows of one token.
 template <int FMT, int ROT, int L>
-__global__ void __launch_bounds__(256, 4) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(256, blocks_of(FMT, ROT)) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kRows = 32 / L;
   pdl_trigger();
   pdl_wait();
