@@ -551,7 +551,8 @@ typedef struct {
   void* k;              /* codes [num_pages, page_size, num_kv_heads, head_dim / 2], 16-byte aligned: byte j of a head's row
                            holds value 2j in its low four bits and 2j + 1 in its high ones */
   void* v;              /* same shape as k */
-  void* k_scale;        /* e4m3 [num_pages, page_size, num_kv_heads, head_dim / 16], 16-byte aligned */
+  void* k_scale;        /* e4m3 [num_pages, page_size, num_kv_heads, head_dim / 16]; the attention wants 4-byte alignment, and is
+                           faster with 16 */
   void* v_scale;        /* same shape as k_scale */
   int64_t num_pages;
   int32_t page_size;    /* >= 1 */
@@ -603,7 +604,7 @@ pkv_status pkv_paged_decode_fp4(const pkv_pool_fp4* pool, const void* q, int32_t
  * a slot (a bf16 K: num_kv_heads * head_dim * 2).  At most 256 tensors a call.
  */
 typedef struct {
-  void* base;         /* device, 16-byte aligned */
+  void* base;         /* device; with base and slot_bytes multiples of 16 its bytes move fastest */
   int64_t slot_bytes; /* > 0 */
 } pkv_plane;
 

@@ -59,7 +59,7 @@ bool valid_pool4(const pkv_pool_fp4* p) {
   if ((p->head_dim % 16) != 0) return false;
   for (const float g : {p->k_global, p->v_global})  // with a block's scale 2^-9 .. 448 all products stay normal numbers
     if (!(g >= 0x1p-64f && g <= 0x1p64f)) return false;
-  return aligned16(p->k) && aligned16(p->v) && aligned16(p->k_scale) && aligned16(p->v_scale);
+  return aligned16(p->k) && aligned16(p->v);  // of the scales each kernel takes the pieces that their places allow
 }
 
 namespace {

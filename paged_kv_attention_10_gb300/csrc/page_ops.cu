@@ -1,8 +1,8 @@
 // Movements of rows within a paged cache of any format, in many tensors (the K, V and scale tensors of all layers) at
 // once: copies of whole or begun pages, and the accepted tokens of drafted trees moved behind their prefix.
 //
-// Nothing is computed: bytes move, in pieces of the largest power of two up to 16 that divides a tensor's bytes per
-// slot.  Bound by HBM for many pages, by latency for a few.
+// Nothing is computed: bytes move, in pieces of the largest power of two up to 16 that divides a tensor's address and its
+// bytes per slot.  Bound by HBM for many pages, by latency for a few.
 #include <algorithm>
 
 #include "quant.cuh"
@@ -17,6 +17,7 @@ template <int N>
 struct Planes {
   void* base[N];
   uint32_t slot_bytes[N];
+  uint8_t piece[N];   // bytes of a lane's copy
   uint32_t first[N];  // of the plane's tiles (chunks), counted from those of plane 0 (see each kernel)
   int32_t count;
 };
@@ -90,11 +91,13 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
   const int64_t page = (int64_t)slot * a.page_size;
   const char* from = (const char*)a.planes.base[p] + src * page;
   char* to = (char*)a.planes.base[p] + dst * page;
-  if (slot % 16 == 0) copy_tile<uint4>(from, to, bytes, tile);
-  else if (slot % 8 == 0) copy_tile<uint2>(from, to, bytes, tile);
-  else if (slot % 4 == 0) copy_tile<uint32_t>(from, to, bytes, tile);
-  else if (slot % 2 == 0) copy_tile<uint16_t>(from, to, bytes, tile);
-  else copy_tile<uint8_t>(from, to, bytes, tile);
+  switch (a.planes.piece[p]) {
+    case 16: copy_tile<uint4>(from, to, bytes, tile); break;
+    case 8: copy_tile<uint2>(from, to, bytes, tile); break;
+    case 4: copy_tile<uint32_t>(from, to, bytes, tile); break;
+    case 2: copy_tile<uint16_t>(from, to, bytes, tile); break;
+    default: copy_tile<uint8_t>(from, to, bytes, tile);
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -172,7 +175,7 @@ PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, Slot src
   }
 }
 
-// kWide: every tensor's bytes per slot are a multiple of 16, and slots have 31-bit numbers.
+// kWide: every tensor moves in pieces of 16 bytes, and slots have 31-bit numbers.
 template <int N, bool kWide>
 __global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
   pdl_trigger();
@@ -208,12 +211,17 @@ __global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(co
       if (p + 1 < a.planes.count && a.planes.first[p + 1] <= r) ++p;
       const uint32_t chunk = r - a.planes.first[p], slot = a.planes.slot_bytes[p];
       char* base = (char*)a.planes.base[p];
-      if constexpr (kWide) move_rows<uint4, int32_t>(base, slot, chunk, (int32_t)src, (int32_t)dst, n);
-      else if (slot % 16 == 0) move_rows<uint4>(base, slot, chunk, src, dst, n);
-      else if (slot % 8 == 0) move_rows<uint2>(base, slot, chunk, src, dst, n);
-      else if (slot % 4 == 0) move_rows<uint32_t>(base, slot, chunk, src, dst, n);
-      else if (slot % 2 == 0) move_rows<uint16_t>(base, slot, chunk, src, dst, n);
-      else move_rows<uint8_t>(base, slot, chunk, src, dst, n);
+      if constexpr (kWide) {
+        move_rows<uint4, int32_t>(base, slot, chunk, (int32_t)src, (int32_t)dst, n);
+      } else {
+        switch (a.planes.piece[p]) {
+          case 16: move_rows<uint4>(base, slot, chunk, src, dst, n); break;
+          case 8: move_rows<uint2>(base, slot, chunk, src, dst, n); break;
+          case 4: move_rows<uint32_t>(base, slot, chunk, src, dst, n); break;
+          case 2: move_rows<uint16_t>(base, slot, chunk, src, dst, n); break;
+          default: move_rows<uint8_t>(base, slot, chunk, src, dst, n);
+        }
+      }
     }
   }
 }
@@ -221,16 +229,16 @@ __global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(co
 // ---------------------------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------------------------
-uint32_t piece_bytes(int64_t slot_bytes) {
+uint32_t piece_bytes(const pkv_plane& p) {
   uint32_t v = 16;
-  while (slot_bytes % v) v >>= 1;
+  while (((uintptr_t)p.base | (uintptr_t)p.slot_bytes) % v) v >>= 1;
   return v;
 }
 
 pkv_status check_planes(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size) {
   if (num_planes < 0 || num_pages <= 0 || page_size <= 0 || (num_planes > 0 && !planes)) return PKV_ERR_INVALID_ARG;
   for (int32_t i = 0; i < num_planes; ++i) {
-    if (!planes[i].base || planes[i].slot_bytes <= 0 || !pkv_host::aligned16(planes[i].base)) return PKV_ERR_INVALID_ARG;
+    if (!planes[i].base || planes[i].slot_bytes <= 0) return PKV_ERR_INVALID_ARG;
     // 31-bit numbers of the bytes and pieces of a page
     if (planes[i].slot_bytes > 0x7fffffff / page_size) return PKV_ERR_UNSUPPORTED;
   }
@@ -245,6 +253,7 @@ int64_t fill_planes(Planes<N>& to, const pkv_plane* planes, int32_t num_planes, 
   for (int32_t i = 0; i < num_planes; ++i) {
     to.base[i] = planes[i].base;
     to.slot_bytes[i] = (uint32_t)planes[i].slot_bytes;
+    to.piece[i] = (uint8_t)piece_bytes(planes[i]);
     to.first[i] = (uint32_t)sum;
     sum += items(planes[i]);
     if (sum > 0x7fffffffLL) return -1;
@@ -258,7 +267,7 @@ pkv_status copy_pages(const pkv_plane* planes, int32_t num_planes, int64_t num_p
                       uint32_t* err_word, cudaStream_t st) {
   CopyArgs<N> a;
   const int64_t tiles = fill_planes(a.planes, planes, num_planes, [&](const pkv_plane& p) {
-    const int64_t tile = 32 * kFlight * piece_bytes(p.slot_bytes);
+    const int64_t tile = 32 * kFlight * piece_bytes(p);
     return (p.slot_bytes * page_size + tile - 1) / tile;
   });
   if (tiles < 0 || tiles * num_copies > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
@@ -280,7 +289,7 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
                    cudaStream_t st) {
   CompactArgs<N> a;
   const int64_t chunks = fill_planes(a.planes, planes, num_planes, [&](const pkv_plane& p) {
-    return (p.slot_bytes / piece_bytes(p.slot_bytes) + 31) / 32;
+    return (p.slot_bytes / piece_bytes(p) + 31) / 32;
   });
   if (chunks < 0 || chunks * batch > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   // Runs of two chunks once there are more than warps for all places of the GPU, 32 an SM (64 trees in 36 layers: one
@@ -302,7 +311,7 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
   a.items = (uint32_t)(warps * batch);
   a.err_word = err_word;
   bool wide = num_pages * page_size <= 0x7fffffffLL;
-  for (int32_t i = 0; i < num_planes; ++i) wide = wide && planes[i].slot_bytes % 16 == 0;
+  for (int32_t i = 0; i < num_planes; ++i) wide = wide && a.planes.piece[i] == 16;
   return wide ? pkv_host::launch_after(compact_accepted_kernel<N, true>, dim3((a.items + 7) / 8), 256, 0, st, a)
               : pkv_host::launch_after(compact_accepted_kernel<N, false>, dim3((a.items + 7) / 8), 256, 0, st, a);
 }

@@ -132,5 +132,5 @@ struct FastDiv {
 
 namespace pkv_host {
 bool valid_pool8(const pkv_pool_fp8* p);  // non-null, positive sizes, head_dim % 8 == 0, 16-byte aligned
-bool valid_pool4(const pkv_pool_fp4* p);  // the same with head_dim % 16 == 0 and cache scales within 2^-64 .. 2^64
+bool valid_pool4(const pkv_pool_fp4* p);  // the same with head_dim % 16 == 0, scales anywhere, cache scales within 2^-64 .. 2^64
 }  // namespace pkv_host

@@ -66,7 +66,8 @@ struct QuantDecodeArgs {
   int32_t box_rows;      // TMA instance: rows of a box (32, 16 or 8)
   int32_t row_stride;    // row-copy instance: shared-memory bytes per token row
   FastDiv piece_div;     // boxed rows: by the 16-byte pieces of a row of HC heads
-  int32_t scale_piece;   // ... bytes of one copy of scales: 16, 8 or 4
+  int32_t scale_piece;   // bytes of one copy of a row's scales by a lane: 16, 8 or 4
+  int32_t scales_at_16;  // whether k_scale and v_scale are 16-byte aligned, and so the scales of every box
   int32_t parts;         // producer warps each for K and V
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // kStep * W
@@ -109,6 +110,40 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Copies of 32 rows of PIECES 16-byte pieces, HC heads of RH bytes (a power of two of them), and their scales, into the
+// places of a box of 32 rows, [head][row] with swizzled pieces, and [row][head].  Lane t has row t's first piece's number in
+// the pool in `from` (~0: no row).  Neighbouring lanes copy neighbouring pieces; everything but the row's address is fixed
+// when the loop is unrolled (with the general loop below, 64 requests of 1000 to 6000 positions of 32/8 heads of 128 at
+// page size 1 took 96 us, 69 so).
+template <int RH, int PIECES>
+PKV_DEV void copy_round(uint32_t from, const uint8_t* pool, const uint8_t* scale, uint32_t to, uint32_t sto) {
+  constexpr int HP = RH / 16, kStep = 32 / PIECES;  // pieces of a head, rows of a round of copies
+  const uint32_t lane = threadIdx.x & 31, ch = lane % PIECES, t0 = lane / PIECES, pc = ch % HP;
+  const uint8_t* src = pool + ch * 16;
+  const uint32_t at = to + ch / HP * (32 * RH) + t0 * RH;
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) {
+    const uint32_t t = t0 + k * kStep;
+    const uint32_t f = __shfl_sync(0xffffffffu, from, t);
+    const uint32_t swz = RH == 64 ? pc ^ ((t >> 1) & 3) : pc ^ ((t >> 2) & 1);
+    if (f != ~0u) cp_async16(at + k * kStep * RH + swz * 16, src + (uint64_t)f * 16);
+  }
+  constexpr int kScales = 2 * PIECES, kPiece = kScales < 16 ? kScales : 16, kCount = kScales / kPiece;  // bytes of a row's
+  const uint32_t sch = lane % kCount * kPiece, s0 = lane / kCount;
+#pragma unroll
+  for (int k = 0; k < kCount; ++k) {
+    const uint32_t t = s0 + k * (32 / kCount);
+    const uint32_t f = __shfl_sync(0xffffffffu, from, t);
+    const uint32_t sd = sto + t * kScales + sch;
+    const uint8_t* sp = scale + (uint64_t)f * 2 + sch;  // a piece of 32 codes has two scales
+    if (f != ~0u) {
+      if (kPiece == 16) cp_async16(sd, sp);
+      else if (kPiece == 8) cp_async8(sd, sp);
+      else cp_async4(sd, sp);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -236,14 +271,19 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         }
         return (int64_t)page * a.page_size + in_page;
       };
-      auto copy_scales = [&](int64_t row, int j) {  // token j's scales of HC heads, in pieces of up to 16 bytes
+      auto copy_piece = [&](uint32_t to, const uint8_t* from) {  // of scales
+        if (a.scale_piece == 16) cp_async16(to, from);
+        else if (a.scale_piece == 8) cp_async8(to, from);
+        else cp_async4(to, from);
+      };
+      auto copy_scales = [&](int64_t row, int j) {  // token j's scales of HC heads
         const int n = HC * SH;
         const uint8_t* src = scale + (row * a.num_kv_heads + hg * HC) * SH;
         const uint32_t sd = smem_u32(sdst) + (uint32_t)(j * n);
-        if ((n & 15) == 0) {
+        if (F::kParts > 1) {
+          for (int i = 0; i < n; i += a.scale_piece) copy_piece(sd + i, src + i);
+        } else if ((n & 15) == 0) {
           for (int i = 0; i < n; i += 16) cp_async16(sd + i, src + i);
-        } else if (SH == 8) {
-          for (int i = 0; i < n; i += 8) cp_async8(sd + i, src + i);
         } else {
           for (int i = 0; i < n; i += 4) cp_async4(sd + i, src + i);
         }
@@ -256,7 +296,8 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         const int sh = 31 - __clz(a.box_rows), nbox = Ts >> sh;
         // Side by side, and enough of them for a bulk copy, which costs about 65 cycles of the copy unit whatever it
         // brings (4 bits, one head of 128 at page size 16, 720000 positions: 42 us with 128-byte copies of them).
-        const bool side_by_side = nhg == 1 && (F::kParts == 1 || (HC * SH << (31 - __clz(a.box_rows))) >= 512);
+        const bool side_by_side =
+            nhg == 1 && (F::kParts == 1 || (a.scales_at_16 && (HC * SH << (31 - __clz(a.box_rows))) >= 512));
         const uint32_t box = (uint32_t)(HC * RH) << sh, sbox = (uint32_t)(HC * SH) << sh;
 #pragma unroll 1
         for (int i0 = 0; i0 < (kManyBoxes ? nbox : 1); i0 += 32 * P) {
@@ -274,20 +315,18 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
             if (side_by_side) bulk_g2s(sdst + box_i * sbox, scale + row * a.num_kv_heads * SH, sbox, bar);
           }
           if (!side_by_side) {
-            if (F::kParts > 1 && nhg == 1) {  // 16 bytes a lane of this warp's boxes' scales
-              const int psh = 27 - __clz(sbox);  // sbox is 16 times a power of two, or HC is not: see below
-              if ((sbox & (sbox - 1)) == 0) {
-                const int mine = min((nbox - i0 + P - 1) / P, 32);
-                for (int r = 0; r < mine << psh; r += 32) {
-                  const int k = r + lane, bi = k >> psh;
-                  const int first_row = __shfl_sync(0xffffffffu, (int)row, bi & 31);
-                  const uint32_t off = (uint32_t)(k & ((1 << psh) - 1)) * 16;
-                  if (bi < mine && first_row >= 0)
-                    cp_async16(smem_u32(sdst) + (i0 + P * bi + part) * sbox + off,
-                               scale + (int64_t)first_row * a.num_kv_heads * SH + off);
-                }
-                continue;
+            if (F::kParts > 1 && nhg == 1 && a.scales_at_16 && (sbox & (sbox - 1)) == 0) {
+              // 16 bytes a lane of this warp's boxes' scales
+              const int psh = 27 - __clz(sbox), mine = min((nbox - i0 + P - 1) / P, 32);
+              for (int r = 0; r < mine << psh; r += 32) {
+                const int k = r + lane, bi = k >> psh;
+                const int first_row = __shfl_sync(0xffffffffu, (int)row, bi & 31);
+                const uint32_t off = (uint32_t)(k & ((1 << psh) - 1)) * 16;
+                if (bi < mine && first_row >= 0)
+                  cp_async16(smem_u32(sdst) + (i0 + P * bi + part) * sbox + off,
+                             scale + (int64_t)first_row * a.num_kv_heads * SH + off);
               }
+              continue;
             }
             // lane by lane the rows of this warp's boxes
             const int rounds = kManyBoxes ? min((nbox - i0 + P - 1) / P, 32) << sh : Ts;
@@ -300,7 +339,6 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         }
       } else if constexpr (F::kBoxedRows) {
         // Single rows, 16 bytes a lane, into the places that a box of 32 rows has: [slice][head][row], pieces swizzled.
-        // Rows lie together in shared memory by head, so a warp's 32 pieces come from as few rows as hold them.
         constexpr int HP = RH / 16;  // pieces of a head's row
         if (flags & kSegFirst) {
           ahead_tok = tok0;
@@ -308,6 +346,9 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           p0 = ahead_page(), p1 = ahead_page(), p2 = ahead_page(), p3 = ahead_page();
         }
         const int pieces = HC * HP, spieces = HC * SH / a.scale_piece;
+        // a power of two, and the scales' place allows the pieces that copy_round takes
+        const bool native = (pieces & (pieces - 1)) == 0 && a.scale_piece == min(2 * pieces, 16);
+        const bool narrow = a.num_pages * a.page_size * (int64_t)(a.num_kv_heads * HP) < 0xffffffffLL;  // 32-bit piece numbers
 #pragma unroll 1
         for (int r = part; r < W; r += P) {
           const int j = lane + 32 * r;
@@ -317,30 +358,33 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           const int32_t page = p0;
           p0 = p1, p1 = p2, p2 = p3, p3 = ahead_page();
           const int64_t row = row_at(pidx, in_page, page, in);
-          const int64_t from = row * a.num_kv_heads + hg * HC;  // in heads; negative where there is no row
+          const int64_t from = row < 0 ? -1 : row * a.num_kv_heads + hg * HC;  // in heads
           const uint32_t to = smem_u32(dst) + (uint32_t)(r * HC * 32) * RH;
           const uint32_t sto = smem_u32(sdst) + (uint32_t)(r * 32 * HC) * SH;
-          const int rows = min(32, ntok - 32 * r);
+          if (narrow && native) {
+            const uint32_t f = row < 0 ? ~0u : (uint32_t)(from * HP);
+            switch (pieces) {
+              case 2: copy_round<RH, 2>(f, pool, scale, to, sto); break;
+              case 4: copy_round<RH, 4>(f, pool, scale, to, sto); break;
+              case 8: copy_round<RH, 8>(f, pool, scale, to, sto); break;
+              case 16: copy_round<RH, 16>(f, pool, scale, to, sto); break;
+              default: copy_round<RH, 32>(f, pool, scale, to, sto);
+            }
+          } else {
 #pragma unroll 4
-          for (int it = lane; it < 32 * pieces; it += 32) {
-            uint32_t t, ch;
-            pieces_div.divmod((uint32_t)it, t, ch);
-            const int64_t src = __shfl_sync(0xffffffffu, from, t & 31);
-            const uint32_t hd = ch / HP, pc = ch % HP;
-            const uint32_t swz = RH == 64 ? pc ^ ((t >> 1) & 3) : pc ^ ((t >> 2) & 1);
-            if ((int)t < rows && src >= 0)
-              cp_async16(to + (hd * 32 + t) * RH + swz * 16, pool + src * RH + ch * 16);
-          }
+            for (int it = lane; it < 32 * pieces; it += 32) {
+              uint32_t t, ch;
+              pieces_div.divmod((uint32_t)it, t, ch);
+              const int64_t f = __shfl_sync(0xffffffffu, from, t);
+              const uint32_t hd = ch / HP, pc = ch % HP;
+              const uint32_t swz = RH == 64 ? pc ^ ((t >> 1) & 3) : pc ^ ((t >> 2) & 1);
+              if (f >= 0) cp_async16(to + (hd * 32 + t) * RH + swz * 16, pool + f * RH + ch * 16);
+            }
 #pragma unroll 1
-          for (int it = lane; it < 32 * spieces; it += 32) {
-            const uint32_t t = (uint32_t)it / (uint32_t)spieces, ch = (uint32_t)it % (uint32_t)spieces;
-            const int64_t src = __shfl_sync(0xffffffffu, from, t & 31);
-            if ((int)t < rows && src >= 0) {
-              const uint32_t sd = sto + t * HC * SH + ch * a.scale_piece;
-              const uint8_t* sp = scale + src * SH + ch * a.scale_piece;
-              if (a.scale_piece == 16) cp_async16(sd, sp);
-              else if (a.scale_piece == 8) cp_async8(sd, sp);
-              else cp_async4(sd, sp);
+            for (int it = lane; it < 32 * spieces; it += 32) {
+              const uint32_t t = (uint32_t)it / (uint32_t)spieces, ch = (uint32_t)it % (uint32_t)spieces;
+              const int64_t f = __shfl_sync(0xffffffffu, from, t);
+              if (f >= 0) copy_piece(sto + t * HC * SH + ch * a.scale_piece, scale + f * SH + ch * a.scale_piece);
             }
           }
         }
@@ -757,8 +801,12 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   // One warp each issues a few boxes and their scales in time, and more warps' walks would take issue slots from the
   // consumers (4 bits, 256 requests of 32/8 heads: 140 us with one, 144 with two; copied row by row, 48/16 heads of 64: 47, 40).
   a.parts = F::kParts == 1 || (p.tma && p.Ts / p.R <= 4 && p.nhg == 1) ? 1 : F::kParts;
-  const int scales = p.HC * F::kScaleBytes;
-  a.scale_piece = scales % 16 == 0 ? 16 : scales % 8 == 0 ? 8 : 4;
+  // a piece divides a row's scales and the addresses of all of them
+  const uintptr_t places = (uintptr_t)pool->k_scale | (uintptr_t)pool->v_scale;
+  const uintptr_t pieces = places | (uintptr_t)(p.HC * F::kScaleBytes);
+  if (pieces & 3) return PKV_ERR_INVALID_ARG;
+  a.scale_piece = pieces % 16 == 0 ? 16 : pieces % 8 == 0 ? 8 : 4;
+  a.scales_at_16 = places % 16 == 0;
   if (!p.tma && F::kBoxedRows) p.R = a.box_rows = kSlice;
   const bool boxed = p.tma || F::kBoxedRows;
   a.eight = boxed ? (uint32_t)(8 * F::kRowBytes * (p.R == 8 ? p.HC : 1)) : (uint32_t)(8 * p.RS);

@@ -238,6 +238,25 @@ def test_deterministic_and_on_another_stream(lib):
         assert torch.equal(o2, out) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("shape", [((100, 31), 8, 1, 64, 1), ((100, 700), 8, 2, 128, 16), ((100, 700), 32, 8, 128, 16),
+                                   ((100, 700), 33, 11, 128, 16), ((90, 250), 9, 3, 64, 5)], ids=str)
+@pytest.mark.parametrize("shift", [4, 8, 12])
+def test_scales_at_any_four_bytes(lib, shape, shift):
+    lens, Hq, Hkv, D, page = shape
+    s = make(13, lens, Hq, Hkv, D, page)
+    want = decode(lib, s)
+    for at in (2, 3):
+        t = s["pool"][at]
+        room = torch.zeros(t.numel() + 16, dtype=torch.uint8, device="cuda")
+        room[shift: shift + t.numel()] = t.flatten()
+        s["pool"][at] = room[shift: shift + t.numel()].view(t.shape)
+    out, lse, err = decode(lib, s)
+    assert err == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    s["pool"][2] = torch.zeros(s["pool"][2].numel() + 1, dtype=torch.uint8, device="cuda")[1:].view(s["pool"][2].shape)
+    with pytest.raises(lib.PagedKVError, match="invalid"):
+        decode(lib, s)
+
+
 def test_shared_pages(lib):
     """Two requests that list the same pages."""
     s = make(12, (128, 100), 8, 2, 128, 16)

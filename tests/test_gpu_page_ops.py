@@ -82,6 +82,24 @@ def test_copy_pages(lib, kind, page, Hkv, D, layers, copies, partial):
     check(tensors, before, moves[:, 0], moves[:, 1])
 
 
+@pytest.mark.parametrize("shift", [1, 2, 4, 8])
+def test_tensors_at_any_place(lib, shift):
+    """Views that do not begin at a multiple of 16 bytes, beside one that does."""
+    def view(shape):
+        n = int(np.prod(shape))
+        return torch.randint(0, 256, (n + 16,), dtype=torch.uint8, device="cuda")[shift: shift + n].view(shape)
+
+    tensors = [view((9, 4, 2, 64)), view((9, 4, 2, 4)), cache(8, "bf16", 9, 4, 2, 64)[0], view((9, 4, 33))]
+    before = [raw(x) for x in tensors]
+    lib.copy_pages(tensors, i32([0, 1]), i32([7, 8]), rows=i32([3, 4]))
+    src, dst = [0, 1, 2, 4, 5, 6, 7], [28, 29, 30, 32, 33, 34, 35]
+    check(tensors, before, src, dst)
+    before = [raw(x) for x in tensors]
+    lib.compact_accepted(tensors, i32([0, 3]), i32([2, 5, 3]), i32([2]), i32([0, 4]), i32([1, 3, 4, 9]))
+    slot = lambda p: [2, 5, 3][p // 4] * 4 + p % 4  # noqa: E731
+    check(tensors, before, [slot(p) for p in (3, 5, 6, 11)], [slot(p) for p in (2, 3, 4, 5)])
+
+
 def test_copy_reports_what_it_skips(lib):
     def run(src, dst, rows=None):
         t = cache(2, "bf16", 6, 4, 2, 64)
