@@ -217,11 +217,12 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
     }
 
     int left = h.left;
+    const int sharers = min(W, (left + kStep - 1) / kStep);  // warps of a head with positions in the segment
     while (true) {  // the segment's stages
       if (!wait(&full[stage])) return;
       const int nv = left - si * kStep;  // positions of the step, at least where it is below kStep
-      // A segment's last stage is held when warps share a head: its memory carries their merge.
-      const bool last = left <= Ts, hold = last && W > 1;
+      // A segment's last stage is held when warps share its head: its memory carries their merge.
+      const bool last = left <= Ts, hold = last && sharers > 1;
       const uint32_t at = (uint32_t)stage * a.stage_bytes;
       float s[NH][4];
       if (nv > 0) {
@@ -396,14 +397,14 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
       }
     }
 
-    if (W > 1) {
-      // Combine the W warps that split this head's positions (all consumer warps reach the segment end on
-      // the same stage).  A warp without a position in the segment holds a maximum of -inf and sums of 0.
+    if (sharers > 1) {
+      // Combine the warps that split this head's positions (all consumer warps reach the segment end on
+      // the same stage).
       bool met = meet();
       float* buf = reinterpret_cast<float*>(stages + (size_t)stage * a.stage_bytes) + lane;
       // all but one at once where their states fit into the stage, else half of them, or as many as do, at a time
       const int room = (int)(a.stage_bytes / (uint32_t)(HV * MF * 128));
-      for (int some = W; met && some > 1;) {
+      for (int some = sharers; met && some > 1;) {
         const int keep = some - 1 <= room ? 1 : max(some / 2, some - room);
         if (si >= keep && si < some) {
           float* to = buf + ((si - keep) * HV + hv) * MF * 32;

@@ -11,8 +11,8 @@ namespace {
 
 using namespace pkv;
 
-constexpr int kRows = 16;
 constexpr int kThreads = 256;
+constexpr int kMostRows = 128;  // of a tile
 
 struct GatherArgs {
   const uint8_t* k_pool;
@@ -26,8 +26,9 @@ struct GatherArgs {
   const int32_t* out_indptr;
   int32_t batch, num_out_rows, page_size, Hkv;
   int64_t num_pages;
-  FastDiv cpr;  // 8-byte chunks of a token row
-  FastDiv cph;  // ... of a head
+  int32_t rows;  // of a tile
+  FastDiv cpr;   // 8-byte chunks of a token row
+  FastDiv cph;   // ... of a head
   uint4* k_out;
   uint4* v_out;
   uint32_t* err_word;
@@ -107,7 +108,8 @@ PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
 
 template <class F>
 __global__ void __launch_bounds__(kThreads) paged_gather_quant_kernel(const __grid_constant__ GatherArgs a) {
-  __shared__ int64_t s_slot[2][kRows];
+  __shared__ int64_t s_slot[2][kMostRows];
+  const int kRows = a.rows;
   pdl_trigger();
   pdl_wait();
   // what the copies below cannot see: a request whose rows do not hold its length, or lie outside out
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) paged_gather_quant_kernel(const __gr
   int buf = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
     const int32_t row0 = tile * kRows;
-    if (threadIdx.x < kRows)
+    if ((int)threadIdx.x < kRows)
       s_slot[buf][threadIdx.x] = row0 + (int)threadIdx.x < a.num_out_rows ? find_slot(a, row0 + threadIdx.x) : -1;
     __syncthreads();  // one per tile: the next tile's slots go to the other buffer
     const uint32_t n = kRows * cpr;
@@ -173,7 +175,10 @@ pkv_status gather(const Pool* pool, int32_t row_bytes, float k_global, float v_g
   if (!kv_indptr || !kv_indices || !kv_lens || !out_indptr || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
   if (!pkv_host::aligned16(k_out) || !pkv_host::aligned16(v_out)) return PKV_ERR_INVALID_ARG;
   const int64_t cpr = (int64_t)pool->num_kv_heads * (row_bytes / 8);
-  if (cpr > 0x7fffffffLL / kRows || num_out_rows > 0x7fffffff - kRows) return PKV_ERR_UNSUPPORTED;
+  if (cpr > 0x7fffffffLL / kMostRows || num_out_rows > 0x7fffffff - kMostRows) return PKV_ERR_UNSUPPORTED;
+  // Sixteen rows, or as many as give every thread four chunks: a tile's slots are looked up before its copies start.
+  int rows = 16;
+  while (rows < kMostRows && rows * cpr < 4 * kThreads) rows *= 2;
   GatherArgs a;
   a.k_pool = (const uint8_t*)pool->k;
   a.v_pool = (const uint8_t*)pool->v;
@@ -190,12 +195,13 @@ pkv_status gather(const Pool* pool, int32_t row_bytes, float k_global, float v_g
   a.page_size = pool->page_size;
   a.Hkv = pool->num_kv_heads;
   a.num_pages = pool->num_pages;
+  a.rows = rows;
   a.cpr = FastDiv((uint32_t)cpr);
   a.cph = FastDiv((uint32_t)(row_bytes / 8));
   a.k_out = (uint4*)k_out;
   a.v_out = (uint4*)v_out;
   a.err_word = err_word;
-  int64_t blocks = (num_out_rows + kRows - 1) / kRows;
+  int64_t blocks = (num_out_rows + rows - 1) / rows;
   const int64_t cap = (int64_t)pkv_host::sm_count() * 8;
   if (cap > 0 && blocks > cap) blocks = cap;
   return pkv_host::launch_after(paged_gather_quant_kernel<F>, dim3((unsigned)blocks), kThreads, 0,
