@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+from test_stream_allocations import SIDE, Side, made  # noqa: F401
 from test_operators_host import ODD, SOME, _rotary, INVALID, OK, UNSUPPORTED, pkv, lib  # noqa: F401
 
 
@@ -185,3 +186,19 @@ def test_binding_refuses_host_tensors_and_wrong_types(pkv):  # noqa: F811
         pkv.copy_pages([3], slots.int(), slots.int())
     with pytest.raises(ValueError, match="CUDA"):
         pkv.compact_accepted((codes,), slots.int(), slots.int(), slots.int(), slots.int(), slots.int())
+
+
+def test_what_the_decode_makes_belongs_to_its_stream(pkv, made, monkeypatch):  # noqa: F811
+    """Its workspace, which is dropped when the call returns, and its results, which the caller's stream reads."""
+    log, calls = made
+    read_by = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "the caller's")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, stream: read_by.append(stream))
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    pool = [torch.zeros(4, 16, 2, n, dtype=torch.uint8) for n in (32, 32, 4, 4)]
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    log.clear()
+    pkv.paged_decode_fp4(q, *pool, i32(0, 1, 2), i32(0, 1), i32(5, 6), 0.1, stream=Side())
+    assert [at for fn, at in log if at is not None] == [SIDE] * 3, log
+    assert calls and all(stream == SIDE for _, stream in calls)
+    assert read_by == ["the caller's"] * 2
