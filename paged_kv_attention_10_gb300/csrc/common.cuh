@@ -99,20 +99,6 @@ PKV_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same, for a wait that is expected to be long: the thread may sleep for up to about `ns` before it tries again
-// (a producer that polls takes issue slots from the warps that it waits for).
-PKV_DEV bool mbar_try_wait_ns(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait for the phase with the given parity to complete; gives up after kWaitLimitNs and returns
 // false (the caller reports PKV_DEVERR_TIMEOUT and unwinds).
 PKV_DEV bool mbar_wait(uint64_t* bar, uint32_t parity) {
@@ -120,15 +106,6 @@ PKV_DEV bool mbar_wait(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  }
-}
-
-PKV_DEV bool mbar_wait_ns(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (mbar_try_wait_ns(bar, parity, ns)) return true;
     if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
   }
 }

@@ -18,6 +18,8 @@
 //  * The sixteen score rows of an MMA are the positions in an order in which the loads of K (two positions by four
 //    quarters at a time) and of V (four positions by four eighths) meet no shared-memory bank twice, see position().
 //  * Softmax weights are rounded to f16 in [0, 2^15]; O and the sum of the weights carry that 2^15, which cancels.
+#include <type_traits>
+
 #include "quant_decode.cuh"
 
 namespace {
@@ -40,7 +42,8 @@ PKV_DEV int position(int r) {
 
 template <int D, bool FEW>
 struct Format4 {
-  static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kWarps = 8, kStep = 64, kParts = 2;
+  static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kStep = 64, kParts = 2;
+  static constexpr int kWarps = D == 64 ? 16 : 8;
   static constexpr bool kBoxedRows = true, kJoint = true;
   static constexpr int kTiles = FEW ? D / 32 : D / 16;  // row tiles of O
   static constexpr int kMergeFloats = 4 + 4 * kTiles;
@@ -107,7 +110,6 @@ template <bool>
 __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                          uint64_t* full, uint64_t* empty, uint64_t* meet_bar) {
   constexpr int RH = kRowBytes, SH = kScaleBytes, NT = kTiles;
-  constexpr int NH = kStep / 16;      // score tiles of a step
   constexpr int NM = D / 16;          // MMAs of a score tile
   constexpr int KW = D / 32;          // words of a lane's share of a K row
   constexpr int VW = D / 64;          // ... of a V row
@@ -224,8 +226,10 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
       // A segment's last stage is held when warps share its head: its memory carries their merge.
       const bool last = left <= Ts, hold = last && sharers > 1;
       const uint32_t at = (uint32_t)stage * a.stage_bytes;
-      float s[NH][4];
-      if (nv > 0) {
+      // A step of NH tiles of 16 positions.
+      auto step = [&](auto tiles) {
+        constexpr int NH = decltype(tiles)::value;
+        float s[NH][4];
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
           const uint32_t ka = k_at + at + tile_off(hf), sa = s_at + at + 2 * hf * s_eight;
@@ -288,10 +292,8 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             }
           }
         }
-      }
-      uint32_t bp[NH][2];
-      if (nv > 0) {
-        if (nv < kStep) {
+        uint32_t bp[NH][2];
+        if (nv < 16 * NH) {
 #pragma unroll
           for (int hf = 0; hf < NH; ++hf)
 #pragma unroll
@@ -335,8 +337,6 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             l[1] += w1;
             bp[hf][i] = movmatrix_t(pack_f16x2(w0, w1));
           }
-      }
-      if (nv > 0) {
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
           const uint32_t aa = va_at + at + tile_off(hf), ab = vb_at + at + tile_off(hf);
@@ -349,7 +349,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             uint32_t two = scales(sa + i * s_eight);
             // Rows past the request's end hold unused pool slots (the boxes bring them) or what shared memory held
             // before, NaN scales among them: with a scale of 0 their values are 0, and 0 times their weight 0 stays 0.
-            if (nv < kStep && 16 * hf + 8 * i + pk >= nv) two = 0;
+            if (nv < 16 * NH && 16 * hf + 8 * i + pk >= nv) two = 0;
             // position g's scales of two blocks become block g's (g / 2's) scales of two positions
             vs[i] = movmatrix_t(unpack_e4m3x2(two));
           }
@@ -386,7 +386,9 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
             }
           }
         }
-      }
+      };
+      if (nv > kStep / 2) step(std::integral_constant<int, kStep / 16>());
+      else if (nv > 0) step(std::integral_constant<int, kStep / 32>());
       __syncwarp();
       if (!hold && lane == 0) mbar_arrive(&empty[stage]);
       if (last) break;

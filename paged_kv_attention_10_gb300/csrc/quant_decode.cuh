@@ -9,7 +9,7 @@
 //    CTA takes every KV head (a box's lie side by side then), by cp.async otherwise.
 //
 // A format F is a struct with kDim (head_dim), kRowBytes and kScaleBytes (of one head of one position), kWarps
-// (consumer warps), kStep (positions of a warp's step), kParts (most producer warps each for K and V), kJoint (whether K
+// (consumer warps), kStep (positions of a warp's step), kParts (producer warps each for K and V), kJoint (whether K
 // and V share a stage's barriers), kMergeFloats (of a lane's state, see consume),
 // kBoxedRows (whether row copies make boxes of 32 rows of a head in the boxes' swizzle, or rows row_stride(their bytes)
 // apart), and consume<TMA>, a consumer warp.
@@ -68,7 +68,6 @@ struct QuantDecodeArgs {
   FastDiv piece_div;     // boxed rows: by the 16-byte pieces of a row of HC heads
   int32_t scale_piece;   // bytes of one copy of a row's scales by a lane: 16, 8 or 4
   int32_t scales_at_16;  // whether k_scale and v_scale are 16-byte aligned, and so the scales of every box
-  int32_t parts;         // producer warps each for K and V
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // kStep * W
   int32_t num_stages, num_parts;
@@ -156,7 +155,7 @@ template <class F, bool TMA>
 __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                  uint64_t* full, uint64_t* empty, bool v, int part) {
   constexpr int D = F::kDim, RH = F::kRowBytes, SH = F::kScaleBytes;  // bytes of a head's row and of its scales
-  const int P = F::kParts == 1 ? 1 : a.parts;
+  constexpr int P = F::kParts;
   const int lane = threadIdx.x & 31;
   const int NS = a.num_stages, Ts = a.stage_tokens, HC = a.HC, nhg = a.nhg;
   const int W = Ts / kSlice;  // rounds of 32 positions
@@ -532,9 +531,8 @@ __global__ void __launch_bounds__((F::kWarps + 2 * F::kParts) * 32, 1) quant_dec
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) mbar_init(&hdr_full[s], 1);
     mbar_init(meet_bar, NC);
-    const int parts = F::kParts == 1 ? 1 : a.parts;
     for (int s = 0; s < 2 * NS; ++s) {
-      mbar_init(&full[s], 33 * parts * (F::kJoint ? 2 : 1));  // each producer's go-ahead, and every lane's copies
+      mbar_init(&full[s], 33 * F::kParts * (F::kJoint ? 2 : 1));  // each producer's go-ahead, and every lane's copies
       mbar_init(&empty[s], NC);
     }
     fence_mbar_init();
@@ -582,14 +580,14 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
     else
       *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(v[0], v[1]);
   };
-  if (ld(a.kv_lens + b) <= 0) {
+  const int len = ld(a.kv_lens + b), first = ld(a.unit_first + u), last = ld(a.unit_last + u);  // in one round of loads
+  if (len <= 0) {
     if (blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, PKV_DEVERR_LENGTH);
     const float zero[VPL] = {};
     store(zero);
     if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
     return;
   }
-  const int first = a.unit_first[u], last = a.unit_last[u];
   if (first == last) return;  // written directly
   if (first < 0 || last >= a.num_parts || last < first) {  // a wait gave up somewhere
     if (lane == 0) report(a.err_word, PKV_DEVERR_TIMEOUT);
@@ -734,7 +732,7 @@ pkv_status launch_quant_decode(const QuantDecodePlan& p, const QuantDecodeArgs& 
     }
     if (dev < 64) configured[dev].store(true, std::memory_order_relaxed);
   }
-  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2 * a.parts) * 32, p.smem, st, a);
+  const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2 * F::kParts) * 32, p.smem, st, a);
   if (s != PKV_OK) return s;
   return pkv_host::launch_after(quant_decode_merge_kernel<F>, dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8)),
                                 256, 0, st, a);
@@ -798,9 +796,6 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   a.box_rows = p.R;
   a.row_stride = p.RS;
   a.piece_div = FastDiv((uint32_t)(p.HC * F::kRowBytes / 16));
-  // One warp each issues a few boxes and their scales in time, and more warps' walks would take issue slots from the
-  // consumers (4 bits, 256 requests of 32/8 heads: 140 us with one, 144 with two; copied row by row, 48/16 heads of 64: 47, 40).
-  a.parts = F::kParts == 1 || (p.tma && p.Ts / p.R <= 4 && p.nhg == 1) ? 1 : F::kParts;
   // a piece divides a row's scales and the addresses of all of them
   const uintptr_t places = (uintptr_t)pool->k_scale | (uintptr_t)pool->v_scale;
   const uintptr_t pieces = places | (uintptr_t)(p.HC * F::kScaleBytes);
