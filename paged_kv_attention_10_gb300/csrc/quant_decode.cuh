@@ -557,24 +557,29 @@ __global__ void __launch_bounds__((F::kWarps + 2 * F::kParts) * 32, 1) quant_dec
 }
 
 // ---------------------------------------------------------------------------------------------
-// Merge of the split partials: one warp per (unit, query head), a programmatic dependent of the
-// decode kernel.  Bound by latency: 4 us after 8 requests of 32768 positions, 7 after 256 requests.
+// Merge of the split partials, a programmatic dependent of the decode kernel: S warps per (unit, query head), each over
+// every S-th partial.  Bound by latency, so a warp's loads are issued together, and where a unit can be split
+// among 16 CTAs and more eight warps share its partials (4 bits, one request of 4000 positions, 32/8 heads of 128: 8.8 us
+// in all with eight, 13.4 with one; 8 requests of 32768: 57.1, 58.3; 8 of 300, which are split less: 8.3, 7.9), else one
+// does (16 requests of 16384: 57.7, 59.2 with eight; 64 of 1000: 21.3, 31.1).
 // ---------------------------------------------------------------------------------------------
-template <class F>
+template <class F, int S>
 __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_constant__ QuantDecodeArgs a) {
   constexpr int D = F::kDim;
+  constexpr int VPL = D / 32;  // values per lane
   pdl_trigger();
   pdl_wait();
   const int u = blockIdx.x;
   const int b = u / a.nhg, hg = u % a.nhg;
   const int HQU = a.HC * a.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qhl = blockIdx.y * 8 + warp;
-  if (qhl >= HQU) return;
-  constexpr int VPL = D / 32;  // values per lane
+  const int part = warp % S;
+  const int qhl = (int)blockIdx.y * (8 / S) + warp / S;
+  const bool in = qhl < HQU;
+  if (S == 1 && !in) return;
   const int64_t row = (int64_t)b * a.num_q_heads + (int64_t)hg * HQU + qhl;
-  __nv_bfloat16* op = a.out + row * D + lane * VPL;
   auto store = [&](const float (&v)[VPL]) {
+    __nv_bfloat16* op = a.out + row * D + lane * VPL;
     if constexpr (VPL == 4)
       *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     else
@@ -583,9 +588,11 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
   const int len = ld(a.kv_lens + b), first = ld(a.unit_first + u), last = ld(a.unit_last + u);  // in one round of loads
   if (len <= 0) {
     if (blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, PKV_DEVERR_LENGTH);
-    const float zero[VPL] = {};
-    store(zero);
-    if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
+    if (in && part == 0) {
+      const float zero[VPL] = {};
+      store(zero);
+      if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
+    }
     return;
   }
   if (first == last) return;  // written directly
@@ -594,19 +601,19 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
     return;
   }
   // One pass: the partials' LSEs (one per lane) and the first sixteen partial rows are loaded together,
-  // so up to 32 partials cost one trip to L2; more rescale what they found.
+  // so up to 16 partials a warp cost one trip to L2; more rescale what they found.
   const float* plse = a.part_lse + qhl;
   const float* po = a.part_o + (int64_t)qhl * D + lane * VPL;
   float mx = -INFINITY, tot = 0.f;
   float acc[VPL] = {};
-  for (int base = first; base <= last; base += 32) {
-    const int n = min(32, last - base + 1);
-    const float pl = lane < n ? ld(plse + (int64_t)(base + lane) * HQU) : -INFINITY;
+  for (int base = first + part; in && base <= last; base += 32 * S) {
+    const int n = min(32, (last - base) / S + 1);
+    const float pl = lane < n ? ld(plse + (int64_t)(base + S * lane) * HQU) : -INFINITY;
     float x[16][VPL];
     auto load = [&](int i0) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float* src = po + (int64_t)(base + i0 + k) * HQU * D;
+        const float* src = po + (int64_t)(base + S * (i0 + k)) * HQU * D;
         if (i0 + k < n) {
           if constexpr (VPL == 4)
             *reinterpret_cast<float4*>(x[k]) = ld(reinterpret_cast<const float4*>(src));
@@ -623,9 +630,9 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
     mn = fmaxf(mx, mn);
-    const float corr = __expf(mx - mn);  // 0 on the first round
+    const float corr = mx == mn ? 1.f : __expf(mx - mn);  // 0 on the first round
     mx = mn;
-    const float w = lane < n ? __expf(pl - mx) : 0.f;
+    const float w = lane < n && pl != -INFINITY ? __expf(pl - mx) : 0.f;
     tot = tot * corr + w;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] *= corr;
@@ -640,6 +647,35 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
     }
   }
   tot = warp_sum(tot);
+  if constexpr (S > 1) {
+    // the first of a head's warps joins them; one without a partial has mx = -inf and sums of 0
+    __shared__ float joined[8][2 + VPL][32];
+    if (part > 0) {
+      joined[warp][0][lane] = mx;
+      joined[warp][1][lane] = tot;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) joined[warp][2 + v][lane] = acc[v];
+    }
+    __syncthreads();
+    if (part > 0) return;
+    float m[S], top = mx;
+    m[0] = mx;
+#pragma unroll
+    for (int w = 1; w < S; ++w) top = fmaxf(top, m[w] = joined[warp + w][0][lane]);
+    const float corr = mx == -INFINITY ? 1.f : __expf(mx - top);
+    tot *= corr;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) acc[v] *= corr;
+#pragma unroll
+    for (int w = 1; w < S; ++w) {
+      const float f = m[w] == -INFINITY ? 1.f : __expf(m[w] - top);
+      tot += joined[warp + w][1][lane] * f;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) acc[v] += joined[warp + w][2 + v][lane] * f;
+    }
+    mx = top;
+  }
+  if (!in) return;
   const float inv = 1.f / tot;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) acc[v] *= inv;
@@ -656,6 +692,7 @@ struct QuantDecodePlan {
   uint32_t region, stage;
   size_t smem;
   int64_t nunits, nparts;
+  int merge_warps;
   size_t off_first, off_last, off_plse, off_po, ws_bytes;
 };
 
@@ -694,6 +731,7 @@ bool make_plan(int B, int Hq, int Hkv, int ncta, QuantDecodePlan& p, int page_si
   p.nunits = (int64_t)B * p.nhg;
   p.nparts = p.ncta + p.nunits;
   const int HQU = p.HC * p.G;
+  p.merge_warps = p.ncta / 16 >= p.nunits ? 8 : 1;
   p.off_first = 0;
   p.off_last = align256(p.off_first + (size_t)p.nunits * 4);
   p.off_plse = align256(p.off_last + (size_t)p.nunits * 4);
@@ -734,8 +772,9 @@ pkv_status launch_quant_decode(const QuantDecodePlan& p, const QuantDecodeArgs& 
   }
   const pkv_status s = pkv_host::launch_after(kern, dim3(p.ncta), (p.HC * p.NT * p.W + 2 * F::kParts) * 32, p.smem, st, a);
   if (s != PKV_OK) return s;
-  return pkv_host::launch_after(quant_decode_merge_kernel<F>, dim3((unsigned)p.nunits, (unsigned)((p.HC * p.G + 7) / 8)),
-                                256, 0, st, a);
+  const dim3 grid((unsigned)p.nunits, (unsigned)((p.HC * p.G * p.merge_warps + 7) / 8));
+  if (p.merge_warps == 8) return pkv_host::launch_after(quant_decode_merge_kernel<F, 8>, grid, 256, 0, st, a);
+  return pkv_host::launch_after(quant_decode_merge_kernel<F, 1>, grid, 256, 0, st, a);
 }
 
 // The checks that the entry points of both formats share, before head_dim chooses the instance.
