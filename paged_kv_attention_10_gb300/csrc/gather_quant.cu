@@ -1,10 +1,13 @@
 // Read-back of an 8-bit or a 4-bit paged cache: every request's rows in position order as bf16.
 //
 // bf16(x8 * scale) per value, exact for the power-of-two scales the append writes; bf16(x4 * scale * global) with one
-// scale per 16 values.  Bound by HBM (one byte, or a little over half of one, in, two out).  A CTA takes tiles of 16 output rows: 16 threads find the request of a row
-// by binary search over out_indptr (which its L1 holds after the first tile) and the row's slot,
-// then all threads copy 8 bytes at a time, K and V, with the loads of several chunks in flight.  16
-// requests of 1 to 4096 positions, 8 heads of 128: 36 us, 5.7 TB/s, 83 % of what a device copy of 1 GB reaches.
+// scale per 16 values.  Bound by HBM (one byte, or a little over half of one, in, two out).  A CTA takes a tile of
+// consecutive output rows: a thread a row finds its request by binary search over out_indptr and its slot, then
+// all threads copy 8 bytes at a time, K and V, with the loads of four chunks each in flight.  The search is a chain of
+// loads that the copies of other CTAs hide, so a CTA takes one tile and no more, and the tile is just large enough for
+// the four chunks.  64 requests of 1 to 4096 positions, 8 heads of 128: 124 us (8 bits), 106 (4 bits), 97 and 96 % of what a
+// device copy reaches (with tiles of sixteen rows taken in turn by eight CTAs an SM 135 and 117; with twice the rows
+// a tile 127 and 109); 16 requests 34 and 29 us (36 and 31; 38 and 34).
 #include "quant.cuh"
 
 namespace {
@@ -27,6 +30,7 @@ struct GatherArgs {
   int32_t batch, num_out_rows, page_size, Hkv;
   int64_t num_pages;
   int32_t rows;  // of a tile
+  FastDiv page_div;
   FastDiv cpr;   // 8-byte chunks of a token row
   FastDiv cph;   // ... of a head
   uint4* k_out;
@@ -90,11 +94,12 @@ PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
     else hi = mid - 1;
   }
   if (lo == a.batch) return -1;
-  const int32_t j = row - ld(a.out_indptr + lo);
-  if (j < 0 || j >= ld(a.kv_lens + lo)) return -1;
-  const int32_t p0 = ld(a.kv_indptr + lo), np = ld(a.kv_indptr + lo + 1) - p0;
-  const int32_t pidx = j / a.page_size;
-  if (pidx >= np) {
+  const int32_t o0 = ld(a.out_indptr + lo), len = ld(a.kv_lens + lo), p0 = ld(a.kv_indptr + lo);  // in one round of loads
+  const int32_t np = ld(a.kv_indptr + lo + 1) - p0, j = row - o0;
+  if (j < 0 || j >= len) return -1;
+  uint32_t pidx, in_page;
+  a.page_div.divmod((uint32_t)j, pidx, in_page);
+  if ((int32_t)pidx >= np) {
     report(a.err_word, PKV_DEVERR_LENGTH);
     return -1;
   }
@@ -103,12 +108,12 @@ PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
     report(a.err_word, PKV_DEVERR_PAGE_OOB);
     return -1;
   }
-  return (int64_t)page * a.page_size + (j - pidx * a.page_size);
+  return (int64_t)page * a.page_size + in_page;
 }
 
 template <class F>
 __global__ void __launch_bounds__(kThreads) paged_gather_quant_kernel(const __grid_constant__ GatherArgs a) {
-  __shared__ int64_t s_slot[2][kMostRows];
+  __shared__ int64_t s_slot[kMostRows];
   const int kRows = a.rows;
   pdl_trigger();
   pdl_wait();
@@ -125,41 +130,37 @@ __global__ void __launch_bounds__(kThreads) paged_gather_quant_kernel(const __gr
   const uint2* v_in = reinterpret_cast<const uint2*>(a.v_pool);
   const Scale* k_scale = reinterpret_cast<const Scale*>(a.k_scale);
   const Scale* v_scale = reinterpret_cast<const Scale*>(a.v_scale);
-  const int tiles = (a.num_out_rows + kRows - 1) / kRows;
-  int buf = 0;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    const int32_t row0 = tile * kRows;
-    if ((int)threadIdx.x < kRows)
-      s_slot[buf][threadIdx.x] = row0 + (int)threadIdx.x < a.num_out_rows ? find_slot(a, row0 + threadIdx.x) : -1;
-    __syncthreads();  // one per tile: the next tile's slots go to the other buffer
-    const uint32_t n = kRows * cpr;
-    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * kThreads) {
-      uint2 k[4], v[4];
-      Scale ks[4], vs[4];
-      bool on[4];
+  const int32_t row0 = blockIdx.x * kRows;
+  if ((int)threadIdx.x < kRows)
+    s_slot[threadIdx.x] = row0 + (int)threadIdx.x < a.num_out_rows ? find_slot(a, row0 + threadIdx.x) : -1;
+  __syncthreads();
+  const uint32_t n = kRows * cpr;
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * kThreads) {
+    uint2 k[4], v[4];
+    Scale ks[4], vs[4];
+    bool on[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t i = i0 + u * kThreads;
-        uint32_t r, c;
-        a.cpr.divmod(i < n ? i : 0, r, c);
-        const int64_t slot = s_slot[buf][r];
-        on[u] = i < n && slot >= 0;
-        if (on[u]) {
-          const int64_t src = slot * cpr + c;
-          k[u] = ld(k_in + src);
-          v[u] = ld(v_in + src);
-          const int64_t hs = F::scale_at(a, slot, c);
-          ks[u] = ld(k_scale + hs);
-          vs[u] = ld(v_scale + hs);
-        }
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t i = i0 + u * kThreads;
+      uint32_t r, c;
+      a.cpr.divmod(i < n ? i : 0, r, c);
+      const int64_t slot = s_slot[r];
+      on[u] = i < n && slot >= 0;
+      if (on[u]) {
+        const int64_t src = slot * cpr + c;
+        k[u] = ld(k_in + src);
+        v[u] = ld(v_in + src);
+        const int64_t hs = F::scale_at(a, slot, c);
+        ks[u] = ld(k_scale + hs);
+        vs[u] = ld(v_scale + hs);
       }
+    }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (on[u]) {
-          const int64_t dst = ((int64_t)row0 * cpr + i0 + u * kThreads) * F::kWords;
-          F::store(a.k_out + dst, k[u], ks[u], a.k_global);
-          F::store(a.v_out + dst, v[u], vs[u], a.v_global);
-        }
+    for (int u = 0; u < 4; ++u) {
+      if (on[u]) {
+        const int64_t dst = ((int64_t)row0 * cpr + i0 + u * kThreads) * F::kWords;
+        F::store(a.k_out + dst, k[u], ks[u], a.k_global);
+        F::store(a.v_out + dst, v[u], vs[u], a.v_global);
       }
     }
   }
@@ -176,8 +177,8 @@ pkv_status gather(const Pool* pool, int32_t row_bytes, float k_global, float v_g
   if (!pkv_host::aligned16(k_out) || !pkv_host::aligned16(v_out)) return PKV_ERR_INVALID_ARG;
   const int64_t cpr = (int64_t)pool->num_kv_heads * (row_bytes / 8);
   if (cpr > 0x7fffffffLL / kMostRows || num_out_rows > 0x7fffffff - kMostRows) return PKV_ERR_UNSUPPORTED;
-  // Sixteen rows, or as many as give every thread four chunks: a tile's slots are looked up before its copies start.
-  int rows = 16;
+  // Four rows, or as many as give every thread four chunks: a tile's slots are looked up before its copies start.
+  int rows = 4;
   while (rows < kMostRows && rows * cpr < 4 * kThreads) rows *= 2;
   GatherArgs a;
   a.k_pool = (const uint8_t*)pool->k;
@@ -196,14 +197,13 @@ pkv_status gather(const Pool* pool, int32_t row_bytes, float k_global, float v_g
   a.Hkv = pool->num_kv_heads;
   a.num_pages = pool->num_pages;
   a.rows = rows;
+  a.page_div = FastDiv((uint32_t)pool->page_size);
   a.cpr = FastDiv((uint32_t)cpr);
   a.cph = FastDiv((uint32_t)(row_bytes / 8));
   a.k_out = (uint4*)k_out;
   a.v_out = (uint4*)v_out;
   a.err_word = err_word;
-  int64_t blocks = (num_out_rows + rows - 1) / rows;
-  const int64_t cap = (int64_t)pkv_host::sm_count() * 8;
-  if (cap > 0 && blocks > cap) blocks = cap;
+  const int64_t blocks = ((int64_t)num_out_rows + rows - 1) / rows;
   return pkv_host::launch_after(paged_gather_quant_kernel<F>, dim3((unsigned)blocks), kThreads, 0,
                                 (cudaStream_t)stream, a);
 }
