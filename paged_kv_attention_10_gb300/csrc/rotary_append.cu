@@ -13,9 +13,10 @@
 // neighbouring pairs (and without a rotation) two chunks side by side.  A warp takes two such steps of
 // one token, all of whose loads are issued before the token's position and slot are needed, and
 // loads the token's cosines and sines once for both.  (With one chunk per lane, a shuffle for the
-// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us, 39 so, and 36
-// started beside the kernel before it: 5.6 TB/s, 83 % of what a device copy of 1 GB reaches.  2304 tokens
-// into an 8-bit cache, R 128: 12 us, 64 %, bound by latency, as are the few tokens of a decode step: 2.6 us.)
+// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us, 39 so; 35 now, R 64, 5.8 TB/s,
+// 85 % of what a device copy of 1 GB reaches.  R 128: 33.6 us, 35.2 into an 8-bit cache, 36.7 (73 %) into a 4-bit one,
+// whose divisions keep the issue slots 60 % busy.  2304 tokens of it: 10.2, 10.7 and 11.1 us, bound by latency, as are
+// the few tokens of a decode step: 2.6 to 3.1 us.)
 // Widths that are no multiple of 16 (half) or 8 (neighbours) take a
 // kernel of one chunk per lane that reads its partners one by one: 8191 tokens of 32/8 heads of 80, R 20, 74 us,
 // 1.7 TB/s, where R 32 takes 27.
@@ -151,23 +152,28 @@ PKV_DEV bool slot_ok(const AppendArgs& a, int64_t slot, bool reporter) {
   return false;
 }
 
-// Steps and blocks per SM, measured on 8191 tokens of 32/8 heads at D 128, R 64 (and quantising 2304 with
-// R 128): 2 steps and 4 blocks 39.0 us (15.3), 4 and 3 39.5 (16.8), 4 and 2 41.1 (17.3), 1 and 4 46.0
-// (17.1); more blocks spill.  All of these before the kernel started beside the one before it, with which the
-// chosen setting takes 35.9 us (12.2).  A device copy of the same bytes takes 37.1 us (16.5).  The 4-bit write without a
-// rotation fits five blocks (8191 tokens of eight heads: 13.1 us with four, 12.2).
+// Steps, and 32 warps an SM, measured on 8191 tokens of 32/8 heads at D 128, R 64 (and quantising 2304 with
+// R 128): 2 steps and 32 warps 39.0 us (15.3), 4 and 24 39.5 (16.8), 4 and 16 41.1 (17.3), 1 and 32 46.0
+// (17.1); more warps spill.  All of these in blocks of eight and before the kernel started beside the one before it, with
+// which the chosen setting took 35.9 us (12.2).  A device copy of the same bytes takes 37.1 us (16.5).
+// Blocks are small, since a warp's K and V rows cost more than its Q rows and a block keeps its place until its last warp
+// is done.  8191 tokens of 32/8 heads, R 128, in blocks of eight, four and two warps: 4 bits 41.3, 38.2 and 37.2 us,
+// 8 bits 37.1, 35.2 and 34.7, bf16 34.8, 33.6 and 33.7 (2304 tokens 10.5, 10.2 and 10.6).  The 4-bit write of half-split pairs
+// spills less with 28 warps (36.7 us), and without a rotation it takes 12.1 us with 28 and 12.4 with 32 (neighbouring
+// pairs: 35.0 and 34.4).
 constexpr int kSteps = 2;
-constexpr int blocks_of(int format, int rotation) { return format == kE2m1 && rotation == kNone ? 5 : 4; }
+constexpr int warps_of(int format) { return format == kE2m1 ? 2 : 4; }  // of a block
+constexpr int blocks_of(int format, int rotation) { return (format == kE2m1 && rotation != kPairs ? 28 : 32) / warps_of(format); }
 
 // L lanes hold a row (the power of two at or above its units of two chunks); a warp takes kSteps
 // times 32 / L rows of one token.
 template <int FMT, int ROT, int L>
-__global__ void __launch_bounds__(256, blocks_of(FMT, ROT)) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(32 * warps_of(FMT), blocks_of(FMT, ROT)) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kRows = 32 / L;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t item = blockIdx.x * warps_of(FMT) + (threadIdx.x >> 5);
   if (item >= a.items) return;
   uint32_t t, part;
   a.item_div.divmod(item, t, part);
@@ -379,13 +385,14 @@ pkv_status launch_rows(AppendArgs a, cudaStream_t st) {
   const int64_t parts = (a.heads + rows - 1) / rows;
   a.items = (uint32_t)(parts * a.T);
   a.item_div = FastDiv((uint32_t)parts);
-  const unsigned g = (a.items + 7) / 8;
+  constexpr int kWarps = warps_of(FMT);
+  const unsigned g = (a.items + kWarps - 1) / kWarps;
   switch (L) {
-    case 1: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 1>, dim3(g), 256, 0, st, a);
-    case 2: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 2>, dim3(g), 256, 0, st, a);
-    case 4: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 4>, dim3(g), 256, 0, st, a);
-    case 8: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 8>, dim3(g), 256, 0, st, a);
-    default: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 16>, dim3(g), 256, 0, st, a);
+    case 1: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 1>, dim3(g), 32 * kWarps, 0, st, a);
+    case 2: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 2>, dim3(g), 32 * kWarps, 0, st, a);
+    case 4: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 4>, dim3(g), 32 * kWarps, 0, st, a);
+    case 8: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 8>, dim3(g), 32 * kWarps, 0, st, a);
+    default: return pkv_host::launch_after(append_rows_kernel<FMT, ROT, 16>, dim3(g), 32 * kWarps, 0, st, a);
   }
 }
 
