@@ -120,7 +120,6 @@ struct CompactArgs {
   FastDiv item_div;  // by the warps of a request
   FastDiv page_div;
   uint32_t chunks, run;  // of a request in all tensors, and of a warp
-  uint32_t items;
   uint32_t* err_word;
 };
 
@@ -142,7 +141,7 @@ PKV_DEV int64_t slot_at(const CompactArgs<N>& a, int32_t p0, int32_t np, int64_t
 }
 
 // A warp's pieces `chunk` (32 side by side) of the n rows of lane l's (source, target) slots, kMoves pieces a lane in
-// flight: four, with four blocks an SM, since more spill (64 trees of 16 in 36 layers: eight 22.6 us, four 18.5).
+// flight: four, with 32 warps an SM (64 trees in 36 layers: two 17.6 us, four 15.8, eight with 24 warps 16.0).
 constexpr int kMoves = 4;
 
 template <typename V, typename Slot>
@@ -175,16 +174,17 @@ PKV_DEV void move_rows(char* base, uint32_t slot_bytes, uint32_t chunk, Slot src
   }
 }
 
-// kWide: every tensor moves in pieces of 16 bytes, and slots have 31-bit numbers.
+// kWide: every tensor moves in pieces of 16 bytes, and slots have 31-bit numbers.  Blocks of one warp, 32 an SM: requests
+// have different numbers of rows, and a block keeps its place until its last warp is done (64 trees in 36 layers: eight
+// warps 17.4 us, two 17.0, one 15.5).
+constexpr int kCompactWarps = 32;
 template <int N, bool kWide>
-__global__ void __launch_bounds__(256, kWide ? 4 : 2) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
+__global__ void __launch_bounds__(32, kWide ? kCompactWarps : kCompactWarps / 2) compact_accepted_kernel(const __grid_constant__ CompactArgs<N> a) {
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (item >= a.items) return;
+  const int lane = threadIdx.x;
   uint32_t b, part;
-  a.item_div.divmod(item, b, part);
+  a.item_div.divmod(blockIdx.x, b, part);
   const int32_t i0 = ld(a.accepted_indptr + b), i1 = ld(a.accepted_indptr + b + 1), prefix = ld(a.prefix_lens + b);
   const int32_t p0 = ld(a.kv_indptr + b), np = ld(a.kv_indptr + b + 1) - p0;
   if (i0 < 0 || i1 > a.num_accepted || prefix < 0) {
@@ -292,9 +292,10 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
     return (p.slot_bytes / piece_bytes(p) + 31) / 32;
   });
   if (chunks < 0 || chunks * batch > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  // Runs of two chunks once there are more than warps for all places of the GPU, 32 an SM (64 trees in 36 layers: one
-  // 18.7 us, two 17.5, four 18.5).
-  const int64_t run = chunks * batch > (int64_t)pkv_host::sm_count() * 32 ? 2 : 1;
+  // Runs of up to four chunks, so that one round of warps takes them all where it can (64 trees in 36 layers: one chunk
+  // 21.0 us, two 15.8, three 15.9, four 15.5).
+  const int64_t places = (int64_t)std::max(1, pkv_host::sm_count()) * kCompactWarps;
+  const int64_t run = std::min<int64_t>(4, (chunks * batch + places - 1) / places);
   const int64_t warps = (chunks + run - 1) / run;
   a.kv_indptr = kv_indptr;
   a.kv_indices = kv_indices;
@@ -308,12 +309,12 @@ pkv_status compact(const pkv_plane* planes, int32_t num_planes, int64_t num_page
   a.page_div = FastDiv((uint32_t)page_size);
   a.chunks = (uint32_t)chunks;
   a.run = (uint32_t)run;
-  a.items = (uint32_t)(warps * batch);
   a.err_word = err_word;
+  const dim3 grid((unsigned)(warps * batch));
   bool wide = num_pages * page_size <= 0x7fffffffLL;
   for (int32_t i = 0; i < num_planes; ++i) wide = wide && a.planes.piece[i] == 16;
-  return wide ? pkv_host::launch_after(compact_accepted_kernel<N, true>, dim3((a.items + 7) / 8), 256, 0, st, a)
-              : pkv_host::launch_after(compact_accepted_kernel<N, false>, dim3((a.items + 7) / 8), 256, 0, st, a);
+  return wide ? pkv_host::launch_after(compact_accepted_kernel<N, true>, grid, 32, 0, st, a)
+              : pkv_host::launch_after(compact_accepted_kernel<N, false>, grid, 32, 0, st, a);
 }
 
 }  // namespace
