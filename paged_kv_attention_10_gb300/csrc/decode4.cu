@@ -5,19 +5,39 @@
 // The plan is the 8-bit decode's (quant_decode.cuh).  A position's bytes are nearly halved again, the values are as
 // many, so the loop has to be lean: the conversions alone are an instruction for every two values.
 //
-//  * A code times its block's scale is exact in f16 (two bits times four), so the scales go into the matrix
-//    operands by f16 products, and the caches' scales g into the score's scale and the result's.  Both products run
-//    as f16 m16n8k16 MMAs with fp32 accumulators, Q scaled per head by a power of two into f16's range as in the 8-bit
-//    decode.
+//  * A code times its block's scale is exact in f16 (two bits times four), and the caches' scales g go into the score's
+//    scale and the result's.  Both products run as f16 m16n8k16 MMAs with fp32 accumulators, Q scaled per head by a
+//    power of two into f16's range as in the 8-bit decode.
 //  * A product's k-slots may hold the dimensions in any order if both operands agree, and so may the rows of its
 //    result.  A lane therefore takes consecutive bytes of a row: of K, a quarter of a position's row (dims 32c ..
 //    32c + 31 of 128), which holds whole blocks, so that it needs two scales of the eight; of V, an eighth (dims 16g ..
-//    16g + 15), one block, of the positions that its k-slots stand for.  No ldmatrix, no exchange between lanes.
+//    16g + 15), one block, of the positions that its k-slots stand for.
 //  * V's operand pairs two positions in a register: the codes of both are put side by side in bytes first (two
 //    instructions for four pairs), then converted.
+//  * Groups of up to four query heads (FEW) leave half of a product's eight columns idle, and the instructions that would
+//    prepare the operands are what the loop is made of.  So the columns take the heads twice.  Of K, columns 0 to 3 see
+//    Q in the dimensions of even blocks and zeros elsewhere, 4 to 7 those of odd blocks: the codes go into the product
+//    unscaled (whole words of a row, by ldmatrix), and two blocks' sums come out apart and are scaled in fp32.  Of V, columns
+//    0 to 3 sum the even dimensions and 4 to 7 the odd ones: a byte, which holds one of each of one position, is converted
+//    as it is, and the weights of the other position's slots are 0.
 //  * The sixteen score rows of an MMA are the positions in an order in which the loads of K (two positions by four
 //    quarters at a time) and of V (four positions by four eighths) meet no shared-memory bank twice, see position().
-//  * Softmax weights are rounded to f16 in [0, 2^15]; O and the sum of the weights carry that 2^15, which cancels.
+//  * A step is 64 positions of a head, four score tiles whose chains overlap: there are only two consumer warps to a
+//    scheduler, since each holds O for all of its heads (32 and 64 values a lane) and the operands of a tile.  (Sixteen
+//    warps with 32 positions each spill: 62 us where eight with 64 take 58; 38.6 and 34.8 with 28/4 heads.)  Of head_dim
+//    64 all of that is half as much and sixteen warps with 64 positions fit.  A step with at most 32 positions left takes two tiles.
+//  * Softmax weights are rounded to f16 in [0, 2^15], 11 bits of each (8 in the bf16 decode); their sum is taken before the
+//    rounding, so that the LSE is that of the scores.  O and the sum carry 2^(kWeightExp), which cancels.
+//
+// Bound by HBM in the long run (32/8 heads of 128, page size 16: from 8 requests of 32768 positions to 8 of 98304 a
+// position more costs what it does at 6.7 TB/s, 98 % of what a device copy reaches), and by about 12 us that do not
+// depend on the length: the loads that come before the first stage 3, the CTAs' different speeds 2, the last stage's
+// step 1.4, the grid's end 1.7, the merge 2 to 3.  8 requests of 32768 positions 57 us, 302 MB at 5.3 TB/s (78 %); 256 of 512
+// to 4096 122 us, 5.6 TB/s (83 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 51 % used, the conversions'
+// pipe 46 %, the tensor pipe 28 %.  32 requests of 100 to 640 positions, 16/8 heads, at page size 1 11.6 us; 4 short ones of
+// 14/2 heads of 64 7.6 us, a chain of latencies.  With head_dim 64 a box's rows are 32 bytes and a position's boxes cost
+// the copy unit what 128's do: 16 requests of 32000 positions, 16/8 heads 62 us at page size 32, 67 at 16, of 43.5 that their bytes
+// take.
 #include <type_traits>
 
 #include "quant_decode.cuh"
@@ -43,11 +63,11 @@ PKV_DEV int position(int r) {
 template <int D, bool FEW>
 struct Format4 {
   static constexpr int kDim = D, kRowBytes = D / 2, kScaleBytes = D / 16, kStep = 64, kParts = 2;
-  static constexpr int kWarps = D == 64 ? 16 : 8;
-  static constexpr bool kBoxedRows = true, kJoint = true;
+  static constexpr int kWarps = D == 64 ? 16 : 8;  // 16 requests of 32000 positions, 16/8 heads of 64: 62 us with sixteen, 75 with eight
+  static constexpr bool kBoxedRows = true, kJoint = true, kScalesAnywhere = true;
+  static constexpr int kRowPad = 0;
   static constexpr int kTiles = FEW ? D / 32 : D / 16;  // row tiles of O
   static constexpr int kMergeFloats = 4 + 4 * kTiles;
-  static int row_stride(int bytes) { return bytes; }
   template <bool>
   static __device__ void consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                  uint64_t* full, uint64_t* empty, uint64_t* meet_bar);
@@ -103,7 +123,7 @@ PKV_DEV uint32_t mul_f16x2_high(uint32_t a, uint32_t b) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Consumer warps: 32-position steps of one KV head with its G query heads.
+// Consumer warps: steps of kStep positions of one KV head with its G query heads (eight of them, of groups of more).
 // ---------------------------------------------------------------------------------------------
 template <int D, bool FEW>
 template <bool>

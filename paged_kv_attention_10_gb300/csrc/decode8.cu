@@ -40,10 +40,10 @@ using namespace pkv;
 template <int D>
 struct Format8 {
   static constexpr int kDim = D, kRowBytes = D, kScaleBytes = 4, kWarps = 8, kStep = 32, kParts = 1;
-  static constexpr bool kBoxedRows = false, kJoint = false;
+  static constexpr bool kBoxedRows = false, kJoint = false, kScalesAnywhere = false;
   static constexpr int kMergeFloats = 6 + D / 4;
   // the bytes of a row are a multiple of 64: rows 16 bytes off a multiple of 32 keep ldmatrix free of conflicts
-  static int row_stride(int bytes) { return bytes + 16; }
+  static constexpr int kRowPad = 16;
   template <bool TMA>
   static __device__ void consume(const QuantDecodeArgs& a, uint8_t* stages, StageHdr* hdr, uint64_t* hdr_full,
                                  uint64_t* full, uint64_t* empty, uint64_t* meet_bar);

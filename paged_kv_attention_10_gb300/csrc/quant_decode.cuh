@@ -1,18 +1,18 @@
 // Paged decode attention over a quantised cache (one query per request): what the 8-bit and the 4-bit kernels
-// share, which is all but a consumer warp's arithmetic on its 32 positions.
+// share, which is all but a consumer warp's arithmetic on its positions.
 //
 //  * One persistent CTA per SM over an equal share of the stream of slices of 32 positions of all (request,
-//    head group) units; producer warps for K and for V fill a ring of stages, eight or sixteen consumer warps read
-//    them, a second kernel merges the units that the shares cut.
+//    head group) units; one or two producer warps each for K and for V fill a ring of stages, eight or sixteen consumer
+//    warps read them, a second kernel merges the units that the shares cut.
 //  * K and V come in TMA boxes of 32, 16 or 8 rows (the largest that divides the page size), by copies of single
 //    rows for other page sizes.  The scales come into the same stage: by bulk copies beside the boxes where the
-//    CTA takes every KV head (a box's lie side by side then), by cp.async otherwise.
+//    CTA takes every KV head (a box's lie side by side then) and there are enough of them, by cp.async otherwise.
 //
 // A format F is a struct with kDim (head_dim), kRowBytes and kScaleBytes (of one head of one position), kWarps
 // (consumer warps), kStep (positions of a warp's step), kParts (producer warps each for K and V), kJoint (whether K
-// and V share a stage's barriers), kMergeFloats (of a lane's state, see consume),
-// kBoxedRows (whether row copies make boxes of 32 rows of a head in the boxes' swizzle, or rows row_stride(their bytes)
-// apart), and consume<TMA>, a consumer warp.
+// and V share a stage's barriers), kMergeFloats (of a lane's state, see consume), kBoxedRows (whether row copies make boxes of
+// 32 rows of a head in the boxes' swizzle, or whole rows kRowPad bytes apart), kScalesAnywhere (whether the pool's scales
+// need not be 16-byte aligned), and consume<TMA>, a consumer warp.
 #pragma once
 
 #include <atomic>
@@ -78,7 +78,7 @@ struct QuantDecodeArgs {
 // No request has more positions than the pool has rows; a longer kv_lens[b] (reported, its pages run
 // out) must not take the token counter past 31 bits.
 constexpr int kMaxLen = 0x7fff0000;
-constexpr int kSlice = 32;  // positions of a warp's step, and the unit of the work split
+constexpr int kSlice = 32;  // positions: the unit of the work split
 constexpr int kMaxStages = 8;
 
 PKV_DEV void cp_async4(uint32_t dst, const void* src) {
@@ -115,7 +115,7 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
 // places of a box of 32 rows, [head][row] with swizzled pieces, and [row][head].  Lane t has row t's first piece's number in
 // the pool in `from` (~0: no row).  Neighbouring lanes copy neighbouring pieces; everything but the row's address is fixed
 // when the loop is unrolled (with the general loop below, 64 requests of 1000 to 6000 positions of 32/8 heads of 128 at
-// page size 1 took 96 us, 69 so).
+// page size 1 took 96 us; 58 now).
 template <int RH, int PIECES>
 PKV_DEV void copy_round(uint32_t from, const uint8_t* pool, const uint8_t* scale, uint32_t to, uint32_t sto) {
   constexpr int HP = RH / 16, kStep = 32 / PIECES;  // pieces of a head, rows of a round of copies
@@ -279,7 +279,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         const int n = HC * SH;
         const uint8_t* src = scale + (row * a.num_kv_heads + hg * HC) * SH;
         const uint32_t sd = smem_u32(sdst) + (uint32_t)(j * n);
-        if (F::kParts > 1) {
+        if (F::kScalesAnywhere) {
           for (int i = 0; i < n; i += a.scale_piece) copy_piece(sd + i, src + i);
         } else if ((n & 15) == 0) {
           for (int i = 0; i < n; i += 16) cp_async16(sd + i, src + i);
@@ -296,7 +296,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         // Side by side, and enough of them for a bulk copy, which costs about 65 cycles of the copy unit whatever it
         // brings (4 bits, one head of 128 at page size 16, 720000 positions: 42 us with 128-byte copies of them).
         const bool side_by_side =
-            nhg == 1 && (F::kParts == 1 || (a.scales_at_16 && (HC * SH << (31 - __clz(a.box_rows))) >= 512));
+            nhg == 1 && (!F::kScalesAnywhere || (a.scales_at_16 && (HC * SH << (31 - __clz(a.box_rows))) >= 512));
         const uint32_t box = (uint32_t)(HC * RH) << sh, sbox = (uint32_t)(HC * SH) << sh;
 #pragma unroll 1
         for (int i0 = 0; i0 < (kManyBoxes ? nbox : 1); i0 += 32 * P) {
@@ -314,7 +314,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
             if (side_by_side) bulk_g2s(sdst + box_i * sbox, scale + row * a.num_kv_heads * SH, sbox, bar);
           }
           if (!side_by_side) {
-            if (F::kParts > 1 && nhg == 1 && a.scales_at_16 && (sbox & (sbox - 1)) == 0) {
+            if (F::kScalesAnywhere && nhg == 1 && a.scales_at_16 && (sbox & (sbox - 1)) == 0) {
               // 16 bytes a lane of this warp's boxes' scales
               const int psh = 27 - __clz(sbox), mine = min((nbox - i0 + P - 1) / P, 32);
               for (int r = 0; r < mine << psh; r += 32) {
@@ -712,7 +712,7 @@ bool make_plan(int B, int Hq, int Hkv, int ncta, QuantDecodePlan& p, int page_si
   p.W = F::kWarps / (p.HC * p.NT);
   p.Ts = F::kStep * p.W;
   const int RB = p.HC * F::kRowBytes;
-  p.RS = F::kBoxedRows ? RB : F::row_stride(RB);
+  p.RS = RB + F::kRowPad;
   p.R = page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 8;
   p.tma = page_size > 0 && page_size % 8 == 0 && num_pages * (int64_t)page_size < 0x7fffffffLL;
   p.region = p.tma ? (uint32_t)(p.Ts * RB) : (uint32_t)(p.Ts * p.RS);
