@@ -33,7 +33,7 @@
 // position more costs what it does at 6.7 TB/s, 98 % of what a device copy reaches), and by about 12 us that do not
 // depend on the length: the loads that come before the first stage 3, the CTAs' different speeds 2, the last stage's
 // step 1.4, the grid's end 1.7, the merge 2 to 3.  8 requests of 32768 positions 57 us, 302 MB at 5.3 TB/s (78 %); 256 of 512
-// to 4096 122 us, 5.6 TB/s (83 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 51 % used, the conversions'
+// to 4096 122 us, 5.6 TB/s (83 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 56 % used, the conversions'
 // pipe 46 %, the tensor pipe 28 %.  32 requests of 100 to 640 positions, 16/8 heads, at page size 1 11.6 us; 4 short ones of
 // 14/2 heads of 64 7.6 us, a chain of latencies.  With head_dim 64 a box's rows are 32 bytes and a position's boxes cost
 // the copy unit what 128's do: 16 requests of 32000 positions, 16/8 heads 62 us at page size 32, 67 at 16, of 43.5 that their bytes

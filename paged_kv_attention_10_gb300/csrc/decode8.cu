@@ -1,4 +1,4 @@
-// Paged decode attention over an 8-bit cache (one query per request) and its split-KV merge.
+// Paged decode attention over an 8-bit cache (one query per request).
 //
 // What it computes: with the cache rows k8[j] ks[j] and v8[j] vs[j] (e4m3 values and one scale per row
 // and head),  out = sum_j softmax_j(scale q . k8[j] ks[j]) vs[j] v8[j],  page lists, GQA and LSE as in the
@@ -27,9 +27,9 @@
 //  * The rest is the bf16 decode's plan, shared with the 4-bit cache (quant_decode.cuh), with boxes in the 128- or
 //    64-byte swizzle.
 // Measured with 32/8 heads of 128 at page size 16: 8 requests of 32768 positions 90 us, 6.1 TB/s, 90 % of
-// what a device copy reaches; 256 requests of 512 to 4096 positions 196 to 198 us, 93 %.  DRAM reads are the cache's
+// what a device copy reaches; 256 requests of 512 to 4096 positions 194 to 197 us, 93 %.  DRAM reads are the cache's
 // bytes (554 MB of 554), the tensor pipe is 18 % busy, 43 % of the issue slots are used.  Small KV head counts are
-// bound by the producers' issue instead: one head of 128, 720000 positions, 50 us at page size 16, 41 at
+// bound by the producers' issue instead: one head of 128, 720000 positions, 52 us at page size 16, 41 at
 // 64 and 151 at 1 of the 28 that the bytes take; two heads at page size 1 118 of 28.
 #include "quant_decode.cuh"
 

@@ -13,8 +13,8 @@
 // neighbouring pairs (and without a rotation) two chunks side by side.  A warp takes two such steps of
 // one token, all of whose loads are issued before the token's position and slot are needed, and
 // loads the token's cosines and sines once for both.  (With one chunk per lane, a shuffle for the
-// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us, 39 so; 35 now, R 64, 5.8 TB/s,
-// 85 % of what a device copy of 1 GB reaches.  R 128: 33.6 us, 35.2 into an 8-bit cache, 36.7 (73 %) into a 4-bit one,
+// partner and the table read again for every head, 8191 tokens of 32/8 heads took 43 us, 39 so; 34.5 now, R 64, 5.9 TB/s,
+// 86 % of what a device copy of 1 GB reaches.  R 128: 33.6 us, 35.2 into an 8-bit cache, 36.7 (73 %) into a 4-bit one,
 // whose divisions keep the issue slots 60 % busy.  2304 tokens of it: 10.2, 10.7 and 11.1 us, bound by latency, as are
 // the few tokens of a decode step: 2.6 to 3.1 us.)
 // Widths that are no multiple of 16 (half) or 8 (neighbours) take a
