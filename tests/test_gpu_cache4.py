@@ -236,3 +236,21 @@ def test_gather_reports_what_it_skips(lib):
     assert run([0, 1, 2], [0, -1], [4, 3], [0, 4, 8]) == (lib.DEVERR_PAGE_OOB, [0, 1, 2, 3])
     assert run([0, 1, 2], [0, 1], [6, 3], [0, 6, 9]) == (lib.DEVERR_LENGTH, [0, 1, 2, 3, 6, 7, 8])
     assert run([0, 1, 2], [0, 1], [4, 3], [0, 30, 33]) == (lib.DEVERR_ROW_OOB, [0, 1, 2, 3, 30, 31])
+
+
+@pytest.mark.parametrize("k_off,v_off", [(8, 0), (0, 8), (8, 24), (16, 32)])
+def test_gather_into_rows_that_begin_at_16_bytes(lib, k_off, v_off):
+    """Any 16-byte aligned place for the results will do, in a tensor of more rows' memory."""
+    N, Hkv, D, page = 50, 2, 64, 16
+    rng = np.random.default_rng(8)
+    codes = rng.integers(0, 256, (2, 4, page, Hkv, D // 2)).astype(np.uint8)
+    scale = rng.integers(0, 127, (2, 4, page, Hkv, D // 16)).astype(np.uint8)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    flat = [torch.full((N * Hkv * D + 64,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ko, vo = (f[o: o + N * Hkv * D].view(N, Hkv, D) for f, o in zip(flat, (k_off, v_off)))
+    lib.paged_gather_fp4(*[torch.tensor(c).cuda() for c in codes], *[torch.tensor(x).cuda() for x in scale], i32([0, 4]),
+                         i32([2, 0, 3, 1]), i32([N]), i32([0, N]), ko, vo, k_global=0.25, v_global=0.5)
+    for at, (f, out, off) in enumerate(((flat[0], ko, k_off), (flat[1], vo, v_off))):
+        held = cache4.values(codes[at], scale[at], 0.25 * (1 + at))[[2, 0, 3, 1]].reshape(-1, Hkv, D)[:N]
+        assert bits_equal(out, torch.tensor(held).float().to(torch.bfloat16))
+        assert (f[:off] == 7.0).all() and (f[off + N * Hkv * D:] == 7.0).all()
