@@ -601,7 +601,7 @@ pkv_status pkv_paged_decode_fp4(const pkv_pool_fp4* pool, const void* q, int32_t
 /*
  * Movements of rows within a cache, in several tensors at once: the K, V and scale tensors of one layer or of all of them,
  * of any of the formats above.  Every tensor is [num_pages, page_size, ...], contiguous, and holds slot_bytes bytes for
- * a slot (a bf16 K: num_kv_heads * head_dim * 2).  At most 256 tensors a call.
+ * a slot (a bf16 K: num_kv_heads * head_dim * 2).  At most 256 tensors a call, no two of which share memory.
  */
 typedef struct {
   void* base;         /* device; with base and slot_bytes multiples of 16 its bytes move fastest */

@@ -1016,7 +1016,8 @@ def _planes(tensors):
 def copy_pages(tensors, src_pages, dst_pages, rows=None, err_word=None, stream=None) -> None:
     """Copy page src_pages[i] (its first rows[i] rows where rows is given) to page dst_pages[i] (negative = skip) in
     every one of the cache's tensors [num_pages, page_size, ...]: K, V and scales of a layer or of all layers, of any type, at
-    most 256.  No page may be a target twice, or a target and another copy's source (validate_page_copies)."""
+    most 256, no two over the same memory.  No page may be a target twice, or a target and another copy's source
+    (validate_page_copies)."""
     if _done((_checked or _load_checked()).copy_pages(
             tensors, src_pages, dst_pages, rows, err_word, None if stream is None else stream.cuda_stream),
             "pkv_copy_pages"):

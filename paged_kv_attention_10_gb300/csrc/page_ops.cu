@@ -4,6 +4,7 @@
 // Nothing is computed: bytes move, in pieces of the largest power of two up to 16 that divides a tensor's address and its
 // bytes per slot.  Bound by HBM for many pages, by latency for a few.
 #include <algorithm>
+#include <utility>
 
 #include "quant.cuh"
 
@@ -245,6 +246,20 @@ pkv_status check_planes(const pkv_plane* planes, int32_t num_planes, int64_t num
   return num_planes > kMaxPlanes ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
+// Whether two tensors share bytes: those would move twice, and a compaction would read what it has overwritten.
+bool overlap(const pkv_plane* planes, int32_t num_planes, int64_t num_pages, int32_t page_size) {
+  std::pair<uintptr_t, uintptr_t> at[kMaxPlanes];  // first byte, and the one behind the last
+  for (int32_t i = 0; i < num_planes; ++i) {
+    const uint64_t first = (uintptr_t)planes[i].base, page = (uint64_t)planes[i].slot_bytes * page_size;  // 31 bits
+    if ((uint64_t)num_pages > (UINT64_MAX - first) / page) return true;  // no such tensor
+    at[i] = {first, first + num_pages * page};
+  }
+  if (!std::is_sorted(at, at + num_planes)) std::sort(at, at + num_planes);
+  for (int32_t i = 1; i < num_planes; ++i)
+    if (at[i].first < at[i - 1].second) return true;
+  return false;
+}
+
 // Fills the planes, items(i) of each; the sum of those, or -1 where it passes 31 bits.
 template <int N, typename Items>
 int64_t fill_planes(Planes<N>& to, const pkv_plane* planes, int32_t num_planes, Items items) {
@@ -329,7 +344,7 @@ pkv_status pkv_copy_pages(const pkv_plane* planes, int32_t num_planes, int64_t n
   if (s != PKV_OK) return s;
   if (num_copies < 0) return PKV_ERR_INVALID_ARG;
   if (num_copies == 0 || num_planes == 0) return PKV_OK;
-  if (!src_pages || !dst_pages) return PKV_ERR_INVALID_ARG;
+  if (!src_pages || !dst_pages || overlap(planes, num_planes, num_pages, page_size)) return PKV_ERR_INVALID_ARG;
   return num_planes <= kFewPlanes
              ? copy_pages<kFewPlanes>(planes, num_planes, num_pages, page_size, src_pages, dst_pages, rows, num_copies,
                                       err_word, (cudaStream_t)stream)
@@ -347,6 +362,7 @@ pkv_status pkv_compact_accepted(const pkv_plane* planes, int32_t num_planes, int
   if (batch_size < 0 || num_accepted < 0) return PKV_ERR_INVALID_ARG;
   if (batch_size == 0 || num_accepted == 0 || num_planes == 0) return PKV_OK;
   if (!kv_indptr || !kv_indices || !prefix_lens || !accepted_indptr || !accepted) return PKV_ERR_INVALID_ARG;
+  if (overlap(planes, num_planes, num_pages, page_size)) return PKV_ERR_INVALID_ARG;
   return num_planes <= kFewPlanes
              ? compact<kFewPlanes>(planes, num_planes, num_pages, page_size, kv_indptr, kv_indices, prefix_lens,
                                    batch_size, accepted_indptr, accepted, num_accepted, err_word, (cudaStream_t)stream)

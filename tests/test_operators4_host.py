@@ -139,6 +139,16 @@ def test_compact_refusals(pkv, lib):  # noqa: F811
     assert call(planes=_planes(pkv, (BASE, 1 << 26)), count=1, B=1 << 30) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("name", ["pkv_copy_pages", "pkv_compact_accepted"])
+def test_tensors_that_share_memory_are_refused(pkv, lib, name):  # noqa: F811
+    """The same tensor twice, one within another, one that begins on another's last byte, in any order; 4 pages of 16 slots."""
+    pages = 4
+    tail = [SOME, SOME, None, 1] if name == "pkv_copy_pages" else [SOME, SOME, SOME, 1, SOME, SOME, 1]
+    for planes in ([(BASE, 64), (BASE, 64)], [(BASE, 64), (BASE + 1024, 1)], [(BASE + 4095, 8), (BASE, 64)],
+                   [(BASE + 8192, 64), (BASE, 64), (BASE + 4096, 65)], [((1 << 64) - 4096, 65)]):
+        assert getattr(lib, name)(_planes(pkv, *planes), len(planes), pages, 16, *tail, None, None) == INVALID, planes
+
+
 def test_page_copies_are_validated(pkv):  # noqa: F811
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
 
