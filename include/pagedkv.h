@@ -624,7 +624,7 @@ pkv_status pkv_copy_pages(const pkv_plane* planes, int32_t num_planes, int64_t n
 /*
  * Host-side check of a call of pkv_copy_pages, on HOST copies: pages in [0, num_pages) (negative targets are padding),
  * no target twice, no target that is another copy's source.  PKV_OK, or PKV_ERR_INVALID_ARG with the first offending copy in
- * *bad_copy (nullable; -1 when none).
+ * *bad_copy (nullable; -1 when none).  PKV_ERR_UNSUPPORTED without the memory to check so many.
  */
 pkv_status pkv_validate_page_copies(const int32_t* src_pages, const int32_t* dst_pages, int32_t num_copies,
                                     int64_t num_pages, int32_t* bad_copy);

@@ -2,6 +2,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <exception>
 #include <atomic>
 #include <utility>
 #include <vector>
@@ -261,7 +262,11 @@ pkv_status pkv_validate_page_copies(const int32_t* src_pages, const int32_t* dst
   if (num_copies == 0) return PKV_OK;
   if (!src_pages || !dst_pages) return PKV_ERR_INVALID_ARG;
   std::vector<std::pair<int32_t, int32_t>> to;  // (target, copy), without padding
-  to.reserve((size_t)num_copies);
+  try {
+    to.reserve((size_t)num_copies);
+  } catch (const std::exception&) {  // no memory to check so many
+    return PKV_ERR_UNSUPPORTED;
+  }
   int32_t bad = num_copies;  // the first offending copy
   for (int32_t i = 0; i < num_copies; ++i) {
     if (dst_pages[i] < 0) continue;
