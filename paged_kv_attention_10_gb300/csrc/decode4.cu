@@ -35,9 +35,10 @@
 // step 1.4, the grid's end 1.7, the merge 2 to 3.  8 requests of 32768 positions 57 us, 302 MB at 5.3 TB/s (78 %); 256 of 512
 // to 4096 122 us, 5.6 TB/s (83 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 56 % used, the conversions'
 // pipe 46 %, the tensor pipe 28 %.  32 requests of 100 to 640 positions, 16/8 heads, at page size 1 11.6 us; 4 short ones of
-// 14/2 heads of 64 7.6 us, a chain of latencies.  With head_dim 64 a box's rows are 32 bytes and a position's boxes cost
-// the copy unit what 128's do: 16 requests of 32000 positions, 16/8 heads 62 us at page size 32, 67 at 16, of 43.5 that their bytes
-// take.
+// 14/2 heads of 64 7.6 us, a chain of latencies.  With head_dim 64 the softmax of a position, the
+// scales and the loop's frame cost what they cost with 128, so the consumers do not keep up: 16 requests of 32000 positions,
+// 16/8 heads 61 us at page size 32, 63 at 16, of 43.5 that their bytes take and 52 that they take to arrive.  (28/4 heads of 128,
+// 64 requests of 1000 to 6000: 34.6 us, 29.6 to arrive, 19.0 for the bytes.)
 #include <type_traits>
 
 #include "quant_decode.cuh"
@@ -53,11 +54,12 @@ constexpr int kWeightExp = 8, kHeadroom = 7;
 
 // The position, of eight consecutive ones, that row r of a score tile stands for.  K's loads of rows 2i and 2i + 1 and
 // V's of rows 0, 2, 4, 6 and of 1, 3, 5, 7 are then free of bank conflicts.  Rows of 64 bytes, 16-byte pieces p of row t at
-// p ^ (t >> 1 & 3): 0 1 3 2 4 5 7 6; rows of 32 bytes: 0 2 1 3 6 4 7 5.
+// p ^ (t >> 1 & 3): 0 1 3 2 4 5 7 6 where a head has the whole row, 0 1 5 4 6 7 3 2 where it has half; rows of 32 bytes:
+// 0 2 1 3 6 4 7 5.
 template <int D>
-PKV_DEV int position(int r) {
+PKV_DEV int position(int r, bool pair) {
   if (D == 128) return r ^ ((r >> 1) & 1);
-  return (0x57463120 >> (4 * r)) & 7;
+  return ((pair ? 0x23764510 : 0x57463120) >> (4 * r)) & 7;
 }
 
 template <int D, bool FEW>
@@ -147,15 +149,18 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
   // Shared-memory places within a stage of the slice's first eight positions: of K, of V's rows 2c and 2c + 1 (the
   // lane's eighth g), and of the scales of row g.
   const int t0 = si * kStep;
-  const uint32_t first = (uint32_t)(((t0 / a.box_rows) * HC + hl) * a.box_rows + t0 % a.box_rows) * RH;
+  const bool pair = D == 64 && a.pair == 2;  // two heads to a box's row
+  const int in_pair = pair ? hl & 1 : 0;
+  const uint32_t first = (uint32_t)(((t0 / a.box_rows) * HC + hl - in_pair) * a.box_rows + t0 % a.box_rows * (pair ? 2 : 1)) * RH;
   auto piece = [&](int t, int p) -> uint32_t {  // 16-byte piece p of position t of eight, in the boxes' swizzle
-    return first + (uint32_t)(t * RH + ((D == 128 ? p ^ ((t >> 1) & 3) : p ^ ((t >> 2) & 1)) << 4));
+    if (D == 128 || pair) return first + (uint32_t)(t * 64 + (((p + 2 * in_pair) ^ ((t >> 1) & 3)) << 4));
+    return first + (uint32_t)(t * 32 + ((p ^ ((t >> 2) & 1)) << 4));
   };
-  const int pk = position<D>(g), pa = position<D>(2 * c), pb = position<D>(2 * c + 1);
+  const int pk = position<D>(g, pair), pa = position<D>(2 * c, pair), pb = position<D>(2 * c + 1, pair);
   const uint32_t base = smem_u32(stages);
   // FEW: the row that the lane addresses for ldmatrix, of piece lane / 8 of four (of two, of the next eight positions'
   // row from lane 16 on).  Else its own bytes of row g.
-  const int pl = position<D>(lane & 7);
+  const int pl = position<D>(lane & 7, pair);
   const uint32_t k_at =
       base + (FEW ? D == 128 ? piece(pl, lane >> 3) : piece(pl, (lane >> 3) & 1) + (lane >= 16 ? a.eight : 0u)
                   : D == 128 ? piece(pk, c) : piece(pk, c >> 1) + (c & 1) * 8);

@@ -68,6 +68,7 @@ struct QuantDecodeArgs {
   FastDiv piece_div;     // boxed rows: by the 16-byte pieces of a row of HC heads
   int32_t scale_piece;   // bytes of one copy of a row's scales by a lane: 16, 8 or 4
   int32_t scales_at_16;  // whether k_scale and v_scale are 16-byte aligned, and so the scales of every box
+  int32_t pair;          // KV heads side by side in a box's row: 1 or, of 32-byte rows, 2
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // kStep * W
   int32_t num_stages, num_parts;
@@ -310,7 +311,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           if (lane == 0) mbar_expect_tx(bar, n * (box + (side_by_side ? sbox : 0u)));
           __syncwarp();
           if (row >= 0) {
-            tma_load_3d(smem_u32(dst) + box_i * box, tm, 0, (int)row, hg * HC, bar);
+            tma_load_3d(smem_u32(dst) + box_i * box, tm, 0, (int)row, (hg * HC) >> (a.pair - 1), bar);
             if (side_by_side) bulk_g2s(sdst + box_i * sbox, scale + row * a.num_kv_heads * SH, sbox, bar);
           }
           if (!side_by_side) {
@@ -843,18 +844,22 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   a.scales_at_16 = places % 16 == 0;
   if (!p.tma && F::kBoxedRows) p.R = a.box_rows = kSlice;
   const bool boxed = p.tma || F::kBoxedRows;
-  a.eight = boxed ? (uint32_t)(8 * F::kRowBytes * (p.R == 8 ? p.HC : 1)) : (uint32_t)(8 * p.RS);
-  a.sixteen = boxed ? (uint32_t)(16 * F::kRowBytes * (p.R <= 16 ? p.HC : 1)) : (uint32_t)(16 * p.RS);
+  // The copy unit takes a box row by row: rows of 64 bytes, two heads' codes, where the heads pair up (16 requests of 32000
+  // positions, 16/8 heads of 64, 4 bits, page size 16: 67 us with rows of 32 bytes, 63 so; page size 32: 62 and 61).
+  const int pair = p.tma && F::kRowBytes == 32 && p.HC % 2 == 0 ? 2 : 1;
+  a.pair = pair;
+  a.eight = boxed ? (uint32_t)(8 * F::kRowBytes * (p.R == 8 ? p.HC : pair)) : (uint32_t)(8 * p.RS);
+  a.sixteen = boxed ? (uint32_t)(16 * F::kRowBytes * (p.R <= 16 ? p.HC : pair)) : (uint32_t)(16 * p.RS);
   a.stage_tokens = p.Ts;
   a.num_stages = p.NS;
   a.num_parts = (int32_t)p.nparts;
   a.kv_region = p.region;
   a.stage_bytes = p.stage;
   if (p.tma) {
-    const uint64_t Hkv = pool->num_kv_heads, RH = F::kRowBytes;
+    const uint64_t Hkv = pool->num_kv_heads / pair, RH = F::kRowBytes * pair;
     const uint64_t rows = (uint64_t)pool->num_pages * pool->page_size;
-    if (!pkv_host::encode_tmap_3d_u8(&a.tm_k, pool->k, RH, rows, Hkv, Hkv * RH, RH, RH, p.R, p.HC) ||
-        !pkv_host::encode_tmap_3d_u8(&a.tm_v, pool->v, RH, rows, Hkv, Hkv * RH, RH, RH, p.R, p.HC))
+    if (!pkv_host::encode_tmap_3d_u8(&a.tm_k, pool->k, RH, rows, Hkv, Hkv * RH, RH, RH, p.R, p.HC / pair) ||
+        !pkv_host::encode_tmap_3d_u8(&a.tm_v, pool->v, RH, rows, Hkv, Hkv * RH, RH, RH, p.R, p.HC / pair))
       return PKV_ERR_CUDA;
   }
   return p.tma ? launch_quant_decode<F, true>(p, a, c.stream) : launch_quant_decode<F, false>(p, a, c.stream);
