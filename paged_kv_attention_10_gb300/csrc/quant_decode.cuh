@@ -71,7 +71,7 @@ struct QuantDecodeArgs {
   int32_t pair;          // KV heads side by side in a box's row: 1 or, of 32-byte rows, 2
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // kStep * W
-  int32_t num_stages, num_parts;
+  int32_t num_stages, num_parts, num_ctas;
   uint32_t kv_region;    // bytes of the K (or V) part of one stage
   uint32_t stage_bytes;  // K, V and the scales
 };
@@ -146,6 +146,14 @@ PKV_DEV void copy_round(uint32_t from, const uint8_t* pool, const uint8_t* scale
   }
 }
 
+// x / d for x >= 0, d > 0.
+PKV_DEV int64_t quotient(int64_t x, int64_t d) {
+  return (uint64_t)(x | d) >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
+}
+
+// Slices of each of n CTAs, of a stream of T.
+PKV_DEV int64_t share_of(int64_t T, int n) { return max((int64_t)1, quotient(T + n - 1, n)); }
+
 // ---------------------------------------------------------------------------------------------
 // Producer warps, one for K and one for V: each walks the CTA's share of the slice stream and fills
 // its part of the stages; K's also writes the headers.  A stage is a few hundred cycles of address work
@@ -183,8 +191,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
   }
   sumS = warp_sum(sumS);
   const int64_t T = sumS * nhg;
-  int64_t share = (T + gridDim.x - 1) / gridDim.x;
-  if (share < 1) share = 1;
+  const int64_t share = share_of(T, gridDim.x);
   const int64_t c0 = (int64_t)blockIdx.x * share;
   const int64_t c1 = min(T, c0 + share);
 
@@ -569,11 +576,30 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
   constexpr int D = F::kDim;
   constexpr int VPL = D / 32;  // values per lane
   pdl_trigger();
-  pdl_wait();
   const int u = blockIdx.x;
   const int b = u / a.nhg, hg = u % a.nhg;
   const int HQU = a.HC * a.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int len = 0, first = 0, last = -1;
+  if (a.batch <= 32) {
+    // The CTAs that the unit's slices went to, as the producers share them out: before the decode's end, which spares a trip to
+    // L2 after it.  (The lengths are final: every CTA of the decode has waited for what ran before it.)
+    const int n = lane < a.batch ? ld(a.kv_lens + lane) : 0;
+    const uint32_t s = ((uint32_t)min(max(0, n), kMaxLen) + kSlice - 1) / kSlice;
+    uint32_t incl = s;  // at most 2^31
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int64_t share = share_of((int64_t)__shfl_sync(0xffffffffu, incl, 31) * a.nhg, a.num_ctas);
+    const uint32_t mine = __shfl_sync(0xffffffffu, s, b);
+    const int64_t begin = (int64_t)__shfl_sync(0xffffffffu, incl - s, b) * a.nhg + (int64_t)hg * mine;
+    len = __shfl_sync(0xffffffffu, n, b);
+    first = (int)quotient(begin, share) + u;
+    last = (int)quotient(begin + mine - 1, share) + u;
+  }
+  pdl_wait();
   const int part = warp % S;
   const int qhl = (int)blockIdx.y * (8 / S) + warp / S;
   const bool in = qhl < HQU;
@@ -586,7 +612,7 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
     else
       *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(v[0], v[1]);
   };
-  const int len = ld(a.kv_lens + b), first = ld(a.unit_first + u), last = ld(a.unit_last + u);  // in one round of loads
+  if (a.batch > 32) len = ld(a.kv_lens + b), first = ld(a.unit_first + u), last = ld(a.unit_last + u);  // in one round of loads
   if (len <= 0) {
     if (blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, PKV_DEVERR_LENGTH);
     if (in && part == 0) {
@@ -853,6 +879,7 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   a.stage_tokens = p.Ts;
   a.num_stages = p.NS;
   a.num_parts = (int32_t)p.nparts;
+  a.num_ctas = p.ncta;
   a.kv_region = p.region;
   a.stage_bytes = p.stage;
   if (p.tma) {
