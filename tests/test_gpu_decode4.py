@@ -299,3 +299,46 @@ def test_pool_past_32_bits(lib):
     lib.copy_pages(pool, pages, pages + 20)
     o3, l3 = lib.paged_decode_fp4(q, *pool, i32([0, 20]), pages + 20, i32([320]), 0.1, **scales)
     assert torch.equal(o16, o3) and torch.equal(l16, l3)
+
+
+@pytest.mark.parametrize("page", [8, 16, 24, 32, 64])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 2), (14, 2), (9, 3), (24, 4), (64, 4), (30, 6), (12, 12), (40, 10)])
+def test_head_dim_64_with_heads_in_pairs_and_single(lib, Hq, Hkv, page):
+    """An even number of KV heads to a CTA lies in pairs in a box's rows; steps with half and all of their positions."""
+    s = make(Hq + page, (200, 64, 31, 97, 1), Hq, Hkv, 64, page)
+    out, lse, err = decode(lib, s)
+    assert err == 0
+    verify(s, out, lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 1, 128), (7, 1, 64), (32, 8, 128)])
+@pytest.mark.parametrize("B", [1, 9, 10, 32, 33])
+def test_merges_of_few_and_of_many_units(lib, B, Hq, Hkv, D):
+    """One warp and eight for a head's partials; the unit's CTAs worked out by the merge (32 requests) and read (33)."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(1, 3000 // B + 40, B)]
+    lens[B // 2] = 6000 // B + 700
+    if B > 2:
+        lens[0] = 0  # reported; its neighbours' shares do not move
+    s = make(B, lens, Hq, Hkv, D, 16, "any")
+    out, lse, err = decode(lib, s)
+    assert err == (lib.DEVERR_LENGTH if B > 2 else 0)
+    if B > 2:
+        assert not out[0].any() and (lse[0] == float("-inf")).all()
+    keep = [b for b in range(B) if lens[b]]
+    s.update(q=s["q"][keep], lens=[lens[b] for b in keep], rows=[s["rows"][b] for b in keep])
+    verify(s, out[keep], lse[keep])
+
+
+def test_shares_whose_weights_are_all_0(lib):
+    """Scores far below the others': the CTAs that hold them leave weights of 0, not NaN, to the merge."""
+    s = make(12, (9000,), 8, 1, 128, 16)
+    far = np.arange(9000) < 8900
+    s["scale"][0][s["rows"][0][far]] = 0x7E  # 448
+    s["codes"][0][s["rows"][0][far]] = 0xFF  # -6
+    s["pool"][0].copy_(torch.tensor(s["codes"][0]).view(s["pool"][0].shape))
+    s["pool"][2].copy_(torch.tensor(s["scale"][0]).view(s["pool"][2].shape))
+    s["q"] = s["q"].abs() + 1
+    out, lse, err = decode(lib, s)
+    assert err == 0
+    verify(s, out, lse)
