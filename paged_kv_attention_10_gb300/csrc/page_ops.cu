@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(32, kWide ? kCompactWarps : kCompactWarps / 2)
     int p = plane_of(a.planes, r0);
     if constexpr (kWide) {
       // Row by row, with the loads of all of the run's chunks together.  A lane reads and writes the same columns only, so its
-      // own order of loads and stores is all that is needed.  (64 trees in 36 layers 14.3 us, chunk by chunk 15.6; two rows at a
-      // time with 24 warps an SM 14.2.)  Where no chunk is whole several rows at a time are better (2 heads of 64, 32 rows a
-      // tree: 13.1 us, 15.1 row by row).
+      // own order of loads and stores is all that is needed.  (64 trees in 36 layers 14.3 us, chunk by chunk 15.5; over
+      // inputs that L2 does not hold 16.6 and 17.0; two rows at a time with 24 warps an SM 14.2 and 16.2.)  Where no chunk is
+      // whole several rows at a time are better (2 heads of 64, 32 rows a tree: 16 us, 29 row by row).
       char* at[kRun];
       uint32_t slot[kRun];
       bool whole = false;
