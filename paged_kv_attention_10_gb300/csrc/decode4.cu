@@ -17,7 +17,8 @@
 //  * Groups of up to four query heads (FEW) leave half of a product's eight columns idle, and the instructions that would
 //    prepare the operands are what the loop is made of.  So the columns take the heads twice.  Of K, columns 0 to 3 see
 //    Q in the dimensions of even blocks and zeros elsewhere, 4 to 7 those of odd blocks: the codes go into the product
-//    unscaled (whole words of a row, by ldmatrix), and two blocks' sums come out apart and are scaled in fp32.  Of V, columns
+//    unscaled (whole words of a row, by ldmatrix), and two blocks' sums come out apart and are scaled in fp32.  The two lanes
+//    with the parts of the same scores add them up for half of the rows each, so a weight is formed once.  Of V, columns
 //    0 to 3 sum the even dimensions and 4 to 7 the odd ones: a byte, which holds one of each of one position, is converted
 //    as it is, and the weights of the other position's slots are 0.
 //  * The sixteen score rows of an MMA are the positions in an order in which the loads of K (two positions by four
@@ -32,12 +33,12 @@
 // Bound by HBM in the long run (32/8 heads of 128, page size 16: from 8 requests of 32768 positions to 8 of 98304 a
 // position more costs what it does at 6.7 TB/s, 98 % of what a device copy reaches), and by about 12 us that do not
 // depend on the length: the loads that come before the first stage 3, the CTAs' different speeds 2, the last stage's
-// step 1.4, the grid's end 1.7, the merge 2.  8 requests of 32768 positions 55.7 us, 302 MB at 5.4 TB/s (80 %); 256 of 512
-// to 4096 121 us, 5.7 TB/s (83 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 56 % used, the conversions'
+// step 1.4, the grid's end 1.7, the merge 2.  8 requests of 32768 positions 55.5 us, 302 MB at 5.4 TB/s (80 %); 256 of 512
+// to 4096 120 us, 5.7 TB/s (84 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 56 % used, the conversions'
 // pipe 46 %, the tensor pipe 28 %.  32 requests of 100 to 640 positions, 16/8 heads, at page size 1 11.3 us; 4 short ones of
 // 14/2 heads of 64 7.3 us, a chain of latencies.  With head_dim 64 the softmax of a position, the
 // scales and the loop's frame cost what they cost with 128, so the consumers do not keep up: 16 requests of 32000 positions,
-// 16/8 heads 61 us at page size 32, 63 at 16, of 43.5 that their bytes take and 52 that they take to arrive.  (28/4 heads of 128,
+// 16/8 heads 59 us at page size 32, 62 at 16, of 43.5 that their bytes take and 52 that they take to arrive.  (28/4 heads of 128,
 // 64 requests of 1000 to 6000: 34.6 us, 29.6 to arrive, 19.0 for the bytes.)
 #include <type_traits>
 
@@ -106,6 +107,13 @@ PKV_DEV void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Four bytes of a and b (4 to 7), each by its nibble of `which`; with 8 added, its sign in all eight bits.
+PKV_DEV uint32_t prmt(uint32_t a, uint32_t b, uint32_t which) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(which));
+  return d;
+}
+
 PKV_DEV float2 half2_to_floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
 // The product of an f16 pair with the low (high) half of another, which the instruction reads in place.
@@ -172,9 +180,13 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
   auto tile_off = [&](int hf) -> uint32_t { return (hf & 1) * a.sixteen + (hf >> 1) * (uint32_t)(HC * 32 * RH); };
   // two scales of a row: of the blocks 2c and 2c + 1 of eight, or twice of block c of four
   auto scales = [&](uint32_t at) -> uint32_t { return D == 128 ? lds_u16(at + 2 * c) : lds_u8(at + c) * 0x101u; };
-  // FEW: which bytes of a row's scales are those of the lane's blocks; where the halves of a pair of weights go in B
+  // FEW: which bytes of a row's scales are those of the lane's blocks, and how the weights of rows 2c and 2c + 1 of each half
+  // of a tile go into B, out of the two halves' registers (a 9 takes a weight's sign, which is 0).
   const uint32_t pick = c < 2 ? 0x6420u : 0x7531u;
-  const uint32_t put_a = g < 4 ? 0x4410u : 0x1044u, put_b = g < 4 ? 0x4432u : 0x3244u;
+  const uint32_t put_a[2] = {g < 4 ? 0x9910u : 0x5499u, g < 4 ? 0x9954u : 0x1099u};
+  const uint32_t put_b[2] = {g < 4 ? 0x9932u : 0x7699u, g < 4 ? 0x9976u : 0x3299u};
+  constexpr int NR = FEW ? 1 : 2;        // rows of a tile that a lane has the scores of: g and g + 8, or one of them
+  const int row8 = FEW && c >= 2 ? 8 : 0;  // FEW: g + 8 in the upper columns' lanes
 
   uint32_t qf[NM][2];
   float qs[2];       // score scale (log2 units) of the lane's two heads, positive
@@ -254,7 +266,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
       // A step of NH tiles of 16 positions.
       auto step = [&](auto tiles) {
         constexpr int NH = decltype(tiles)::value;
-        float s[NH][4];
+        float s[NH][2 * NR];
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
           const uint32_t ka = k_at + at + tile_off(hf), sa = s_at + at + 2 * hf * s_eight;
@@ -281,6 +293,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
                 ks[i][2 * j + 1] = f.y;
               }
             }
+            float t[4];
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
               uint32_t x[4], y[4];
@@ -290,10 +303,12 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
               mma_f16_16816_zero(d, x[0], y[0], x[1], y[1], qf[2 * j][0], qf[2 * j][1]);
               mma_f16_16816(d, x[2], y[2], x[3], y[3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[hf][i] = j == 0 ? d[i] * ks[i / 2][0] : fmaf(d[i], ks[i / 2][j], s[hf][i]);
+              for (int i = 0; i < 4; ++i) t[i] = j == 0 ? d[i] * ks[i / 2][0] : fmaf(d[i], ks[i / 2][j], t[i]);
             }
+            // lanes c and c ^ 2 have the two parts of the same scores: one adds them up for row g, the other for g + 8
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[hf][i] += __shfl_xor_sync(0xffffffffu, s[hf][i], 2);
+            for (int k = 0; k < 2; ++k)
+              s[hf][k] = (row8 ? t[2 + k] : t[k]) + __shfl_xor_sync(0xffffffffu, row8 ? t[k] : t[2 + k], 2);
           } else {
             uint32_t w[2][KW];  // rows g and g + 8: codes, and the scales of the two halves of the lane's quarter
             lds<KW>(ka, w[0]);
@@ -322,21 +337,21 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
 #pragma unroll
           for (int hf = 0; hf < NH; ++hf)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (16 * hf + 8 * (i >> 1) + pk >= nv) s[hf][i] = -INFINITY;
+            for (int i = 0; i < 2 * NR; ++i)
+              if (16 * hf + 8 * (i >> 1) + row8 + pk >= nv) s[hf][i] = -INFINITY;
         }
         float top[2];
         bool far = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          top[k] = fmaxf(s[0][k], s[0][2 + k]);
+          top[k] = s[0][k];
 #pragma unroll
-          for (int hf = 1; hf < NH; ++hf) top[k] = fmaxf(top[k], fmaxf(s[hf][k], s[hf][2 + k]));
+          for (int i = 1; i < NR * NH; ++i) top[k] = fmaxf(top[k], s[i / NR][2 * (i % NR) + k]);
           far |= fmaf(top[k], qs[k], -m[k]) > (float)kHeadroom;
         }
         if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1)
+          for (int off = FEW ? 2 : 4; off < 32; off <<= 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], off));
           float corr[2];
@@ -356,12 +371,16 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < NR; ++i) {
             const float w0 = ex2(fmaf(s[hf][2 * i], qs[0], b0)), w1 = ex2(fmaf(s[hf][2 * i + 1], qs[1], b1));
             l[0] += w0;
             l[1] += w1;
             bp[hf][i] = movmatrix_t(pack_f16x2(w0, w1));
           }
+        if constexpr (FEW) {  // column g's weights of one half of the tile's rows; of the other from the lanes of column g ^ 4
+#pragma unroll
+          for (int hf = 0; hf < NH; ++hf) bp[hf][1] = __shfl_xor_sync(0xffffffffu, bp[hf][0], 16);
+        }
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
           const uint32_t aa = va_at + at + tile_off(hf), ab = vb_at + at + tile_off(hf);
@@ -382,7 +401,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               // row 2c's weight and row 2c + 1's, for the even dims in columns 0 to 3, for the odd ones in 4 to 7
-              const uint32_t b0 = __byte_perm(bp[hf][i], 0, put_a), b1 = __byte_perm(bp[hf][i], 0, put_b);
+              const uint32_t b0 = prmt(bp[hf][0], bp[hf][1], put_a[i]), b1 = prmt(bp[hf][0], bp[hf][1], put_b[i]);
 #pragma unroll
               for (int j = 0; j < VW; ++j) {
                 uint32_t x[4], y[4];
@@ -484,7 +503,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
     if (si == 0) {
       const bool whole = (h.flags & kStartsUnit) && (h.flags & kEndsUnit);
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
+      for (int off = FEW ? 2 : 4; off < 32; off <<= 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
       // Four consecutive dims g D/8 + 4j .. + 3 of query head `col` of the group, in r[j].
