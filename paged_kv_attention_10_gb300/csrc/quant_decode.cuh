@@ -370,12 +370,11 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
           const uint32_t sto = smem_u32(sdst) + (uint32_t)(r * 32 * HC) * SH;
           if (narrow && native) {
             const uint32_t f = row < 0 ? ~0u : (uint32_t)(from * HP);
-            switch (pieces) {
-              case 2: copy_round<RH, 2>(f, pool, scale, to, sto); break;
-              case 4: copy_round<RH, 4>(f, pool, scale, to, sto); break;
-              case 8: copy_round<RH, 8>(f, pool, scale, to, sto); break;
-              case 16: copy_round<RH, 16>(f, pool, scale, to, sto); break;
-              default: copy_round<RH, 32>(f, pool, scale, to, sto);
+            switch (HC) {
+              case 1: copy_round<RH, HP>(f, pool, scale, to, sto); break;
+              case 2: copy_round<RH, 2 * HP>(f, pool, scale, to, sto); break;
+              case 4: copy_round<RH, 4 * HP>(f, pool, scale, to, sto); break;
+              default: copy_round<RH, 8 * HP>(f, pool, scale, to, sto);
             }
           } else {
 #pragma unroll 4
