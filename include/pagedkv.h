@@ -508,7 +508,8 @@ pkv_status pkv_rotary_kv_append_fp8(const pkv_pool_fp8* pool, const void* k_new,
  * of k_out and v_out as bf16(k8 * k_scale).  Other rows are left as they were.  With out_indptr at
  * multiples of a page size the copy is a paged cache itself, for the calls that read bf16 (an
  * extend over cached prefixes, say).
- *   kv_indptr, kv_indices, kv_lens  as for pkv_paged_gather; kv_lens[b] >= 0
+ *   kv_indptr, kv_indices, kv_lens  as for pkv_paged_gather; kv_lens[b] >= 0, and kv_indices may be NULL where no request
+ *                 has a page
  *   out_indptr    int32 [batch_size+1] (device), non-decreasing
  *   k_out, v_out  bf16 [num_out_rows, num_kv_heads, head_dim] (device), 16-byte aligned
  *   err_word      nullable; PKV_DEVERR_LENGTH for a request longer than its pages or than

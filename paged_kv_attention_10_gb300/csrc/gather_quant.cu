@@ -106,7 +106,7 @@ PKV_DEV int64_t find_slot(const GatherArgs& a, int32_t row) {
   if (j < 0 || j >= len) return -1;
   uint32_t pidx, in_page;
   a.page_div.divmod((uint32_t)j, pidx, in_page);
-  if ((int32_t)pidx >= np) {
+  if ((int32_t)pidx >= np || !a.kv_indices) {
     report(a.err_word, PKV_DEVERR_LENGTH);
     return -1;
   }
@@ -180,7 +180,7 @@ pkv_status gather(const Pool* pool, int32_t row_bytes, float k_global, float v_g
                   int32_t num_out_rows, void* k_out, void* v_out, uint32_t* err_word, void* stream) {
   if (batch_size < 0 || num_out_rows < 0) return PKV_ERR_INVALID_ARG;
   if (batch_size == 0 || num_out_rows == 0) return PKV_OK;
-  if (!kv_indptr || !kv_indices || !kv_lens || !out_indptr || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
+  if (!kv_indptr || !kv_lens || !out_indptr || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
   if (!pkv_host::aligned16(k_out) || !pkv_host::aligned16(v_out)) return PKV_ERR_INVALID_ARG;
   const int64_t cpr = (int64_t)pool->num_kv_heads * (row_bytes / 8);
   if (cpr > 0x7fffffffLL / kMostRows || num_out_rows > 0x7fffffff - kMostRows) return PKV_ERR_UNSUPPORTED;

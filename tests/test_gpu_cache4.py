@@ -254,3 +254,21 @@ def test_gather_into_rows_that_begin_at_16_bytes(lib, k_off, v_off):
         held = cache4.values(codes[at], scale[at], 0.25 * (1 + at))[[2, 0, 3, 1]].reshape(-1, Hkv, D)[:N]
         assert bits_equal(out, torch.tensor(held).float().to(torch.bfloat16))
         assert (f[:off] == 7.0).all() and (f[off + N * Hkv * D:] == 7.0).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_gather_of_empty_prefixes_alone(lib, bits):
+    """A batch in which nobody has a page: an empty list of pages, and rows that stay what they were."""
+    pool = empty(2, 16, 2, 64) if bits == 4 else [torch.zeros(2, 16, 2, 64, dtype=torch.float8_e4m3fn, device="cuda")] * 2 + [
+        torch.ones(2, 16, 2, device="cuda")] * 2
+    gather = lib.paged_gather_fp4 if bits == 4 else lib.paged_gather_fp8
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ko = torch.full((6, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    vo, err = ko.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    gather(*pool, i32(0, 0, 0), i32(), i32(0, 0), i32(0, 3, 6), ko, vo, err_word=err)
+    assert int(err) == 0
+    gather(*pool, i32(0, 0, 0), i32(), i32(0, 2), i32(0, 3, 6), ko, vo, err_word=err)
+    assert int(err) == lib.DEVERR_LENGTH
+    gather(*pool, i32(0, 1, 1), i32(), i32(2, 0), i32(0, 3, 6), ko, vo, err_word=err)  # a list that is not there
+    assert int(err) == lib.DEVERR_LENGTH
+    assert (ko == 3.0).all() and (vo == 3.0).all()
