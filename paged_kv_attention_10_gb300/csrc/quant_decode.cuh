@@ -556,8 +556,16 @@ __global__ void __launch_bounds__((F::kWarps + 2 * F::kParts) * 32, 1) quant_dec
   if (warp >= NC) {
     const int p = warp - NC;  // K's and V's in turn
     const bool v = p & 1;
-    quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, v && !F::kJoint ? full + NS : full,
-                                  v && !F::kJoint ? empty + NS : empty, v, F::kParts == 1 ? 0 : p >> 1);
+    uint64_t *v_full = F::kJoint ? full : full + NS, *v_empty = F::kJoint ? empty : empty + NS;
+    // One producer each: the code twice, each for its tensor (8 bits, one KV head at page size 16, 720000 positions: 49.4 us, 51.7
+    // with one for both).  Two each: once, since four warps in two copies of it miss the instruction cache (4 bits, 64 requests of
+    // 1000 to 6000, 32/8 heads, page size 1: 58 us, 65 with two; 8 of 200 to 900 of one head 8.2, 9.2).
+    if constexpr (F::kParts == 1) {
+      if (v) quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, v_full, v_empty, true, 0);
+      else quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, full, empty, false, 0);
+    } else {
+      quant_decode_producer<F, TMA>(a, stages, hdr, hdr_full, v ? v_full : full, v ? v_empty : empty, v, p >> 1);
+    }
   } else {
     F::template consume<TMA>(a, stages, hdr, hdr_full, full, empty, meet_bar);
   }
