@@ -20,7 +20,8 @@
 //    unscaled (whole words of a row, by ldmatrix), and two blocks' sums come out apart and are scaled in fp32.  The two lanes
 //    with the parts of the same scores add them up for half of the rows each, so a weight is formed once.  Of V, columns
 //    0 to 3 sum the even dimensions and 4 to 7 the odd ones: a byte, which holds one of each of one position, is converted
-//    as it is, and the weights of the other position's slots are 0.
+//    as it is, and the weights of the other position's slots are 0.  (8 requests of 32768, 32/8 heads: 56.2 us, 58.6 as for
+//    larger groups; 16 of 32000, 16/8 heads of 64: 62.0, 66.7; one KV head at page size 64: 28.3, 30.7.)
 //  * The sixteen score rows of an MMA are the positions in an order in which the loads of K (two positions by four
 //    quarters at a time) and of V (four positions by four eighths) meet no shared-memory bank twice, see position().
 //  * A step is 64 positions of a head, four score tiles whose chains overlap: there are only two consumer warps to a

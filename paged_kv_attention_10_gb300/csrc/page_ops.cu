@@ -13,7 +13,7 @@ namespace {
 using namespace pkv;
 
 // The tensors of a call.  N: how many it has room for; a call of a few (one layer) does not carry the room of all layers
-// through its launch.
+// through its launch (a copy of 4 pages 2.1 us, 2.4 with all of it).
 template <int N>
 struct Planes {
   void* base[N];
@@ -36,8 +36,9 @@ PKV_DEV int plane_of(const Planes<N>& p, uint32_t r) {
   return lo;
 }
 
-// Pieces that a lane has in flight.
-constexpr int kFlight = 8;
+// Pieces that a lane has in flight, and so the tile of a warp (256 pages in 36 layers: 91.5 us with eight, 91.1 with four, 92.7
+// with two and 118.7 with one; 4 pages of one layer 2.1, 1.7, 1.6 and 1.5).
+constexpr int kFlight = 4;
 
 // ---------------------------------------------------------------------------------------------
 // Copies of pages.  A warp takes a tile of one page of one tensor: 32 lanes times kFlight pieces.
