@@ -589,7 +589,8 @@ pkv_status pkv_paged_gather_fp4(const pkv_pool_fp4* pool, const int32_t* kv_indp
 /*
  * Paged decode over a 4-bit cache: pkv_paged_decode_fp8 over its values.  Arguments, limits and errors as there.  The
  * softmax weights are rounded to f16 for the second product (11 bits; one below 2^-32 of the largest may become 0); sums are
- * fp32.  A NaN in K makes the rows of its KV head's queries NaN, one in V the sixteen values of its block.
+ * fp32.  A NaN in K makes the rows of its KV head's queries NaN, one in V the sixteen values of its block.  Scores are fp32
+ * numbers: a row where sm_scale k_global |q| |k| passes their range may be NaN.
  */
 size_t pkv_decode_fp4_workspace_size(int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
                                      int32_t head_dim);
