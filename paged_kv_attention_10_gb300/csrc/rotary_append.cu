@@ -99,10 +99,11 @@ PKV_DEV float max_abs(float m, float x) {
 
 // x / d, correctly rounded where r = 1 / d is and nothing overflows or loses bits to underflow: a product with the reciprocal
 // and one correction by the remainder (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990).  x r alone is off the ties that x / d meets (1 / 1.875: 2.5 * 1.875 becomes 2.5000002).
+// processor", 1990).  x r alone is off the ties that x / d meets (1 / 1.875: 2.5 * 1.875 becomes 2.5000002).  d > 0; the remainder
+// is y d - x and is subtracted, so that a zero x keeps its sign (a remainder x - y d of +0 would be added to -0).
 PKV_DEV float quotient(float x, float d, float r) {
   const float y = x * r;
-  return fmaf(fmaf(-y, d, x), r, y);
+  return fmaf(fmaf(y, d, -x), -r, y);
 }
 
 // The e4m3 scale of a 4-bit block: its largest |x| over 6 g (d, and r = 1 / d).
