@@ -71,7 +71,7 @@ struct QuantDecodeArgs {
   int32_t pair;          // KV heads side by side in a box's row: 1 or, of 32-byte rows, 2
   uint32_t eight, sixteen;  // shared-memory bytes from positions 0 .. 7 of a slice to the next eight, and to the next sixteen
   int32_t stage_tokens;  // kStep * W
-  int32_t num_stages, num_parts, num_ctas;
+  int32_t num_stages, num_parts;
   uint32_t kv_region;    // bytes of the K (or V) part of one stage
   uint32_t stage_bytes;  // K, V and the scales
 };
@@ -146,13 +146,11 @@ PKV_DEV void copy_round(uint32_t from, const uint8_t* pool, const uint8_t* scale
   }
 }
 
-// x / d for x >= 0, d > 0.
-PKV_DEV int64_t quotient(int64_t x, int64_t d) {
-  return (uint64_t)(x | d) >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
-}
-
 // Slices of each of n CTAs, of a stream of T.
-PKV_DEV int64_t share_of(int64_t T, int n) { return max((int64_t)1, quotient(T + n - 1, n)); }
+PKV_DEV int64_t share_of(int64_t T, uint32_t n) {
+  const uint64_t x = (uint64_t)(T + n - 1);
+  return max((int64_t)1, (int64_t)(x >> 32 ? x / n : (uint32_t)x / n));
+}
 
 // ---------------------------------------------------------------------------------------------
 // Producer warps, one for K and one for V: each walks the CTA's share of the slice stream and fills
@@ -588,26 +586,6 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
   const int b = u / a.nhg, hg = u % a.nhg;
   const int HQU = a.HC * a.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int len = 0, first = 0, last = -1;
-  if (a.batch <= 32) {
-    // The CTAs that the unit's slices went to, as the producers share them out: before the decode's end, which spares a trip to
-    // L2 after it (4 short requests 7.3 us, 7.6 without).  More requests would each be a round of loads.  (The lengths are
-    // final: every CTA of the decode has waited for what ran before it.)
-    const int n = lane < a.batch ? ld(a.kv_lens + lane) : 0;
-    const uint32_t s = ((uint32_t)min(max(0, n), kMaxLen) + kSlice - 1) / kSlice;
-    uint32_t incl = s;  // at most 2^31
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const int64_t share = share_of((int64_t)__shfl_sync(0xffffffffu, incl, 31) * a.nhg, a.num_ctas);
-    const uint32_t mine = __shfl_sync(0xffffffffu, s, b);
-    const int64_t begin = (int64_t)__shfl_sync(0xffffffffu, incl - s, b) * a.nhg + (int64_t)hg * mine;
-    len = __shfl_sync(0xffffffffu, n, b);
-    first = (int)quotient(begin, share) + u;
-    last = (int)quotient(begin + mine - 1, share) + u;
-  }
   pdl_wait();
   const int part = warp % S;
   const int qhl = (int)blockIdx.y * (8 / S) + warp / S;
@@ -621,7 +599,7 @@ __global__ void __launch_bounds__(256) quant_decode_merge_kernel(const __grid_co
     else
       *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(v[0], v[1]);
   };
-  if (a.batch > 32) len = ld(a.kv_lens + b), first = ld(a.unit_first + u), last = ld(a.unit_last + u);  // in one round of loads
+  const int len = ld(a.kv_lens + b), first = ld(a.unit_first + u), last = ld(a.unit_last + u);  // in one round of loads
   if (len <= 0) {
     if (blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, PKV_DEVERR_LENGTH);
     if (in && part == 0) {
@@ -888,7 +866,6 @@ pkv_status run_quant_decode(const Pool* pool, const QuantDecodeCall& c, float sc
   a.stage_tokens = p.Ts;
   a.num_stages = p.NS;
   a.num_parts = (int32_t)p.nparts;
-  a.num_ctas = p.ncta;
   a.kv_region = p.region;
   a.stage_bytes = p.stage;
   if (p.tma) {
