@@ -166,7 +166,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
   const int lane = threadIdx.x & 31;
   const int NS = a.num_stages, Ts = a.stage_tokens, HC = a.HC, nhg = a.nhg;
   const int W = Ts / kSlice;  // rounds of 32 positions
-  constexpr bool kManyBoxes = F::kWarps * F::kStep > 256;  // a stage may have more boxes than a warp has lanes
+  constexpr bool kManyBoxes = F::kWarps * F::kStep > 256 * P;  // a stage may have more boxes than the tensor's warps have lanes
   const uint32_t region = a.kv_region;
   const CUtensorMap* tm = v ? &a.tm_v : &a.tm_k;
   const uint8_t* pool = v ? a.v_pool : a.k_pool;
@@ -297,7 +297,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
         // Lane i fetches box i, box_rows tokens inside one page, and their scales, which lie side by side when
         // the CTA takes all KV heads.  (One lookup a stage: with one per 32 tokens the eight of a stage of
         // one KV head took 4 us, and 720000 positions of it 96 us; 48 now, of the 28 that their bytes take.)
-        // Only boxes of 8 rows in a stage of 512 positions are more than the lanes.
+        // Only boxes of 8 rows in a stage of 1024 positions (one KV head of 64, 4 bits) are more than the two warps' lanes.
         const int sh = 31 - __clz(a.box_rows), nbox = Ts >> sh;
         // Side by side, and enough of them for a bulk copy, which costs about 65 cycles of the copy unit whatever it
         // brings (4 bits: one head of 128 at page size 16, 720000 positions, 36.1 us with copies of 128 bytes and 34.2 with
@@ -335,7 +335,7 @@ __device__ void quant_decode_producer(const QuantDecodeArgs& a, uint8_t* stages,
               continue;
             }
             // lane by lane the rows of this warp's boxes
-            const int rounds = kManyBoxes ? min((nbox - i0 + P - 1) / P, 32) << sh : Ts;
+            const int rounds = kManyBoxes ? min((nbox - i0 + P - 1) / P, 32) << sh : Ts / P;
             for (int r = 0; r < rounds; r += 32) {
               const int k = r + lane, j = (i0 + P * (k >> sh) + part) * a.box_rows + (k & (a.box_rows - 1));
               const int first_row = __shfl_sync(0xffffffffu, (int)row, (k >> sh) & 31);
