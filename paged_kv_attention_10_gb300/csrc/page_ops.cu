@@ -36,8 +36,9 @@ PKV_DEV int plane_of(const Planes<N>& p, uint32_t r) {
   return lo;
 }
 
-// Pieces that a lane has in flight, and so the tile of a warp (256 pages in 36 layers: 91.5 us with eight, 91.1 with four, 92.7
-// with two and 118.7 with one; 4 pages of one layer 2.1, 1.7, 1.6 and 1.5).
+// Pieces that a lane has in flight, and so the tile of a warp.  With eight, four, two and one: 256 pages of 16 slots of a 4-bit
+// cache, 8 heads of 128, 36 layers, among the sources pages that several copies read, 48.7, 48.4, 51.5 and 68.2 us; of a bf16
+// cache, 8 heads of 64, every page once, 91.5, 91.2, 92.6 and 115.9; 4 pages of bf16, one layer, on the device alone, 2.0, 1.7, 1.5 and 1.5.
 constexpr int kFlight = 4;
 
 // ---------------------------------------------------------------------------------------------
