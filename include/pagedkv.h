@@ -559,7 +559,7 @@ typedef struct {
   int32_t page_size;    /* >= 1 */
   int32_t num_kv_heads; /* >= 1 */
   int32_t head_dim;     /* attention: 64 or 128; append and read-back: any multiple of 16 */
-  float k_global;       /* in [2^-64, 2^64] */
+  float k_global;       /* in [2^-64, 2^64]; the same in every call on the cache, which does not hold it */
   float v_global;
 } pkv_pool_fp4;
 

@@ -922,7 +922,9 @@ def kv_append_fp4(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, 
                   v_global: float = 1.0, err_word=None, stream=None) -> None:
     """Quantise k_new[t], v_new[t] to e2m1 with an e4m3 scale for every 16 values (and the cache's own scales k_global,
     v_global) and write them into pool slot slot_mapping[t] (negative = skip).  k_pool and v_pool are
-    uint8 [num_pages, page_size, num_kv_heads, head_dim / 2], k_scale and v_scale float8_e4m3fn [..., head_dim / 16]."""
+    uint8 [num_pages, page_size, num_kv_heads, head_dim / 2], k_scale and v_scale float8_e4m3fn [..., head_dim / 16].
+    k_global and v_global belong to the cache: every call on it, of any kind, has to be given the same two (nothing in the
+    cache tells a call that left one out); 1.0 is for a cache whose calls all leave them out."""
     if _done((_checked or _load_checked()).kv_append_fp4(
             k_pool, v_pool, k_scale, v_scale, k_global, v_global, k_new, v_new, slot_mapping, err_word,
             None if stream is None else stream.cuda_stream), "pkv_kv_append_fp4"):
@@ -935,7 +937,8 @@ def kv_append_fp4(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, 
 def rotary_kv_append_fp4(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, positions, cos_sin,
                          q=None, q_out=None, interleaved: bool = False, k_global: float = 1.0, v_global: float = 1.0,
                          err_word=None, stream=None) -> None:
-    """rotary_kv_append into a 4-bit cache: K (rotated) and V quantised as by kv_append_fp4."""
+    """rotary_kv_append into a 4-bit cache: K (rotated) and V quantised as by kv_append_fp4, with the cache's own k_global and
+    v_global as there."""
     if _done((_checked or _load_checked()).rotary_kv_append_fp4(
             k_pool, v_pool, k_scale, v_scale, k_global, v_global, k_new, v_new, slot_mapping, positions, cos_sin, q,
             q_out, bool(interleaved), err_word, None if stream is None else stream.cuda_stream),
@@ -963,7 +966,8 @@ def paged_gather_fp4(k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices, kv
                      v_out, k_global: float = 1.0, v_global: float = 1.0, err_word=None,
                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Read a 4-bit cache back as bf16: position j of request b goes to row out_indptr[b] + j of
-    k_out/v_out [num_out_rows, num_kv_heads, head_dim]; other rows are left as they were."""
+    k_out/v_out [num_out_rows, num_kv_heads, head_dim]; other rows are left as they were.  k_global and v_global are those that
+    the cache was written with."""
     if _done((_checked or _load_checked()).paged_gather_fp4(
             k_pool, v_pool, k_scale, v_scale, k_global, v_global, kv_indptr, kv_indices, kv_lens, out_indptr, k_out,
             v_out, err_word, None if stream is None else stream.cuda_stream), "pkv_paged_gather_fp4"):
@@ -983,7 +987,7 @@ def paged_decode_fp4(q, k_pool, v_pool, k_scale, v_scale, kv_indptr, kv_indices,
                      out=None, lse=None, workspace=None, k_global: float = 1.0, v_global: float = 1.0, err_word=None,
                      stream=None, return_lse=True, max_ctas=0):
     """Decode attention of q [B, Hq, D] over each request's pages of a 4-bit cache.  Returns
-    (out, lse); arguments as for paged_decode, and the cache's own scales."""
+    (out, lse); arguments as for paged_decode, and the k_global and v_global that the cache was written with."""
     if out is not None and workspace is not None and (lse is not None or not return_lse) and _done(
             (_checked or _load_checked()).paged_decode_fp4(
                 k_pool, v_pool, k_scale, v_scale, k_global, v_global, q, out, lse, kv_indptr, kv_indices, kv_lens,

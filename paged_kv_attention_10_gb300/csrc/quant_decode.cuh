@@ -1,5 +1,5 @@
 // Paged decode attention over a quantised cache (one query per request): what the 8-bit and the 4-bit kernels
-// share, which is all but a consumer warp's arithmetic on its positions.
+// share, which is all but a consumer warp: its arithmetic on its positions, and the join of the warps of a head, whose states differ.
 //
 //  * One persistent CTA per SM over an equal share of the stream of slices of 32 positions of all (request,
 //    head group) units; one or two producer warps each for K and for V fill a ring of stages, eight or sixteen consumer
