@@ -49,15 +49,14 @@ namespace {
 
 using namespace pkv;
 
-// The weights of a row are 2^(x - m + kWeightExp) with m a score near the largest so far: m moves only when a score is more
-// than kHeadroom above it, so that most steps need no maximum over lanes and no rescaling.  Weights then stand in [0, 2^15],
-// the top of f16's range; one as small as 2^-32 of m's own is still counted.
+// The weights of a row are 2^((s - m) scale + kWeightExp), s a product before its scale and m one near the largest so far: m moves
+// only when a score is more than kHeadroom above it, so that most steps need no maximum over lanes and no rescaling.  Weights then
+// stand in [0, 2^15], the top of f16's range; one as small as 2^-32 of m's own is still counted.  The difference comes first since it
+// is exact next to m, whatever the scores' size.  As an fma of s with kWeightExp - m scale, one instruction less, an exponent is
+// off by a unit in the last place of the score, at 2^27 (base 2) by 16: past f16's largest, or 0.  (So, and as that fma: 8 requests
+// of 32768, 32/8 heads, 56.0 and 55.8 us; 256 of 512 to 4096 118.8 both; 64 of 1000 to 6000, 28/4 heads, 34.5 both.  The fma below
+// scores of 2^20 and the difference above: 56.2, 120.0 and 34.9.)
 constexpr int kWeightExp = 8, kHeadroom = 7;
-// x - m + kWeightExp is one fma of the product and kWeightExp - m.  The product is not rounded there, as m was, and the
-// difference is: an exponent is off by a unit in the last place of m, 2^-3 below 2^20, and stays below 16.  At 2^27 it would be
-// off by 16, a weight past f16's largest or 0.  From 2^20 on the product is rounded and m subtracted, which is exact next to m, before
-// the constant is added.
-constexpr float kExactBelow = 1048576.f;
 
 // The position, of eight consecutive ones, that row r of a score tile stands for.  K's loads of rows 2i and 2i + 1 and
 // V's of rows 0, 2, 4, 6 and of 1, 3, 5, 7 are then free of bank conflicts.  Rows of 64 bytes, 16-byte pieces p of row t at
@@ -197,7 +196,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
   uint32_t qf[NM][2];
   float qs[2];       // score scale (log2 units) of the lane's two heads, positive
   float o[NT][4];
-  float m[2], l[2];  // what the weights are relative to, w = 2^(x - m + kWeightExp), and the sum of the lane's own
+  float m[2], l[2];  // what the weights are relative to (before the scale, in the segment's steps), and the sum of the lane's own
 
   int stage = 0;
   uint32_t phase = 0, met_phase = 0;
@@ -353,7 +352,7 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
           top[k] = s[0][k];
 #pragma unroll
           for (int i = 1; i < NR * NH; ++i) top[k] = fmaxf(top[k], s[i / NR][2 * (i % NR) + k]);
-          far |= __fmul_rn(top[k], qs[k]) - m[k] > (float)kHeadroom;
+          far |= (top[k] - m[k]) * qs[k] > (float)kHeadroom;
         }
         if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
@@ -363,8 +362,8 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
           float corr[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float mn = fmaxf(m[k], __fmul_rn(top[k], qs[k]));
-            corr[k] = m[k] == -INFINITY ? 1.f : ex2(m[k] - mn);  // nothing so far, or NaN: sums that stay what they are
+            const float mn = fmaxf(m[k], top[k]);
+            corr[k] = m[k] == -INFINITY ? 1.f : ex2((m[k] - mn) * qs[k]);  // nothing so far, or NaN: sums that stay what they are
             m[k] = mn;
             l[k] *= corr[k];
           }
@@ -373,20 +372,12 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[t][i] *= corr[i & 1];
         }
-        float by[2] = {qs[0], qs[1]}, b0 = (float)kWeightExp - m[0], b1 = (float)kWeightExp - m[1];
-        if (fmaxf(fabsf(m[0]), fabsf(m[1])) >= kExactBelow) {
-#pragma unroll
-          for (int hf = 0; hf < NH; ++hf)
-#pragma unroll
-            for (int i = 0; i < 2 * NR; ++i) s[hf][i] = __fmul_rn(s[hf][i], qs[i & 1]) - m[i & 1];
-          by[0] = by[1] = 1.f;
-          b0 = b1 = (float)kWeightExp;
-        }
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf)
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
-            const float w0 = ex2(fmaf(s[hf][2 * i], by[0], b0)), w1 = ex2(fmaf(s[hf][2 * i + 1], by[1], b1));
+            const float w0 = ex2(fmaf(s[hf][2 * i] - m[0], qs[0], (float)kWeightExp)),
+                        w1 = ex2(fmaf(s[hf][2 * i + 1] - m[1], qs[1], (float)kWeightExp));
             l[0] += w0;
             l[1] += w1;
             bp[hf][i] = movmatrix_t(pack_f16x2(w0, w1));
@@ -457,6 +448,8 @@ __device__ void Format4<D, FEW>::consume(const QuantDecodeArgs& a, uint8_t* stag
       }
     }
 
+#pragma unroll
+    for (int k = 0; k < 2; ++k) m[k] *= qs[k];  // log2 units, as the other warps' and the LSE
     if (sharers > 1) {
       // Combine the warps that split this head's positions (all consumer warps reach the segment end on
       // the same stage).
