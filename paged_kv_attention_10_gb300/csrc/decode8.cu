@@ -9,7 +9,8 @@
 //    into the softmax weights of the second product, w_j = p_j vs[j], which f16 must hold: they are
 //    formed as 2^(x_j + e_j - M) m_j 2^14 with vs[j] = m_j 2^e_j and M a running maximum of x_j + e_j of its
 //    own, so that they stay in [0, 2^15) whatever the scales' range.  The softmax's own sum keeps its
-//    own running maximum, and the two meet when a segment ends.
+//    own running maximum m, and the two meet when a segment ends.  M is held as its distance to m, and a weight's exponent
+//    is formed from x_j - m, exact next to m: of scores of 2^24 and more x_j + e_j would not hold e_j.
 //  * Both products run as f16 m16n8k16 MMAs with fp32 accumulators: e4m3 converts to f16 exactly, two
 //    values per instruction.  Q, bf16, is scaled per head by a power of two into f16's range (largest
 //    value in [2^14, 2^15)): exact for every value within 2^-31 of the largest.  Weights are rounded
@@ -97,7 +98,7 @@ __device__ void Format8<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
   float qs[2];        // score scale (log2 units) of the lane's heads head0 + 2c, + 1
   float o[NK][4];
   float m[2], l[2];   // running maximum of x and sum of 2^(x - m)
-  float mw[2];        // running maximum of x + e, which O is relative to
+  float mw[2];        // running maximum of x + e less m, which O is relative to beside m
 
   int stage = 0;
   uint32_t phase = 0, met_phase = 0;
@@ -228,7 +229,7 @@ __device__ void Format8<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
       }
       uint32_t bp[2][2];
       float x[2][4];
-      float mx[2] = {-INFINITY, -INFINITY}, mxe[2] = {-INFINITY, -INFINITY};
+      float mx[2] = {-INFINITY, -INFINITY}, mxe[2] = {-INFINITY, -INFINITY};  // of x, and of x + e less that
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -237,22 +238,30 @@ __device__ void Format8<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
           const float v = (s[hf][0][i] + s[hf][1][i]) * qs[i & 1] * ksc[row];
           x[hf][i] = g + 8 * row < nv ? v : -INFINITY;
           mx[i & 1] = fmaxf(mx[i & 1], x[hf][i]);
-          mxe[i & 1] = fmaxf(mxe[i & 1], x[hf][i] + ve[row]);
         }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mxe[i & 1] = fmaxf(mxe[i & 1], x[hf][i] - mx[i & 1] + ve[2 * hf + (i >> 1)]);
+      // Two lanes' maxima: what each says of x + e is moved to the larger of their x.  (Of lanes without a position both are
+      // -inf and the difference is NaN, which fmaxf drops.)
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
-          mxe[k] = fmaxf(mxe[k], __shfl_xor_sync(0xffffffffu, mxe[k], off));
+          const float ox = __shfl_xor_sync(0xffffffffu, mx[k], off), oxe = __shfl_xor_sync(0xffffffffu, mxe[k], off);
+          const float top = fmaxf(mx[k], ox);
+          mxe[k] = fmaxf(mx[k] - top + mxe[k], ox - top + oxe);
+          mx[k] = top;
         }
       }
       float corr[2], corrw[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float mn = fmaxf(m[k], mx[k]), wn = fmaxf(mw[k], mxe[k]);
+        const float mn = fmaxf(m[k], mx[k]);
+        const float held = m[k] - mn + mw[k], wn = fmaxf(held, mx[k] - mn + mxe[k]);
         corr[k] = ex2(m[k] - mn);
-        corrw[k] = ex2(mw[k] - wn);
+        corrw[k] = ex2(held - wn);
         m[k] = mn;
         mw[k] = wn;
         l[k] *= corr[k];
@@ -263,8 +272,9 @@ __device__ void Format8<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = 2 * hf + (i >> 1), k = i & 1;
-          l[k] += ex2(x[hf][i] - m[k]);
-          w[i] = ex2(x[hf][i] + ve[row] - mw[k]) * vm[row];
+          const float d = x[hf][i] - m[k];
+          l[k] += ex2(d);
+          w[i] = ex2(d + ve[row] - mw[k]) * vm[row];
         }
         bp[hf][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
         bp[hf][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
@@ -327,15 +337,16 @@ __device__ void Format8<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
             for (int w = si; w < left - keep; w += keep) {
               const float* ob = buf + (w * HV + hv) * MF * 32;
               auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
+              auto moved = [](float m, float top, float w) { return m == -INFINITY ? -INFINITY : m - top + w; };
               int e = 0;
               float fa[2], fb[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const float om = ob[(e++) * 32], ol = ob[(e++) * 32], ow = ob[(e++) * 32];
-                const float mn = fmaxf(m[k], om), wn = fmaxf(mw[k], ow);
+                const float mn = fmaxf(m[k], om), wa = moved(m[k], mn, mw[k]), wb = moved(om, mn, ow), wn = fmaxf(wa, wb);
                 l[k] = l[k] * weight(m[k], mn) + ol * weight(om, mn);
-                fa[k] = weight(mw[k], wn);
-                fb[k] = weight(ow, wn);
+                fa[k] = weight(wa, wn);
+                fb[k] = weight(wb, wn);
                 m[k] = mn;
                 mw[k] = wn;
               }
@@ -368,7 +379,7 @@ __device__ void Format8<D>::consume(const QuantDecodeArgs& a, uint8_t* stages, S
           lt += __shfl_xor_sync(0xffffffffu, lt, 8);
           lt += __shfl_xor_sync(0xffffffffu, lt, 16);
           const int col = head0 + 2 * c + k;  // query head within the group
-          const float inv = ex2(mw[k] - m[k]) / lt;
+          const float inv = ex2(mw[k]) / lt;
           const float unit = exp2i(-kWeightExp);  // first of the two: inv can be as small as fp32 goes
           const float lse_v = (m[k] + log2f(lt)) * kLn2;
           if (col < G) {
