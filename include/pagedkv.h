@@ -23,6 +23,8 @@
  *                 requests' lists (shared prefixes).
  *   GQA           query head h reads KV head h / (num_q_heads / num_kv_heads).
  *   LSE           natural log of sum_j exp(sm_scale * q . k_j), fp32.
+ *   scores        sm_scale * q . k_j, fp32.  The calls with several query rows a request (extend, tree, the cascade's shared
+ *                 part) are for scores below 2^29 in size; above, their rows may be zeros or NaN.
  *
  * Calls are asynchronous on the given stream (a cudaStream_t passed as void*, NULL = legacy
  * default stream), never synchronise the host and never allocate: every scratch buffer

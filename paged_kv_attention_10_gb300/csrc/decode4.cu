@@ -34,10 +34,10 @@
 // Bound by HBM in the long run (32/8 heads of 128, page size 16: from 8 requests of 32768 positions to 8 of 98304 a
 // position more costs what it does at 6.7 TB/s, 98 % of what a device copy reaches), and by about 12 us that do not
 // depend on the length: the loads that come before the first stage 3, the CTAs' different speeds 2, the last stage's
-// step 1.4, the grid's end 1.7, the merge 2.  8 requests of 32768 positions 55.5 us, 302 MB at 5.4 TB/s (80 %); 256 of 512
-// to 4096 120 us, 5.7 TB/s (84 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 55 % used, the conversions'
-// pipe 48 %, the tensor pipe 28 %.  32 requests of 100 to 640 positions, 16/8 heads, at page size 1 11.3 us; 4 short ones of
-// 14/2 heads of 64 7.3 us, a chain of latencies.  With head_dim 64 the softmax of a position, the
+// step 1.4, the grid's end 1.7, the merge 2.  8 requests of 32768 positions 56 us, 302 MB at 5.4 TB/s (80 %); 256 of 512
+// to 4096 120 us, 5.7 TB/s (84 %).  DRAM reads are the cache's bytes (302 of 302 MB), the issue slots 56 % used, the conversions'
+// pipe 48 %, the tensor pipe 28 %.  32 requests of 100 to 640 positions, 16/8 heads, at page size 1 11.5 us; 4 short ones of
+// 14/2 heads of 64 7.5 us, a chain of latencies.  With head_dim 64 the softmax of a position, the
 // scales and the loop's frame cost what they cost with 128, so the consumers do not keep up: 16 requests of 32000 positions,
 // 16/8 heads 59 us at page size 32, 62 at 16, of 43.5 that their bytes take and 52 that they take to arrive.  (28/4 heads of 128,
 // 64 requests of 1000 to 6000: 34.6 us, 29.6 to arrive, 19.0 for the bytes.)

@@ -27,10 +27,10 @@
 //    the maxima, the rescaling of O and the barrier round are paid half as often.
 //  * The rest is the bf16 decode's plan, shared with the 4-bit cache (quant_decode.cuh), with boxes in the 128- or
 //    64-byte swizzle.
-// Measured with 32/8 heads of 128 at page size 16: 8 requests of 32768 positions 89 us, 6.2 TB/s, 92 % of
-// what a device copy reaches; 256 requests of 512 to 4096 positions 194 to 197 us, 93 %.  DRAM reads are the cache's
+// Measured with 32/8 heads of 128 at page size 16: 8 requests of 32768 positions 90 us, 6.2 TB/s, 91 % of
+// what a device copy reaches; 256 requests of 512 to 4096 positions 195 to 196 us, 94 %.  DRAM reads are the cache's
 // bytes (554 MB of 554), the tensor pipe is 18 % busy, 43 % of the issue slots are used.  Small KV head counts are
-// bound by the producers' issue instead: one head of 128, 720000 positions, 49 us at page size 16, 40 at
+// bound by the producers' issue instead: one head of 128, 720000 positions, 50 us at page size 16, 41 at
 // 64 and 151 at 1 of the 28 that the bytes take; two heads at page size 1 118 of 28.
 #include "quant_decode.cuh"
 
