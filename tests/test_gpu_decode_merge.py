@@ -89,3 +89,46 @@ def test_what_a_cta_that_gave_up_leaves(merge, lib, slices, warps, end):
     assert err == lib.DEVERR_TIMEOUT
     assert np.all(out[-1] == 7) and np.all(lse[-1] == 7)
     p.verify(out, lse, np.arange(len(slices) - 1))
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,page,first", [(4, 14, 2, 64, 16, 40), (8, 32, 8, 128, 16, 900), (32, 16, 8, 128, 1, 100),
+                                                   (40, 8, 1, 128, 16, 300)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_lengths_that_grow_between_decodes(lib, bits, B, Hq, Hkv, D, page, first):
+    """Each step a kernel raises the lengths in place and the next decode starts beside it: the results are those of steps that are
+    waited for one by one."""
+    steps = 150
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    need = -(-(first + steps) // page)
+    head = (B * need, page, Hkv)
+    u8 = lambda *s, lo=0, hi=256: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda", generator=gen)  # noqa: E731
+    if bits == 4:
+        pool = [u8(*head, D // 2), u8(*head, D // 2), u8(*head, D // 16, lo=0x30, hi=0x48), u8(*head, D // 16, lo=0x30, hi=0x48)]
+        call, size, extra = lib.paged_decode_fp4, lib.decode_fp4_workspace_size, dict(k_global=0.05, v_global=0.01)
+    else:
+        pool = [u8(*head, D, hi=0x40).view(torch.float8_e4m3fn) for _ in range(2)]
+        pool += [torch.rand(head, device="cuda", generator=gen) + 0.5 for _ in range(2)]
+        call, size, extra = lib.paged_decode_fp8, lib.decode_fp8_workspace_size, {}
+    indptr = torch.arange(B + 1, dtype=torch.int32, device="cuda") * need
+    pages = torch.randperm(B * need, device="cuda", generator=gen).int()
+    q = torch.randn(B, Hq, D, device="cuda", generator=gen).to(torch.bfloat16)
+    ws = torch.empty(size(B, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        lens = torch.full((B,), first, dtype=torch.int32, device="cuda")
+        out = torch.empty(steps, B, Hq, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(steps, B, Hq, device="cuda")
+        for t in range(steps):
+            lens.add_(1)
+            if wait:
+                torch.cuda.synchronize()
+            call(q, *pool, indptr, pages, lens, D ** -0.5, out=out[t], lse=lse[t], workspace=ws, **extra)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return out, lse
+
+    want = run(True)
+    assert torch.isfinite(want[1]).all() and not torch.equal(want[0][0], want[0][-1])
+    for _ in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(want, run(False)))
